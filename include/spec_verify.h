@@ -294,6 +294,130 @@ int spec_verify_commit(const int32_t* out_tokens, const int32_t* out_num_accepte
                        int32_t* new_kv_len, int32_t* anchor, int32_t* n_free,
                        int32_t* free_slots, void* stream);
 
+/* ------------------------------------------------- training the drafter
+ *
+ * What a drafter is trained with, over the same vocabulary rows: the record of
+ * a target row that a drafter learns from, the distillation loss against it,
+ * and the cross entropy of a linear head whose logits are never stored.
+ *
+ * Conventions of these calls
+ *   - Matrices are given by a pointer and a row stride in elements, at least the
+ *     row's length; elements of a row are consecutive. Any stride and any
+ *     alignment to the element size is accepted; rows that all start on 16
+ *     bytes are fastest.
+ *   - Sums, maxima and losses are float32 whatever the inputs' type; gradients
+ *     are rounded once to the type of what they are gradients of.
+ *   - No result depends on the order in which workgroups run: a call repeated on
+ *     the same inputs gives the same bits.
+ *   - Workspaces need no initialisation, are 256-byte aligned, hold nothing
+ *     between calls, and may be reused by later calls on the same stream; calls
+ *     (and captured graphs) that may run concurrently need separate ones.
+ *     A workspace of 0 bytes may be NULL. */
+
+/* Largest number of kept logits per row. */
+#define SV_MAX_TOP 1024
+
+/* The K largest logits of every row, in descending order, the lower id first
+ * among equal values (-0 == +0), and the log-normaliser of the whole row.
+ *   logits      [R][V] of dtype, row stride logits_stride >= V; the target
+ *               logits of spec_verify_sample are R = B*(gamma+1) rows.
+ *   temperature > 0 and finite; only out_lse depends on it.
+ *   out_ids     [R][K] int32 ids, out_values [R][K] float their logits (not
+ *               tempered). -inf and NaN logits are not candidates: a row with
+ *               fewer than K candidates is filled up with id -1, value -inf.
+ *   out_lse     [R] float log sum_v exp(logit_v / temperature), or NULL; -inf
+ *               for a row of -inf only, NaN for a row holding NaN or +inf.
+ * Limits: 1 <= R < 2^31, 1 <= K <= SV_MAX_TOP, K <= V, V < 2^31 and
+ * at most 2^31 - 1 workgroups. Errors: SV_EINVAL, SV_EDTYPE,
+ * SV_EWORKSPACE, SV_ESIZE, SV_EHIP. */
+size_t spec_verify_top_logits_workspace_bytes(int32_t R, int32_t V, int32_t K);
+int spec_verify_top_logits(const void* logits, int64_t logits_stride, sv_dtype dtype, int32_t R,
+                           int32_t V, int32_t K, float temperature, int32_t* out_ids,
+                           float* out_values, float* out_lse, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* Distillation from a teacher's kept logits. With T = temperature,
+ *   p_k = exp(teacher_logits_k / T - L),
+ *   L   = log sum_k exp(teacher_logits_k / T) over the row's slots, or
+ *         teacher_lse[r] (then the kept slots keep their share of the whole row),
+ *   q   = softmax(logits / T) over the vocabulary, P = sum_k p_k:
+ *   loss = sum_k p_k (log p_k - log q_{id_k}),
+ *   d loss / d logit_v = (P q_v - sum_{k: id_k = v} p_k) / T.
+ *   logits         [R][V] of dtype: the drafter's (student's) rows.
+ *   teacher_ids    [R][K] int32, teacher_logits [R][K] float, contiguous, in any
+ *                  order, as spec_verify_top_logits writes them. A slot whose id
+ *                  lies outside [0, V) or whose tempered logit is -inf is empty;
+ *                  an id may appear more than once: its masses add up.
+ *   teacher_lse    [R] float (spec_verify_top_logits at the same temperature), or
+ *                  NULL.
+ *   row_weight     [R] float weights of out_grad (d total / d loss_r), or NULL (1).
+ *   out_loss       [R] float, not weighted.
+ *   out_stats      [R][2] float: the row's largest logit m, and
+ *                  log sum_v exp((logit_v - m) / T).
+ *   out_grad       [R][V] of dtype, row stride grad_stride >= V, or NULL (loss only).
+ *                  It may be `logits` itself with the same stride (every value is
+ *                  read before it is overwritten); any other overlap is an error
+ *                  of the caller. Elements behind V are left as they are.
+ * A row without a filled slot has loss 0 and gradient 0. A row whose
+ * logits are all -inf has gradient 0, and loss +inf against a filled slot, as
+ * has a row that gives a kept token of positive mass -inf. NaN or +inf among a
+ * row's logits, or NaN in its slots, make its loss and gradient NaN.
+ * Limits: 1 <= K <= SV_MAX_TOP, 1 <= R, V < 2^31. */
+size_t spec_verify_distill_workspace_bytes(int32_t R, int32_t V);
+int spec_verify_distill(const void* logits, int64_t logits_stride, sv_dtype dtype, int32_t R,
+                        int32_t V, const int32_t* teacher_ids, const float* teacher_logits,
+                        const float* teacher_lse, int32_t K, float temperature,
+                        const float* row_weight, float* out_loss, float* out_stats, void* out_grad,
+                        int64_t grad_stride, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The gradient alone, from the statistics an earlier spec_verify_distill call
+ * wrote for the same rows, teacher and temperature; grad_loss [R] float is the
+ * gradient of each row's loss (NULL: 1). Needs no workspace. */
+int spec_verify_distill_backward(const void* logits, int64_t logits_stride, sv_dtype dtype,
+                                 int32_t R, int32_t V, const int32_t* teacher_ids,
+                                 const float* teacher_logits, const float* teacher_lse, int32_t K,
+                                 float temperature, const float* stats, const float* grad_loss,
+                                 void* out_grad, int64_t grad_stride, void* stream);
+
+/* Softmax cross entropy of a linear head over the vocabulary, without storing
+ * the logits z = hidden weight^T:
+ *   loss_n = log sum_v exp(z_nv) - z_{n, label_n}.
+ *   hidden [N][D] and weight [V][D] of dtype (row strides >= D), labels [N] int32.
+ *   A row whose label lies outside [0, V) (such as -100) is left out: loss 0, no
+ *   gradient.
+ *   out_loss  [N] float; out_stats [N][2] float: the row's largest logit m, and
+ *             log sum_v exp(z_nv - m), also for the rows left out.
+ * bfloat16 products are exact and summed in float32. float32 operands are taken as
+ * three bfloat16 parts each, whose products down to 2^-24 of the largest are
+ * summed in float32.
+ * Inputs are finite; NaN or infinities make the rows (and with them the
+ * gradients) they meet NaN.
+ * Limits: 1 <= N, V < 2^31 - 256, 1 <= D <= 2^24. */
+size_t spec_verify_linear_ce_workspace_bytes(int32_t N, int32_t D, int32_t V, sv_dtype dtype);
+int spec_verify_linear_ce(const void* hidden, int64_t hidden_stride, const void* weight,
+                          int64_t weight_stride, sv_dtype dtype, const int32_t* labels, int32_t N,
+                          int32_t D, int32_t V, float* out_loss, float* out_stats, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* Its gradients, from the statistics an earlier spec_verify_linear_ce call wrote
+ * for the same inputs. The logits are made again, a piece of the vocabulary at a
+ * time: with dz_nv = grad_loss_n (softmax(z)_nv - [v = label_n]),
+ *   out_grad_hidden [N][D] = dz weight,  out_grad_weight [V][D] = dz^T hidden,
+ * both of dtype, with row strides >= D; either may be NULL (then not computed),
+ * not both. grad_loss [N] float, or NULL (1).
+ * For bfloat16, dz is rounded to bfloat16 before its products, which are summed
+ * in float32. Outputs must not overlap inputs. Elements behind D are left as
+ * they are. */
+size_t spec_verify_linear_ce_backward_workspace_bytes(int32_t N, int32_t D, int32_t V,
+                                                      sv_dtype dtype, int want_grad_hidden,
+                                                      int want_grad_weight);
+int spec_verify_linear_ce_backward(const void* hidden, int64_t hidden_stride, const void* weight,
+                                   int64_t weight_stride, sv_dtype dtype, const int32_t* labels,
+                                   const float* stats, const float* grad_loss, int32_t N, int32_t D,
+                                   int32_t V, void* out_grad_hidden, int64_t grad_hidden_stride,
+                                   void* out_grad_weight, int64_t grad_weight_stride,
+                                   void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* spec_verify_strerror(int status);
 

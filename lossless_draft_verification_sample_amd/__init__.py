@@ -1,9 +1,10 @@
-"""Lossless speculative-sampling verifier for AMD MI355X (gfx950).
+"""Lossless speculative-sampling verifier for AMD MI355X (gfx950), and the
+losses its drafter is trained with.
 
 Thin Python binding over the C interface of include/spec_verify.h. The
 functions below only marshal arguments (device pointers of torch tensors, the
-current HIP stream) and allocate outputs; every step of verification runs in
-the HIP kernels of libspecverify.so. PyTorch supplies device memory and
+current HIP stream) and allocate outputs; every step runs in the HIP kernels of
+libspecverify.so. PyTorch supplies device memory and
 streams. If the library is missing, every call raises.
 """
 
@@ -27,6 +28,7 @@ from ._lib import (  # noqa: F401
     SV_FLAG_TOKEN_RANGE,
     SV_MAX_BANNED,
     SV_MAX_HISTORY,
+    SV_MAX_TOP,
     SV_NOALLOC_SCRATCH_BYTES,
     SV_OK,
     SvRequests,
@@ -38,6 +40,10 @@ SampleOut = namedtuple("SampleOut",
                        defaults=(None, None))
 GreedyOut = namedtuple("GreedyOut", "tokens num_accepted flags accept_hist", defaults=(None,))
 CommitOut = namedtuple("CommitOut", "new_kv_len anchor n_free free_slots")
+TopLogitsOut = namedtuple("TopLogitsOut", "ids values lse")
+DistillOut = namedtuple("DistillOut", "loss stats grad")
+LinearCeOut = namedtuple("LinearCeOut", "loss stats")
+LinearCeGrads = namedtuple("LinearCeGrads", "hidden weight")
 # Per-request settings of a mixed batch (see sv_requests in include/spec_verify.h):
 # gamma [B] int32, target / draft [B, 12] uint8 sv_sampler records (sampler_array),
 # banned_draft [B, m] int32, history [B, H] int32, penalty / penalty_draft [B]
@@ -328,6 +334,294 @@ def spec_verify_commit(tokens, num_accepted, kv_len, slots=None, gamma_b=None, o
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_verify_commit")
     return out
+
+
+# ------------------------------------------------------- training the drafter
+
+
+def _matrix(t, name, device=None, dtype=None, cols=None):
+    """(pointer, row stride) of a tensor whose last dimension is consecutive and
+    whose leading dimensions are rows at one stride."""
+    torch = _torch()
+    if not torch.is_tensor(t) or not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() < 2 or t.numel() == 0:
+        raise ValueError(f"{name} must have at least one row and one column, got {tuple(t.shape)}")
+    if cols is not None and t.shape[-1] != cols:
+        raise ValueError(f"{name} must have rows of {cols}, got {tuple(t.shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have consecutive elements in a row")
+    stride, rows = None, 1
+    for size, step in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if stride is None:
+            stride = step
+        elif step != stride * rows:
+            raise ValueError(f"{name} must have its rows at one stride")
+        rows *= size
+    if stride is None:
+        stride = t.shape[-1]   # a single row
+    if stride < t.shape[-1]:
+        raise ValueError(f"{name} must not have overlapping rows")
+    return t.data_ptr(), stride
+
+
+def _vector(t, name, dtype, shape, device):
+    """Pointer of a contiguous tensor (or None) of this type, shape and device."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    p = _dev_ptr(t, name, dtype)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    return p
+
+
+def _on(device, stream):
+    """The device as current, and the call's stream on it: (context, handle, stream)."""
+    import contextlib
+    torch = _torch()
+    with torch.cuda.device(device):
+        handle, strm = _stream(stream)
+    ctx = contextlib.ExitStack()
+    ctx.enter_context(torch.cuda.device(device))
+    ctx.enter_context(torch.cuda.stream(strm))
+    return ctx, handle
+
+
+def _space(workspace, need, device):
+    """(pointer, bytes) of a workspace, allocated when the caller gave none; the
+    tensor comes along so that it lives until the call is queued."""
+    torch = _torch()
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = torch.empty((need,), dtype=torch.uint8, device=device)
+    elif workspace.device != device:
+        raise ValueError(f"workspace is on {workspace.device}, not on {device}")
+    return _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(), workspace
+
+
+def spec_verify_top_logits_workspace_bytes(R, V, K):
+    return int(_lib.load().spec_verify_top_logits_workspace_bytes(int(R), int(V), int(K)))
+
+
+def spec_verify_top_logits(logits, k, temperature=1.0, want_lse=True, workspace=None, out=None,
+                           stream=None, lib=None):
+    """The k largest logits of every row, descending, the lower id first among
+    equals, and the row's log-normaliser at `temperature` (see
+    include/spec_verify.h): what a drafter is distilled from.
+
+    logits [..., V] bf16 or fp32, rows at one stride (the target logits
+    [B, gamma+1, V] of spec_verify_sample as they are, or columns cut from a wider
+    buffer).
+    Returns TopLogitsOut(ids [..., k] int32, values [..., k] float32, lse [...]
+    float32 or None).
+    """
+    torch = _torch()
+    lib = lib or _lib.load()
+    ptr, stride = _matrix(logits, "logits")
+    dt, dev, lead, V = _dtype_code(logits), logits.device, tuple(logits.shape[:-1]), logits.shape[-1]
+    R, k = logits.numel() // V, int(k)
+    ctx, handle = _on(dev, stream)
+    with ctx:
+        if out is None:
+            if k < 1:
+                raise SpecVerifyError(SV_EINVAL, "spec_verify_top_logits")
+            out = TopLogitsOut(
+                torch.empty((*lead, k), dtype=torch.int32, device=dev),
+                torch.empty((*lead, k), dtype=torch.float32, device=dev),
+                torch.empty(lead, dtype=torch.float32, device=dev) if want_lse else None)
+        ws, ws_bytes, keep = _space(
+            workspace, lib.spec_verify_top_logits_workspace_bytes(R, V, k), dev)
+        rc = lib.spec_verify_top_logits(
+            ptr, stride, dt, R, V, k, float(temperature),
+            _vector(out.ids, "out.ids", torch.int32, (*lead, k), dev),
+            _vector(out.values, "out.values", torch.float32, (*lead, k), dev),
+            _vector(out.lse, "out.lse", torch.float32, lead, dev), ws, ws_bytes, handle)
+    del keep
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_verify_top_logits")
+    return out
+
+
+def spec_verify_distill_workspace_bytes(R, V):
+    return int(_lib.load().spec_verify_distill_workspace_bytes(int(R), int(V)))
+
+
+def _distill_inputs(logits, teacher_ids, teacher_logits, teacher_lse):
+    torch = _torch()
+    ptr, stride = _matrix(logits, "logits")
+    dt, dev, lead, V = _dtype_code(logits), logits.device, tuple(logits.shape[:-1]), logits.shape[-1]
+    if teacher_ids.dim() < 1 or tuple(teacher_ids.shape[:-1]) != lead:
+        raise ValueError(f"teacher_ids must be {lead} rows of kept ids, got {tuple(teacher_ids.shape)}")
+    K = int(teacher_ids.shape[-1])
+    return (ptr, stride, dt, logits.numel() // V, V,
+            _vector(teacher_ids, "teacher_ids", torch.int32, (*lead, K), dev),
+            _vector(teacher_logits, "teacher_logits", torch.float32, (*lead, K), dev),
+            _vector(teacher_lse, "teacher_lse", torch.float32, lead, dev), K), dev, lead
+
+
+def _grad_out(t, like, name):
+    """A gradient's tensor, its pointer and row stride; a new one when None."""
+    if t is None:
+        t = _torch().empty(like.shape, dtype=like.dtype, device=like.device)
+    elif tuple(t.shape) != tuple(like.shape):
+        raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
+    return (t, *_matrix(t, name, like.device, like.dtype))
+
+
+def spec_verify_distill(logits, teacher_ids, teacher_logits, temperature=1.0, teacher_lse=None,
+                        row_weight=None, want_grad=False, workspace=None, out=None, stream=None,
+                        lib=None):
+    """Distillation loss of student rows against a teacher's kept logits, and
+    with want_grad its gradient in the same call (see include/spec_verify.h).
+
+    logits [..., V] bf16 or fp32 (rows at one stride), teacher_ids [..., K] int32
+    and teacher_logits [..., K] float32 as spec_verify_top_logits returns them,
+    teacher_lse [...] float32 (its lse at the same temperature) or None to
+    renormalise over the kept ids; row_weight [...] float32 scales the gradient's
+    rows (not the loss). out: a DistillOut; its grad may be `logits` itself.
+    Returns DistillOut(loss [...], stats [..., 2], grad like logits or None);
+    stats serve spec_verify_distill_backward.
+    """
+    torch = _torch()
+    lib = lib or _lib.load()
+    args, dev, lead = _distill_inputs(logits, teacher_ids, teacher_logits, teacher_lse)
+    ctx, handle = _on(dev, stream)
+    with ctx:
+        if out is None:
+            out = DistillOut(torch.empty(lead, dtype=torch.float32, device=dev),
+                             torch.empty((*lead, 2), dtype=torch.float32, device=dev), None)
+        grad, gptr, gstride = out.grad, None, 0
+        if want_grad or grad is not None:
+            grad, gptr, gstride = _grad_out(grad, logits, "out.grad")
+            out = out._replace(grad=grad)
+        ws, ws_bytes, keep = _space(
+            workspace, lib.spec_verify_distill_workspace_bytes(args[3], args[4]), dev)
+        rc = lib.spec_verify_distill(
+            *args, float(temperature),
+            _vector(row_weight, "row_weight", torch.float32, lead, dev),
+            _vector(out.loss, "out.loss", torch.float32, lead, dev),
+            _vector(out.stats, "out.stats", torch.float32, (*lead, 2), dev), gptr, gstride,
+            ws, ws_bytes, handle)
+    del keep
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_verify_distill")
+    return out
+
+
+def spec_verify_distill_backward(logits, teacher_ids, teacher_logits, stats, grad_loss=None,
+                                 temperature=1.0, teacher_lse=None, out=None, stream=None, lib=None):
+    """Gradient of spec_verify_distill's loss from its stats; grad_loss [...]
+    float32 or None (1). out: the gradient's tensor, which may be `logits`.
+    Returns the gradient, like logits."""
+    torch = _torch()
+    lib = lib or _lib.load()
+    args, dev, lead = _distill_inputs(logits, teacher_ids, teacher_logits, teacher_lse)
+    ctx, handle = _on(dev, stream)
+    with ctx:
+        out, gptr, gstride = _grad_out(out, logits, "out")
+        if stats is None:
+            raise ValueError("stats are those of spec_verify_distill")
+        rc = lib.spec_verify_distill_backward(
+            *args, float(temperature), _vector(stats, "stats", torch.float32, (*lead, 2), dev),
+            _vector(grad_loss, "grad_loss", torch.float32, lead, dev), gptr, gstride, handle)
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_verify_distill_backward")
+    return out
+
+
+def spec_verify_linear_ce_workspace_bytes(N, D, V, dtype=SV_BF16):
+    return int(_lib.load().spec_verify_linear_ce_workspace_bytes(int(N), int(D), int(V), int(dtype)))
+
+
+def spec_verify_linear_ce_backward_workspace_bytes(N, D, V, dtype=SV_BF16, want_hidden=True,
+                                                   want_weight=True):
+    return int(_lib.load().spec_verify_linear_ce_backward_workspace_bytes(
+        int(N), int(D), int(V), int(dtype), int(bool(want_hidden)), int(bool(want_weight))))
+
+
+def _ce_inputs(hidden, weight, labels):
+    torch = _torch()
+    hptr, hstride = _matrix(hidden, "hidden")
+    dt, dev, lead, D = _dtype_code(hidden), hidden.device, tuple(hidden.shape[:-1]), hidden.shape[-1]
+    if weight.dim() != 2:
+        raise ValueError(f"weight must be [V, D], got {tuple(weight.shape)}")
+    wptr, wstride = _matrix(weight, "weight", dev, hidden.dtype, D)
+    if labels is None:
+        raise ValueError("labels must be a device tensor")
+    return (hptr, hstride, wptr, wstride, dt,
+            _vector(labels, "labels", torch.int32, lead, dev)), hidden.numel() // D, dev, lead
+
+
+def spec_verify_linear_ce(hidden, weight, labels, workspace=None, out=None, stream=None, lib=None):
+    """Softmax cross entropy of a linear head without storing its logits (see
+    include/spec_verify.h).
+
+    hidden [..., D] and weight [V, D] (bf16 or fp32, rows at one stride each),
+    labels [...] int32; rows whose label lies outside [0, V), such as -100, are
+    left out (loss 0).
+    Returns LinearCeOut(loss [...], stats [..., 2]), both float32; stats serve
+    spec_verify_linear_ce_backward.
+    """
+    torch = _torch()
+    lib = lib or _lib.load()
+    args, N, dev, lead = _ce_inputs(hidden, weight, labels)
+    V, D = weight.shape
+    ctx, handle = _on(dev, stream)
+    with ctx:
+        if out is None:
+            out = LinearCeOut(torch.empty(lead, dtype=torch.float32, device=dev),
+                              torch.empty((*lead, 2), dtype=torch.float32, device=dev))
+        ws, ws_bytes, keep = _space(
+            workspace, lib.spec_verify_linear_ce_workspace_bytes(N, D, V, args[4]), dev)
+        rc = lib.spec_verify_linear_ce(
+            *args, N, D, V, _vector(out.loss, "out.loss", torch.float32, lead, dev),
+            _vector(out.stats, "out.stats", torch.float32, (*lead, 2), dev), ws, ws_bytes, handle)
+    del keep
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_verify_linear_ce")
+    return out
+
+
+def spec_verify_linear_ce_backward(hidden, weight, labels, stats, grad_loss=None, want_hidden=True,
+                                   want_weight=True, workspace=None, out=None, stream=None,
+                                   lib=None):
+    """Gradients of spec_verify_linear_ce's loss from its stats; grad_loss [...]
+    float32 or None (1). want_hidden / want_weight: which ones (a frozen head needs
+    the first alone). out: a LinearCeGrads of tensors for those wanted.
+    Returns LinearCeGrads(hidden, weight), None where not wanted."""
+    torch = _torch()
+    lib = lib or _lib.load()
+    args, N, dev, lead = _ce_inputs(hidden, weight, labels)
+    V, D = weight.shape
+    if stats is None:
+        raise ValueError("stats are those of spec_verify_linear_ce")
+    ctx, handle = _on(dev, stream)
+    with ctx:
+        gh, ghp, ghs, gw, gwp, gws = None, None, 0, None, None, 0
+        if want_hidden:
+            gh, ghp, ghs = _grad_out(out and out.hidden, hidden, "out.hidden")
+        if want_weight:
+            gw, gwp, gws = _grad_out(out and out.weight, weight, "out.weight")
+        ws, ws_bytes, keep = _space(
+            workspace, lib.spec_verify_linear_ce_backward_workspace_bytes(
+                N, D, V, args[4], int(bool(want_hidden)), int(bool(want_weight))), dev)
+        rc = lib.spec_verify_linear_ce_backward(
+            *args, _vector(stats, "stats", torch.float32, (*lead, 2), dev),
+            _vector(grad_loss, "grad_loss", torch.float32, lead, dev), N, D, V, ghp, ghs, gwp, gws,
+            ws, ws_bytes, handle)
+    del keep
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_verify_linear_ce_backward")
+    return LinearCeGrads(gh, gw)
 
 
 def bench_profile_start(max_launches_per_kernel):

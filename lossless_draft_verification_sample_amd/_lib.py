@@ -35,6 +35,7 @@ SV_FLAG_BAD_PARAM = 32
 
 SV_MAX_BANNED = 2048
 SV_MAX_HISTORY = 1984
+SV_MAX_TOP = 1024
 
 # kernel indices of sv_bench_profile_stop (csrc/sv_bench_timing.h)
 SV_K_ROW_STATS = 0
@@ -64,7 +65,11 @@ class SvRequests(ctypes.Structure):
 _c = ctypes
 _vp = _c.c_void_p
 _i32 = _c.c_int32
+_i64 = _c.c_int64
 _u64 = _c.c_uint64
+_f32 = _c.c_float
+_size = _c.c_size_t
+_int = _c.c_int
 
 SIGNATURES = {
     "spec_verify_workspace_bytes": (_c.c_size_t, [_i32, _i32, _i32]),
@@ -79,6 +84,20 @@ SIGNATURES = {
                                       _vp, _vp, _vp]),
     "spec_verify_commit": (_c.c_int, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp,
                                       _vp]),
+    "spec_verify_top_logits_workspace_bytes": (_size, [_i32, _i32, _i32]),
+    "spec_verify_top_logits": (_int, [_vp, _i64, _int, _i32, _i32, _i32, _f32, _vp, _vp, _vp, _vp,
+                                      _size, _vp]),
+    "spec_verify_distill_workspace_bytes": (_size, [_i32, _i32]),
+    "spec_verify_distill": (_int, [_vp, _i64, _int, _i32, _i32, _vp, _vp, _vp, _i32, _f32, _vp, _vp,
+                                   _vp, _vp, _i64, _vp, _size, _vp]),
+    "spec_verify_distill_backward": (_int, [_vp, _i64, _int, _i32, _i32, _vp, _vp, _vp, _i32, _f32,
+                                            _vp, _vp, _vp, _i64, _vp]),
+    "spec_verify_linear_ce_workspace_bytes": (_size, [_i32, _i32, _i32, _int]),
+    "spec_verify_linear_ce": (_int, [_vp, _i64, _vp, _i64, _int, _vp, _i32, _i32, _i32, _vp, _vp,
+                                     _vp, _size, _vp]),
+    "spec_verify_linear_ce_backward_workspace_bytes": (_size, [_i32, _i32, _i32, _int, _int, _int]),
+    "spec_verify_linear_ce_backward": (_int, [_vp, _i64, _vp, _i64, _int, _vp, _vp, _vp, _i32, _i32,
+                                              _i32, _vp, _i64, _vp, _i64, _vp, _size, _vp]),
     "spec_verify_strerror": (_c.c_char_p, [_c.c_int]),
 }
 BENCH_SIGNATURES = {

@@ -24,7 +24,8 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 OBJ_DIR = os.path.join(ROOT, "_build")
 LIB_NAME = "libspecverify.so"
 BENCH_LIB_NAME = "libspecverify_bench.so"
-KERNEL_SOURCES = ["row_stats.hip", "verify.hip", "overlap.hip", "greedy.hip", "commit.hip"]
+KERNEL_SOURCES = ["row_stats.hip", "verify.hip", "overlap.hip", "greedy.hip", "commit.hip",
+                  "top_logits.hip", "distill.hip", "linear_ce.hip", "train_api.cpp"]
 API_SOURCE = "api.cpp"
 # HBM read-bandwidth calibration (bench.py --read-ceiling); not on the path
 CALIB_LIB_NAME = "libsvcalib.so"

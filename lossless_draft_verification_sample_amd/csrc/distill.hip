@@ -1,0 +1,269 @@
+// Distillation of a student row z from a teacher's kept logits (t_k, id_k):
+//   p_k = exp(t_k / T - L),  L = log sum_k exp(t_k / T) or the teacher's own
+//   log-normaliser;  q = softmax(z / T) over the vocabulary;  P = sum_k p_k
+//   loss = sum_k p_k (log p_k - log q_{id_k})
+//   d loss / d z_v = (P q_v - p_v) / T,  p_v = sum of the p_k with id_k = v.
+// The row's statistics are its largest logit m and logsum = log sum exp((z - m) / T),
+// kept apart: their sum would lose logsum where m is large.
+//
+// Bound: reading the row for the loss, and reading and writing it for the
+// gradient. The dense part P q_v is streamed; the K slots are written after it
+// by the workgroup that owns their part of the row, so nothing is added
+// atomically and repeated ids give one sum.
+
+#include "sv_train.hpp"
+
+namespace sv {
+
+namespace {
+
+constexpr int DIS_THREADS = 512;
+
+struct DisLds {
+  int32_t id[DIS_MAX_K];
+  float p[DIS_MAX_K];
+  float zid[DIS_MAX_K];     // student logits of the slots, read before they are overwritten
+  float red[DIS_THREADS / WAVE];
+  MaxSum scratch[DIS_THREADS / WAVE];
+};
+
+// Teacher's masses of row r into LDS (an empty slot: id -1, mass 0); returns P.
+// log p_k - what the loss needs besides - comes back through L.zid.
+__device__ float teacher(const DistillArgs& a, DisLds& L, int64_t r) {
+  const int tid = threadIdx.x;
+  float tm = -INFINITY;
+  for (int k = tid; k < a.K; k += DIS_THREADS) {
+    const int32_t id = a.ids[r * a.K + k];
+    const float t = a.tl[r * a.K + k] / a.temperature;
+    const bool ok = id >= 0 && id < a.V && t != -INFINITY;
+    L.id[k] = ok ? id : -1;
+    L.p[k] = t;
+    if (ok) tm = fmaxf(tm, t);
+  }
+  float lse;
+  if (a.tlse) {
+    lse = a.tlse[r];
+  } else {
+    tm = block_max<DIS_THREADS>(tm, L.red);
+    float s = 0.0f;
+    for (int k = tid; k < a.K; k += DIS_THREADS)
+      if (L.id[k] >= 0) s += expf(L.p[k] - tm);
+    s = block_sum<DIS_THREADS>(s, L.red);
+    lse = tm + logf(s);
+  }
+  float P = 0.0f;
+  for (int k = tid; k < a.K; k += DIS_THREADS) {
+    const float lp = L.p[k] - lse;
+    L.zid[k] = lp;
+    L.p[k] = L.id[k] >= 0 ? expf(lp) : 0.0f;
+    P += L.p[k];
+  }
+  return block_sum<DIS_THREADS>(P, L.red);
+}
+
+// loss of row r from its statistics; teacher() has run. All threads get it.
+template <typename Elem>
+__device__ float row_loss(const DistillArgs& a, DisLds& L, const Row<Elem>& row, float m,
+                          float logsum) {
+  float l = 0.0f;
+  for (int k = threadIdx.x; k < a.K; k += DIS_THREADS) {
+    if (!(L.p[k] == 0.0f)) {   // an empty slot, or a mass that is 0: no part in the loss
+      const float z = to_f32(row.p + L.id[k]);
+      const float lq = m == -INFINITY ? -INFINITY : (z - m) * a.inv_t - logsum;
+      l += L.p[k] * (L.zid[k] - lq);
+    }
+  }
+  return block_sum<DIS_THREADS>(l, L.red);
+}
+
+// Running set of the groups [v0, v1) of the row, with its head and tail in the
+// first and last part.
+template <typename Elem>
+__device__ MaxSum row_set(const DistillArgs& a, DisLds& L, const Row<Elem>& row, int part, int v0,
+                          int v1) {
+  constexpr int EPV = Row<Elem>::EPV;
+  constexpr int AHEAD = 4;
+  const int tid = threadIdx.x;
+  MaxSum sum{-INFINITY, 0.0f};
+  float one[1];
+  if (part == 0 && tid < row.head) {
+    one[0] = to_f32(row.p + tid);
+    add_logits(sum, one, a.c);
+  }
+  if (part == a.parts - 1 && tid < row.tail()) {
+    one[0] = to_f32(row.p + row.tail0() + tid);
+    add_logits(sum, one, a.c);
+  }
+  int j = v0 + tid;
+  for (; j + (AHEAD - 1) * DIS_THREADS < v1; j += AHEAD * DIS_THREADS) {
+    vu32x4 w[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) w[i] = row.vec(j + i * DIS_THREADS);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      float z[EPV];
+      unpack(w[i], z);
+      add_logits(sum, z, a.c);
+    }
+  }
+  for (; j < v1; j += DIS_THREADS) {
+    float z[EPV];
+    unpack(row.vec(j), z);
+    add_logits(sum, z, a.c);
+  }
+  return block_join<DIS_THREADS>(sum, L.scratch, a.c);
+}
+
+// Gradient of the groups [v0, v1) (and head or tail); teacher() has run.
+template <typename Elem>
+__device__ void row_grad(const DistillArgs& a, DisLds& L, const Row<Elem>& row, int64_t r, int part,
+                         int v0, int v1, float P, float m, float logsum) {
+  constexpr int EPV = Row<Elem>::EPV;
+  const int tid = threadIdx.x;
+  Elem* out = (Elem*)a.grad + r * a.grad_stride;
+  const float g = (a.weight ? a.weight[r] : 1.0f) * a.inv_t;
+  // nothing to learn from: no teacher mass, or a row that rules out every token
+  const bool none = P == 0.0f || m == -INFINITY;
+  const float scale = g * P;
+  const float ls2 = logsum * LOG2E;
+  auto q = [&](float z) { return fast_exp2((z - m) * a.c - ls2); };
+  auto dense = [&](float z) { return none ? 0.0f : scale * q(z); };
+  const int lo = part == 0 ? 0 : row.head + v0 * EPV;
+  const int hi = part == a.parts - 1 ? a.V : row.head + v1 * EPV;
+  // the slots' student logits, before an in-place gradient overwrites them
+  for (int k = tid; k < a.K; k += DIS_THREADS) {
+    const int id = L.id[k];
+    if (id >= lo && id < hi) L.zid[k] = to_f32(row.p + id);
+  }
+  __syncthreads();
+  // the output row has its own alignment: whole groups where both agree
+  const bool same = (((uintptr_t)out ^ (uintptr_t)row.p) & 15u) == 0;
+  if (part == 0 && tid < row.head) put(out + tid, dense(to_f32(row.p + tid)));
+  if (part == a.parts - 1 && tid < row.tail())
+    put(out + row.tail0() + tid, dense(to_f32(row.p + row.tail0() + tid)));
+  for (int j = v0 + tid; j < v1; j += DIS_THREADS) {
+    float z[EPV];
+    unpack(row.vec(j), z);
+#pragma unroll
+    for (int i = 0; i < EPV; ++i) z[i] = dense(z[i]);
+    Elem* o = out + row.head + (int64_t)j * EPV;
+    if (same) {
+      __builtin_nontemporal_store(pack(z), (vu32x4*)o);
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPV; ++i) put(o + i, z[i]);
+    }
+  }
+  __syncthreads();   // orders the dense writes before the slots'
+  if (none) return;
+  for (int k = tid; k < a.K; k += DIS_THREADS) {
+    const int id = L.id[k];
+    if (id < lo || id >= hi) continue;
+    float p = 0.0f;
+    for (int j = 0; j < a.K; ++j) p += L.id[j] == id ? L.p[j] : 0.0f;
+    put(out + id, scale * q(L.zid[k]) - g * p);
+  }
+}
+
+template <typename Elem>
+__device__ __forceinline__ void part_of(const Row<Elem>& row, int parts, int part, int* v0, int* v1) {
+  const int per = (row.nvec + parts - 1) / parts;
+  *v0 = min(row.nvec, part * per);
+  *v1 = min(row.nvec, *v0 + per);
+}
+
+__device__ __forceinline__ float log_of(const MaxSum& s) {
+  return s.m == -INFINITY && s.s == 0.0f ? -INFINITY : logf(s.s);
+}
+
+// One workgroup a row: statistics, loss, gradient.
+template <typename Elem>
+__global__ __launch_bounds__(DIS_THREADS) void distill_row_kernel(DistillArgs a) {
+  __shared__ DisLds L;
+  const int64_t r = blockIdx.x;
+  const Row<Elem> row(a.logits, a.stride, r, a.V);
+  const MaxSum s = row_set(a, L, row, 0, 0, row.nvec);
+  const float logsum = log_of(s);
+  const float P = teacher(a, L, r);
+  const float loss = row_loss(a, L, row, s.m, logsum);
+  if (threadIdx.x == 0) {
+    a.loss[r] = loss;
+    if (a.stats) {
+      a.stats[2 * r] = s.m;
+      a.stats[2 * r + 1] = logsum;
+    }
+  }
+  if (a.grad) row_grad(a, L, row, r, 0, 0, row.nvec, P, s.m, logsum);
+}
+
+// Few rows: the statistics of a part of a row ...
+template <typename Elem>
+__global__ __launch_bounds__(DIS_THREADS) void distill_part_kernel(DistillArgs a) {
+  __shared__ DisLds L;
+  const int64_t r = blockIdx.x / a.parts;
+  const int part = blockIdx.x % a.parts;
+  const Row<Elem> row(a.logits, a.stride, r, a.V);
+  int v0, v1;
+  part_of(row, a.parts, part, &v0, &v1);
+  const MaxSum s = row_set(a, L, row, part, v0, v1);
+  if (threadIdx.x == 0) a.sums[blockIdx.x] = s;
+}
+
+// ... the join of a row's parts and its loss ...
+template <typename Elem>
+__global__ __launch_bounds__(DIS_THREADS) void distill_join_kernel(DistillArgs a) {
+  __shared__ DisLds L;
+  const int64_t r = blockIdx.x;
+  const Row<Elem> row(a.logits, a.stride, r, a.V);
+  MaxSum s{-INFINITY, 0.0f};
+  if ((int)threadIdx.x < a.parts) s = a.sums[r * a.parts + threadIdx.x];
+  s = block_join<DIS_THREADS>(s, L.scratch, a.c);
+  const float logsum = log_of(s);
+  teacher(a, L, r);
+  const float loss = row_loss(a, L, row, s.m, logsum);
+  if (threadIdx.x == 0) {
+    a.loss[r] = loss;
+    a.stats[2 * r] = s.m;
+    a.stats[2 * r + 1] = logsum;
+  }
+}
+
+// ... and the gradient of a part, from the statistics.
+template <typename Elem>
+__global__ __launch_bounds__(DIS_THREADS) void distill_grad_kernel(DistillArgs a) {
+  __shared__ DisLds L;
+  const int64_t r = blockIdx.x / a.parts;
+  const int part = blockIdx.x % a.parts;
+  const Row<Elem> row(a.logits, a.stride, r, a.V);
+  int v0, v1;
+  part_of(row, a.parts, part, &v0, &v1);
+  const float P = teacher(a, L, r);
+  __syncthreads();   // row_grad reuses L.zid
+  row_grad(a, L, row, r, part, v0, v1, P, a.stats[2 * r], a.stats[2 * r + 1]);
+}
+
+template <typename Elem>
+int distill(const DistillArgs& a, bool backward, hipStream_t st) {
+  const dim3 block(DIS_THREADS), rows((uint32_t)a.R), all((uint32_t)a.R * (uint32_t)a.parts);
+  if (!backward && a.parts == 1) {
+    hipLaunchKernelGGL(distill_row_kernel<Elem>, rows, block, 0, st, a);
+  } else {
+    if (!backward) {
+      hipLaunchKernelGGL(distill_part_kernel<Elem>, all, block, 0, st, a);
+      hipLaunchKernelGGL(distill_join_kernel<Elem>, rows, block, 0, st, a);
+    }
+    if (a.grad) hipLaunchKernelGGL(distill_grad_kernel<Elem>, all, block, 0, st, a);
+  }
+  return hipGetLastError() == hipSuccess ? 0 : -1;
+}
+
+}  // namespace
+
+int launch_distill(const DistillArgs& a, int bf16, hipStream_t st) {
+  return bf16 ? distill<uint16_t>(a, false, st) : distill<float>(a, false, st);
+}
+int launch_distill_backward(const DistillArgs& a, int bf16, hipStream_t st) {
+  return bf16 ? distill<uint16_t>(a, true, st) : distill<float>(a, true, st);
+}
+
+}  // namespace sv

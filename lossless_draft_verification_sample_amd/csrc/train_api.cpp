@@ -1,0 +1,392 @@
+// Host side of the drafter-training calls of include/spec_verify.h: argument
+// checks before anything touches the device, how the work is cut into parts,
+// workspace carving and the launches on the caller's stream.
+
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "../../include/spec_verify.h"
+#include "sv_train.hpp"
+
+static_assert(SV_MAX_TOP == sv::TOP_MAX_K && SV_MAX_TOP == sv::DIS_MAX_K, "kept logits per row");
+static_assert(sv::TOP_CAP - sv::TOP_STEP >= sv::TOP_MAX_K, "a cut list leaves room for a step");
+
+namespace {
+
+constexpr size_t WS_ALIGN = 256;
+constexpr float LOG2E_D = sv::LOG2E;
+
+size_t align_up(size_t x) { return (x + WS_ALIGN - 1) / WS_ALIGN * WS_ALIGN; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+
+bool known(sv_dtype t) { return t == SV_F32 || t == SV_BF16; }
+size_t size_of(sv_dtype t) { return t == SV_BF16 ? 2 : 4; }
+bool aligned(const void* p, size_t to) { return (uintptr_t)p % to == 0; }
+bool workspace_ok(const void* p, size_t have, size_t need) {
+  return need == 0 || (p && aligned(p, WS_ALIGN) && have >= need);
+}
+bool temperature_ok(float t) { return t > 0.0f && isfinite(t); }
+
+// Carves a workspace front to back.
+struct Carver {
+  size_t off = 0;
+  size_t take(size_t bytes) {
+    const size_t at = off;
+    off = align_up(off + bytes);
+    return at;
+  }
+};
+
+// ---------------------------------------------------------------- vocabulary rows
+
+// Workgroups per row: one when there are rows enough for every CU, else as many
+// as give TARGET in all, none shorter than MIN logits.
+int64_t row_parts(int64_t R, int64_t V, int64_t target, int64_t min_logits) {
+  int64_t parts = target / R;
+  const int64_t most = ceil_div(V, min_logits);
+  if (parts > most) parts = most;
+  return parts < 1 ? 1 : parts;
+}
+
+constexpr int64_t TOP_TARGET_WGS = 512, TOP_MIN_LOGITS = 8192;
+constexpr int64_t DIS_TARGET_WGS = 1024, DIS_MIN_LOGITS = 4096;
+
+struct TopLayout {
+  int parts;
+  size_t keys, sums, total;
+};
+bool top_layout(int32_t R, int32_t V, int32_t K, TopLayout* L) {
+  if (R < 1 || V < 1 || K < 1 || K > SV_MAX_TOP || K > V) return false;
+  int64_t parts = row_parts(R, V, TOP_TARGET_WGS, TOP_MIN_LOGITS);
+  if (parts > sv::TOP_CAP / K) parts = sv::TOP_CAP / K;   // what the join holds
+  L->parts = (int)parts;
+  Carver c;
+  L->keys = c.take(parts > 1 ? (size_t)R * parts * K * sizeof(uint64_t) : 0);
+  L->sums = c.take(parts > 1 ? (size_t)R * parts * sizeof(sv::MaxSum) : 0);
+  L->total = c.off;
+  return true;
+}
+
+int distill_parts(int32_t R, int32_t V) { return (int)row_parts(R, V, DIS_TARGET_WGS, DIS_MIN_LOGITS); }
+
+int distill_args(const void* logits, int64_t logits_stride, sv_dtype dtype, int32_t R, int32_t V,
+                 const int32_t* ids, const float* tl, const float* tlse, int32_t K,
+                 float temperature, void* grad, int64_t grad_stride, sv::DistillArgs* a) {
+  if (!logits || !ids || !tl) return SV_EINVAL;
+  if (!known(dtype)) return SV_EDTYPE;
+  if (R < 1 || V < 1 || K < 1 || K > SV_MAX_TOP || !temperature_ok(temperature)) return SV_EINVAL;
+  if (logits_stride < V || (grad && grad_stride < V)) return SV_EINVAL;
+  if (!aligned(logits, size_of(dtype)) || !aligned(grad, size_of(dtype))) return SV_EINVAL;
+  if (grad == logits && grad_stride != logits_stride) return SV_EINVAL;
+  a->logits = logits;
+  a->stride = logits_stride;
+  a->ids = ids;
+  a->tl = tl;
+  a->tlse = tlse;
+  a->R = R;
+  a->V = V;
+  a->K = K;
+  a->parts = distill_parts(R, V);
+  a->temperature = temperature;
+  a->inv_t = 1.0f / temperature;
+  a->c = (float)((double)LOG2E_D / temperature);
+  a->grad = grad;
+  a->grad_stride = grad_stride;
+  return SV_OK;
+}
+
+// ---------------------------------------------------------------- linear cross entropy
+
+// Most bytes of one piece's operands in the workspace: the last-level cache
+// holds 256 MB, so a piece of this size is still there when it is read back.
+constexpr int64_t CE_PIECE_BYTES = 128ll << 20;
+constexpr int64_t CE_MAX_ROWS = 1 << 22;
+constexpr int64_t CE_PIECE_STEP = 256;    // a multiple of every tile height
+constexpr int64_t CE_MAX_PIECE = 1 << 20;
+
+struct CeShape {
+  int64_t N, D, V, kp;   // kp: depth of the logits' product, a multiple of CE_BK
+  int planes;
+};
+bool ce_shape(int32_t N, int32_t D, int32_t V, sv_dtype dtype, CeShape* s) {
+  if (N < 1 || D < 1 || V < 1 || !known(dtype)) return false;
+  if (N > CE_MAX_ROWS || D > sv::CE_MAX_D || V >= INT32_MAX - 1024) return false;
+  *s = CeShape{N, D, V, round_up(D, sv::CE_BK), dtype == SV_BF16 ? 1 : 3};
+  // tiles of any product, and of the transposes
+  if (ceil_div(V, 128) * ceil_div(N, 32) >= INT32_MAX || ceil_div(N, 64) * ceil_div(D, 64) >= INT32_MAX)
+    return false;
+  return true;
+}
+
+// Tokens whose rows take at most CE_PIECE_BYTES at `bytes` each.
+int64_t piece_rows(const CeShape& s, int64_t bytes) {
+  int64_t rows = CE_PIECE_BYTES / bytes / CE_PIECE_STEP * CE_PIECE_STEP;
+  if (rows < 4 * CE_PIECE_STEP) rows = 4 * CE_PIECE_STEP;
+  if (rows > CE_MAX_PIECE) rows = CE_MAX_PIECE;
+  const int64_t all = round_up(s.V, CE_PIECE_STEP);
+  return rows < all ? rows : all;
+}
+
+struct CeForward {
+  int64_t piece;               // tokens a piece where the weight is packed
+  size_t partial, zlabel, hidden, weight, total;
+};
+CeForward ce_forward(const CeShape& s) {
+  CeForward f;
+  Carver c;
+  f.piece = piece_rows(s, s.planes * s.kp * 2);
+  f.partial = c.take((size_t)(ceil_div(s.V, sv::ce_tile_m((int)s.N)) * s.N) * sizeof(sv::MaxSum));
+  f.zlabel = c.take((size_t)s.N * sizeof(float));
+  f.hidden = c.take((size_t)(s.planes * s.N * s.kp) * 2);
+  f.weight = c.take((size_t)(s.planes * f.piece * s.kp) * 2);
+  f.total = c.off;
+  return f;
+}
+
+struct CeBackward {
+  int64_t piece, n_pad, acc_ld;
+  int splits;
+  size_t hidden, weight, hidden_t, weight_t, dz, dzt, acc, total;
+};
+CeBackward ce_backward(const CeShape& s, bool want_h, bool want_w) {
+  CeBackward b;
+  Carver c;
+  b.n_pad = round_up(s.N, sv::CE_BK);
+  // dz and its transpose are what a piece makes; the weight's rows what it reads
+  const int64_t wide = b.n_pad > s.kp ? b.n_pad : s.kp;
+  b.piece = piece_rows(s, s.planes * wide * 2);
+  b.acc_ld = round_up(s.D, 4);
+  const int64_t tiles = ceil_div(s.D, sv::ce_tile_m((int)s.N)) * ceil_div(s.N, sv::ce_tile_n((int)s.N));
+  int64_t splits = 512 / tiles;
+  const int64_t steps = b.piece / sv::CE_BK * (s.planes == 1 ? 1 : 6);
+  if (splits > steps / 4) splits = steps / 4;
+  const int64_t fit = CE_PIECE_BYTES / (s.N * b.acc_ld * 4);
+  if (splits > fit) splits = fit;
+  b.splits = splits < 1 ? 1 : (int)splits;
+  b.hidden = c.take((size_t)(s.planes * s.N * s.kp) * 2);
+  b.weight = c.take((size_t)(s.planes * b.piece * s.kp) * 2);
+  b.hidden_t = c.take(want_w ? (size_t)(s.planes * s.D * b.n_pad) * 2 : 0);
+  b.weight_t = c.take(want_h ? (size_t)(s.planes * s.D * b.piece) * 2 : 0);
+  b.dz = c.take(want_h ? (size_t)(s.planes * s.N * b.piece) * 2 : 0);
+  b.dzt = c.take(want_w ? (size_t)(s.planes * b.piece * b.n_pad) * 2 : 0);
+  b.acc = c.take(want_h ? (size_t)(b.splits * s.N * b.acc_ld) * 4 : 0);
+  b.total = c.off;
+  return b;
+}
+
+// A matrix as the products take it: rows of bfloat16 (parts), kp long, on 16
+// bytes. Used as it is where it has that form, else packed.
+struct Operand {
+  const uint16_t* p;
+  int64_t ld, plane;
+};
+bool ce_direct(const void* p, int64_t stride, const CeShape& s) {
+  return s.planes == 1 && s.kp == s.D && aligned(p, 16) && stride % 8 == 0 && stride <= sv::CE_MAX_D;
+}
+int ce_operand(const void* src, int64_t stride, int64_t row0, int64_t rows, const CeShape& s,
+               uint16_t* room, hipStream_t st, Operand* out) {
+  const char* at = (const char*)src + row0 * stride * (s.planes == 1 ? 2 : 4);
+  if (ce_direct(src, stride, s)) {
+    *out = Operand{(const uint16_t*)at, stride, 0};
+    return 0;
+  }
+  sv::CePack p{at, stride, s.planes == 1, (int)rows, (int)s.D, s.planes, room, s.kp, rows * s.kp};
+  *out = Operand{room, s.kp, p.plane};
+  return sv::launch_ce_pack(p, false, st);
+}
+int ce_transposed(const void* src, int64_t stride, int64_t row0, int64_t rows, int64_t ld,
+                  const CeShape& s, uint16_t* room, hipStream_t st, Operand* out) {
+  const char* at = (const char*)src + row0 * stride * (s.planes == 1 ? 2 : 4);
+  sv::CePack p{at, stride, s.planes == 1, (int)rows, (int)s.D, s.planes, room, ld, s.D * ld};
+  *out = Operand{room, ld, p.plane};
+  return sv::launch_ce_pack(p, true, st);
+}
+sv::CeGemm ce_gemm(const Operand& a, int64_t M, const Operand& b, int64_t N, int64_t K, int planes) {
+  return sv::CeGemm{a.p, b.p, a.ld, b.ld, a.plane, b.plane, (int)M, (int)N, (int)K, planes == 1 ? 1 : 6, 1};
+}
+
+int ce_check(const void* hidden, int64_t hidden_stride, const void* weight, int64_t weight_stride,
+             sv_dtype dtype, const int32_t* labels, int32_t N, int32_t D, int32_t V, CeShape* s) {
+  if (!hidden || !weight || !labels) return SV_EINVAL;
+  if (!known(dtype)) return SV_EDTYPE;
+  if (N < 1 || D < 1 || V < 1 || hidden_stride < D || weight_stride < D) return SV_EINVAL;
+  if (!aligned(hidden, size_of(dtype)) || !aligned(weight, size_of(dtype))) return SV_EINVAL;
+  return ce_shape(N, D, V, dtype, s) ? SV_OK : SV_ESIZE;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t spec_verify_top_logits_workspace_bytes(int32_t R, int32_t V, int32_t K) {
+  TopLayout L;
+  return top_layout(R, V, K, &L) ? L.total : 0;
+}
+
+int spec_verify_top_logits(const void* logits, int64_t logits_stride, sv_dtype dtype, int32_t R,
+                           int32_t V, int32_t K, float temperature, int32_t* out_ids,
+                           float* out_values, float* out_lse, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  if (!logits || !out_ids || !out_values) return SV_EINVAL;
+  if (!known(dtype)) return SV_EDTYPE;
+  if (!temperature_ok(temperature) || logits_stride < V || !aligned(logits, size_of(dtype)))
+    return SV_EINVAL;
+  TopLayout L;
+  if (!top_layout(R, V, K, &L)) return SV_EINVAL;
+  if (!workspace_ok(workspace, workspace_bytes, L.total)) return SV_EWORKSPACE;
+  sv::TopArgs a{};
+  a.logits = logits;
+  a.stride = logits_stride;
+  a.R = R;
+  a.V = V;
+  a.K = K;
+  a.parts = L.parts;
+  a.c = (float)((double)LOG2E_D / temperature);
+  a.temperature = temperature;
+  a.ids = out_ids;
+  a.values = out_values;
+  a.lse = out_lse;
+  a.keys = (uint64_t*)((char*)workspace + L.keys);
+  a.sums = (sv::MaxSum*)((char*)workspace + L.sums);
+  return sv::launch_top_logits(a, dtype == SV_BF16, (hipStream_t)stream) ? SV_EHIP : SV_OK;
+}
+
+size_t spec_verify_distill_workspace_bytes(int32_t R, int32_t V) {
+  if (R < 1 || V < 1) return 0;
+  const int parts = distill_parts(R, V);
+  return parts > 1 ? align_up((size_t)R * parts * sizeof(sv::MaxSum)) : 0;
+}
+
+int spec_verify_distill(const void* logits, int64_t logits_stride, sv_dtype dtype, int32_t R,
+                        int32_t V, const int32_t* teacher_ids, const float* teacher_logits,
+                        const float* teacher_lse, int32_t K, float temperature,
+                        const float* row_weight, float* out_loss, float* out_stats, void* out_grad,
+                        int64_t grad_stride, void* workspace, size_t workspace_bytes, void* stream) {
+  sv::DistillArgs a{};
+  if (!out_loss || !out_stats) return SV_EINVAL;
+  const int rc = distill_args(logits, logits_stride, dtype, R, V, teacher_ids, teacher_logits,
+                              teacher_lse, K, temperature, out_grad, grad_stride, &a);
+  if (rc != SV_OK) return rc;
+  if (!workspace_ok(workspace, workspace_bytes, spec_verify_distill_workspace_bytes(R, V)))
+    return SV_EWORKSPACE;
+  a.weight = row_weight;
+  a.loss = out_loss;
+  a.stats = out_stats;
+  a.sums = (sv::MaxSum*)workspace;
+  return sv::launch_distill(a, dtype == SV_BF16, (hipStream_t)stream) ? SV_EHIP : SV_OK;
+}
+
+int spec_verify_distill_backward(const void* logits, int64_t logits_stride, sv_dtype dtype,
+                                 int32_t R, int32_t V, const int32_t* teacher_ids,
+                                 const float* teacher_logits, const float* teacher_lse, int32_t K,
+                                 float temperature, const float* stats, const float* grad_loss,
+                                 void* out_grad, int64_t grad_stride, void* stream) {
+  sv::DistillArgs a{};
+  if (!stats || !out_grad) return SV_EINVAL;
+  const int rc = distill_args(logits, logits_stride, dtype, R, V, teacher_ids, teacher_logits,
+                              teacher_lse, K, temperature, out_grad, grad_stride, &a);
+  if (rc != SV_OK) return rc;
+  a.weight = grad_loss;
+  a.stats = const_cast<float*>(stats);   // only read
+  return sv::launch_distill_backward(a, dtype == SV_BF16, (hipStream_t)stream) ? SV_EHIP : SV_OK;
+}
+
+size_t spec_verify_linear_ce_workspace_bytes(int32_t N, int32_t D, int32_t V, sv_dtype dtype) {
+  CeShape s;
+  return ce_shape(N, D, V, dtype, &s) ? ce_forward(s).total : 0;
+}
+
+int spec_verify_linear_ce(const void* hidden, int64_t hidden_stride, const void* weight,
+                          int64_t weight_stride, sv_dtype dtype, const int32_t* labels, int32_t N,
+                          int32_t D, int32_t V, float* out_loss, float* out_stats, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  CeShape s;
+  if (!out_loss || !out_stats) return SV_EINVAL;
+  const int rc = ce_check(hidden, hidden_stride, weight, weight_stride, dtype, labels, N, D, V, &s);
+  if (rc != SV_OK) return rc;
+  const CeForward f = ce_forward(s);
+  if (!workspace_ok(workspace, workspace_bytes, f.total)) return SV_EWORKSPACE;
+  hipStream_t st = (hipStream_t)stream;
+  char* ws = (char*)workspace;
+  sv::MaxSum* partial = (sv::MaxSum*)(ws + f.partial);
+  float* zlabel = (float*)(ws + f.zlabel);
+  Operand h, w;
+  if (ce_operand(hidden, hidden_stride, 0, N, s, (uint16_t*)(ws + f.hidden), st, &h)) return SV_EHIP;
+  const int bm = sv::ce_tile_m(N);
+  const int64_t piece = ce_direct(weight, weight_stride, s) ? V : f.piece;
+  for (int64_t v0 = 0; v0 < V; v0 += piece) {
+    const int64_t rows = V - v0 < piece ? V - v0 : piece;
+    if (ce_operand(weight, weight_stride, v0, rows, s, (uint16_t*)(ws + f.weight), st, &w)) return SV_EHIP;
+    const sv::CeStatsOut o{labels, (int)v0, V, partial + v0 / bm * N, zlabel};
+    if (sv::launch_ce_stats(ce_gemm(w, rows, h, N, s.kp, s.planes), o, st)) return SV_EHIP;
+  }
+  return sv::launch_ce_join(partial, zlabel, labels, (int)ceil_div(V, bm), N, V, out_loss, out_stats, st)
+             ? SV_EHIP : SV_OK;
+}
+
+size_t spec_verify_linear_ce_backward_workspace_bytes(int32_t N, int32_t D, int32_t V,
+                                                      sv_dtype dtype, int want_grad_hidden,
+                                                      int want_grad_weight) {
+  CeShape s;
+  if (!want_grad_hidden && !want_grad_weight) return 0;
+  return ce_shape(N, D, V, dtype, &s) ? ce_backward(s, want_grad_hidden, want_grad_weight).total : 0;
+}
+
+int spec_verify_linear_ce_backward(const void* hidden, int64_t hidden_stride, const void* weight,
+                                   int64_t weight_stride, sv_dtype dtype, const int32_t* labels,
+                                   const float* stats, const float* grad_loss, int32_t N, int32_t D,
+                                   int32_t V, void* out_grad_hidden, int64_t grad_hidden_stride,
+                                   void* out_grad_weight, int64_t grad_weight_stride,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+  CeShape s;
+  if (!stats || (!out_grad_hidden && !out_grad_weight)) return SV_EINVAL;
+  const int rc = ce_check(hidden, hidden_stride, weight, weight_stride, dtype, labels, N, D, V, &s);
+  if (rc != SV_OK) return rc;
+  if ((out_grad_hidden && (grad_hidden_stride < D || !aligned(out_grad_hidden, size_of(dtype)))) ||
+      (out_grad_weight && (grad_weight_stride < D || !aligned(out_grad_weight, size_of(dtype)))))
+    return SV_EINVAL;
+  const CeBackward b = ce_backward(s, out_grad_hidden, out_grad_weight);
+  if (!workspace_ok(workspace, workspace_bytes, b.total)) return SV_EWORKSPACE;
+  hipStream_t st = (hipStream_t)stream;
+  char* ws = (char*)workspace;
+  const int bf16 = dtype == SV_BF16;
+  const size_t es = size_of(dtype);
+  uint16_t* dz = out_grad_hidden ? (uint16_t*)(ws + b.dz) : nullptr;
+  uint16_t* dzt = out_grad_weight ? (uint16_t*)(ws + b.dzt) : nullptr;
+  float* acc = (float*)(ws + b.acc);
+  Operand h, ht{}, w, wt{};
+  if (ce_operand(hidden, hidden_stride, 0, N, s, (uint16_t*)(ws + b.hidden), st, &h)) return SV_EHIP;
+  if (dzt && ce_transposed(hidden, hidden_stride, 0, N, b.n_pad, s, (uint16_t*)(ws + b.hidden_t), st, &ht))
+    return SV_EHIP;
+  const int mat_vec = dzt && aligned(out_grad_weight, 4 * es) && grad_weight_stride % 4 == 0;
+  for (int64_t v0 = 0; v0 < V; v0 += b.piece) {
+    const int64_t rows = V - v0 < b.piece ? V - v0 : b.piece;
+    const int64_t depth = round_up(rows, sv::CE_BK);
+    if (ce_operand(weight, weight_stride, v0, rows, s, (uint16_t*)(ws + b.weight), st, &w)) return SV_EHIP;
+    const sv::CeDzOut o{labels, stats, grad_loss, (int)v0, V, s.planes, dz, depth, N * depth,
+                        dzt, b.n_pad, rows * b.n_pad, (int)b.n_pad};
+    if (sv::launch_ce_dz(ce_gemm(w, rows, h, N, s.kp, s.planes), o, st)) return SV_EHIP;
+    if (dz) {
+      if (ce_transposed(weight, weight_stride, v0, rows, depth, s, (uint16_t*)(ws + b.weight_t), st, &wt))
+        return SV_EHIP;
+      sv::CeGemm g = ce_gemm(wt, D, Operand{dz, depth, N * depth}, N, depth, s.planes);
+      g.splits = b.splits;
+      const sv::CeAccOut ao{acc, b.acc_ld, N * b.acc_ld, v0 > 0};
+      if (sv::launch_ce_acc(g, ao, st)) return SV_EHIP;
+    }
+    if (dzt) {
+      const sv::CeGemm g = ce_gemm(ht, D, Operand{dzt, b.n_pad, rows * b.n_pad}, rows, b.n_pad, s.planes);
+      const sv::CeMatOut mo{(char*)out_grad_weight + v0 * grad_weight_stride * es, grad_weight_stride, bf16,
+                            mat_vec};
+      if (sv::launch_ce_mat(g, mo, st)) return SV_EHIP;
+    }
+  }
+  if (dz && sv::launch_ce_sum(acc, b.splits, N * b.acc_ld, b.acc_ld, N, D, out_grad_hidden,
+                              grad_hidden_stride, bf16, st))
+    return SV_EHIP;
+  return SV_OK;
+}
+
+}  // extern "C"
