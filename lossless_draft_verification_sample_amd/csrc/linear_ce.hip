@@ -27,11 +27,12 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 typedef __attribute__((address_space(3))) void lds_void;
-typedef __attribute__((address_space(1))) const void glb_void;
 
 // s_waitcnt operand: no vector memory operation outstanding, other counters free
 // (vmcnt in bits 3:0 and 15:14, expcnt in 6:4, lgkmcnt in 11:8).
 constexpr int WAIT_VM0 = 0x0F70;
+// Last word of a raw buffer resource: 32-bit data, no swizzle.
+constexpr int RSRC_WORD3 = 0x00027000;
 
 // Part products of float32 operands, in the order in which they are summed.
 __device__ __forceinline__ void part_pair(int i, int* pa, int* pb) {
@@ -49,11 +50,6 @@ struct Tile {
   static constexpr int STAGE = (BM + BN) * CE_BK;    // bfloat16 elements
   static_assert(LA * THREADS == BM * 8 && LB * THREADS == BN * 8, "whole rounds of loads");
 };
-
-// One 16-byte group a lane from global memory into LDS, lanes in order.
-__device__ __forceinline__ void copy_to_lds(const uint16_t* base, uint32_t byte_off, uint16_t* lds) {
-  __builtin_amdgcn_global_load_lds((glb_void*)((const char*)base + byte_off), (lds_void*)lds, 16, 0, 0);
-}
 
 // Tile indices of a workgroup: consecutive workgroups go to different XCDs (8),
 // so each XCD takes a run of consecutive tiles, ordered in groups of 8 rows of
@@ -74,11 +70,13 @@ __device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int* t
 }
 
 template <int BM, int BN, int WM, int WN, typename Epi>
-__global__ __launch_bounds__(WM* WN* WAVE) void ce_gemm_kernel(CeGemm g, int tiles_m, int tiles_n,
-                                                               typename Epi::Args ea) {
+__global__ __launch_bounds__(WM* WN* WAVE, WM* WN == 8 ? 2 : 1) void ce_gemm_kernel(
+    CeGemm g, int tiles_m, int tiles_n, typename Epi::Args ea) {
+#if defined(__HIP_DEVICE_COMPILE__)   // buffer resources exist on the device side only
   using T = Tile<BM, BN, WM, WN>;
   __shared__ __align__(16) uint16_t lds[2 * T::STAGE];
-  const int tid = threadIdx.x, lane = tid & (WAVE - 1), wave = tid / WAVE;
+  const int tid = threadIdx.x, lane = tid & (WAVE - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
   const int wm = wave / WN, wn = wave % WN;
   int tm, tn;
   tile_of(blockIdx.x, tiles_m, tiles_n, &tm, &tn);
@@ -108,19 +106,29 @@ __global__ __launch_bounds__(WM* WN* WAVE) void ce_gemm_kernel(CeGemm g, int til
   const int per = (total + g.splits - 1) / g.splits;
   const int first = min(total, (int)blockIdx.y * per), last = min(total, first + per);
 
-  auto issue = [&](int step, int stage) {
-    const int pair = step / steps_k;
-    const int64_t k = (int64_t)(step - pair * steps_k) * CE_BK;
+  // Loads go straight into LDS: per lane a 32-bit offset from the tile's first
+  // row, per step a scalar one. next_*: what is to be loaded next.
+  int next_pair = first / steps_k, next_k = (first - next_pair * steps_k) * CE_BK;
+  auto issue = [&](int stage) {
     int pa = 0, pb = 0;
-    if (g.parts > 1) part_pair(pair, &pa, &pb);
-    const uint16_t* a = rowa + pa * g.plane_a + k;
-    const uint16_t* b = rowb + pb * g.plane_b + k;
-    uint16_t* la = lds + stage * T::STAGE;
+    if (g.parts > 1) part_pair(next_pair, &pa, &pb);
+    const auto ra = __builtin_amdgcn_make_buffer_rsrc((void*)(rowa + pa * g.plane_a), 0, -1, RSRC_WORD3);
+    const auto rb = __builtin_amdgcn_make_buffer_rsrc((void*)(rowb + pb * g.plane_b), 0, -1, RSRC_WORD3);
+    uint16_t* la = lds + stage * T::STAGE + wave * WAVE * 8;
     uint16_t* lb = la + BM * CE_BK;
 #pragma unroll
-    for (int i = 0; i < T::LA; ++i) copy_to_lds(a, offa[i], la + (i * T::THREADS + wave * WAVE) * 8);
+    for (int i = 0; i < T::LA; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(la + i * T::THREADS * 8), 16, (int)offa[i],
+                                               next_k * 2, 0, 0);
 #pragma unroll
-    for (int i = 0; i < T::LB; ++i) copy_to_lds(b, offb[i], lb + (i * T::THREADS + wave * WAVE) * 8);
+    for (int i = 0; i < T::LB; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(lb + i * T::THREADS * 8), 16, (int)offb[i],
+                                               next_k * 2, 0, 0);
+    next_k += CE_BK;
+    if (next_k == g.K) {
+      next_k = 0;
+      ++next_pair;
+    }
   };
 
   f32x4 acc[T::MI][T::NI];
@@ -130,32 +138,61 @@ __global__ __launch_bounds__(WM* WN* WAVE) void ce_gemm_kernel(CeGemm g, int til
     for (int j = 0; j < T::NI; ++j) acc[i][j] = (f32x4)(0.0f);
 
   const int fr = lane & 15, fk = lane >> 4;
-  if (first < last) issue(first, 0);
-  for (int step = first; step < last; ++step) {
-    const int stage = (step - first) & 1;
+  const int grp0 = (fk ^ (fr & 7)) * 8, grp1 = ((4 + fk) ^ (fr & 7)) * 8;
+  auto step = [&](int s, int stage) {
     // this stage has arrived for every wave, and every wave is done with the other
     __builtin_amdgcn_s_waitcnt(WAIT_VM0);
     __syncthreads();
-    if (step + 1 < last) issue(step + 1, stage ^ 1);
+    if (s + 1 < last) issue(stage ^ 1);
     const uint16_t* la = lds + stage * T::STAGE + (wm * T::TM + fr) * CE_BK;
     const uint16_t* lb = lds + stage * T::STAGE + BM * CE_BK + (wn * T::TN + fr) * CE_BK;
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
-      const int grp = ((kk * 4 + fk) ^ (fr & 7)) * 8;
+      const int grp = kk ? grp1 : grp0;
       bf16x8 fa[T::MI], fb[T::NI];
 #pragma unroll
-      for (int i = 0; i < T::MI; ++i) fa[i] = *(const bf16x8*)(la + i * 16 * CE_BK + grp);
-#pragma unroll
       for (int j = 0; j < T::NI; ++j) fb[j] = *(const bf16x8*)(lb + j * 16 * CE_BK + grp);
+#pragma unroll
+      for (int i = 0; i < T::MI; ++i) fa[i] = *(const bf16x8*)(la + i * 16 * CE_BK + grp);
 #pragma unroll
       for (int i = 0; i < T::MI; ++i)
 #pragma unroll
         for (int j = 0; j < T::NI; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
     }
+    // Order of issue: all of B's fragments and two of A's, then each row of
+    // matrix instructions with the fragment read that the row after the next needs.
+    constexpr int MFMA = 0x008, DS_READ = 0x100;
+    if constexpr (T::MI > 2) {
+      __builtin_amdgcn_sched_group_barrier(DS_READ, T::NI + 2, 0);
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+        for (int i = 0; i < T::MI - 2; ++i) {
+          __builtin_amdgcn_sched_group_barrier(MFMA, T::NI, 0);
+          __builtin_amdgcn_sched_group_barrier(DS_READ, 1, 0);
+        }
+        if (kk == 0) {
+          __builtin_amdgcn_sched_group_barrier(MFMA, T::NI, 0);
+          __builtin_amdgcn_sched_group_barrier(DS_READ, T::NI, 0);
+          __builtin_amdgcn_sched_group_barrier(MFMA, T::NI, 0);
+          __builtin_amdgcn_sched_group_barrier(DS_READ, 2, 0);
+        } else {
+          __builtin_amdgcn_sched_group_barrier(MFMA, 2 * T::NI, 0);
+        }
+      }
+    }
+  };
+  if (first < last) issue(0);
+  int s = first;
+  for (; s + 1 < last; s += 2) {
+    step(s, 0);
+    step(s + 1, 1);
   }
+  if (s < last) step(s, 0);
   __syncthreads();
   Epi::template run<T>(ea, g, acc, m0 + wm * T::TM, n0 + wn * T::TN, tm, wm, wn, lane, (char*)lds);
+#endif
 }
 
 // Element i of acc[mi][ni] of lane l is C[m][n] with
@@ -426,17 +463,19 @@ int gemm(const CeGemm& g, const typename Epi::Args& ea, int cover, hipStream_t s
   const int tiles_m = (g.M + bm - 1) / bm;
   const int tiles_n = (cover + bn - 1) / bn;
   const dim3 grid((uint32_t)tiles_m * (uint32_t)tiles_n, (uint32_t)g.splits);
-  if (bn == 32)
-    hipLaunchKernelGGL((ce_gemm_kernel<256, 32, 4, 1, Epi>), grid, dim3(256), 0, st, g, tiles_m, tiles_n, ea);
-  else
-    hipLaunchKernelGGL((ce_gemm_kernel<128, 128, 2, 2, Epi>), grid, dim3(256), 0, st, g, tiles_m, tiles_n, ea);
+#define CE_LAUNCH(BM, BN, WM, WN) \
+  hipLaunchKernelGGL((ce_gemm_kernel<BM, BN, WM, WN, Epi>), grid, dim3(WM * WN * WAVE), 0, st, g, tiles_m, tiles_n, ea)
+  if (bn == 32) CE_LAUNCH(256, 32, 4, 1);
+  else if (bn == 128) CE_LAUNCH(128, 128, 2, 2);
+  else CE_LAUNCH(256, 256, 2, 4);
+#undef CE_LAUNCH
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
 }  // namespace
 
-int ce_tile_m(int rows_b) { return rows_b <= 32 ? 256 : 128; }
-int ce_tile_n(int rows_b) { return rows_b <= 32 ? 32 : 128; }
+int ce_tile_m(int rows_b) { return rows_b <= 32 || rows_b > 128 ? 256 : 128; }
+int ce_tile_n(int rows_b) { return rows_b <= 32 ? 32 : rows_b <= 128 ? 128 : 256; }
 
 int launch_ce_stats(const CeGemm& g, const CeStatsOut& o, hipStream_t st) { return gemm<EpiStats>(g, o, g.N, st); }
 int launch_ce_dz(const CeGemm& g, const CeDzOut& o, hipStream_t st) { return gemm<EpiDz>(g, o, o.dzt ? o.n_pad : g.N, st); }
