@@ -1,15 +1,14 @@
 // Softmax cross entropy of a linear head without its logits. Every product is
-// C[m][n] = sum_k A[m][k] B[n][k] with both operands contiguous along k, made by
-// one tiled kernel whose epilogues differ:
+// C[m][n] = sum_k A[m][k] B[n][k], made by one tiled kernel whose epilogues differ:
 //   stats  A = W (tokens), B = h (states): a tile's logits become each state's
 //          maximum and sum of exp over the tile's tokens; a second kernel joins
 //          the tiles of a state;
 //   dz     the same product again: dz = g (exp(z - m - logsum) - [v = y]),
-//          rounded to bfloat16, as [state][token] and as [token][state];
-//   acc    A = W^T of a piece of the vocabulary, B = dz: adds to dh in float32;
+//          rounded to bfloat16, as [state][token] of a piece of the vocabulary;
+//   acc    A = W^T of the piece, B = dz: adds to dh in float32;
 //   mat    A = h^T, B = dz^T: rows of dW, complete after one product.
-// The operands of the last two are transposed into the workspace first, so one
-// access pattern serves all four.
+// The last two read their transposed operands from W, h and dz as they lie in
+// memory; the transposition happens in the read from LDS.
 //
 // float32 operands are split into three bfloat16 parts x = x1 + x2 + x3 (each the
 // rounding of what the parts before leave: 24 bits in all), and a product sums
@@ -26,13 +25,19 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef int vs32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 // s_waitcnt operand: no vector memory operation outstanding, other counters free
 // (vmcnt in bits 3:0 and 15:14, expcnt in 6:4, lgkmcnt in 11:8).
 constexpr int WAIT_VM0 = 0x0F70;
 // Last word of a raw buffer resource: 32-bit data, no swizzle.
 constexpr int RSRC_WORD3 = 0x00027000;
+// Range of the buffer resources, and the offset of a load that shall read zeros.
+// A tile's own offsets stay below it: 255 rows of at most 2^22 elements.
+constexpr uint32_t BEYOND = 0x80000000u;
 
 // Part products of float32 operands, in the order in which they are summed.
 __device__ __forceinline__ void part_pair(int i, int* pa, int* pb) {
@@ -69,10 +74,107 @@ __device__ __forceinline__ void tile_of(int id, int tiles_m, int tiles_n, int* t
   *tn = in / rows;
 }
 
+// Thread of the workgroup, made anew from the lane counter: kept in a register
+// across the products it would cost them one.
+__device__ __forceinline__ int thread_again(int wave) {
+  return wave * WAVE + (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+}
+
+// One 16-byte group a lane from base + byte_off into LDS at `lds`, lanes in order;
+// an offset from BEYOND on reads as zeros. Asynchronous: it counts as a vector
+// memory operation, and the caller waits for it (WAIT_VM0). In assembly because the
+// compiler, which cannot tell the two halves of LDS apart, else waits for it before
+// the next transposing read. It has no result register.
+__device__ __forceinline__ void copy_to_lds(vs32x4 rsrc, uint32_t byte_off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :: "s"(lds), "v"(byte_off), "s"(rsrc) : "memory");
+}
+
+// One operand of a tile: how ROWS rows by CE_BK of depth get from memory into LDS,
+// and its fragments from there.
+//   plain       memory [row][k]: LDS row of 8 groups of 16 bytes; slot s of row r
+//               holds group s ^ (r & 7), so that a fragment's 16 rows spread over
+//               the banks.
+//   transposed  memory [k][row]: LDS as in memory, ROWS / 8 groups a k; a
+//               fragment is made by the transposing LDS read, which gives lane i of
+//               16 the i-th of 16 columns of 4 consecutive k. Pairs of groups are
+//               permuted by pair ^ f(k), f from bits 0, 1 and 3 of k: the 16 k that
+//               one read touches are then spread over the banks.
+// Groups behind the depth, or (transposed) behind the last row, are loaded from
+// beyond the buffer resource's range, which reads as zero.
+template <bool TRANS, int ROWS, int FRAGS, int LOADS, int THREADS>
+struct Side {
+  static constexpr int GROUPS = TRANS ? ROWS / 8 : CE_BK / 8;   // of 16 bytes, a line of LDS
+  static constexpr int READS = TRANS ? 2 : 1;                   // LDS reads a fragment
+  uint32_t off[LOADS];
+  uint32_t at[TRANS ? FRAGS : 2];   // transposed: per fragment; plain: per half of the depth
+
+  static __device__ __forceinline__ int line(int i, int tid) { return (i * THREADS + tid) / GROUPS; }
+  static __device__ __forceinline__ int group(int i, int tid) {
+    const int slot = (i * THREADS + tid) % GROUPS, l = line(i, tid);
+    if (!TRANS) return slot ^ (l & 7);
+    return (((slot >> 1) ^ (twist(l) & (GROUPS / 2 - 1))) << 1) | (slot & 1);
+  }
+  static __device__ __forceinline__ int twist(int k) { return (k & 3) | ((k >> 3) & 1) << 2; }
+
+  // base: first row of the tile; rows, ld: of the operand; wave_row: first row of
+  // this wave's fragments in the tile.
+  __device__ __forceinline__ void init(int base, int rows, int64_t ld, int wave_row, int lane) {
+    const int fr = lane & 15, fk = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      const int l = line(i, threadIdx.x), gr = group(i, threadIdx.x);
+      if (TRANS) off[i] = base + gr * 8 < rows ? (uint32_t)(l * ld + gr * 8) * 2u : BEYOND;
+      else off[i] = (uint32_t)(min(l, rows - 1 - base) * ld + gr * 8) * 2u;   // rows past the end repeat
+    }
+    if (TRANS) {
+      const int f = twist(fk * 8 + (fr >> 2)) & (GROUPS / 2 - 1);
+#pragma unroll
+      for (int i = 0; i < FRAGS; ++i)
+        at[i] = (uint32_t)((fk * 8 + (fr >> 2)) * ROWS + ((wave_row / 16 + i) ^ f) * 16 + (fr & 3) * 4);
+    } else {
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk)
+        at[kk] = (uint32_t)((wave_row + fr) * CE_BK + (((kk * 4 + fk) ^ (fr & 7)) * 8));
+    }
+  }
+  // Loads the tile's depth k.. of the operand that begins at p (the tile's first
+  // row, k = 0); depth: where the operand ends.
+  __device__ __forceinline__ void load(const uint16_t* p, int64_t ld, int k, int depth, uint32_t lds,
+                                       int wave) {
+    const uint64_t base = (uint64_t)(uintptr_t)(p + (TRANS ? (int64_t)k * ld : (int64_t)k));
+    const vs32x4 r = {(int)(uint32_t)base, (int)(uint32_t)(base >> 32), (int)BEYOND, RSRC_WORD3};
+    if (k + CE_BK <= depth) {
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) copy_to_lds(r, off[i], lds + i * THREADS * 16);
+    } else {   // the operand's last, shorter step
+      const int tid = thread_again(wave);
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) {
+        const bool in = k + (TRANS ? line(i, tid) : group(i, tid) * 8) < depth;
+        copy_to_lds(r, in ? off[i] : BEYOND, lds + i * THREADS * 16);
+      }
+    }
+  }
+  __device__ __forceinline__ bf16x8 frag(const uint16_t* lds, int i, int kk) const {
+#if defined(__HIP_DEVICE_COMPILE__)
+    if constexpr (TRANS) {
+      const uint16_t* p = lds + at[i] + kk * 32 * ROWS;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * ROWS));
+      return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      return *(const bf16x8*)(lds + at[kk] + i * 16 * CE_BK);
+    }
+#else
+    return bf16x8{};
+#endif
+  }
+};
+
 template <int BM, int BN, int WM, int WN, typename Epi>
 __global__ __launch_bounds__(WM* WN* WAVE, WM* WN == 8 ? 2 : 1) void ce_gemm_kernel(
     CeGemm g, int tiles_m, int tiles_n, typename Epi::Args ea) {
-#if defined(__HIP_DEVICE_COMPILE__)   // buffer resources exist on the device side only
   using T = Tile<BM, BN, WM, WN>;
   __shared__ __align__(16) uint16_t lds[2 * T::STAGE];
   const int tid = threadIdx.x, lane = tid & (WAVE - 1);
@@ -81,51 +183,30 @@ __global__ __launch_bounds__(WM* WN* WAVE, WM* WN == 8 ? 2 : 1) void ce_gemm_ker
   int tm, tn;
   tile_of(blockIdx.x, tiles_m, tiles_n, &tm, &tn);
   const int m0 = tm * BM, n0 = tn * BN;
-  // rows past the end repeat the last one; a tile may lie behind it altogether
-  const int mb = min(m0, g.M - 1), nb = min(n0, g.N - 1);
 
-  // This thread's loads: row of the tile, and the 16-byte slot it fills. Slot s
-  // of row r holds group s ^ (r & 7), which spreads a fragment's rows over banks.
-  uint32_t offa[T::LA], offb[T::LB];
-#pragma unroll
-  for (int i = 0; i < T::LA; ++i) {
-    const int c = i * T::THREADS + tid, row = c >> 3, grp = (c & 7) ^ (row & 7);
-    offa[i] = (uint32_t)(min(row, g.M - 1 - mb) * g.lda + grp * 8) * 2u;
-  }
-#pragma unroll
-  for (int i = 0; i < T::LB; ++i) {
-    const int c = i * T::THREADS + tid, row = c >> 3, grp = (c & 7) ^ (row & 7);
-    offb[i] = (uint32_t)(min(row, g.N - 1 - nb) * g.ldb + grp * 8) * 2u;
-  }
-  const uint16_t* rowa = g.A + (int64_t)mb * g.lda;
-  const uint16_t* rowb = g.B + (int64_t)nb * g.ldb;
+  Side<Epi::TRANS_A, BM, T::MI, T::LA, T::THREADS> sa;
+  Side<Epi::TRANS_B, BN, T::NI, T::LB, T::THREADS> sb;
+  sa.init(m0, g.M, g.lda, wm * T::TM, lane);
+  sb.init(n0, g.N, g.ldb, wn * T::TN, lane);
+  const uint16_t* pa = g.A + (Epi::TRANS_A ? (int64_t)m0 : m0 * g.lda);
+  const uint16_t* pb = g.B + (Epi::TRANS_B ? (int64_t)n0 : n0 * g.ldb);
 
-  // steps of this split
-  const int steps_k = g.K / CE_BK;
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(lds_void*)lds);
+
+  // steps of this split; next_*: what is to be loaded next
+  const int steps_k = (g.K + CE_BK - 1) / CE_BK;
   const int total = steps_k * g.parts;
   const int per = (total + g.splits - 1) / g.splits;
   const int first = min(total, (int)blockIdx.y * per), last = min(total, first + per);
-
-  // Loads go straight into LDS: per lane a 32-bit offset from the tile's first
-  // row, per step a scalar one. next_*: what is to be loaded next.
   int next_pair = first / steps_k, next_k = (first - next_pair * steps_k) * CE_BK;
   auto issue = [&](int stage) {
-    int pa = 0, pb = 0;
-    if (g.parts > 1) part_pair(next_pair, &pa, &pb);
-    const auto ra = __builtin_amdgcn_make_buffer_rsrc((void*)(rowa + pa * g.plane_a), 0, -1, RSRC_WORD3);
-    const auto rb = __builtin_amdgcn_make_buffer_rsrc((void*)(rowb + pb * g.plane_b), 0, -1, RSRC_WORD3);
-    uint16_t* la = lds + stage * T::STAGE + wave * WAVE * 8;
-    uint16_t* lb = la + BM * CE_BK;
-#pragma unroll
-    for (int i = 0; i < T::LA; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(la + i * T::THREADS * 8), 16, (int)offa[i],
-                                               next_k * 2, 0, 0);
-#pragma unroll
-    for (int i = 0; i < T::LB; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(lb + i * T::THREADS * 8), 16, (int)offb[i],
-                                               next_k * 2, 0, 0);
+    int ia = 0, ib = 0;
+    if (g.parts > 1) part_pair(next_pair, &ia, &ib);
+    const uint32_t la = lds0 + (stage * T::STAGE + wave * WAVE * 8) * 2;
+    sa.load(pa + ia * g.plane_a, g.lda, next_k, g.K, la, wave);
+    sb.load(pb + ib * g.plane_b, g.ldb, next_k, g.K, la + BM * CE_BK * 2, wave);
     next_k += CE_BK;
-    if (next_k == g.K) {
+    if (next_k >= g.K) {
       next_k = 0;
       ++next_pair;
     }
@@ -137,23 +218,20 @@ __global__ __launch_bounds__(WM* WN* WAVE, WM* WN == 8 ? 2 : 1) void ce_gemm_ker
 #pragma unroll
     for (int j = 0; j < T::NI; ++j) acc[i][j] = (f32x4)(0.0f);
 
-  const int fr = lane & 15, fk = lane >> 4;
-  const int grp0 = (fk ^ (fr & 7)) * 8, grp1 = ((4 + fk) ^ (fr & 7)) * 8;
   auto step = [&](int s, int stage) {
     // this stage has arrived for every wave, and every wave is done with the other
     __builtin_amdgcn_s_waitcnt(WAIT_VM0);
     __syncthreads();
     if (s + 1 < last) issue(stage ^ 1);
-    const uint16_t* la = lds + stage * T::STAGE + (wm * T::TM + fr) * CE_BK;
-    const uint16_t* lb = lds + stage * T::STAGE + BM * CE_BK + (wn * T::TN + fr) * CE_BK;
+    const uint16_t* la = lds + stage * T::STAGE;
+    const uint16_t* lb = la + BM * CE_BK;
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
-      const int grp = kk ? grp1 : grp0;
       bf16x8 fa[T::MI], fb[T::NI];
 #pragma unroll
-      for (int j = 0; j < T::NI; ++j) fb[j] = *(const bf16x8*)(lb + j * 16 * CE_BK + grp);
+      for (int j = 0; j < T::NI; ++j) fb[j] = sb.frag(lb, j, kk);
 #pragma unroll
-      for (int i = 0; i < T::MI; ++i) fa[i] = *(const bf16x8*)(la + i * 16 * CE_BK + grp);
+      for (int i = 0; i < T::MI; ++i) fa[i] = sa.frag(la, i, kk);
 #pragma unroll
       for (int i = 0; i < T::MI; ++i)
 #pragma unroll
@@ -161,22 +239,23 @@ __global__ __launch_bounds__(WM* WN* WAVE, WM* WN == 8 ? 2 : 1) void ce_gemm_ker
           acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
     }
     // Order of issue: all of B's fragments and two of A's, then each row of
-    // matrix instructions with the fragment read that the row after the next needs.
+    // matrix instructions with the fragment reads that the row after the next needs.
     constexpr int MFMA = 0x008, DS_READ = 0x100;
+    constexpr int RA = decltype(sa)::READS, RB = decltype(sb)::READS;
     if constexpr (T::MI > 2) {
-      __builtin_amdgcn_sched_group_barrier(DS_READ, T::NI + 2, 0);
+      __builtin_amdgcn_sched_group_barrier(DS_READ, RB * T::NI + 2 * RA, 0);
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
 #pragma unroll
         for (int i = 0; i < T::MI - 2; ++i) {
           __builtin_amdgcn_sched_group_barrier(MFMA, T::NI, 0);
-          __builtin_amdgcn_sched_group_barrier(DS_READ, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(DS_READ, RA, 0);
         }
         if (kk == 0) {
           __builtin_amdgcn_sched_group_barrier(MFMA, T::NI, 0);
-          __builtin_amdgcn_sched_group_barrier(DS_READ, T::NI, 0);
+          __builtin_amdgcn_sched_group_barrier(DS_READ, RB * T::NI, 0);
           __builtin_amdgcn_sched_group_barrier(MFMA, T::NI, 0);
-          __builtin_amdgcn_sched_group_barrier(DS_READ, 2, 0);
+          __builtin_amdgcn_sched_group_barrier(DS_READ, 2 * RA, 0);
         } else {
           __builtin_amdgcn_sched_group_barrier(MFMA, 2 * T::NI, 0);
         }
@@ -192,7 +271,6 @@ __global__ __launch_bounds__(WM* WN* WAVE, WM* WN == 8 ? 2 : 1) void ce_gemm_ker
   if (s < last) step(s, 0);
   __syncthreads();
   Epi::template run<T>(ea, g, acc, m0 + wm * T::TM, n0 + wn * T::TN, tm, wm, wn, lane, (char*)lds);
-#endif
 }
 
 // Element i of acc[mi][ni] of lane l is C[m][n] with
@@ -200,6 +278,7 @@ __global__ __launch_bounds__(WM* WN* WAVE, WM* WN == 8 ? 2 : 1) void ce_gemm_ker
 
 struct EpiStats {
   typedef CeStatsOut Args;
+  static constexpr bool TRANS_A = false, TRANS_B = false;
   template <typename T, typename Acc>
   static __device__ __forceinline__ void run(const Args& o, const CeGemm& g, Acc& acc, int mw, int nw,
                                              int tm, int wm, int wn, int lane, char* lds) {
@@ -257,8 +336,11 @@ __device__ __forceinline__ void split3(float x, uint16_t (&p)[3]) {
   }
 }
 
+// PARTS: 1 writes dz rounded to bfloat16, 3 its three parts.
+template <int PARTS>
 struct EpiDz {
   typedef CeDzOut Args;
+  static constexpr bool TRANS_A = false, TRANS_B = false;
   template <typename T, typename Acc>
   static __device__ __forceinline__ void run(const Args& o, const CeGemm& g, Acc& acc, int mw, int nw,
                                              int, int, int, int lane, char*) {
@@ -266,18 +348,15 @@ struct EpiDz {
 #pragma unroll
     for (int j = 0; j < T::NI; ++j) {
       const int n = nw + 16 * j + fr;
-      if (n >= o.n_pad) continue;
-      int lab = -1;
+      int lab = n < g.N ? o.labels[n] : -1;
       float m = 0.0f, ls2 = 0.0f, gl = 0.0f;
-      if (n < g.N) {
-        const int l = o.labels[n];
-        if (l >= 0 && l < o.V) {
-          lab = l - o.v0;
-          m = o.stats[2 * (int64_t)n];
-          ls2 = o.stats[2 * (int64_t)n + 1] * LOG2E;
-          gl = o.grad_loss ? o.grad_loss[n] : 1.0f;
-        }
+      if (lab >= 0 && lab < o.V) {
+        lab -= o.v0;
+        m = o.stats[2 * (int64_t)n];
+        ls2 = o.stats[2 * (int64_t)n + 1] * LOG2E;
+        gl = o.grad_loss ? o.grad_loss[n] : 1.0f;
       }
+      uint16_t* row = o.dz + (int64_t)n * o.ldz;
 #pragma unroll
       for (int i = 0; i < T::MI; ++i) {
         const int r = mw + 16 * i + 4 * fk;
@@ -286,35 +365,18 @@ struct EpiDz {
         for (int e = 0; e < 4; ++e) {
           float q = fast_exp2((acc[i][j][e] - m) * LOG2E - ls2);
           if (r + e == lab) q -= 1.0f;
-          // a row left out, and what lies behind the last state or token, is 0
+          // a state left out, and what lies behind the last token, is 0
           d[e] = gl == 0.0f || r + e >= g.M ? 0.0f : gl * q;
         }
-        for (int p = 0; p < o.planes; ++p) {
-          uint16_t h[4];
-          if (o.planes == 1) {
-            const uint32_t lo = pack_bf16(d[0], d[1]), hi = pack_bf16(d[2], d[3]);
-            h[0] = (uint16_t)lo;
-            h[1] = (uint16_t)(lo >> 16);
-            h[2] = (uint16_t)hi;
-            h[3] = (uint16_t)(hi >> 16);
-          } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint16_t t[3];
-              split3(d[e], t);
-              h[e] = p == 0 ? t[0] : p == 1 ? t[1] : t[2];
-            }
-          }
-          if (o.dz && n < g.N && r < o.ldz) {   // ldz is a multiple of 4
-            uint2 w;
-            w.x = (uint32_t)h[0] | ((uint32_t)h[1] << 16);
-            w.y = (uint32_t)h[2] | ((uint32_t)h[3] << 16);
-            *(uint2*)(o.dz + p * o.plane_dz + (int64_t)n * o.ldz + r) = w;
-          }
-          if (o.dzt) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (r + e < g.M) o.dzt[p * o.plane_dzt + (int64_t)(r + e) * o.ldt + n] = h[e];
+        for (int p = 0; p < PARTS; ++p) {
+          const uint2 w = make_uint2(pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]));
+          if (n < g.N && r < o.ldz) *(uint2*)(row + p * o.plane_dz + r) = w;   // ldz is a multiple of 4
+          if (p + 1 < PARTS) {   // what the next part has to hold
+            d[0] -= __uint_as_float(w.x << 16);
+            d[1] -= __uint_as_float(w.x & 0xFFFF0000u);
+            d[2] -= __uint_as_float(w.y << 16);
+            d[3] -= __uint_as_float(w.y & 0xFFFF0000u);
           }
         }
       }
@@ -324,6 +386,7 @@ struct EpiDz {
 
 struct EpiAcc {
   typedef CeAccOut Args;
+  static constexpr bool TRANS_A = true, TRANS_B = false;
   template <typename T, typename Acc>
   static __device__ __forceinline__ void run(const Args& o, const CeGemm& g, Acc& acc, int mw, int nw,
                                              int, int, int, int lane, char*) {
@@ -348,6 +411,7 @@ struct EpiAcc {
 
 struct EpiMat {
   typedef CeMatOut Args;
+  static constexpr bool TRANS_A = true, TRANS_B = true;
   template <typename T, typename Acc>
   static __device__ __forceinline__ void run(const Args& o, const CeGemm& g, Acc& acc, int mw, int nw,
                                              int, int, int, int lane, char*) {
@@ -401,25 +465,6 @@ __global__ __launch_bounds__(256) void ce_pack_kernel(CePack p) {
   }
 }
 
-// 64 x 64 tiles through LDS.
-__global__ __launch_bounds__(256) void ce_transpose_kernel(CePack p, int tiles_c) {
-  __shared__ uint16_t t[64][66];
-  const int64_t r0 = (int64_t)(blockIdx.x / tiles_c) * 64;
-  const int c0 = (int)(blockIdx.x % tiles_c) * 64;
-  const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
-  for (int k = 0; k < p.planes; ++k) {
-    for (int i = y; i < 64; i += 4) {
-      uint16_t h[3] = {0, 0, 0};
-      if (r0 + i < p.rows && c0 + x < p.cols) load_parts(p, r0 + i, c0 + x, h);
-      t[i][x] = h[k];
-    }
-    __syncthreads();
-    for (int i = y; i < 64; i += 4)
-      if (c0 + i < p.cols && r0 + x < p.ld) p.dst[k * p.plane + (int64_t)(c0 + i) * p.ld + r0 + x] = t[x][i];
-    __syncthreads();
-  }
-}
-
 // ---------------------------------------------------------------- joins
 
 // 32 states a workgroup; 8 threads a state take every eighth tile.
@@ -456,12 +501,11 @@ __global__ __launch_bounds__(256) void ce_sum_kernel(const float* acc, int split
   }
 }
 
-// cover: rows of B's side that the tiles have to reach (its padding, if any).
 template <typename Epi>
-int gemm(const CeGemm& g, const typename Epi::Args& ea, int cover, hipStream_t st) {
+int gemm(const CeGemm& g, const typename Epi::Args& ea, hipStream_t st) {
   const int bm = ce_tile_m(g.N), bn = ce_tile_n(g.N);
   const int tiles_m = (g.M + bm - 1) / bm;
-  const int tiles_n = (cover + bn - 1) / bn;
+  const int tiles_n = (g.N + bn - 1) / bn;
   const dim3 grid((uint32_t)tiles_m * (uint32_t)tiles_n, (uint32_t)g.splits);
 #define CE_LAUNCH(BM, BN, WM, WN) \
   hipLaunchKernelGGL((ce_gemm_kernel<BM, BN, WM, WN, Epi>), grid, dim3(WM * WN * WAVE), 0, st, g, tiles_m, tiles_n, ea)
@@ -476,23 +520,20 @@ int gemm(const CeGemm& g, const typename Epi::Args& ea, int cover, hipStream_t s
 
 int ce_tile_m(int rows_b) { return rows_b <= 32 || rows_b > 128 ? 256 : 128; }
 int ce_tile_n(int rows_b) { return rows_b <= 32 ? 32 : rows_b <= 128 ? 128 : 256; }
+int ce_tiles_per_cu(int rows_b) { return rows_b > 128 ? 1 : 2; }
 
-int launch_ce_stats(const CeGemm& g, const CeStatsOut& o, hipStream_t st) { return gemm<EpiStats>(g, o, g.N, st); }
-int launch_ce_dz(const CeGemm& g, const CeDzOut& o, hipStream_t st) { return gemm<EpiDz>(g, o, o.dzt ? o.n_pad : g.N, st); }
-int launch_ce_acc(const CeGemm& g, const CeAccOut& o, hipStream_t st) { return gemm<EpiAcc>(g, o, g.N, st); }
-int launch_ce_mat(const CeGemm& g, const CeMatOut& o, hipStream_t st) { return gemm<EpiMat>(g, o, g.N, st); }
+int launch_ce_stats(const CeGemm& g, const CeStatsOut& o, hipStream_t st) { return gemm<EpiStats>(g, o, st); }
+int launch_ce_dz(const CeGemm& g, const CeDzOut& o, hipStream_t st) {
+  return g.parts == 1 ? gemm<EpiDz<1>>(g, o, st) : gemm<EpiDz<3>>(g, o, st);
+}
+int launch_ce_acc(const CeGemm& g, const CeAccOut& o, hipStream_t st) { return gemm<EpiAcc>(g, o, st); }
+int launch_ce_mat(const CeGemm& g, const CeMatOut& o, hipStream_t st) { return gemm<EpiMat>(g, o, st); }
 
-int launch_ce_pack(const CePack& p, bool transposed, hipStream_t st) {
-  if (transposed) {
-    const int tiles_c = (p.cols + 63) / 64;
-    const int64_t tiles_r = (p.ld + 63) / 64;
-    hipLaunchKernelGGL(ce_transpose_kernel, dim3((uint32_t)(tiles_r * tiles_c)), dim3(256), 0, st, p, tiles_c);
-  } else {
-    const int64_t bx = (p.ld + 255) / 256;
-    const dim3 grid((uint32_t)(bx < 64 ? bx : 64), (uint32_t)(p.rows < 65535 ? p.rows : 65535),
-                    (uint32_t)((p.rows + 65534) / 65535));
-    hipLaunchKernelGGL(ce_pack_kernel, grid, dim3(256), 0, st, p);
-  }
+int launch_ce_pack(const CePack& p, hipStream_t st) {
+  const int64_t bx = (p.ld + 255) / 256;
+  const dim3 grid((uint32_t)(bx < 64 ? bx : 64), (uint32_t)(p.rows < 65535 ? p.rows : 65535),
+                  (uint32_t)((p.rows + 65534) / 65535));
+  hipLaunchKernelGGL(ce_pack_kernel, grid, dim3(256), 0, st, p);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 

@@ -186,13 +186,14 @@ int launch_distill_backward(const DistillArgs& a, int bf16, hipStream_t s);
 constexpr int CE_BK = 64;          // depth of one step of the products, in bfloat16
 constexpr int CE_MAX_D = 1 << 22;
 
-// One product C[m][n] = sum_k A[m][k] B[n][k] of bfloat16 parts: rows of A and
-// B are contiguous along k, K is a multiple of CE_BK.
+// One product C[m][n] = sum_k A[m][k] B[n][k] of bfloat16 parts. An operand lies
+// in memory as [row][k] or, where the epilogue takes it transposed, as [k][row];
+// rows of memory start on 16 bytes and can be read in whole groups of 8 elements.
 struct CeGemm {
   const uint16_t *A, *B;
-  int64_t lda, ldb;          // row strides, elements
+  int64_t lda, ldb;          // strides of memory's rows, elements, at most CE_MAX_D
   int64_t plane_a, plane_b;  // distance of a float32 operand's three parts
-  int M, N, K;               // rows of A and B that exist, depth
+  int M, N, K;               // rows of A and B, depth
   int parts;                 // 1: bfloat16 operands; 6: products of float32's parts
   int splits;                // workgroups that share one tile's depth
 };
@@ -208,12 +209,8 @@ struct CeDzOut {
   const float* stats;        // [N][2]
   const float* grad_loss;    // [N] or nullptr
   int v0, V;
-  int planes;                // 1 or 3
-  uint16_t* dz;              // [planes][N][ldz], or nullptr
+  uint16_t* dz;              // [planes][N][ldz], zeros behind the piece's last token
   int64_t ldz, plane_dz;
-  uint16_t* dzt;             // [planes][rows of A][ldt], or nullptr
-  int64_t ldt, plane_dzt;
-  int n_pad;                 // columns of dzt, zeros from N on
 };
 struct CeAccOut {
   float* acc;                // [splits][N][ld]
@@ -227,21 +224,23 @@ struct CeMatOut {
   int vec;                   // rows of four can be stored at once
 };
 
+// Rows as the products take them: [planes][rows][ld] bfloat16, zeros from cols to ld.
 struct CePack {
   const void* src;           // [rows][cols], float32 or bfloat16
   int64_t stride;
   int bf16;
   int rows, cols;
   int planes;
-  uint16_t* dst;             // plain: [planes][rows][ld]; transposed: [planes][cols][ld]
-  int64_t ld, plane;         // columns from cols (rows) to ld are zeros
+  uint16_t* dst;
+  int64_t ld, plane;
 };
 
 // Tile shapes by the rows of B: see linear_ce.hip.
 int ce_tile_m(int rows_b);
 int ce_tile_n(int rows_b);
+int ce_tiles_per_cu(int rows_b);   // workgroups of that shape a CU holds at once
 
-int launch_ce_pack(const CePack& p, bool transposed, hipStream_t s);
+int launch_ce_pack(const CePack& p, hipStream_t s);
 int launch_ce_stats(const CeGemm& g, const CeStatsOut& o, hipStream_t s);
 int launch_ce_dz(const CeGemm& g, const CeDzOut& o, hipStream_t s);
 int launch_ce_acc(const CeGemm& g, const CeAccOut& o, hipStream_t s);

@@ -99,32 +99,38 @@ int distill_args(const void* logits, int64_t logits_stride, sv_dtype dtype, int3
 
 // ---------------------------------------------------------------- linear cross entropy
 
-// Most bytes of one piece's operands in the workspace: the last-level cache
-// holds 256 MB, so a piece of this size is still there when it is read back.
-constexpr int64_t CE_PIECE_BYTES = 128ll << 20;
 constexpr int64_t CE_MAX_ROWS = 1 << 22;
+// Bytes of a piece's operands in the workspace. A piece is a whole number of
+// rounds of tiles over the CUs (ce_round_rows); as many rounds as stay within
+// CE_PIECE_BYTES, half of what the last-level cache holds, and at least one unless
+// that takes more than CE_PIECE_MOST.
+constexpr int64_t CE_PIECE_BYTES = 128ll << 20, CE_PIECE_MOST = 512ll << 20;
 constexpr int64_t CE_PIECE_STEP = 256;    // a multiple of every tile height
-constexpr int64_t CE_MAX_PIECE = 1 << 20;
+constexpr int64_t CE_CUS = 256;
 
 struct CeShape {
-  int64_t N, D, V, kp;   // kp: depth of the logits' product, a multiple of CE_BK
+  int64_t N, D, V, kp;   // kp: row length of packed operands, a multiple of CE_BK
   int planes;
 };
 bool ce_shape(int32_t N, int32_t D, int32_t V, sv_dtype dtype, CeShape* s) {
   if (N < 1 || D < 1 || V < 1 || !known(dtype)) return false;
   if (N > CE_MAX_ROWS || D > sv::CE_MAX_D || V >= INT32_MAX - 1024) return false;
   *s = CeShape{N, D, V, round_up(D, sv::CE_BK), dtype == SV_BF16 ? 1 : 3};
-  // tiles of any product, and of the transposes
-  if (ceil_div(V, 128) * ceil_div(N, 32) >= INT32_MAX || ceil_div(N, 64) * ceil_div(D, 64) >= INT32_MAX)
-    return false;
-  return true;
+  // tiles of any product
+  return ceil_div(V, 128) * ceil_div(N, 32) < INT32_MAX;
 }
 
-// Tokens whose rows take at most CE_PIECE_BYTES at `bytes` each.
+// Tokens of a piece whose operands take `bytes` a token.
 int64_t piece_rows(const CeShape& s, int64_t bytes) {
-  int64_t rows = CE_PIECE_BYTES / bytes / CE_PIECE_STEP * CE_PIECE_STEP;
+  const int64_t tn = ceil_div(s.N, sv::ce_tile_n((int)s.N)), bm = sv::ce_tile_m((int)s.N);
+  const int64_t per_cu = sv::ce_tiles_per_cu((int)s.N);
+  int64_t round = round_up(ceil_div(CE_CUS * per_cu, tn) * bm, CE_PIECE_STEP);
+  int64_t rows = CE_PIECE_BYTES / bytes / round * round;
+  if (rows < round) rows = round;
+  const int64_t most = CE_PIECE_MOST / bytes / CE_PIECE_STEP * CE_PIECE_STEP;
+  if (rows > most) rows = most;
   if (rows < 4 * CE_PIECE_STEP) rows = 4 * CE_PIECE_STEP;
-  if (rows > CE_MAX_PIECE) rows = CE_MAX_PIECE;
+  if (rows > sv::CE_MAX_D) rows = sv::CE_MAX_D;   // dz's row length
   const int64_t all = round_up(s.V, CE_PIECE_STEP);
   return rows < all ? rows : all;
 }
@@ -146,20 +152,19 @@ CeForward ce_forward(const CeShape& s) {
 }
 
 struct CeBackward {
-  int64_t piece, n_pad, acc_ld;
+  int64_t piece, acc_ld;
   int splits;
-  size_t hidden, weight, hidden_t, weight_t, dz, dzt, acc, total;
+  size_t hidden, weight, dz, acc, total;
 };
-CeBackward ce_backward(const CeShape& s, bool want_h, bool want_w) {
+CeBackward ce_backward(const CeShape& s, bool want_h) {
   CeBackward b;
   Carver c;
-  b.n_pad = round_up(s.N, sv::CE_BK);
-  // dz and its transpose are what a piece makes; the weight's rows what it reads
-  const int64_t wide = b.n_pad > s.kp ? b.n_pad : s.kp;
-  b.piece = piece_rows(s, s.planes * wide * 2);
+  b.piece = piece_rows(s, s.planes * (s.N > s.kp ? s.N : s.kp) * 2);
   b.acc_ld = round_up(s.D, 4);
+  // dh has few tiles and a long depth: its depth is split until every CU has one
   const int64_t tiles = ceil_div(s.D, sv::ce_tile_m((int)s.N)) * ceil_div(s.N, sv::ce_tile_n((int)s.N));
-  int64_t splits = 512 / tiles;
+  int64_t splits = ceil_div(CE_CUS * sv::ce_tiles_per_cu((int)s.N), tiles);
+  if (tiles >= CE_CUS) splits = 1;
   const int64_t steps = b.piece / sv::CE_BK * (s.planes == 1 ? 1 : 6);
   if (splits > steps / 4) splits = steps / 4;
   const int64_t fit = CE_PIECE_BYTES / (s.N * b.acc_ld * 4);
@@ -167,45 +172,38 @@ CeBackward ce_backward(const CeShape& s, bool want_h, bool want_w) {
   b.splits = splits < 1 ? 1 : (int)splits;
   b.hidden = c.take((size_t)(s.planes * s.N * s.kp) * 2);
   b.weight = c.take((size_t)(s.planes * b.piece * s.kp) * 2);
-  b.hidden_t = c.take(want_w ? (size_t)(s.planes * s.D * b.n_pad) * 2 : 0);
-  b.weight_t = c.take(want_h ? (size_t)(s.planes * s.D * b.piece) * 2 : 0);
-  b.dz = c.take(want_h ? (size_t)(s.planes * s.N * b.piece) * 2 : 0);
-  b.dzt = c.take(want_w ? (size_t)(s.planes * b.piece * b.n_pad) * 2 : 0);
+  b.dz = c.take((size_t)(s.planes * s.N * b.piece) * 2);
   b.acc = c.take(want_h ? (size_t)(b.splits * s.N * b.acc_ld) * 4 : 0);
   b.total = c.off;
   return b;
 }
 
-// A matrix as the products take it: rows of bfloat16 (parts), kp long, on 16
-// bytes. Used as it is where it has that form, else packed.
+// A matrix as the products take it: bfloat16 (parts), rows on 16 bytes, read in
+// groups of 8. Used as it is where it has that form, else packed.
 struct Operand {
   const uint16_t* p;
   int64_t ld, plane;
+  int64_t cols;
 };
 bool ce_direct(const void* p, int64_t stride, const CeShape& s) {
-  return s.planes == 1 && s.kp == s.D && aligned(p, 16) && stride % 8 == 0 && stride <= sv::CE_MAX_D;
+  return s.planes == 1 && s.D % 8 == 0 && aligned(p, 16) && stride % 8 == 0 && stride <= sv::CE_MAX_D;
 }
 int ce_operand(const void* src, int64_t stride, int64_t row0, int64_t rows, const CeShape& s,
                uint16_t* room, hipStream_t st, Operand* out) {
   const char* at = (const char*)src + row0 * stride * (s.planes == 1 ? 2 : 4);
   if (ce_direct(src, stride, s)) {
-    *out = Operand{(const uint16_t*)at, stride, 0};
+    *out = Operand{(const uint16_t*)at, stride, 0, s.D};
     return 0;
   }
   sv::CePack p{at, stride, s.planes == 1, (int)rows, (int)s.D, s.planes, room, s.kp, rows * s.kp};
-  *out = Operand{room, s.kp, p.plane};
-  return sv::launch_ce_pack(p, false, st);
-}
-int ce_transposed(const void* src, int64_t stride, int64_t row0, int64_t rows, int64_t ld,
-                  const CeShape& s, uint16_t* room, hipStream_t st, Operand* out) {
-  const char* at = (const char*)src + row0 * stride * (s.planes == 1 ? 2 : 4);
-  sv::CePack p{at, stride, s.planes == 1, (int)rows, (int)s.D, s.planes, room, ld, s.D * ld};
-  *out = Operand{room, ld, p.plane};
-  return sv::launch_ce_pack(p, true, st);
+  *out = Operand{room, s.kp, p.plane, s.kp};
+  return sv::launch_ce_pack(p, st);
 }
 sv::CeGemm ce_gemm(const Operand& a, int64_t M, const Operand& b, int64_t N, int64_t K, int planes) {
   return sv::CeGemm{a.p, b.p, a.ld, b.ld, a.plane, b.plane, (int)M, (int)N, (int)K, planes == 1 ? 1 : 6, 1};
 }
+// Depth of the logits' product: what both operands have in whole groups.
+int64_t ce_depth(const Operand& a, const Operand& b) { return a.cols < b.cols ? a.cols : b.cols; }
 
 int ce_check(const void* hidden, int64_t hidden_stride, const void* weight, int64_t weight_stride,
              sv_dtype dtype, const int32_t* labels, int32_t N, int32_t D, int32_t V, CeShape* s) {
@@ -320,7 +318,7 @@ int spec_verify_linear_ce(const void* hidden, int64_t hidden_stride, const void*
     const int64_t rows = V - v0 < piece ? V - v0 : piece;
     if (ce_operand(weight, weight_stride, v0, rows, s, (uint16_t*)(ws + f.weight), st, &w)) return SV_EHIP;
     const sv::CeStatsOut o{labels, (int)v0, V, partial + v0 / bm * N, zlabel};
-    if (sv::launch_ce_stats(ce_gemm(w, rows, h, N, s.kp, s.planes), o, st)) return SV_EHIP;
+    if (sv::launch_ce_stats(ce_gemm(w, rows, h, N, ce_depth(w, h), s.planes), o, st)) return SV_EHIP;
   }
   return sv::launch_ce_join(partial, zlabel, labels, (int)ceil_div(V, bm), N, V, out_loss, out_stats, st)
              ? SV_EHIP : SV_OK;
@@ -331,7 +329,7 @@ size_t spec_verify_linear_ce_backward_workspace_bytes(int32_t N, int32_t D, int3
                                                       int want_grad_weight) {
   CeShape s;
   if (!want_grad_hidden && !want_grad_weight) return 0;
-  return ce_shape(N, D, V, dtype, &s) ? ce_backward(s, want_grad_hidden, want_grad_weight).total : 0;
+  return ce_shape(N, D, V, dtype, &s) ? ce_backward(s, want_grad_hidden).total : 0;
 }
 
 int spec_verify_linear_ce_backward(const void* hidden, int64_t hidden_stride, const void* weight,
@@ -347,44 +345,40 @@ int spec_verify_linear_ce_backward(const void* hidden, int64_t hidden_stride, co
   if ((out_grad_hidden && (grad_hidden_stride < D || !aligned(out_grad_hidden, size_of(dtype)))) ||
       (out_grad_weight && (grad_weight_stride < D || !aligned(out_grad_weight, size_of(dtype)))))
     return SV_EINVAL;
-  const CeBackward b = ce_backward(s, out_grad_hidden, out_grad_weight);
+  const CeBackward b = ce_backward(s, out_grad_hidden);
   if (!workspace_ok(workspace, workspace_bytes, b.total)) return SV_EWORKSPACE;
   hipStream_t st = (hipStream_t)stream;
   char* ws = (char*)workspace;
   const int bf16 = dtype == SV_BF16;
   const size_t es = size_of(dtype);
-  uint16_t* dz = out_grad_hidden ? (uint16_t*)(ws + b.dz) : nullptr;
-  uint16_t* dzt = out_grad_weight ? (uint16_t*)(ws + b.dzt) : nullptr;
+  uint16_t* dz = (uint16_t*)(ws + b.dz);
   float* acc = (float*)(ws + b.acc);
-  Operand h, ht{}, w, wt{};
+  Operand h, w;
   if (ce_operand(hidden, hidden_stride, 0, N, s, (uint16_t*)(ws + b.hidden), st, &h)) return SV_EHIP;
-  if (dzt && ce_transposed(hidden, hidden_stride, 0, N, b.n_pad, s, (uint16_t*)(ws + b.hidden_t), st, &ht))
-    return SV_EHIP;
-  const int mat_vec = dzt && aligned(out_grad_weight, 4 * es) && grad_weight_stride % 4 == 0;
+  const int mat_vec = aligned(out_grad_weight, 4 * es) && grad_weight_stride % 4 == 0;
   for (int64_t v0 = 0; v0 < V; v0 += b.piece) {
     const int64_t rows = V - v0 < b.piece ? V - v0 : b.piece;
-    const int64_t depth = round_up(rows, sv::CE_BK);
+    const int64_t ldz = round_up(rows, sv::CE_BK);
     if (ce_operand(weight, weight_stride, v0, rows, s, (uint16_t*)(ws + b.weight), st, &w)) return SV_EHIP;
-    const sv::CeDzOut o{labels, stats, grad_loss, (int)v0, V, s.planes, dz, depth, N * depth,
-                        dzt, b.n_pad, rows * b.n_pad, (int)b.n_pad};
-    if (sv::launch_ce_dz(ce_gemm(w, rows, h, N, s.kp, s.planes), o, st)) return SV_EHIP;
-    if (dz) {
-      if (ce_transposed(weight, weight_stride, v0, rows, depth, s, (uint16_t*)(ws + b.weight_t), st, &wt))
-        return SV_EHIP;
-      sv::CeGemm g = ce_gemm(wt, D, Operand{dz, depth, N * depth}, N, depth, s.planes);
+    const sv::CeDzOut o{labels, stats, grad_loss, (int)v0, V, dz, ldz, N * ldz};
+    if (sv::launch_ce_dz(ce_gemm(w, rows, h, N, ce_depth(w, h), s.planes), o, st)) return SV_EHIP;
+    const Operand z{dz, ldz, N * ldz, ldz};
+    if (out_grad_hidden) {
+      sv::CeGemm g = ce_gemm(w, D, z, N, rows, s.planes);
       g.splits = b.splits;
       const sv::CeAccOut ao{acc, b.acc_ld, N * b.acc_ld, v0 > 0};
       if (sv::launch_ce_acc(g, ao, st)) return SV_EHIP;
     }
-    if (dzt) {
-      const sv::CeGemm g = ce_gemm(ht, D, Operand{dzt, b.n_pad, rows * b.n_pad}, rows, b.n_pad, s.planes);
+    if (out_grad_weight) {
+      const sv::CeGemm g = ce_gemm(h, D, z, rows, N, s.planes);
       const sv::CeMatOut mo{(char*)out_grad_weight + v0 * grad_weight_stride * es, grad_weight_stride, bf16,
                             mat_vec};
       if (sv::launch_ce_mat(g, mo, st)) return SV_EHIP;
     }
   }
-  if (dz && sv::launch_ce_sum(acc, b.splits, N * b.acc_ld, b.acc_ld, N, D, out_grad_hidden,
-                              grad_hidden_stride, bf16, st))
+  if (out_grad_hidden &&
+      sv::launch_ce_sum(acc, b.splits, N * b.acc_ld, b.acc_ld, N, D, out_grad_hidden,
+                        grad_hidden_stride, bf16, st))
     return SV_EHIP;
   return SV_OK;
 }
