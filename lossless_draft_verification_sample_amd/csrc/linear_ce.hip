@@ -82,10 +82,12 @@ __device__ __forceinline__ int thread_again(int wave) {
 
 // One 16-byte group a lane from base + byte_off into LDS at `lds`, lanes in order;
 // an offset from BEYOND on reads as zeros. Asynchronous: it counts as a vector
-// memory operation, and the caller waits for it (WAIT_VM0). In assembly because the
-// compiler, which cannot tell the two halves of LDS apart, else waits for it before
-// the next transposing read. It has no result register.
-__device__ __forceinline__ void copy_to_lds(vs32x4 rsrc, uint32_t byte_off, uint32_t lds) {
+// memory operation, and the caller waits for it (WAIT_VM0).
+// In assembly because the compiler, which cannot tell the two halves of LDS apart,
+// else waits for it before the next transposing read (dW 632 instead of 450 us a
+// piece of 16,384 tokens at 4,096 states of 4,096). It has no result register.
+__device__ __forceinline__ void copy_to_lds(uint64_t base, uint32_t byte_off, uint32_t lds) {
+  const vs32x4 rsrc = {(int)(uint32_t)base, (int)(uint32_t)(base >> 32), (int)BEYOND, RSRC_WORD3};
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :: "s"(lds), "v"(byte_off), "s"(rsrc) : "memory");
 }
@@ -143,16 +145,15 @@ struct Side {
   __device__ __forceinline__ void load(const uint16_t* p, int64_t ld, int k, int depth, uint32_t lds,
                                        int wave) {
     const uint64_t base = (uint64_t)(uintptr_t)(p + (TRANS ? (int64_t)k * ld : (int64_t)k));
-    const vs32x4 r = {(int)(uint32_t)base, (int)(uint32_t)(base >> 32), (int)BEYOND, RSRC_WORD3};
     if (k + CE_BK <= depth) {
 #pragma unroll
-      for (int i = 0; i < LOADS; ++i) copy_to_lds(r, off[i], lds + i * THREADS * 16);
+      for (int i = 0; i < LOADS; ++i) copy_to_lds(base, off[i], lds + i * THREADS * 16);
     } else {   // the operand's last, shorter step
       const int tid = thread_again(wave);
 #pragma unroll
       for (int i = 0; i < LOADS; ++i) {
         const bool in = k + (TRANS ? line(i, tid) : group(i, tid) * 8) < depth;
-        copy_to_lds(r, in ? off[i] : BEYOND, lds + i * THREADS * 16);
+        copy_to_lds(base, in ? off[i] : BEYOND, lds + i * THREADS * 16);
       }
     }
   }
@@ -450,38 +451,78 @@ struct EpiMat {
 
 // ---------------------------------------------------------------- packing
 
-__device__ __forceinline__ void load_parts(const CePack& p, int64_t r, int c, uint16_t (&h)[3]) {
-  if (p.bf16) h[0] = ((const uint16_t*)p.src)[r * p.stride + c];
-  else split3(((const float*)p.src)[r * p.stride + c], h);
-}
-
+// Four columns a thread; VEC: the source's rows can be read four at a time.
+template <bool VEC>
 __global__ __launch_bounds__(256) void ce_pack_kernel(CePack p) {
-  const int64_t r = blockIdx.y + (int64_t)blockIdx.z * 65535;
-  if (r >= p.rows) return;
-  for (int64_t c = blockIdx.x * 256 + threadIdx.x; c < p.ld; c += (int64_t)gridDim.x * 256) {
-    uint16_t h[3] = {0, 0, 0};
-    if (c < p.cols) load_parts(p, r, (int)c, h);
-    for (int k = 0; k < p.planes; ++k) p.dst[k * p.plane + r * p.ld + c] = h[k];
+  const int64_t quads = p.ld / 4, all = quads * p.rows;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / quads;
+    const int c = (int)(i - r * quads) * 4;
+    uint16_t h[3][4] = {};
+    if (p.bf16) {
+      const uint16_t* src = (const uint16_t*)p.src + r * p.stride + c;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + e < p.cols) h[0][e] = src[e];
+    } else {
+      const float* src = (const float*)p.src + r * p.stride + c;
+      float v[4];
+      if (VEC && c + 3 < p.cols) {
+        const f32x4 q = __builtin_nontemporal_load((const f32x4*)src);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = q[e];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = c + e < p.cols ? src[e] : 0.0f;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint16_t t[3];
+        split3(v[e], t);
+        h[0][e] = t[0];
+        h[1][e] = t[1];
+        h[2][e] = t[2];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      if (k < p.planes) {
+        const uint2 w = make_uint2(h[k][0] | ((uint32_t)h[k][1] << 16), h[k][2] | ((uint32_t)h[k][3] << 16));
+        *(uint2*)(p.dst + k * p.plane + r * p.ld + c) = w;
+      }
   }
 }
 
 // ---------------------------------------------------------------- joins
 
-// 32 states a workgroup; 8 threads a state take every eighth tile.
+// A workgroup joins X states; 256 / X threads a state take every so many-th tile.
+template <int X>
 __global__ __launch_bounds__(256) void ce_join_kernel(const MaxSum* partial, const float* zlabel,
                                                       const int32_t* labels, int tiles, int N, int V,
                                                       float* loss, float* stats) {
-  __shared__ MaxSum red[8][32];
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-  const int64_t n = (int64_t)blockIdx.x * 32 + x;
+  constexpr int Y = 256 / X;
+  __shared__ MaxSum red[Y][X];
+  const int x = threadIdx.x % X, y = threadIdx.x / X;
+  const int64_t n = (int64_t)blockIdx.x * X + x;
   MaxSum s{-INFINITY, 0.0f};
-  if (n < N)
-    for (int t = y; t < tiles; t += 8) s = join(s, partial[(int64_t)t * N + n], LOG2E);
-  red[y][x] = s;
-  __syncthreads();
-  if (y || n >= N) return;
+  if (n < N) {
+    int t = y;
+    for (; t + 3 * Y < tiles; t += 4 * Y) {
+      MaxSum p[4];
 #pragma unroll
-  for (int i = 1; i < 8; ++i) s = join(s, red[i][x], LOG2E);
+      for (int i = 0; i < 4; ++i) p[i] = partial[(int64_t)(t + i * Y) * N + n];
+      s = join(s, join(join(p[0], p[1], LOG2E), join(p[2], p[3], LOG2E), LOG2E), LOG2E);
+    }
+    for (; t < tiles; t += Y) s = join(s, partial[(int64_t)t * N + n], LOG2E);
+  }
+#pragma unroll
+  for (int half = Y / 2; half > 0; half >>= 1) {
+    red[y][x] = s;
+    __syncthreads();
+    if (y < half) s = join(s, red[y + half][x], LOG2E);
+    __syncthreads();
+  }
+  if (y || n >= N) return;
   const float logsum = logf(s.s);
   stats[2 * n] = s.m;
   stats[2 * n + 1] = logsum;
@@ -489,16 +530,25 @@ __global__ __launch_bounds__(256) void ce_join_kernel(const MaxSum* partial, con
   loss[n] = l >= 0 && l < V ? logsum - (zlabel[n] - s.m) : 0.0f;
 }
 
+// Sums the splits of dh in order, four columns a thread.
 __global__ __launch_bounds__(256) void ce_sum_kernel(const float* acc, int splits, int64_t split_stride,
-                                                     int64_t ld, int D, void* out, int64_t out_stride,
-                                                     int bf16) {
-  const int64_t n = blockIdx.x;
-  for (int d = threadIdx.x; d < D; d += 256) {
-    float v = acc[n * ld + d];
-    for (int s = 1; s < splits; ++s) v += acc[s * split_stride + n * ld + d];
-    if (bf16) put((uint16_t*)out + n * out_stride + d, v);
-    else ((float*)out)[n * out_stride + d] = v;
-  }
+                                                     int64_t ld, int64_t quads, int N, int D, void* out,
+                                                     int64_t out_stride, int bf16) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t n = i / quads;
+  if (n >= N) return;
+  const int d = (int)(i - n * quads) * 4;
+  const f32x4* p = (const f32x4*)(acc + n * ld + d);
+  const int64_t step = split_stride / 4;
+  f32x4 v = *p;
+#pragma unroll 8
+  for (int s = 1; s < splits; ++s) v += p[s * step];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (d + e < D) {
+      if (bf16) put((uint16_t*)out + n * out_stride + d + e, v[e]);
+      else ((float*)out)[n * out_stride + d + e] = v[e];
+    }
 }
 
 template <typename Epi>
@@ -509,7 +559,7 @@ int gemm(const CeGemm& g, const typename Epi::Args& ea, hipStream_t st) {
   const dim3 grid((uint32_t)tiles_m * (uint32_t)tiles_n, (uint32_t)g.splits);
 #define CE_LAUNCH(BM, BN, WM, WN) \
   hipLaunchKernelGGL((ce_gemm_kernel<BM, BN, WM, WN, Epi>), grid, dim3(WM * WN * WAVE), 0, st, g, tiles_m, tiles_n, ea)
-  if (bn == 32) CE_LAUNCH(256, 32, 4, 1);
+  if (bn == 32) CE_LAUNCH(128, 32, 4, 1);
   else if (bn == 128) CE_LAUNCH(128, 128, 2, 2);
   else CE_LAUNCH(256, 256, 2, 4);
 #undef CE_LAUNCH
@@ -518,9 +568,9 @@ int gemm(const CeGemm& g, const typename Epi::Args& ea, hipStream_t st) {
 
 }  // namespace
 
-int ce_tile_m(int rows_b) { return rows_b <= 32 || rows_b > 128 ? 256 : 128; }
+int ce_tile_m(int rows_b) { return rows_b > 128 ? 256 : 128; }
 int ce_tile_n(int rows_b) { return rows_b <= 32 ? 32 : rows_b <= 128 ? 128 : 256; }
-int ce_tiles_per_cu(int rows_b) { return rows_b > 128 ? 1 : 2; }
+int ce_tiles_per_cu(int rows_b) { return rows_b > 128 ? 1 : rows_b > 32 ? 2 : 4; }
 
 int launch_ce_stats(const CeGemm& g, const CeStatsOut& o, hipStream_t st) { return gemm<EpiStats>(g, o, st); }
 int launch_ce_dz(const CeGemm& g, const CeDzOut& o, hipStream_t st) {
@@ -530,24 +580,31 @@ int launch_ce_acc(const CeGemm& g, const CeAccOut& o, hipStream_t st) { return g
 int launch_ce_mat(const CeGemm& g, const CeMatOut& o, hipStream_t st) { return gemm<EpiMat>(g, o, st); }
 
 int launch_ce_pack(const CePack& p, hipStream_t st) {
-  const int64_t bx = (p.ld + 255) / 256;
-  const dim3 grid((uint32_t)(bx < 64 ? bx : 64), (uint32_t)(p.rows < 65535 ? p.rows : 65535),
-                  (uint32_t)((p.rows + 65534) / 65535));
-  hipLaunchKernelGGL(ce_pack_kernel, grid, dim3(256), 0, st, p);
+  const int64_t blocks = (p.ld / 4 * p.rows + 255) / 256;
+  const dim3 grid((uint32_t)(blocks < 16384 ? blocks : 16384));
+  const bool vec = !p.bf16 && p.stride % 4 == 0 && (uintptr_t)p.src % 16 == 0;
+  if (vec) hipLaunchKernelGGL(ce_pack_kernel<true>, grid, dim3(256), 0, st, p);
+  else hipLaunchKernelGGL(ce_pack_kernel<false>, grid, dim3(256), 0, st, p);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
 int launch_ce_join(const MaxSum* partial, const float* zlabel, const int32_t* labels, int tiles,
                    int N, int V, float* loss, float* stats, hipStream_t st) {
-  hipLaunchKernelGGL(ce_join_kernel, dim3((uint32_t)((N + 31) / 32)), dim3(256), 0, st, partial, zlabel,
-                     labels, tiles, N, V, loss, stats);
+  // few states: a workgroup each, or the tiles are read one after the other
+  if (N <= 2048)
+    hipLaunchKernelGGL(ce_join_kernel<1>, dim3((uint32_t)N), dim3(256), 0, st, partial, zlabel, labels, tiles,
+                       N, V, loss, stats);
+  else
+    hipLaunchKernelGGL(ce_join_kernel<16>, dim3((uint32_t)((N + 15) / 16)), dim3(256), 0, st, partial, zlabel,
+                       labels, tiles, N, V, loss, stats);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
 int launch_ce_sum(const float* acc, int splits, int64_t split_stride, int64_t ld, int N, int D,
                   void* out, int64_t out_stride, int bf16, hipStream_t st) {
-  hipLaunchKernelGGL(ce_sum_kernel, dim3((uint32_t)N), dim3(256), 0, st, acc, splits, split_stride, ld, D,
-                     out, out_stride, bf16);
+  const int64_t quads = ld / 4;   // ld is D rounded up to 4
+  hipLaunchKernelGGL(ce_sum_kernel, dim3((uint32_t)((quads * N + 255) / 256)), dim3(256), 0, st, acc, splits,
+                     split_stride, ld, quads, N, D, out, out_stride, bf16);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 
