@@ -342,21 +342,25 @@ def spec_verify_commit(tokens, num_accepted, kv_len, slots=None, gamma_b=None, o
 def _matrix(t, name, device=None, dtype=None, cols=None):
     """(pointer, row stride) of a tensor whose last dimension is consecutive and
     whose leading dimensions are rows at one stride."""
-    torch = _torch()
-    if not torch.is_tensor(t) or not t.is_cuda:
+    if not _torch().is_tensor(t) or not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() < 2 or t.numel() == 0:
-        raise ValueError(f"{name} must have at least one row and one column, got {tuple(t.shape)}")
-    if cols is not None and t.shape[-1] != cols:
-        raise ValueError(f"{name} must have rows of {cols}, got {tuple(t.shape)}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    shape = t.shape
+    if len(shape) < 2 or t.numel() == 0:
+        raise ValueError(f"{name} must have at least one row and one column, got {tuple(shape)}")
+    width = shape[-1]
+    if cols is not None and width != cols:
+        raise ValueError(f"{name} must have rows of {cols}, got {tuple(shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), width
+    steps = t.stride()
+    if width > 1 and steps[-1] != 1:
         raise ValueError(f"{name} must have consecutive elements in a row")
     stride, rows = None, 1
-    for size, step in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+    for size, step in zip(reversed(shape[:-1]), reversed(steps[:-1])):
         if size == 1:
             continue
         if stride is None:
@@ -365,8 +369,8 @@ def _matrix(t, name, device=None, dtype=None, cols=None):
             raise ValueError(f"{name} must have its rows at one stride")
         rows *= size
     if stride is None:
-        stride = t.shape[-1]   # a single row
-    if stride < t.shape[-1]:
+        stride = width   # a single row
+    if stride < width:
         raise ValueError(f"{name} must not have overlapping rows")
     return t.data_ptr(), stride
 
@@ -375,18 +379,36 @@ def _vector(t, name, dtype, shape, device):
     """Pointer of a contiguous tensor (or None) of this type, shape and device."""
     if t is None:
         return None
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    p = _dev_ptr(t, name, dtype)
     if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    return p
+        raise ValueError(f"{name} must be on {device}, is on {t.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+class _Current:
+    """The device and stream are torch's current ones already."""
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_CURRENT = _Current()
 
 
 def _on(device, stream):
-    """The device as current, and the call's stream on it: (context, handle, stream)."""
-    import contextlib
+    """(context that makes the device and the call's stream current, stream handle)."""
     torch = _torch()
+    if stream is None and torch.cuda.current_device() == device.index:
+        return _CURRENT, torch.cuda.current_stream(device).cuda_stream
+    import contextlib
     with torch.cuda.device(device):
         handle, strm = _stream(stream)
     ctx = contextlib.ExitStack()

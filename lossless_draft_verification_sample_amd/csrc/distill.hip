@@ -84,15 +84,15 @@ __device__ MaxSum row_set(const DistillArgs& a, DisLds& L, const Row<Elem>& row,
   constexpr int EPV = Row<Elem>::EPV;
   constexpr int AHEAD = 4;
   const int tid = threadIdx.x;
-  MaxSum sum{-INFINITY, 0.0f};
+  Running run;
   float one[1];
   if (part == 0 && tid < row.head) {
     one[0] = to_f32(row.p + tid);
-    add_logits(sum, one, a.c);
+    run.add(one, a.c);
   }
   if (part == a.parts - 1 && tid < row.tail()) {
     one[0] = to_f32(row.p + row.tail0() + tid);
-    add_logits(sum, one, a.c);
+    run.add(one, a.c);
   }
   int j = v0 + tid;
   for (; j + (AHEAD - 1) * DIS_THREADS < v1; j += AHEAD * DIS_THREADS) {
@@ -103,16 +103,50 @@ __device__ MaxSum row_set(const DistillArgs& a, DisLds& L, const Row<Elem>& row,
     for (int i = 0; i < AHEAD; ++i) {
       float z[EPV];
       unpack(w[i], z);
-      add_logits(sum, z, a.c);
+      run.add(z, a.c);
     }
   }
   for (; j < v1; j += DIS_THREADS) {
     float z[EPV];
     unpack(row.vec(j), z);
-    add_logits(sum, z, a.c);
+    run.add(z, a.c);
   }
-  return block_join<DIS_THREADS>(sum, L.scratch, a.c);
+  return block_join<DIS_THREADS>(run.set(a.c), L.scratch, a.c);
 }
+
+// The dense part of a row's gradient, w / T P q_v, as scale exp2(z c - ref): ref is the
+// whole number next to (m / T + logsum) log2 e, and what the rounding leaves is in the
+// scale (beyond 2^100, see Running: relative to m).
+struct Density {
+  float g, scale, ref, m;
+  bool none;   // nothing to learn from: no teacher mass, or a row that rules out every token
+  __device__ __forceinline__ Density(const DistillArgs& a, float P, float weight, float m_, float logsum) {
+    m = m_;
+    g = weight * a.inv_t;
+    none = P == 0.0f || m == -INFINITY;
+    const float ls2 = logsum * LOG2E;
+    if (fabsf(m) < 0x1p100f) {
+      ref = rintf(__builtin_fmaf(m, a.c, ls2));
+      scale = g * P * fast_exp2(__builtin_fmaf(-m, a.c, ref) - ls2);
+    } else {
+      ref = INFINITY;
+      scale = g * P * fast_exp2(-ls2);
+    }
+  }
+  template <int N>
+  __device__ __forceinline__ void apply(float (&z)[N], float c) const {
+    if (none) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) z[i] = 0.0f;
+    } else if (ref != INFINITY) {   // of the row: the same in every thread
+#pragma unroll
+      for (int i = 0; i < N; ++i) z[i] = scale * fast_exp2(__builtin_fmaf(z[i], c, -ref));
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) z[i] = scale * fast_exp2((z[i] - m) * c);
+    }
+  }
+};
 
 // Gradient of the groups [v0, v1) (and head or tail); teacher() has run.
 template <typename Elem>
@@ -121,13 +155,7 @@ __device__ void row_grad(const DistillArgs& a, DisLds& L, const Row<Elem>& row, 
   constexpr int EPV = Row<Elem>::EPV;
   const int tid = threadIdx.x;
   Elem* out = (Elem*)a.grad + r * a.grad_stride;
-  const float g = (a.weight ? a.weight[r] : 1.0f) * a.inv_t;
-  // nothing to learn from: no teacher mass, or a row that rules out every token
-  const bool none = P == 0.0f || m == -INFINITY;
-  const float scale = g * P;
-  const float ls2 = logsum * LOG2E;
-  auto q = [&](float z) { return fast_exp2((z - m) * a.c - ls2); };
-  auto dense = [&](float z) { return none ? 0.0f : scale * q(z); };
+  const Density d(a, P, a.weight ? a.weight[r] : 1.0f, m, logsum);
   const int lo = part == 0 ? 0 : row.head + v0 * EPV;
   const int hi = part == a.parts - 1 ? a.V : row.head + v1 * EPV;
   // the slots' student logits, before an in-place gradient overwrites them
@@ -138,14 +166,17 @@ __device__ void row_grad(const DistillArgs& a, DisLds& L, const Row<Elem>& row, 
   __syncthreads();
   // the output row has its own alignment: whole groups where both agree
   const bool same = (((uintptr_t)out ^ (uintptr_t)row.p) & 15u) == 0;
-  if (part == 0 && tid < row.head) put(out + tid, dense(to_f32(row.p + tid)));
-  if (part == a.parts - 1 && tid < row.tail())
-    put(out + row.tail0() + tid, dense(to_f32(row.p + row.tail0() + tid)));
+  auto single = [&](int v) {
+    float z[1] = {to_f32(row.p + v)};
+    d.apply(z, a.c);
+    put(out + v, z[0]);
+  };
+  if (part == 0 && tid < row.head) single(tid);
+  if (part == a.parts - 1 && tid < row.tail()) single(row.tail0() + tid);
   for (int j = v0 + tid; j < v1; j += DIS_THREADS) {
     float z[EPV];
     unpack(row.vec(j), z);
-#pragma unroll
-    for (int i = 0; i < EPV; ++i) z[i] = dense(z[i]);
+    d.apply(z, a.c);
     Elem* o = out + row.head + (int64_t)j * EPV;
     if (same) {
       __builtin_nontemporal_store(pack(z), (vu32x4*)o);
@@ -155,13 +186,15 @@ __device__ void row_grad(const DistillArgs& a, DisLds& L, const Row<Elem>& row, 
     }
   }
   __syncthreads();   // orders the dense writes before the slots'
-  if (none) return;
+  if (d.none) return;
   for (int k = tid; k < a.K; k += DIS_THREADS) {
     const int id = L.id[k];
     if (id < lo || id >= hi) continue;
     float p = 0.0f;
     for (int j = 0; j < a.K; ++j) p += L.id[j] == id ? L.p[j] : 0.0f;
-    put(out + id, scale * q(L.zid[k]) - g * p);
+    float z[1] = {L.zid[k]};
+    d.apply(z, a.c);
+    put(out + id, z[0] - d.g * p);
   }
 }
 
@@ -242,10 +275,175 @@ __global__ __launch_bounds__(DIS_THREADS) void distill_grad_kernel(DistillArgs a
   row_grad(a, L, row, r, part, v0, v1, P, a.stats[2 * r], a.stats[2 * r + 1]);
 }
 
+struct DisHoldLds {
+  int32_t id[DIS_MAX_K];
+  float p[DIS_MAX_K];
+  float red[HOLD_THREADS / WAVE];
+  MaxSum scratch[HOLD_THREADS / WAVE];
+};
+
+// Many rows that fit a CU's registers: each is read once, for the statistics, the
+// loss and the gradient.
+template <typename Elem, int SIZE>
+__global__ __launch_bounds__(HOLD_THREADS, 2 * HOLD_PER_CU[SIZE]) void distill_hold_kernel(DistillArgs a) {
+  constexpr int NV = HOLD_NV[SIZE];
+  constexpr int EPV = Held<Elem, NV>::EPV;
+  constexpr int SLOTS = DIS_MAX_K / HOLD_THREADS;
+  __shared__ DisHoldLds L;
+  const int tid = threadIdx.x;
+  Held<Elem, NV> h;
+  int32_t id[SLOTS];     // this thread's slots of the row: id (-1: empty), tempered
+  float t[SLOTS], zs[SLOTS];   // teacher's logit, student's logit
+  auto slots = [&](int64_t r) {
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i) {
+      const int k = tid + i * HOLD_THREADS;
+      id[i] = k < a.K ? a.ids[r * a.K + k] : -1;
+      t[i] = k < a.K ? a.tl[r * a.K + k] : 0.0f;
+    }
+  };
+  auto gather = [&](const Row<Elem>& row) {
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i) {
+      t[i] = t[i] / a.temperature;
+      if (!(id[i] >= 0 && id[i] < a.V && t[i] != -INFINITY)) id[i] = -1;
+      zs[i] = id[i] >= 0 ? to_f32(row.p + id[i]) : 0.0f;
+    }
+  };
+  int64_t r = blockIdx.x;
+  Row<Elem> row(a.logits, a.stride, r, a.V);
+  slots(r);
+  h.load(row);
+  gather(row);
+  while (true) {
+    const int64_t next = r + gridDim.x;
+    const bool more = next < a.R;
+    const Row<Elem> after(a.logits, a.stride, more ? next : r, a.V);
+    Running run;
+    {
+      const float one[1] = {h.edge};
+      run.add(one, a.c);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (i * HOLD_THREADS < row.nvec) {
+        float z[EPV];
+        h.get(i, z);
+        run.add(z, a.c);
+      }
+    }
+    const MaxSum sum = block_join<HOLD_THREADS>(run.set(a.c), L.scratch, a.c);
+    const float m = sum.m, logsum = log_of(sum);
+
+    float lse;
+    if (a.tlse) {
+      lse = a.tlse[r];
+    } else {
+      float tm = -INFINITY, ts = 0.0f;
+#pragma unroll
+      for (int i = 0; i < SLOTS; ++i)
+        if (id[i] >= 0) tm = fmaxf(tm, t[i]);
+      tm = block_max<HOLD_THREADS>(tm, L.red);
+#pragma unroll
+      for (int i = 0; i < SLOTS; ++i)
+        if (id[i] >= 0) ts += expf(t[i] - tm);
+      lse = tm + logf(block_sum<HOLD_THREADS>(ts, L.red));
+    }
+    float P = 0.0f, loss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i) {
+      const int k = tid + i * HOLD_THREADS;
+      const float lp = t[i] - lse;
+      const float p = id[i] >= 0 ? expf(lp) : 0.0f;
+      P += p;
+      if (!(p == 0.0f)) {   // an empty slot, or a mass that is 0: no part in the loss
+        const float lq = m == -INFINITY ? -INFINITY : (zs[i] - m) * a.inv_t - logsum;
+        loss += p * (lp - lq);
+      }
+      if (k < a.K) {
+        L.id[k] = id[i];
+        L.p[k] = p;
+      }
+    }
+    loss = block_sum<HOLD_THREADS>(loss, L.red);
+    if (tid == 0) {
+      a.loss[r] = loss;
+      a.stats[2 * r] = m;
+      a.stats[2 * r + 1] = logsum;
+    }
+    P = block_sum<HOLD_THREADS>(P, L.red);
+    Elem* out = (Elem*)a.grad + r * a.grad_stride;
+    const Density d(a, P, a.weight ? a.weight[r] : 1.0f, m, logsum);
+    // this row's slots stay in registers; the next row's are on their way
+    int32_t mine[SLOTS];
+    float mz[SLOTS];
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i) {
+      mine[i] = id[i];
+      mz[i] = zs[i];
+    }
+    if (more) slots(next);
+    const bool same = (((uintptr_t)out ^ (uintptr_t)row.p) & 15u) == 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (i * HOLD_THREADS < row.nvec) {
+        const int j = h.index(i);
+        float z[EPV];
+        h.get(i, z);
+        d.apply(z, a.c);
+        if (j < row.nvec) {
+          Elem* o = out + row.head + (int64_t)j * EPV;
+          if (same) {
+            __builtin_nontemporal_store(pack(z), (vu32x4*)o);
+          } else {
+#pragma unroll
+            for (int e = 0; e < EPV; ++e) put(o + e, z[e]);
+          }
+        }
+      }
+      if (more && i * HOLD_THREADS < after.nvec) h.load_group(after, i);
+    }
+    const int edge = Held<Elem, NV>::edge_id(row);
+    if (edge >= 0) {
+      float z[1] = {h.edge};
+      d.apply(z, a.c);
+      put(out + edge, z[0]);
+    }
+    if (more) {
+      h.load_edge(after);
+      gather(after);
+    }
+    __syncthreads();   // orders the dense writes before the slots'
+    if (!d.none) {
+#pragma unroll
+      for (int i = 0; i < SLOTS; ++i) {
+        if (mine[i] < 0) continue;
+        float p = 0.0f;
+        for (int j = 0; j < a.K; ++j) p += L.id[j] == mine[i] ? L.p[j] : 0.0f;
+        float z[1] = {mz[i]};
+        d.apply(z, a.c);
+        put(out + mine[i], z[0] - d.g * p);
+      }
+    }
+    if (!more) break;
+    r = next;
+    row = after;
+  }
+}
+
 template <typename Elem>
 int distill(const DistillArgs& a, bool backward, hipStream_t st) {
   const dim3 block(DIS_THREADS), rows((uint32_t)a.R), all((uint32_t)a.R * (uint32_t)a.parts);
-  if (!backward && a.parts == 1) {
+  if (!backward && a.hold >= 0) {
+    const int most = HOLD_CUS * HOLD_PER_CU[a.hold];
+    const dim3 grid((uint32_t)(a.R < most ? a.R : most)), held(HOLD_THREADS);
+    if (a.hold == 0)
+      hipLaunchKernelGGL((distill_hold_kernel<Elem, 0>), grid, held, 0, st, a);
+    else if (a.hold == 1)
+      hipLaunchKernelGGL((distill_hold_kernel<Elem, 1>), grid, held, 0, st, a);
+    else
+      hipLaunchKernelGGL((distill_hold_kernel<Elem, 2>), grid, held, 0, st, a);
+  } else if (!backward && a.parts == 1) {
     hipLaunchKernelGGL(distill_row_kernel<Elem>, rows, block, 0, st, a);
   } else {
     if (!backward) {

@@ -119,29 +119,144 @@ __device__ __forceinline__ vu32x4 pack(const float (&z)[4]) {
 __device__ __forceinline__ void put(uint16_t* p, float v) { *p = (uint16_t)pack_bf16(v, 0.0f); }
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 
-// Adds n logits to a running set: the maximum of the new ones first, so that
-// the sum is rescaled at most once. NaN logits do not enter the maximum and
-// make the sum NaN.
-template <int N>
-__device__ __forceinline__ void add_logits(MaxSum& a, const float (&z)[N], float c) {
-  float vm = z[0];
-#pragma unroll
-  for (int i = 1; i < N; ++i) vm = fmaxf(vm, z[i]);
-  if (vm > a.m) {
-    a.s *= fast_exp2((a.m - vm) * c);   // a.m = -inf: a.s is 0
-    a.m = vm;
+// A thread's running set while it streams a row: the sum is kept as
+// sum exp2(z c - ref), ref a whole number, so that a logit costs one fused
+// multiply-add, one exp2 and one addition. The reference is next to m c when it is
+// set, and set again only when a logit lies 2^30 above it (float32 holds sums of
+// 2^31 such terms): a reference that followed every new maximum would be moved in
+// nearly every step, since one lane of the 64 is enough. The fused product is exact,
+// whatever the size of z c. Beyond 2^100 (rows of the type's lowest value) m c may
+// not be representable: there ref is +inf as a mark and the sum is kept relative to m.
+struct Running {
+  float m = -INFINITY;        // largest logit
+  float limit = -INFINITY;    // a larger one sets a new reference
+  float ref = 0.0f, s = 0.0f;
+
+  __device__ __forceinline__ MaxSum set(float c) const {
+    MaxSum r{m, s};
+    if (ref != INFINITY && m != -INFINITY) r.s = s * fast_exp2(__builtin_fmaf(-m, c, ref));
+    return r;
   }
-  const float ref = a.m == -INFINITY ? 0.0f : a.m;
+  // vm: larger than limit. m and s are those before it.
+  __device__ __forceinline__ void raise(float vm, float c) {
+    float t = set(c).s;
+    t *= fast_exp2((m - vm) * c);   // m = -inf: t is 0
+    if (fabsf(vm) < 0x1p100f) {
+      ref = rintf(vm * c);
+      limit = vm + 30.0f / c;
+      s = t * fast_exp2(__builtin_fmaf(vm, c, -ref));
+    } else {
+      ref = INFINITY;
+      limit = vm;
+      s = t;
+    }
+  }
+  // vm: the largest of the N logits (NaN do not count; they make the sum NaN).
+  template <int N>
+  __device__ __forceinline__ void add(const float (&z)[N], float vm, float c) {
+    if (vm > limit) raise(vm, c);
+    m = fmaxf(m, vm);
+    float e[N];
+    if (!__any(ref == INFINITY)) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) a.s += fast_exp2((z[i] - ref) * c);
+      for (int i = 0; i < N; ++i) e[i] = fast_exp2(__builtin_fmaf(z[i], c, -ref));
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        e[i] = fast_exp2(ref == INFINITY ? (z[i] - m) * c : __builtin_fmaf(z[i], c, -ref));
+    }
+#pragma unroll
+    for (int w = N / 2; w > 0; w >>= 1)
+#pragma unroll
+      for (int i = 0; i < w; ++i) e[i] += e[i + w];
+    s += e[0];
+  }
+  template <int N>
+  __device__ __forceinline__ void add(const float (&z)[N], float c) {
+    add(z, largest(z), c);
+  }
+  template <int N>
+  static __device__ __forceinline__ float largest(const float (&z)[N]) {
+    float vm = z[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) vm = fmaxf(vm, z[i]);
+    return vm;
+  }
+};
+
+// ------------------------------------------------------------ held rows
+
+// A workgroup of HOLD_THREADS keeps a whole row in registers, NV 16-byte groups a
+// thread: 152 of 256 registers at NV = 38, so one workgroup fills a CU and walks
+// over rows r, r + grid, ... . A group's registers take the next row's group as
+// soon as the row's last pass over it is done, so that the next row arrives while
+// this one is finished.
+constexpr int HOLD_THREADS = 512;
+constexpr int HOLD_NV[3] = {10, 20, 38};
+// Workgroups a CU holds at once, by their registers.
+constexpr int HOLD_PER_CU[3] = {2, 2, 1};
+constexpr int HOLD_CUS = 256;
+
+// Index into HOLD_NV for rows of V logits of es bytes, or -1: too long.
+inline int hold_size(int64_t V, int es) {
+  for (int i = 0; i < 3; ++i)
+    if (V * es <= (int64_t)HOLD_NV[i] * HOLD_THREADS * 16) return i;
+  return -1;
 }
+
+// One row of it: the groups, and in the threads below 32 the elements before the
+// first and behind the last whole group (threads 0.. and 16..).
+template <typename Elem, int NV>
+struct Held {
+  static constexpr int EPV = 16 / (int)sizeof(Elem);
+  vu32x4 w[NV];
+  float edge;
+  // Index of the thread's i-th group, made anew: the compiler would else keep NV of
+  // them across the rows.
+  static __device__ __forceinline__ int index(int i) {
+    int t = threadIdx.x;
+    asm volatile("" : "+v"(t));
+    return i * HOLD_THREADS + t;
+  }
+  __device__ __forceinline__ void load_group(const Row<Elem>& row, int i) {
+    const uint32_t j = (uint32_t)index(i);
+    // a whole step needs no test of its lanes; a row is below 2^31 bytes
+    const auto at = (const vu32x4*)((const char*)(row.p + row.head) + j * 16u);
+    if ((i + 1) * HOLD_THREADS <= row.nvec) w[i] = __builtin_nontemporal_load(at);
+    else w[i] = (int)j < row.nvec ? __builtin_nontemporal_load(at)
+                                  : (vu32x4)(sizeof(Elem) == 2 ? 0xFF80FF80u : 0xFF800000u);   // -inf
+  }
+  // The group's elements, unpacked anew: the compiler would else keep those of an
+  // earlier pass, twice the registers.
+  __device__ __forceinline__ void get(int i, float (&z)[EPV]) {
+    asm volatile("" : "+v"(w[i]));
+    unpack(w[i], z);
+  }
+  static __device__ __forceinline__ int edge_id(const Row<Elem>& row) {
+    const int t = threadIdx.x;
+    if (t < row.head) return t;
+    if (t >= 16 && t - 16 < row.tail()) return row.tail0() + t - 16;
+    return -1;
+  }
+  __device__ __forceinline__ void load_edge(const Row<Elem>& row) {
+    const int id = edge_id(row);
+    edge = id >= 0 ? to_f32(row.p + id) : -INFINITY;
+  }
+  __device__ __forceinline__ void load(const Row<Elem>& row) {
+    load_edge(row);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (i * HOLD_THREADS < row.nvec) load_group(row, i);
+  }
+};
 
 // ------------------------------------------------------------ top logits
 
-constexpr int TOP_THREADS = 512;
-constexpr int TOP_STEP = TOP_THREADS * 8;   // most candidates one step can add
-constexpr int TOP_CAP = 6144;               // candidates held in LDS
+constexpr int TOP_THREADS = 256;
+constexpr int TOP_STEP = TOP_THREADS * 8;   // most candidates one group a thread can add
+constexpr int TOP_CAP = 3072;               // candidates held in LDS
 constexpr int TOP_MAX_K = 1024;
+constexpr int TOP_THIN = 1024;              // candidates that are thinned without a cut
 
 struct TopArgs {
   const void* logits;
@@ -177,6 +292,7 @@ struct DistillArgs {
   void* grad;                // [R][V] or nullptr
   int64_t grad_stride;
   MaxSum* sums;              // [R][parts] when parts > 1
+  int hold;                  // index into HOLD_NV: rows are held in registers; -1: streamed
 };
 int launch_distill(const DistillArgs& a, int bf16, hipStream_t s);
 int launch_distill_backward(const DistillArgs& a, int bf16, hipStream_t s);

@@ -10,7 +10,7 @@
 #include "sv_train.hpp"
 
 static_assert(SV_MAX_TOP == sv::TOP_MAX_K && SV_MAX_TOP == sv::DIS_MAX_K, "kept logits per row");
-static_assert(sv::TOP_CAP - sv::TOP_STEP >= sv::TOP_MAX_K, "a cut list leaves room for a step");
+static_assert(sv::TOP_CAP - sv::TOP_STEP >= sv::TOP_MAX_K, "a cut list leaves room for a group a thread");
 
 namespace {
 
@@ -41,17 +41,39 @@ struct Carver {
 
 // ---------------------------------------------------------------- vocabulary rows
 
-// Workgroups per row: one when there are rows enough for every CU, else as many
-// as give TARGET in all, none shorter than MIN logits.
-int64_t row_parts(int64_t R, int64_t V, int64_t target, int64_t min_logits) {
-  int64_t parts = target / R;
-  const int64_t most = ceil_div(V, min_logits);
-  if (parts > most) parts = most;
-  return parts < 1 ? 1 : parts;
+// Workgroups per row. All of a launch's workgroups pass through `slots` places in
+// rounds, and a round takes the time of a part: its bytes, and what starting and
+// ending it costs, counted in bytes. Parts have to be joined by a second kernel.
+// Without this, 1,300 rows would take twice the time of 1,280. join_cost(p) counts
+// the second kernel for p parts.
+template <typename Join>
+int row_parts(int64_t R, int64_t bytes, int64_t slots, int64_t part_cost, Join join_cost, int64_t most) {
+  int64_t best = 1, best_cost = INT64_MAX;
+  for (int64_t p = 1; p <= most; ++p) {
+    const int64_t cost = ceil_div(R * p, slots) * (ceil_div(bytes, p) + part_cost) + (p > 1 ? join_cost(p) : 0);
+    if (cost < best_cost) {
+      best = p;
+      best_cost = cost;
+    }
+    if (R * p > 8 * slots) break;
+  }
+  return (int)best;
 }
 
-constexpr int64_t TOP_TARGET_WGS = 512, TOP_MIN_LOGITS = 8192;
-constexpr int64_t DIS_TARGET_WGS = 1024, DIS_MIN_LOGITS = 4096;
+// Places on the GPU, and costs in bytes: a workgroup streams 4 to 5 (top logits) or
+// about 10 (distillation) bytes a nanosecond when few run, so that its own 5 us
+// count as 24,000 (60,000), and the join's 8 to 10 us as 45,000 (80,000).
+constexpr int64_t TOP_SLOTS = 5 * sv::HOLD_CUS, TOP_PART = 24000;
+constexpr int64_t TOP_JOIN = 45000, TOP_JOIN_CUT = 20000;   // more where the join has to cut
+constexpr int64_t DIS_SLOTS = 4 * sv::HOLD_CUS, DIS_PART = 60000, DIS_JOIN = 80000;
+constexpr int64_t HOLD_MIN_ROWS = 192;
+constexpr int64_t ROW_MAX_PARTS = 64;
+
+// Rows held in registers, a workgroup a row at a time: HOLD_NV's index, or -1 where
+// the rows are too long for that or too few to give most CUs one.
+int hold_rows(int64_t R, int64_t V, sv_dtype dtype) {
+  return R < HOLD_MIN_ROWS ? -1 : sv::hold_size(V, (int)size_of(dtype));
+}
 
 struct TopLayout {
   int parts;
@@ -59,9 +81,11 @@ struct TopLayout {
 };
 bool top_layout(int32_t R, int32_t V, int32_t K, TopLayout* L) {
   if (R < 1 || V < 1 || K < 1 || K > SV_MAX_TOP || K > V) return false;
-  int64_t parts = row_parts(R, V, TOP_TARGET_WGS, TOP_MIN_LOGITS);
-  if (parts > sv::TOP_CAP / K) parts = sv::TOP_CAP / K;   // what the join holds
-  L->parts = (int)parts;
+  int64_t most = sv::TOP_CAP / K;   // what the join holds
+  if (most > ROW_MAX_PARTS) most = ROW_MAX_PARTS;
+  const int64_t parts = L->parts = row_parts(
+      R, (int64_t)V * 2, TOP_SLOTS, TOP_PART,
+      [K](int64_t p) { return TOP_JOIN + (p * K > sv::TOP_THIN ? TOP_JOIN_CUT : 0); }, most);
   Carver c;
   L->keys = c.take(parts > 1 ? (size_t)R * parts * K * sizeof(uint64_t) : 0);
   L->sums = c.take(parts > 1 ? (size_t)R * parts * sizeof(sv::MaxSum) : 0);
@@ -69,7 +93,9 @@ bool top_layout(int32_t R, int32_t V, int32_t K, TopLayout* L) {
   return true;
 }
 
-int distill_parts(int32_t R, int32_t V) { return (int)row_parts(R, V, DIS_TARGET_WGS, DIS_MIN_LOGITS); }
+int distill_parts(int32_t R, int32_t V) {
+  return row_parts(R, (int64_t)V * 2, DIS_SLOTS, DIS_PART, [](int64_t) { return DIS_JOIN; }, ROW_MAX_PARTS);
+}
 
 int distill_args(const void* logits, int64_t logits_stride, sv_dtype dtype, int32_t R, int32_t V,
                  const int32_t* ids, const float* tl, const float* tlse, int32_t K,
@@ -89,6 +115,7 @@ int distill_args(const void* logits, int64_t logits_stride, sv_dtype dtype, int3
   a->V = V;
   a->K = K;
   a->parts = distill_parts(R, V);
+  a->hold = grad ? hold_rows(R, V, dtype) : -1;   // the loss alone streams faster
   a->temperature = temperature;
   a->inv_t = 1.0f / temperature;
   a->c = (float)((double)LOG2E_D / temperature);
