@@ -559,8 +559,8 @@ int gemm(const CeGemm& g, const typename Epi::Args& ea, hipStream_t st) {
   const dim3 grid((uint32_t)tiles_m * (uint32_t)tiles_n, (uint32_t)g.splits);
 #define CE_LAUNCH(BM, BN, WM, WN) \
   hipLaunchKernelGGL((ce_gemm_kernel<BM, BN, WM, WN, Epi>), grid, dim3(WM * WN * WAVE), 0, st, g, tiles_m, tiles_n, ea)
-  if (bn == 32) CE_LAUNCH(128, 32, 4, 1);
-  else if (bn == 128) CE_LAUNCH(128, 128, 2, 2);
+  if (bn == 32) CE_LAUNCH(64, 32, 4, 1);
+  else if (bn == 64) CE_LAUNCH(128, 64, 2, 2);
   else CE_LAUNCH(256, 256, 2, 4);
 #undef CE_LAUNCH
   return hipGetLastError() == hipSuccess ? 0 : -1;
@@ -568,9 +568,15 @@ int gemm(const CeGemm& g, const typename Epi::Args& ea, hipStream_t st) {
 
 }  // namespace
 
-int ce_tile_m(int rows_b) { return rows_b > 128 ? 256 : 128; }
-int ce_tile_n(int rows_b) { return rows_b <= 32 ? 32 : rows_b <= 128 ? 128 : 256; }
-int ce_tiles_per_cu(int rows_b) { return rows_b > 128 ? 1 : rows_b > 32 ? 2 : 4; }
+// Tiles by the rows of B (states, or tokens for dW). Few rows leave the read of A as
+// the bound, and many small workgroups in flight keep it busy: logits of 151,936
+// tokens of 1,024 at 17 rows take 52 us in 64 x 32, 55 in 128 x 32, 59 in 256 x 32; at
+// 64 rows 69 us in 128 x 64, 78 in 128 x 128; at 128 rows of 2,048 187 us in 128 x 64, 193 in
+// 128 x 128, 204 in 256 x 128. From there on products bound it, and the largest tile
+// reads LDS least: 1,300 TFLOP/s in 256 x 256, 930 in 256 x 128, 910 to 1,010 in 128 x 128.
+int ce_tile_m(int rows_b) { return rows_b <= 32 ? 64 : rows_b <= 128 ? 128 : 256; }
+int ce_tile_n(int rows_b) { return rows_b <= 32 ? 32 : rows_b <= 128 ? 64 : 256; }
+int ce_tiles_per_cu(int rows_b) { return rows_b <= 32 ? 6 : rows_b <= 128 ? 3 : 1; }   // by LDS
 
 int launch_ce_stats(const CeGemm& g, const CeStatsOut& o, hipStream_t st) { return gemm<EpiStats>(g, o, st); }
 int launch_ce_dz(const CeGemm& g, const CeDzOut& o, hipStream_t st) {

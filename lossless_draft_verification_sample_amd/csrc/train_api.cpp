@@ -144,7 +144,7 @@ bool ce_shape(int32_t N, int32_t D, int32_t V, sv_dtype dtype, CeShape* s) {
   if (N > CE_MAX_ROWS || D > sv::CE_MAX_D || V >= INT32_MAX - 1024) return false;
   *s = CeShape{N, D, V, round_up(D, sv::CE_BK), dtype == SV_BF16 ? 1 : 3};
   // tiles of any product
-  return ceil_div(V, 128) * ceil_div(N, 32) < INT32_MAX;
+  return ceil_div(V, 64) * ceil_div(N, 32) < INT32_MAX;
 }
 
 // Tokens of a piece whose operands take `bytes` a token.
