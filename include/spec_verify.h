@@ -321,16 +321,14 @@ int spec_verify_commit(const int32_t* out_tokens, const int32_t* out_num_accepte
  * among equal values (-0 == +0), and the log-normaliser of the whole row.
  *   logits      [R][V] of dtype, row stride logits_stride >= V; the target
  *               logits of spec_verify_sample are R = B*(gamma+1) rows.
- *   temperature > 0 and finite; only out_lse depends on it.
+ *   temperature > 0, finite and not subnormal; only out_lse depends on it.
  *   out_ids     [R][K] int32 ids, out_values [R][K] float their logits (not
  *               tempered). -inf and NaN logits are not candidates: a row with
  *               fewer than K candidates is filled up with id -1, value -inf.
  *   out_lse     [R] float log sum_v exp(logit_v / temperature), or NULL; -inf
  *               for a row of -inf only, NaN for a row holding NaN or +inf.
- * Limits: 1 <= R < 2^31, 1 <= K <= SV_MAX_TOP, K <= V, V < 2^31 and
- * at most 2^31 - 1 workgroups. Errors: SV_EINVAL, SV_EDTYPE,
- * SV_EWORKSPACE, SV_ESIZE, SV_EHIP. */
-size_t spec_verify_top_logits_workspace_bytes(int32_t R, int32_t V, int32_t K);
+ * Limits: 1 <= K <= SV_MAX_TOP, K <= V < 2^31, 1 <= R <= 2^22 (SV_ESIZE beyond). */
+size_t spec_verify_top_logits_workspace_bytes(int32_t R, int32_t V, int32_t K, sv_dtype dtype);
 int spec_verify_top_logits(const void* logits, int64_t logits_stride, sv_dtype dtype, int32_t R,
                            int32_t V, int32_t K, float temperature, int32_t* out_ids,
                            float* out_values, float* out_lse, void* workspace,
@@ -358,12 +356,12 @@ int spec_verify_top_logits(const void* logits, int64_t logits_stride, sv_dtype d
  *                  It may be `logits` itself with the same stride (every value is
  *                  read before it is overwritten); any other overlap is an error
  *                  of the caller. Elements behind V are left as they are.
- * A row without a filled slot has loss 0 and gradient 0. A row whose
+ * A row without a filled slot has loss 0 and gradient 0, whatever its logits. A row whose
  * logits are all -inf has gradient 0, and loss +inf against a filled slot, as
  * has a row that gives a kept token of positive mass -inf. NaN or +inf among a
  * row's logits, or NaN in its slots, make its loss and gradient NaN.
- * Limits: 1 <= K <= SV_MAX_TOP, 1 <= R, V < 2^31. */
-size_t spec_verify_distill_workspace_bytes(int32_t R, int32_t V);
+ * Limits: 1 <= K <= SV_MAX_TOP, 1 <= V < 2^31, 1 <= R <= 2^22 (SV_ESIZE beyond). */
+size_t spec_verify_distill_workspace_bytes(int32_t R, int32_t V, sv_dtype dtype);
 int spec_verify_distill(const void* logits, int64_t logits_stride, sv_dtype dtype, int32_t R,
                         int32_t V, const int32_t* teacher_ids, const float* teacher_logits,
                         const float* teacher_lse, int32_t K, float temperature,
@@ -392,7 +390,10 @@ int spec_verify_distill_backward(const void* logits, int64_t logits_stride, sv_d
  * summed in float32.
  * Inputs are finite; NaN or infinities make the rows (and with them the
  * gradients) they meet NaN.
- * Limits: 1 <= N, V < 2^31 - 256, 1 <= D <= 2^24. */
+ * Limits: 1 <= N <= 2^22, 1 <= D <= 2^22, 1 <= V < 2^31 - 1024, and 2^23 tiles of
+ * 256 x 256 in N x V and N x D (64 x 32 up to 32 rows, 128 x 64 up to 128); SV_ESIZE
+ * beyond. bfloat16 matrices with D a multiple of 8, rows on 16 bytes and strides of at
+ * most 2^22 are read in place, others are copied into the workspace first. */
 size_t spec_verify_linear_ce_workspace_bytes(int32_t N, int32_t D, int32_t V, sv_dtype dtype);
 int spec_verify_linear_ce(const void* hidden, int64_t hidden_stride, const void* weight,
                           int64_t weight_stride, sv_dtype dtype, const int32_t* labels, int32_t N,

@@ -430,8 +430,8 @@ def _space(workspace, need, device):
     return _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(), workspace
 
 
-def spec_verify_top_logits_workspace_bytes(R, V, K):
-    return int(_lib.load().spec_verify_top_logits_workspace_bytes(int(R), int(V), int(K)))
+def spec_verify_top_logits_workspace_bytes(R, V, K, dtype=SV_BF16):
+    return int(_lib.load().spec_verify_top_logits_workspace_bytes(int(R), int(V), int(K), int(dtype)))
 
 
 def spec_verify_top_logits(logits, k, temperature=1.0, want_lse=True, workspace=None, out=None,
@@ -461,7 +461,7 @@ def spec_verify_top_logits(logits, k, temperature=1.0, want_lse=True, workspace=
                 torch.empty((*lead, k), dtype=torch.float32, device=dev),
                 torch.empty(lead, dtype=torch.float32, device=dev) if want_lse else None)
         ws, ws_bytes, keep = _space(
-            workspace, lib.spec_verify_top_logits_workspace_bytes(R, V, k), dev)
+            workspace, lib.spec_verify_top_logits_workspace_bytes(R, V, k, dt), dev)
         rc = lib.spec_verify_top_logits(
             ptr, stride, dt, R, V, k, float(temperature),
             _vector(out.ids, "out.ids", torch.int32, (*lead, k), dev),
@@ -473,8 +473,8 @@ def spec_verify_top_logits(logits, k, temperature=1.0, want_lse=True, workspace=
     return out
 
 
-def spec_verify_distill_workspace_bytes(R, V):
-    return int(_lib.load().spec_verify_distill_workspace_bytes(int(R), int(V)))
+def spec_verify_distill_workspace_bytes(R, V, dtype=SV_BF16):
+    return int(_lib.load().spec_verify_distill_workspace_bytes(int(R), int(V), int(dtype)))
 
 
 def _distill_inputs(logits, teacher_ids, teacher_logits, teacher_lse):
@@ -526,7 +526,7 @@ def spec_verify_distill(logits, teacher_ids, teacher_logits, temperature=1.0, te
             grad, gptr, gstride = _grad_out(grad, logits, "out.grad")
             out = out._replace(grad=grad)
         ws, ws_bytes, keep = _space(
-            workspace, lib.spec_verify_distill_workspace_bytes(args[3], args[4]), dev)
+            workspace, lib.spec_verify_distill_workspace_bytes(args[3], args[4], args[2]), dev)
         rc = lib.spec_verify_distill(
             *args, float(temperature),
             _vector(row_weight, "row_weight", torch.float32, lead, dev),

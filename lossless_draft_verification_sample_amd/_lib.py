@@ -84,10 +84,10 @@ SIGNATURES = {
                                       _vp, _vp, _vp]),
     "spec_verify_commit": (_c.c_int, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp,
                                       _vp]),
-    "spec_verify_top_logits_workspace_bytes": (_size, [_i32, _i32, _i32]),
+    "spec_verify_top_logits_workspace_bytes": (_size, [_i32, _i32, _i32, _int]),
     "spec_verify_top_logits": (_int, [_vp, _i64, _int, _i32, _i32, _i32, _f32, _vp, _vp, _vp, _vp,
                                       _size, _vp]),
-    "spec_verify_distill_workspace_bytes": (_size, [_i32, _i32]),
+    "spec_verify_distill_workspace_bytes": (_size, [_i32, _i32, _int]),
     "spec_verify_distill": (_int, [_vp, _i64, _int, _i32, _i32, _vp, _vp, _vp, _i32, _f32, _vp, _vp,
                                    _vp, _vp, _i64, _vp, _size, _vp]),
     "spec_verify_distill_backward": (_int, [_vp, _i64, _int, _i32, _i32, _vp, _vp, _vp, _i32, _f32,

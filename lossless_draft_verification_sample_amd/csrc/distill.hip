@@ -22,40 +22,54 @@ constexpr int DIS_THREADS = 512;
 struct DisLds {
   int32_t id[DIS_MAX_K];
   float p[DIS_MAX_K];
+  double lp[DIS_MAX_K];
   float zid[DIS_MAX_K];     // student logits of the slots, read before they are overwritten
   float red[DIS_THREADS / WAVE];
+  double red64[DIS_THREADS / WAVE];
   MaxSum scratch[DIS_THREADS / WAVE];
 };
 
+// A slot is filled when its id is a token and its tempered logit is not -inf.
+__device__ __forceinline__ bool filled(const DistillArgs& a, int32_t id, float t) {
+  return id >= 0 && id < a.V && t / a.temperature != -INFINITY;
+}
+
+// The loss's terms p (log p - log q) are differences of logarithms that nearly agree
+// for the tokens that count, and there are few of them: they are made in float64.
+// log q of a kept token with logit z, of a row with these statistics.
+__device__ __forceinline__ double log_q(const DistillArgs& a, float z, float m, double logsum) {
+  return m == -INFINITY ? (double)-INFINITY : ((double)z - (double)m) * a.inv_t64 - logsum;
+}
+
 // Teacher's masses of row r into LDS (an empty slot: id -1, mass 0); returns P.
-// log p_k - what the loss needs besides - comes back through L.zid.
+// log p_k, which the loss needs besides, comes back through L.lp.
 __device__ float teacher(const DistillArgs& a, DisLds& L, int64_t r) {
   const int tid = threadIdx.x;
   float tm = -INFINITY;
   for (int k = tid; k < a.K; k += DIS_THREADS) {
     const int32_t id = a.ids[r * a.K + k];
-    const float t = a.tl[r * a.K + k] / a.temperature;
-    const bool ok = id >= 0 && id < a.V && t != -INFINITY;
+    const float t = a.tl[r * a.K + k];
+    const bool ok = filled(a, id, t);
     L.id[k] = ok ? id : -1;
     L.p[k] = t;
     if (ok) tm = fmaxf(tm, t);
   }
-  float lse;
+  double lse;
   if (a.tlse) {
     lse = a.tlse[r];
   } else {
     tm = block_max<DIS_THREADS>(tm, L.red);
-    float s = 0.0f;
+    double s = 0.0;
     for (int k = tid; k < a.K; k += DIS_THREADS)
-      if (L.id[k] >= 0) s += expf(L.p[k] - tm);
-    s = block_sum<DIS_THREADS>(s, L.red);
-    lse = tm + logf(s);
+      if (L.id[k] >= 0) s += exp(((double)L.p[k] - (double)tm) * a.inv_t64);
+    s = block_sum<DIS_THREADS>(s, L.red64);
+    lse = (double)tm * a.inv_t64 + log(s);
   }
   float P = 0.0f;
   for (int k = tid; k < a.K; k += DIS_THREADS) {
-    const float lp = L.p[k] - lse;
-    L.zid[k] = lp;
-    L.p[k] = L.id[k] >= 0 ? expf(lp) : 0.0f;
+    const double lp = (double)L.p[k] * a.inv_t64 - lse;
+    L.lp[k] = lp;
+    L.p[k] = L.id[k] >= 0 ? (float)exp(lp) : 0.0f;
     P += L.p[k];
   }
   return block_sum<DIS_THREADS>(P, L.red);
@@ -64,16 +78,14 @@ __device__ float teacher(const DistillArgs& a, DisLds& L, int64_t r) {
 // loss of row r from its statistics; teacher() has run. All threads get it.
 template <typename Elem>
 __device__ float row_loss(const DistillArgs& a, DisLds& L, const Row<Elem>& row, float m,
-                          float logsum) {
-  float l = 0.0f;
+                          double logsum) {
+  double l = 0.0;
   for (int k = threadIdx.x; k < a.K; k += DIS_THREADS) {
-    if (!(L.p[k] == 0.0f)) {   // an empty slot, or a mass that is 0: no part in the loss
-      const float z = to_f32(row.p + L.id[k]);
-      const float lq = m == -INFINITY ? -INFINITY : (z - m) * a.inv_t - logsum;
-      l += L.p[k] * (L.zid[k] - lq);
-    }
+    const double p = L.id[k] >= 0 ? exp(L.lp[k]) : 0.0;
+    if (!(p == 0.0))   // an empty slot, or a mass that is 0: no part in the loss
+      l += p * (L.lp[k] - log_q(a, to_f32(row.p + L.id[k]), m, logsum));
   }
-  return block_sum<DIS_THREADS>(l, L.red);
+  return (float)block_sum<DIS_THREADS>(l, L.red64);
 }
 
 // Running set of the groups [v0, v1) of the row, with its head and tail in the
@@ -125,7 +137,7 @@ struct Density {
     g = weight * a.inv_t;
     none = P == 0.0f || m == -INFINITY;
     const float ls2 = logsum * LOG2E;
-    if (fabsf(m) < 0x1p100f) {
+    if (fabsf(m) < 0x1p100f && fabsf(m * a.c) < 0x1p100f) {
       ref = rintf(__builtin_fmaf(m, a.c, ls2));
       scale = g * P * fast_exp2(__builtin_fmaf(-m, a.c, ref) - ls2);
     } else {
@@ -205,8 +217,8 @@ __device__ __forceinline__ void part_of(const Row<Elem>& row, int parts, int par
   *v1 = min(row.nvec, *v0 + per);
 }
 
-__device__ __forceinline__ float log_of(const MaxSum& s) {
-  return s.m == -INFINITY && s.s == 0.0f ? -INFINITY : logf(s.s);
+__device__ __forceinline__ double log_of(const MaxSum& s) {
+  return s.m == -INFINITY && s.s == 0.0f ? (double)-INFINITY : log((double)s.s);
 }
 
 // One workgroup a row: statistics, loss, gradient.
@@ -216,17 +228,17 @@ __global__ __launch_bounds__(DIS_THREADS) void distill_row_kernel(DistillArgs a)
   const int64_t r = blockIdx.x;
   const Row<Elem> row(a.logits, a.stride, r, a.V);
   const MaxSum s = row_set(a, L, row, 0, 0, row.nvec);
-  const float logsum = log_of(s);
+  const double logsum = log_of(s);
   const float P = teacher(a, L, r);
   const float loss = row_loss(a, L, row, s.m, logsum);
   if (threadIdx.x == 0) {
     a.loss[r] = loss;
     if (a.stats) {
       a.stats[2 * r] = s.m;
-      a.stats[2 * r + 1] = logsum;
+      a.stats[2 * r + 1] = (float)logsum;
     }
   }
-  if (a.grad) row_grad(a, L, row, r, 0, 0, row.nvec, P, s.m, logsum);
+  if (a.grad) row_grad(a, L, row, r, 0, 0, row.nvec, P, s.m, (float)logsum);
 }
 
 // Few rows: the statistics of a part of a row ...
@@ -251,13 +263,13 @@ __global__ __launch_bounds__(DIS_THREADS) void distill_join_kernel(DistillArgs a
   MaxSum s{-INFINITY, 0.0f};
   if ((int)threadIdx.x < a.parts) s = a.sums[r * a.parts + threadIdx.x];
   s = block_join<DIS_THREADS>(s, L.scratch, a.c);
-  const float logsum = log_of(s);
+  const double logsum = log_of(s);
   teacher(a, L, r);
   const float loss = row_loss(a, L, row, s.m, logsum);
   if (threadIdx.x == 0) {
     a.loss[r] = loss;
     a.stats[2 * r] = s.m;
-    a.stats[2 * r + 1] = logsum;
+    a.stats[2 * r + 1] = (float)logsum;
   }
 }
 
@@ -271,7 +283,6 @@ __global__ __launch_bounds__(DIS_THREADS) void distill_grad_kernel(DistillArgs a
   int v0, v1;
   part_of(row, a.parts, part, &v0, &v1);
   const float P = teacher(a, L, r);
-  __syncthreads();   // row_grad reuses L.zid
   row_grad(a, L, row, r, part, v0, v1, P, a.stats[2 * r], a.stats[2 * r + 1]);
 }
 
@@ -279,6 +290,7 @@ struct DisHoldLds {
   int32_t id[DIS_MAX_K];
   float p[DIS_MAX_K];
   float red[HOLD_THREADS / WAVE];
+  double red64[HOLD_THREADS / WAVE];
   MaxSum scratch[HOLD_THREADS / WAVE];
 };
 
@@ -292,7 +304,7 @@ __global__ __launch_bounds__(HOLD_THREADS, 2 * HOLD_PER_CU[SIZE]) void distill_h
   __shared__ DisHoldLds L;
   const int tid = threadIdx.x;
   Held<Elem, NV> h;
-  int32_t id[SLOTS];     // this thread's slots of the row: id (-1: empty), tempered
+  int32_t id[SLOTS];     // this thread's slots of the row: id (-1: empty),
   float t[SLOTS], zs[SLOTS];   // teacher's logit, student's logit
   auto slots = [&](int64_t r) {
 #pragma unroll
@@ -305,8 +317,7 @@ __global__ __launch_bounds__(HOLD_THREADS, 2 * HOLD_PER_CU[SIZE]) void distill_h
   auto gather = [&](const Row<Elem>& row) {
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i) {
-      t[i] = t[i] / a.temperature;
-      if (!(id[i] >= 0 && id[i] < a.V && t[i] != -INFINITY)) id[i] = -1;
+      if (!filled(a, id[i], t[i])) id[i] = -1;
       zs[i] = id[i] >= 0 ? to_f32(row.p + id[i]) : 0.0f;
     }
   };
@@ -333,47 +344,48 @@ __global__ __launch_bounds__(HOLD_THREADS, 2 * HOLD_PER_CU[SIZE]) void distill_h
       }
     }
     const MaxSum sum = block_join<HOLD_THREADS>(run.set(a.c), L.scratch, a.c);
-    const float m = sum.m, logsum = log_of(sum);
+    const float m = sum.m;
+    const double logsum = log_of(sum);
 
-    float lse;
+    double lse;
     if (a.tlse) {
       lse = a.tlse[r];
     } else {
-      float tm = -INFINITY, ts = 0.0f;
+      float tm = -INFINITY;
+      double ts = 0.0;
 #pragma unroll
       for (int i = 0; i < SLOTS; ++i)
         if (id[i] >= 0) tm = fmaxf(tm, t[i]);
       tm = block_max<HOLD_THREADS>(tm, L.red);
 #pragma unroll
       for (int i = 0; i < SLOTS; ++i)
-        if (id[i] >= 0) ts += expf(t[i] - tm);
-      lse = tm + logf(block_sum<HOLD_THREADS>(ts, L.red));
+        if (id[i] >= 0) ts += exp(((double)t[i] - (double)tm) * a.inv_t64);
+      lse = (double)tm * a.inv_t64 + log(block_sum<HOLD_THREADS>(ts, L.red64));
     }
-    float P = 0.0f, loss = 0.0f;
+    float P = 0.0f;
+    double loss = 0.0;
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i) {
       const int k = tid + i * HOLD_THREADS;
-      const float lp = t[i] - lse;
-      const float p = id[i] >= 0 ? expf(lp) : 0.0f;
-      P += p;
-      if (!(p == 0.0f)) {   // an empty slot, or a mass that is 0: no part in the loss
-        const float lq = m == -INFINITY ? -INFINITY : (zs[i] - m) * a.inv_t - logsum;
-        loss += p * (lp - lq);
-      }
+      const double lp = (double)t[i] * a.inv_t64 - lse;
+      const double p = id[i] >= 0 ? exp(lp) : 0.0;
+      P += (float)p;
+      if (!(p == 0.0))   // an empty slot, or a mass that is 0: no part in the loss
+        loss += p * (lp - log_q(a, zs[i], m, logsum));
       if (k < a.K) {
         L.id[k] = id[i];
-        L.p[k] = p;
+        L.p[k] = (float)p;
       }
     }
-    loss = block_sum<HOLD_THREADS>(loss, L.red);
+    loss = block_sum<HOLD_THREADS>(loss, L.red64);
     if (tid == 0) {
-      a.loss[r] = loss;
+      a.loss[r] = (float)loss;
       a.stats[2 * r] = m;
-      a.stats[2 * r + 1] = logsum;
+      a.stats[2 * r + 1] = (float)logsum;
     }
     P = block_sum<HOLD_THREADS>(P, L.red);
     Elem* out = (Elem*)a.grad + r * a.grad_stride;
-    const Density d(a, P, a.weight ? a.weight[r] : 1.0f, m, logsum);
+    const Density d(a, P, a.weight ? a.weight[r] : 1.0f, m, (float)logsum);
     // this row's slots stay in registers; the next row's are on their way
     int32_t mine[SLOTS];
     float mz[SLOTS];

@@ -451,8 +451,7 @@ struct EpiMat {
 
 // ---------------------------------------------------------------- packing
 
-// Four columns a thread; VEC: the source's rows can be read four at a time.
-template <bool VEC>
+// Four columns a thread, read at once whatever their alignment.
 __global__ __launch_bounds__(256) void ce_pack_kernel(CePack p) {
   const int64_t quads = p.ld / 4, all = quads * p.rows;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
@@ -461,19 +460,22 @@ __global__ __launch_bounds__(256) void ce_pack_kernel(CePack p) {
     uint16_t h[3][4] = {};
     if (p.bf16) {
       const uint16_t* src = (const uint16_t*)p.src + r * p.stride + c;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (c + e < p.cols) h[0][e] = src[e];
-    } else {
-      const float* src = (const float*)p.src + r * p.stride + c;
-      float v[4];
-      if (VEC && c + 3 < p.cols) {
-        const f32x4 q = __builtin_nontemporal_load((const f32x4*)src);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = q[e];
+      if (c + 3 < p.cols) {
+        __builtin_memcpy(h[0], src, 8);
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = c + e < p.cols ? src[e] : 0.0f;
+        for (int e = 0; e < 4; ++e)
+          if (c + e < p.cols) h[0][e] = src[e];
+      }
+    } else {
+      const float* src = (const float*)p.src + r * p.stride + c;
+      float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (c + 3 < p.cols) {
+        __builtin_memcpy(v, src, 16);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + e < p.cols) v[e] = src[e];
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -588,9 +590,7 @@ int launch_ce_mat(const CeGemm& g, const CeMatOut& o, hipStream_t st) { return g
 int launch_ce_pack(const CePack& p, hipStream_t st) {
   const int64_t blocks = (p.ld / 4 * p.rows + 255) / 256;
   const dim3 grid((uint32_t)(blocks < 16384 ? blocks : 16384));
-  const bool vec = !p.bf16 && p.stride % 4 == 0 && (uintptr_t)p.src % 16 == 0;
-  if (vec) hipLaunchKernelGGL(ce_pack_kernel<true>, grid, dim3(256), 0, st, p);
-  else hipLaunchKernelGGL(ce_pack_kernel<false>, grid, dim3(256), 0, st, p);
+  hipLaunchKernelGGL(ce_pack_kernel, grid, dim3(256), 0, st, p);
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
 

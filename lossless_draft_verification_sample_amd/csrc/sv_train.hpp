@@ -125,8 +125,9 @@ __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 // set, and set again only when a logit lies 2^30 above it (float32 holds sums of
 // 2^31 such terms): a reference that followed every new maximum would be moved in
 // nearly every step, since one lane of the 64 is enough. The fused product is exact,
-// whatever the size of z c. Beyond 2^100 (rows of the type's lowest value) m c may
-// not be representable: there ref is +inf as a mark and the sum is kept relative to m.
+// whatever the size of z c. Where m or m c passes 2^100 (rows of the type's lowest
+// value, temperatures next to 0) m c may not be representable: there ref is +inf as a
+// mark and the sum is kept relative to m.
 struct Running {
   float m = -INFINITY;        // largest logit
   float limit = -INFINITY;    // a larger one sets a new reference
@@ -141,7 +142,7 @@ struct Running {
   __device__ __forceinline__ void raise(float vm, float c) {
     float t = set(c).s;
     t *= fast_exp2((m - vm) * c);   // m = -inf: t is 0
-    if (fabsf(vm) < 0x1p100f) {
+    if (fabsf(vm) < 0x1p100f && fabsf(vm * c) < 0x1p100f) {
       ref = rintf(vm * c);
       limit = vm + 30.0f / c;
       s = t * fast_exp2(__builtin_fmaf(vm, c, -ref));
@@ -287,6 +288,7 @@ struct DistillArgs {
   int R, V, K;
   int parts;                 // workgroups per row
   float temperature, inv_t, c;
+  double inv_t64;
   float* loss;               // [R] or nullptr (backward alone)
   float* stats;              // [R][2]: largest logit, log of the sum; or nullptr
   void* grad;                // [R][V] or nullptr

@@ -27,7 +27,11 @@ bool aligned(const void* p, size_t to) { return (uintptr_t)p % to == 0; }
 bool workspace_ok(const void* p, size_t have, size_t need) {
   return need == 0 || (p && aligned(p, WS_ALIGN) && have >= need);
 }
-bool temperature_ok(float t) { return t > 0.0f && isfinite(t); }
+bool temperature_ok(float t) { return t > 0.0f && isnormal(t); }   // 1 / t is finite too
+
+// Threads of a launch, 512 a workgroup, are counted in 32 bits.
+constexpr int64_t MAX_WORKGROUPS = 1 << 23;
+constexpr int64_t MAX_VOCAB_ROWS = 1 << 22;
 
 // Carves a workspace front to back.
 struct Carver {
@@ -41,51 +45,28 @@ struct Carver {
 
 // ---------------------------------------------------------------- vocabulary rows
 
-// Workgroups per row. All of a launch's workgroups pass through `slots` places in
-// rounds, and a round takes the time of a part: its bytes, and what starting and
-// ending it costs, counted in bytes. Parts have to be joined by a second kernel.
-// Without this, 1,300 rows would take twice the time of 1,280. join_cost(p) counts
-// the second kernel for p parts.
-template <typename Join>
-int row_parts(int64_t R, int64_t bytes, int64_t slots, int64_t part_cost, Join join_cost, int64_t most) {
-  int64_t best = 1, best_cost = INT64_MAX;
-  for (int64_t p = 1; p <= most; ++p) {
-    const int64_t cost = ceil_div(R * p, slots) * (ceil_div(bytes, p) + part_cost) + (p > 1 ? join_cost(p) : 0);
-    if (cost < best_cost) {
-      best = p;
-      best_cost = cost;
-    }
-    if (R * p > 8 * slots) break;
-  }
-  return (int)best;
+// Workgroups per row when there are few rows: as many as give about `total` in all,
+// each with `least` bytes or more, if that takes more off a row's time than the kernel
+// that joins them costs: `gain` bytes of one workgroup's streaming.
+int64_t row_parts(int64_t R, int64_t bytes, int64_t total, int64_t least, int64_t gain, int64_t most) {
+  int64_t p = total / R;
+  if (p > bytes / least) p = bytes / least;
+  if (p > most) p = most;
+  return p > 1 && bytes - bytes / p >= gain ? p : 1;
 }
 
-// Places on the GPU, and costs in bytes: a workgroup streams 4 to 5 (top logits) or
-// about 10 (distillation) bytes a nanosecond when few run, so that its own 5 us
-// count as 24,000 (60,000), and the join's 8 to 10 us as 45,000 (80,000).
-constexpr int64_t TOP_SLOTS = 5 * sv::HOLD_CUS, TOP_PART = 24000;
-constexpr int64_t TOP_JOIN = 45000, TOP_JOIN_CUT = 20000;   // more where the join has to cut
-constexpr int64_t DIS_SLOTS = 4 * sv::HOLD_CUS, DIS_PART = 60000, DIS_JOIN = 80000;
-constexpr int64_t HOLD_MIN_ROWS = 192;
-constexpr int64_t ROW_MAX_PARTS = 64;
-
-// Rows held in registers, a workgroup a row at a time: HOLD_NV's index, or -1 where
-// the rows are too long for that or too few to give most CUs one.
-int hold_rows(int64_t R, int64_t V, sv_dtype dtype) {
-  return R < HOLD_MIN_ROWS ? -1 : sv::hold_size(V, (int)size_of(dtype));
-}
-
+// Top logits: a workgroup alone takes 7 bytes a nanosecond and 6 us besides, the join
+// 5 to 8 us. 9 rows of 151,936 in bfloat16: 16 parts 16.3 us, 8 parts 18.1, 4 parts 21.4, one
+// about 50. 331 rows of 50,257 in float32: one part 55.5 us, two 52.8, five 59.
 struct TopLayout {
   int parts;
   size_t keys, sums, total;
 };
-bool top_layout(int32_t R, int32_t V, int32_t K, TopLayout* L) {
-  if (R < 1 || V < 1 || K < 1 || K > SV_MAX_TOP || K > V) return false;
-  int64_t most = sv::TOP_CAP / K;   // what the join holds
-  if (most > ROW_MAX_PARTS) most = ROW_MAX_PARTS;
-  const int64_t parts = L->parts = row_parts(
-      R, (int64_t)V * 2, TOP_SLOTS, TOP_PART,
-      [K](int64_t p) { return TOP_JOIN + (p * K > sv::TOP_THIN ? TOP_JOIN_CUT : 0); }, most);
+bool top_layout(int32_t R, int32_t V, int32_t K, sv_dtype dtype, TopLayout* L) {
+  if (R < 1 || R > MAX_VOCAB_ROWS || V < 1 || K < 1 || K > SV_MAX_TOP || K > V || !known(dtype)) return false;
+  const int64_t most = sv::TOP_CAP / K < 64 ? sv::TOP_CAP / K : 64;   // what the join holds
+  const int64_t parts = L->parts =
+      (int)row_parts(R, (int64_t)V * size_of(dtype), 5 * sv::HOLD_CUS, 16000, 66000, most);
   Carver c;
   L->keys = c.take(parts > 1 ? (size_t)R * parts * K * sizeof(uint64_t) : 0);
   L->sums = c.take(parts > 1 ? (size_t)R * parts * sizeof(sv::MaxSum) : 0);
@@ -93,8 +74,22 @@ bool top_layout(int32_t R, int32_t V, int32_t K, TopLayout* L) {
   return true;
 }
 
-int distill_parts(int32_t R, int32_t V) {
-  return row_parts(R, (int64_t)V * 2, DIS_SLOTS, DIS_PART, [](int64_t) { return DIS_JOIN; }, ROW_MAX_PARTS);
+// Distillation: a workgroup alone takes 23 bytes a nanosecond, the join 4.5 us. The loss
+// of 32 rows of 151,936 in bfloat16 in 8 parts: 10.8 us, in one 17.0; of 128 in 4: 15.1,
+// in one 20.2; of 400 in 2: 34, in one 27.
+int distill_parts(int32_t R, int32_t V, sv_dtype dtype) {
+  return (int)row_parts(R, (int64_t)V * size_of(dtype), 2 * sv::HOLD_CUS, 38000, 120000, 64);
+}
+
+// With the gradient, rows are held in registers (HOLD_NV's index) where they fit; -1:
+// streamed. Not short ones, for which the walk over rows costs more than a second read
+// of what the caches hold (4096 rows of 8,000 in bfloat16: held 105 us, streamed 74; of
+// 32,000: 157 and 163; of 151,936: 574 and 708). Nor fewer than 96 long ones, which several
+// workgroups share (32 rows of 151,936: held 31 us, in 8 parts 24; 128: 34 and 38).
+int distill_hold(int32_t R, int32_t V, sv_dtype dtype) {
+  const int64_t bytes = (int64_t)V * size_of(dtype);
+  if (bytes < 40000 || (R < 96 && bytes > 200000)) return -1;
+  return sv::hold_size(V, (int)size_of(dtype));
 }
 
 int distill_args(const void* logits, int64_t logits_stride, sv_dtype dtype, int32_t R, int32_t V,
@@ -106,6 +101,7 @@ int distill_args(const void* logits, int64_t logits_stride, sv_dtype dtype, int3
   if (logits_stride < V || (grad && grad_stride < V)) return SV_EINVAL;
   if (!aligned(logits, size_of(dtype)) || !aligned(grad, size_of(dtype))) return SV_EINVAL;
   if (grad == logits && grad_stride != logits_stride) return SV_EINVAL;
+  if (R > MAX_VOCAB_ROWS) return SV_ESIZE;
   a->logits = logits;
   a->stride = logits_stride;
   a->ids = ids;
@@ -114,10 +110,11 @@ int distill_args(const void* logits, int64_t logits_stride, sv_dtype dtype, int3
   a->R = R;
   a->V = V;
   a->K = K;
-  a->parts = distill_parts(R, V);
-  a->hold = grad ? hold_rows(R, V, dtype) : -1;   // the loss alone streams faster
+  a->parts = distill_parts(R, V, dtype);
+  a->hold = grad ? distill_hold(R, V, dtype) : -1;   // the loss alone streams faster
   a->temperature = temperature;
   a->inv_t = 1.0f / temperature;
+  a->inv_t64 = 1.0 / temperature;
   a->c = (float)((double)LOG2E_D / temperature);
   a->grad = grad;
   a->grad_stride = grad_stride;
@@ -131,7 +128,7 @@ constexpr int64_t CE_MAX_ROWS = 1 << 22;
 // rounds of tiles over the CUs (ce_round_rows); as many rounds as stay within
 // CE_PIECE_BYTES, half of what the last-level cache holds, and at least one unless
 // that takes more than CE_PIECE_MOST.
-constexpr int64_t CE_PIECE_BYTES = 128ll << 20, CE_PIECE_MOST = 512ll << 20;
+constexpr int64_t CE_PIECE_BYTES = 128ll << 20, CE_PIECE_MOST = 1024ll << 20;
 constexpr int64_t CE_PIECE_STEP = 256;    // a multiple of every tile height
 constexpr int64_t CE_CUS = 256;
 
@@ -143,8 +140,10 @@ bool ce_shape(int32_t N, int32_t D, int32_t V, sv_dtype dtype, CeShape* s) {
   if (N < 1 || D < 1 || V < 1 || !known(dtype)) return false;
   if (N > CE_MAX_ROWS || D > sv::CE_MAX_D || V >= INT32_MAX - 1024) return false;
   *s = CeShape{N, D, V, round_up(D, sv::CE_BK), dtype == SV_BF16 ? 1 : 3};
-  // tiles of any product
-  return ceil_div(V, 64) * ceil_div(N, 32) < INT32_MAX;
+  // workgroups of the products over the vocabulary and of dh, and of its sums
+  const int64_t bm = sv::ce_tile_m(N), bn = sv::ce_tile_n(N);
+  return ceil_div(V, bm) * ceil_div(N, bn) < MAX_WORKGROUPS &&
+         ceil_div(D, bm) * ceil_div(N, bn) < MAX_WORKGROUPS && ceil_div(D, 4) * N / 256 < MAX_WORKGROUPS;
 }
 
 // Tokens of a piece whose operands take `bytes` a token.
@@ -245,9 +244,9 @@ int ce_check(const void* hidden, int64_t hidden_stride, const void* weight, int6
 
 extern "C" {
 
-size_t spec_verify_top_logits_workspace_bytes(int32_t R, int32_t V, int32_t K) {
+size_t spec_verify_top_logits_workspace_bytes(int32_t R, int32_t V, int32_t K, sv_dtype dtype) {
   TopLayout L;
-  return top_layout(R, V, K, &L) ? L.total : 0;
+  return top_layout(R, V, K, dtype, &L) ? L.total : 0;
 }
 
 int spec_verify_top_logits(const void* logits, int64_t logits_stride, sv_dtype dtype, int32_t R,
@@ -259,7 +258,7 @@ int spec_verify_top_logits(const void* logits, int64_t logits_stride, sv_dtype d
   if (!temperature_ok(temperature) || logits_stride < V || !aligned(logits, size_of(dtype)))
     return SV_EINVAL;
   TopLayout L;
-  if (!top_layout(R, V, K, &L)) return SV_EINVAL;
+  if (!top_layout(R, V, K, dtype, &L)) return R > MAX_VOCAB_ROWS && V >= 1 ? SV_ESIZE : SV_EINVAL;
   if (!workspace_ok(workspace, workspace_bytes, L.total)) return SV_EWORKSPACE;
   sv::TopArgs a{};
   a.logits = logits;
@@ -278,9 +277,9 @@ int spec_verify_top_logits(const void* logits, int64_t logits_stride, sv_dtype d
   return sv::launch_top_logits(a, dtype == SV_BF16, (hipStream_t)stream) ? SV_EHIP : SV_OK;
 }
 
-size_t spec_verify_distill_workspace_bytes(int32_t R, int32_t V) {
-  if (R < 1 || V < 1) return 0;
-  const int parts = distill_parts(R, V);
+size_t spec_verify_distill_workspace_bytes(int32_t R, int32_t V, sv_dtype dtype) {
+  if (R < 1 || R > MAX_VOCAB_ROWS || V < 1 || !known(dtype)) return 0;
+  const int parts = distill_parts(R, V, dtype);
   return parts > 1 ? align_up((size_t)R * parts * sizeof(sv::MaxSum)) : 0;
 }
 
@@ -294,7 +293,7 @@ int spec_verify_distill(const void* logits, int64_t logits_stride, sv_dtype dtyp
   const int rc = distill_args(logits, logits_stride, dtype, R, V, teacher_ids, teacher_logits,
                               teacher_lse, K, temperature, out_grad, grad_stride, &a);
   if (rc != SV_OK) return rc;
-  if (!workspace_ok(workspace, workspace_bytes, spec_verify_distill_workspace_bytes(R, V)))
+  if (!workspace_ok(workspace, workspace_bytes, spec_verify_distill_workspace_bytes(R, V, dtype)))
     return SV_EWORKSPACE;
   a.weight = row_weight;
   a.loss = out_loss;

@@ -95,6 +95,7 @@ def _check_top(t, z, k, T=1.0, **kw):
     (2, 1023, 64, 1, 1, 0.7), (5, 4097, 1, 0, 0, 1.0), (4, 8192, 33, 0, 0, 2.0),
     (4, 50257, 256, 3, 2, 1.0), (9, 151936, 32, 0, 0, 0.8), (2, 151936, 1024, 0, 0, 1.0),
     (3, 32000, 1000, 7, 5, 1.0), (600, 3001, 17, 0, 0, 1.3), (520, 20011, 300, 9, 4, 1.0),
+    (700, 40003, 64, 0, 0, 1.0), (700, 40003, 65, 1, 0, 1.0), (1, 300007, 1024, 0, 0, 1.0),
 ])
 def test_top_logits(dtype, R, V, K, pad, shift, T):
     rng = np.random.default_rng(R * 7919 + V + K)
@@ -222,6 +223,11 @@ def _check_distill(t, z, ids, values, T=1.0, lse=None, w=None, dtype="bf16", in_
     (8, 32000, 16, 0, 0, 1.0, False, True), (3, 50257, 1024, 1, 0, 3.0, False, True),
     (1030, 1003, 33, 0, 0, 1.0, False, True), (1100, 515, 8, 5, 3, 1.5, True, True),
     (2, 151936, 64, 0, 0, 1.0, False, True), (1026, 8200, 5, 0, 0, 1.0, False, False),
+    # rows held in registers, of each size, one and several to a workgroup; the last
+    # is too long for that in float32
+    (5, 90001, 40, 0, 0, 1.0, True, True), (3, 45001, 7, 2, 1, 0.7, False, False),
+    (530, 20011, 9, 0, 0, 1.0, False, True), (270, 82001, 12, 3, 1, 2.0, True, True),
+    (260, 80001, 6, 0, 0, 1.0, False, True),
 ])
 def test_distill(dtype, R, V, K, pad, shift, T, lse, weighted):
     rng = np.random.default_rng(R + 31 * V + K)
@@ -552,7 +558,8 @@ def test_streams_repeats_and_graph_replays(dtype):
     ids, vals = _teacher(rng, z, 20)
     static = [t.clone(), _dev(ids), _dev(vals), h.clone(), w, _dev(y)]
     code = sv._dtype_code(h)
-    need = [sv.spec_verify_top_logits_workspace_bytes(5, V, 20), sv.spec_verify_distill_workspace_bytes(5, V),
+    need = [sv.spec_verify_top_logits_workspace_bytes(5, V, 20, code),
+            sv.spec_verify_distill_workspace_bytes(5, V, code),
             sv.spec_verify_linear_ce_workspace_bytes(N, D, V, code),
             sv.spec_verify_linear_ce_backward_workspace_bytes(N, D, V, code)]
     spaces = [torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda:0") for n in need]

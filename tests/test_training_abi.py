@@ -63,13 +63,14 @@ def test_top_logits_refusals(lib):
                dict(dtype=0, z=FAKE + 2)):
         assert _top(lib, **kw) == L.SV_EINVAL, kw
     assert _top(lib, dtype=2) == L.SV_EDTYPE
+    assert _top(lib, T=1e-40) == L.SV_EINVAL and _top(lib, R=(1 << 22) + 1) == L.SV_ESIZE
     big = dict(V=151936, stride=151936, R=2)
-    need = lib.spec_verify_top_logits_workspace_bytes(2, 151936, 8)
+    need = lib.spec_verify_top_logits_workspace_bytes(2, 151936, 8, 1)
     assert need > 0 and need % 256 == 0
     for kw in (dict(), dict(ws=FAKE, ws_bytes=need - 1), dict(ws=FAKE + 8, ws_bytes=need)):
         assert _top(lib, **big, **kw) == L.SV_EWORKSPACE, kw
     for bad in ((0, 100, 1), (1, 0, 1), (1, 100, 0), (1, 100, 101), (1, 5000, L.SV_MAX_TOP + 1)):
-        assert lib.spec_verify_top_logits_workspace_bytes(*bad) == 0
+        assert lib.spec_verify_top_logits_workspace_bytes(*bad, 1) == 0
 
 
 def test_distill_refusals(lib):
@@ -81,13 +82,16 @@ def test_distill_refusals(lib):
                    dict(stride=40008, gstride=40000)):   # in place at another stride
             assert _distill(lib, backward, **kw) == L.SV_EINVAL, (backward, kw)
         assert _distill(lib, backward, dtype=7) == L.SV_EDTYPE
+        assert _distill(lib, backward, T=1e-40) == L.SV_EINVAL
+        assert _distill(lib, backward, R=(1 << 22) + 1) == L.SV_ESIZE
     assert _distill(lib, loss=None) == L.SV_EINVAL
     assert _distill(lib, True, grad=None) == L.SV_EINVAL
-    need = lib.spec_verify_distill_workspace_bytes(2, 40000)
+    need = lib.spec_verify_distill_workspace_bytes(2, 200000, 1)
     assert need > 0
+    big = dict(V=200000, stride=200000, gstride=200000)
     for kw in (dict(), dict(ws=FAKE, ws_bytes=need - 1), dict(ws=FAKE + 16, ws_bytes=need)):
-        assert _distill(lib, **kw) == L.SV_EWORKSPACE, kw
-    assert lib.spec_verify_distill_workspace_bytes(0, 10) == 0
+        assert _distill(lib, **big, **kw) == L.SV_EWORKSPACE, kw
+    assert lib.spec_verify_distill_workspace_bytes(0, 10, 1) == 0
 
 
 def test_linear_ce_refusals(lib):
@@ -99,12 +103,13 @@ def test_linear_ce_refusals(lib):
         assert _ce(lib, backward, dtype=-1) == L.SV_EDTYPE
         assert _ce(lib, backward, N=1 << 23) == L.SV_ESIZE
         assert _ce(lib, backward, D=1 << 23, hs=1 << 23, ws=1 << 23) == L.SV_ESIZE
+        assert _ce(lib, backward, N=1 << 22, V=1 << 30) == L.SV_ESIZE   # too many tiles
         assert _ce(lib, backward) == L.SV_EWORKSPACE
     assert _ce(lib, loss=None) == L.SV_EINVAL
     for kw in (dict(gh=None, gw=None), dict(ghs=63), dict(gws=63), dict(gh=FAKE + 1), dict(gw=FAKE + 1)):
         assert _ce(lib, True, **kw) == L.SV_EINVAL, kw
     f, b = lib.spec_verify_linear_ce_workspace_bytes, lib.spec_verify_linear_ce_backward_workspace_bytes
-    assert f(5, 64, 100, 1) > 0 and b(5, 64, 100, 1, 1, 1) > b(5, 64, 100, 1, 1, 0) > 0
+    assert f(5, 64, 100, 1) > 0 and b(5, 64, 100, 1, 1, 1) > b(5, 64, 100, 1, 0, 1) > 0
     assert f(0, 64, 100, 1) == 0 and f(5, 64, 100, 9) == 0 and b(5, 64, 100, 1, 0, 0) == 0
     need = b(5, 64, 100, 1, 1, 1)
     assert _ce(lib, True, space=FAKE, bytes=need - 1) == L.SV_EWORKSPACE
