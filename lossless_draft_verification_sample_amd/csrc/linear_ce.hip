@@ -10,11 +10,14 @@
 // The last two read their transposed operands from W, h and dz as they lie in
 // memory; the transposition happens in the read from LDS.
 //
-// float32 operands are split into three bfloat16 parts x = x1 + x2 + x3 (each the
-// rounding of what the parts before leave: 24 bits in all), and a product sums
-// the six part products down to 2^-24 of the largest, small ones first. Six
-// bfloat16 products take 6/2500 of a second per PFLOP against 1/157 for the
-// float32 matrix instructions.
+// float32 operands, by the number of states (CE_F32_STATES):
+//   few   as they are, with the float32 matrix instructions: what bounds these calls is
+//         the read of W, 4 bytes an element;
+//   many  split into three bfloat16 parts x = x1 + x2 + x3 (each the rounding of what
+//         the parts before leave: 24 bits in all); a product sums the six part products
+//         down to 2^-24 of the largest, small ones first. Six bfloat16 products take
+//         6/2500 of a second per PFLOP against 1/157 for the float32 instructions, but
+//         the parts have to be written first, 6 bytes an element.
 
 #include "sv_train.hpp"
 
@@ -36,7 +39,8 @@ constexpr int WAIT_VM0 = 0x0F70;
 // Last word of a raw buffer resource: 32-bit data, no swizzle.
 constexpr int RSRC_WORD3 = 0x00027000;
 // Range of the buffer resources, and the offset of a load that shall read zeros.
-// A tile's own offsets stay below it: 255 rows of at most 2^22 elements.
+// A tile's own offsets stay below it: 255 rows of at most 2^22 bfloat16, or 127 of
+// as many float elements.
 constexpr uint32_t BEYOND = 0x80000000u;
 
 // Part products of float32 operands, in the order in which they are summed.
@@ -52,8 +56,18 @@ struct Tile {
   static constexpr int TM = BM / WM, TN = BN / WN;   // a wave's tile
   static constexpr int MI = TM / 16, NI = TN / 16;
   static constexpr int LA = BM * 8 / THREADS, LB = BN * 8 / THREADS;   // 16-byte loads a thread
-  static constexpr int STAGE = (BM + BN) * CE_BK;    // bfloat16 elements
+  static constexpr int STAGE = (BM + BN) * CE_LINE;   // bytes
   static_assert(LA * THREADS == BM * 8 && LB * THREADS == BN * 8, "whole rounds of loads");
+};
+
+// Sixteen bytes of depth of one row.
+template <typename E>
+struct Frag {
+  typedef bf16x8 type;
+};
+template <>
+struct Frag<float> {
+  typedef f32x4 type;
 };
 
 // Tile indices of a workgroup: consecutive workgroups go to different XCDs (8),
@@ -92,32 +106,41 @@ __device__ __forceinline__ void copy_to_lds(uint64_t base, uint32_t byte_off, ui
                :: "s"(lds), "v"(byte_off), "s"(rsrc) : "memory");
 }
 
-// One operand of a tile: how ROWS rows by CE_BK of depth get from memory into LDS,
-// and its fragments from there.
+// One operand of a tile, of bfloat16 (uint16_t) or float elements: how ROWS rows by one
+// step of depth (CE_LINE bytes of a row) get from memory into LDS, and its fragments
+// from there: per lane 16 bytes of depth of one row.
 //   plain       memory [row][k]: LDS row of 8 groups of 16 bytes; slot s of row r
 //               holds group s ^ (r & 7), so that a fragment's 16 rows spread over
 //               the banks.
-//   transposed  memory [k][row]: LDS as in memory, ROWS / 8 groups a k; a
-//               fragment is made by the transposing LDS read, which gives lane i of
-//               16 the i-th of 16 columns of 4 consecutive k. Pairs of groups are
-//               permuted by pair ^ f(k), f from bits 0, 1 and 3 of k: the 16 k that
-//               one read touches are then spread over the banks.
+//   transposed  memory [k][row]: LDS as in memory. bfloat16: a fragment is made by the
+//               transposing LDS read, which gives lane i of 16 the i-th of 16 columns of
+//               4 consecutive k; blocks of 16 columns (32 bytes) are permuted by
+//               block ^ f(k), f from bits 0, 1 and 3 of k: the 16 k that one read
+//               touches are then spread over the banks. float: four reads of one element
+//               each; blocks of 16 columns (64 bytes) are permuted by bits 2 and 3 of k.
 // Groups behind the depth, or (transposed) behind the last row, are loaded from
 // beyond the buffer resource's range, which reads as zero.
-template <bool TRANS, int ROWS, int FRAGS, int LOADS, int THREADS>
+template <typename E, bool TRANS, int ROWS, int FRAGS, int LOADS, int THREADS>
 struct Side {
-  static constexpr int GROUPS = TRANS ? ROWS / 8 : CE_BK / 8;   // of 16 bytes, a line of LDS
-  static constexpr int READS = TRANS ? 2 : 1;                   // LDS reads a fragment
-  uint32_t off[LOADS];
-  uint32_t at[TRANS ? FRAGS : 2];   // transposed: per fragment; plain: per half of the depth
+  static constexpr int ES = sizeof(E);
+  static constexpr int EPG = 16 / ES;                           // elements of a group
+  static constexpr int DEPTH = CE_LINE / ES;                    // elements of a step
+  static constexpr int GROUPS = TRANS ? ROWS / EPG : 8;         // of a line of LDS
+  static constexpr int BLOCK = 16 / EPG;                        // groups of 16 columns
+  static constexpr int READS = !TRANS ? 1 : ES == 2 ? 2 : 4;    // LDS reads a fragment
+  typedef typename Frag<E>::type F;
+  uint32_t off[LOADS];              // of this thread's loads from the tile's first row, bytes
+  uint32_t at[TRANS ? FRAGS : 2];   // in LDS, bytes. transposed: per fragment; plain: per half of the depth
 
   static __device__ __forceinline__ int line(int i, int tid) { return (i * THREADS + tid) / GROUPS; }
+  static __device__ __forceinline__ int twist(int k) {
+    return (ES == 2 ? (k & 3) | ((k >> 3) & 1) << 2 : (k >> 2) & 3) & (GROUPS / BLOCK - 1);
+  }
   static __device__ __forceinline__ int group(int i, int tid) {
     const int slot = (i * THREADS + tid) % GROUPS, l = line(i, tid);
     if (!TRANS) return slot ^ (l & 7);
-    return (((slot >> 1) ^ (twist(l) & (GROUPS / 2 - 1))) << 1) | (slot & 1);
+    return (slot / BLOCK ^ twist(l)) * BLOCK + slot % BLOCK;
   }
-  static __device__ __forceinline__ int twist(int k) { return (k & 3) | ((k >> 3) & 1) << 2; }
 
   // base: first row of the tile; rows, ld: of the operand; wave_row: first row of
   // this wave's fragments in the tile.
@@ -126,58 +149,75 @@ struct Side {
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
       const int l = line(i, threadIdx.x), gr = group(i, threadIdx.x);
-      if (TRANS) off[i] = base + gr * 8 < rows ? (uint32_t)(l * ld + gr * 8) * 2u : BEYOND;
-      else off[i] = (uint32_t)(min(l, rows - 1 - base) * ld + gr * 8) * 2u;   // rows past the end repeat
+      if (TRANS) off[i] = base + gr * EPG < rows ? (uint32_t)(l * ld + gr * EPG) * ES : BEYOND;
+      else off[i] = (uint32_t)(min(l, rows - 1 - base) * ld + gr * EPG) * ES;   // rows past the end repeat
     }
     if (TRANS) {
-      const int f = twist(fk * 8 + (fr >> 2)) & (GROUPS / 2 - 1);
+      const int k = ES == 2 ? fk * 8 + (fr >> 2) : fk * 4;
+      const int f = twist(k), in = ES == 2 ? (fr & 3) * 4 : fr;
 #pragma unroll
       for (int i = 0; i < FRAGS; ++i)
-        at[i] = (uint32_t)((fk * 8 + (fr >> 2)) * ROWS + ((wave_row / 16 + i) ^ f) * 16 + (fr & 3) * 4);
+        at[i] = (uint32_t)(k * ROWS + ((wave_row / 16 + i) ^ f) * 16 + in) * ES;
     } else {
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk)
-        at[kk] = (uint32_t)((wave_row + fr) * CE_BK + (((kk * 4 + fk) ^ (fr & 7)) * 8));
+        at[kk] = (uint32_t)((wave_row + fr) * CE_LINE + ((kk * 4 + fk) ^ (fr & 7)) * 16);
     }
   }
   // Loads the tile's depth k.. of the operand that begins at p (the tile's first
   // row, k = 0); depth: where the operand ends.
-  __device__ __forceinline__ void load(const uint16_t* p, int64_t ld, int k, int depth, uint32_t lds,
-                                       int wave) {
+  __device__ __forceinline__ void load(const E* p, int64_t ld, int k, int depth, uint32_t lds, int wave) {
     const uint64_t base = (uint64_t)(uintptr_t)(p + (TRANS ? (int64_t)k * ld : (int64_t)k));
-    if (k + CE_BK <= depth) {
+    if (k + DEPTH <= depth) {
 #pragma unroll
       for (int i = 0; i < LOADS; ++i) copy_to_lds(base, off[i], lds + i * THREADS * 16);
     } else {   // the operand's last, shorter step
       const int tid = thread_again(wave);
 #pragma unroll
       for (int i = 0; i < LOADS; ++i) {
-        const bool in = k + (TRANS ? line(i, tid) : group(i, tid) * 8) < depth;
+        const bool in = k + (TRANS ? line(i, tid) : group(i, tid) * EPG) < depth;
         copy_to_lds(base, in ? off[i] : BEYOND, lds + i * THREADS * 16);
       }
     }
   }
-  __device__ __forceinline__ bf16x8 frag(const uint16_t* lds, int i, int kk) const {
+  __device__ __forceinline__ F frag(const char* lds, int i, int kk) const {
 #if defined(__HIP_DEVICE_COMPILE__)
-    if constexpr (TRANS) {
-      const uint16_t* p = lds + at[i] + kk * 32 * ROWS;
+    if constexpr (!TRANS) {
+      return *(const F*)(lds + at[kk] + i * 16 * CE_LINE);
+    } else if constexpr (ES == 2) {
+      const char* p = lds + at[i] + kk * 32 * ROWS * ES;
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
-      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * ROWS));
-      return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * ROWS * ES));
+      return __builtin_bit_cast(F, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     } else {
-      return *(const bf16x8*)(lds + at[kk] + i * 16 * CE_BK);
+      const char* p = lds + at[i] + kk * 16 * ROWS * ES;
+      F v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = *(const float*)(p + e * ROWS * ES);
+      return v;
     }
 #else
-    return bf16x8{};
+    return F{};
 #endif
   }
 };
 
-template <int BM, int BN, int WM, int WN, typename Epi>
+// C += A B over the 16 bytes of depth of a fragment pair: 32 of bfloat16, or 16 of
+// float32, whose four instructions take element e of every lane: the same k in A and B.
+__device__ __forceinline__ f32x4 multiply(const bf16x8& a, const bf16x8& b, const f32x4& c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 multiply(const f32x4& a, const f32x4& b, f32x4 c) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
+  return c;
+}
+
+template <typename E, int BM, int BN, int WM, int WN, typename Epi>
 __global__ __launch_bounds__(WM* WN* WAVE, WM* WN == 8 ? 2 : 1) void ce_gemm_kernel(
     CeGemm g, int tiles_m, int tiles_n, typename Epi::Args ea) {
   using T = Tile<BM, BN, WM, WN>;
-  __shared__ __align__(16) uint16_t lds[2 * T::STAGE];
+  __shared__ __align__(16) char lds[2 * T::STAGE];
   const int tid = threadIdx.x, lane = tid & (WAVE - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
   const int wm = wave / WN, wn = wave % WN;
@@ -185,28 +225,28 @@ __global__ __launch_bounds__(WM* WN* WAVE, WM* WN == 8 ? 2 : 1) void ce_gemm_ker
   tile_of(blockIdx.x, tiles_m, tiles_n, &tm, &tn);
   const int m0 = tm * BM, n0 = tn * BN;
 
-  Side<Epi::TRANS_A, BM, T::MI, T::LA, T::THREADS> sa;
-  Side<Epi::TRANS_B, BN, T::NI, T::LB, T::THREADS> sb;
+  Side<E, Epi::TRANS_A, BM, T::MI, T::LA, T::THREADS> sa;
+  Side<E, Epi::TRANS_B, BN, T::NI, T::LB, T::THREADS> sb;
   sa.init(m0, g.M, g.lda, wm * T::TM, lane);
   sb.init(n0, g.N, g.ldb, wn * T::TN, lane);
-  const uint16_t* pa = g.A + (Epi::TRANS_A ? (int64_t)m0 : m0 * g.lda);
-  const uint16_t* pb = g.B + (Epi::TRANS_B ? (int64_t)n0 : n0 * g.ldb);
-
+  const E* pa = (const E*)g.A + (Epi::TRANS_A ? (int64_t)m0 : m0 * g.lda);
+  const E* pb = (const E*)g.B + (Epi::TRANS_B ? (int64_t)n0 : n0 * g.ldb);
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(lds_void*)lds);
 
   // steps of this split; next_*: what is to be loaded next
-  const int steps_k = (g.K + CE_BK - 1) / CE_BK;
+  constexpr int DEPTH = decltype(sa)::DEPTH;
+  const int steps_k = (g.K + DEPTH - 1) / DEPTH;
   const int total = steps_k * g.parts;
   const int per = (total + g.splits - 1) / g.splits;
   const int first = min(total, (int)blockIdx.y * per), last = min(total, first + per);
-  int next_pair = first / steps_k, next_k = (first - next_pair * steps_k) * CE_BK;
+  int next_pair = first / steps_k, next_k = (first - next_pair * steps_k) * DEPTH;
   auto issue = [&](int stage) {
     int ia = 0, ib = 0;
     if (g.parts > 1) part_pair(next_pair, &ia, &ib);
-    const uint32_t la = lds0 + (stage * T::STAGE + wave * WAVE * 8) * 2;
+    const uint32_t la = lds0 + stage * T::STAGE + wave * WAVE * 16;
     sa.load(pa + ia * g.plane_a, g.lda, next_k, g.K, la, wave);
-    sb.load(pb + ib * g.plane_b, g.ldb, next_k, g.K, la + BM * CE_BK * 2, wave);
-    next_k += CE_BK;
+    sb.load(pb + ib * g.plane_b, g.ldb, next_k, g.K, la + BM * CE_LINE, wave);
+    next_k += DEPTH;
     if (next_k >= g.K) {
       next_k = 0;
       ++next_pair;
@@ -224,11 +264,11 @@ __global__ __launch_bounds__(WM* WN* WAVE, WM* WN == 8 ? 2 : 1) void ce_gemm_ker
     __builtin_amdgcn_s_waitcnt(WAIT_VM0);
     __syncthreads();
     if (s + 1 < last) issue(stage ^ 1);
-    const uint16_t* la = lds + stage * T::STAGE;
-    const uint16_t* lb = la + BM * CE_BK;
+    const char* la = lds + stage * T::STAGE;
+    const char* lb = la + BM * CE_LINE;
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
-      bf16x8 fa[T::MI], fb[T::NI];
+      typename Frag<E>::type fa[T::MI], fb[T::NI];
 #pragma unroll
       for (int j = 0; j < T::NI; ++j) fb[j] = sb.frag(lb, j, kk);
 #pragma unroll
@@ -236,14 +276,13 @@ __global__ __launch_bounds__(WM* WN* WAVE, WM* WN == 8 ? 2 : 1) void ce_gemm_ker
 #pragma unroll
       for (int i = 0; i < T::MI; ++i)
 #pragma unroll
-        for (int j = 0; j < T::NI; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+        for (int j = 0; j < T::NI; ++j) acc[i][j] = multiply(fa[i], fb[j], acc[i][j]);
     }
     // Order of issue: all of B's fragments and two of A's, then each row of
     // matrix instructions with the fragment reads that the row after the next needs.
     constexpr int MFMA = 0x008, DS_READ = 0x100;
     constexpr int RA = decltype(sa)::READS, RB = decltype(sb)::READS;
-    if constexpr (T::MI > 2) {
+    if constexpr (T::MI > 2 && sizeof(E) == 2) {
       __builtin_amdgcn_sched_group_barrier(DS_READ, RB * T::NI + 2 * RA, 0);
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
@@ -271,7 +310,7 @@ __global__ __launch_bounds__(WM* WN* WAVE, WM* WN == 8 ? 2 : 1) void ce_gemm_ker
   }
   if (s < last) step(s, 0);
   __syncthreads();
-  Epi::template run<T>(ea, g, acc, m0 + wm * T::TM, n0 + wn * T::TN, tm, wm, wn, lane, (char*)lds);
+  Epi::template run<T>(ea, g, acc, m0 + wm * T::TM, n0 + wn * T::TN, tm, wm, wn, lane, lds);
 }
 
 // Element i of acc[mi][ni] of lane l is C[m][n] with
@@ -337,7 +376,7 @@ __device__ __forceinline__ void split3(float x, uint16_t (&p)[3]) {
   }
 }
 
-// PARTS: 1 writes dz rounded to bfloat16, 3 its three parts.
+// PARTS: 1 writes dz rounded to bfloat16, 3 its three parts, 0 float32.
 template <int PARTS>
 struct EpiDz {
   typedef CeDzOut Args;
@@ -357,7 +396,7 @@ struct EpiDz {
         ls2 = o.stats[2 * (int64_t)n + 1] * LOG2E;
         gl = o.grad_loss ? o.grad_loss[n] : 1.0f;
       }
-      uint16_t* row = o.dz + (int64_t)n * o.ldz;
+      uint16_t* row = (uint16_t*)o.dz + (int64_t)n * o.ldz;
 #pragma unroll
       for (int i = 0; i < T::MI; ++i) {
         const int r = mw + 16 * i + 4 * fk;
@@ -369,6 +408,8 @@ struct EpiDz {
           // a state left out, and what lies behind the last token, is 0
           d[e] = gl == 0.0f || r + e >= g.M ? 0.0f : gl * q;
         }
+        if (PARTS == 0 && n < g.N && r < o.ldz)
+          *(f32x4*)((float*)o.dz + (int64_t)n * o.ldz + r) = (f32x4){d[0], d[1], d[2], d[3]};
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) {
           const uint2 w = make_uint2(pack_bf16(d[0], d[1]), pack_bf16(d[2], d[3]));
@@ -477,6 +518,10 @@ __global__ __launch_bounds__(256) void ce_pack_kernel(CePack p) {
         for (int e = 0; e < 4; ++e)
           if (c + e < p.cols) v[e] = src[e];
       }
+      if (p.planes == 0) {   // as they are
+        *(f32x4*)((float*)p.dst + r * p.ld + c) = (f32x4){v[0], v[1], v[2], v[3]};
+        continue;
+      }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         uint16_t t[3];
@@ -490,7 +535,7 @@ __global__ __launch_bounds__(256) void ce_pack_kernel(CePack p) {
     for (int k = 0; k < 3; ++k)
       if (k < p.planes) {
         const uint2 w = make_uint2(h[k][0] | ((uint32_t)h[k][1] << 16), h[k][2] | ((uint32_t)h[k][3] << 16));
-        *(uint2*)(p.dst + k * p.plane + r * p.ld + c) = w;
+        *(uint2*)((uint16_t*)p.dst + k * p.plane + r * p.ld + c) = w;
       }
   }
 }
@@ -553,17 +598,24 @@ __global__ __launch_bounds__(256) void ce_sum_kernel(const float* acc, int split
     }
 }
 
-template <typename Epi>
+template <typename Epi, typename EpiF32>
 int gemm(const CeGemm& g, const typename Epi::Args& ea, hipStream_t st) {
-  const int bm = ce_tile_m(g.N), bn = ce_tile_n(g.N);
-  const int tiles_m = (g.M + bm - 1) / bm;
-  const int tiles_n = (g.N + bn - 1) / bn;
+  const CeTile t = ce_tile(g.M, g.N, g.f32);
+  const int tiles_m = (g.M + t.bm - 1) / t.bm;
+  const int tiles_n = (g.N + t.bn - 1) / t.bn;
   const dim3 grid((uint32_t)tiles_m * (uint32_t)tiles_n, (uint32_t)g.splits);
-#define CE_LAUNCH(BM, BN, WM, WN) \
-  hipLaunchKernelGGL((ce_gemm_kernel<BM, BN, WM, WN, Epi>), grid, dim3(WM * WN * WAVE), 0, st, g, tiles_m, tiles_n, ea)
-  if (bn == 32) CE_LAUNCH(64, 32, 4, 1);
-  else if (bn == 64) CE_LAUNCH(128, 64, 2, 2);
-  else CE_LAUNCH(256, 256, 2, 4);
+#define CE_LAUNCH(E, BM, BN, WM, WN, EPI) \
+  hipLaunchKernelGGL((ce_gemm_kernel<E, BM, BN, WM, WN, EPI>), grid, dim3(WM * WN * WAVE), 0, st, g, tiles_m, tiles_n, ea)
+  if (g.f32) {
+    if (t.bn == 32) CE_LAUNCH(float, 64, 32, 4, 1, EpiF32);
+    else CE_LAUNCH(float, 128, 64, 2, 2, EpiF32);
+  } else if (t.bn == 32) {
+    CE_LAUNCH(uint16_t, 64, 32, 4, 1, Epi);
+  } else if (t.bn == 64) {
+    CE_LAUNCH(uint16_t, 128, 64, 2, 2, Epi);
+  } else {
+    CE_LAUNCH(uint16_t, 256, 256, 2, 4, Epi);
+  }
 #undef CE_LAUNCH
   return hipGetLastError() == hipSuccess ? 0 : -1;
 }
@@ -576,16 +628,21 @@ int gemm(const CeGemm& g, const typename Epi::Args& ea, hipStream_t st) {
 // 64 rows 69 us in 128 x 64, 78 in 128 x 128; at 128 rows of 2,048 187 us in 128 x 64, 193 in
 // 128 x 128, 204 in 256 x 128. From there on products bound it, and the largest tile
 // reads LDS least: 1,300 TFLOP/s in 256 x 256, 930 in 256 x 128, 910 to 1,010 in 128 x 128.
-int ce_tile_m(int rows_b) { return rows_b <= 32 ? 64 : rows_b <= 128 ? 128 : 256; }
-int ce_tile_n(int rows_b) { return rows_b <= 32 ? 32 : rows_b <= 128 ? 64 : 256; }
-int ce_tiles_per_cu(int rows_b) { return rows_b <= 32 ? 6 : rows_b <= 128 ? 3 : 1; }   // by LDS
-
-int launch_ce_stats(const CeGemm& g, const CeStatsOut& o, hipStream_t st) { return gemm<EpiStats>(g, o, st); }
-int launch_ce_dz(const CeGemm& g, const CeDzOut& o, hipStream_t st) {
-  return g.parts == 1 ? gemm<EpiDz<1>>(g, o, st) : gemm<EpiDz<3>>(g, o, st);
+// dh and dW of less than 128 columns (the rows of A) take the smaller tile too.
+CeTile ce_tile(int64_t M, int64_t N, bool f32) {
+  if (N <= 32) return CeTile{64, 32, 6};
+  if (N <= 128 || M <= 128 || f32) return CeTile{128, 64, 3};
+  return CeTile{256, 256, 1};
 }
-int launch_ce_acc(const CeGemm& g, const CeAccOut& o, hipStream_t st) { return gemm<EpiAcc>(g, o, st); }
-int launch_ce_mat(const CeGemm& g, const CeMatOut& o, hipStream_t st) { return gemm<EpiMat>(g, o, st); }
+
+int launch_ce_stats(const CeGemm& g, const CeStatsOut& o, hipStream_t st) {
+  return gemm<EpiStats, EpiStats>(g, o, st);
+}
+int launch_ce_dz(const CeGemm& g, const CeDzOut& o, hipStream_t st) {
+  return g.parts == 1 ? gemm<EpiDz<1>, EpiDz<0>>(g, o, st) : gemm<EpiDz<3>, EpiDz<0>>(g, o, st);
+}
+int launch_ce_acc(const CeGemm& g, const CeAccOut& o, hipStream_t st) { return gemm<EpiAcc, EpiAcc>(g, o, st); }
+int launch_ce_mat(const CeGemm& g, const CeMatOut& o, hipStream_t st) { return gemm<EpiMat, EpiMat>(g, o, st); }
 
 int launch_ce_pack(const CePack& p, hipStream_t st) {
   const int64_t blocks = (p.ld / 4 * p.rows + 255) / 256;

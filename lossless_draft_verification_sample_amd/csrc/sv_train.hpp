@@ -301,19 +301,20 @@ int launch_distill_backward(const DistillArgs& a, int bf16, hipStream_t s);
 
 // ------------------------------------------------------------ linear cross entropy
 
-constexpr int CE_BK = 64;          // depth of one step of the products, in bfloat16
+constexpr int CE_LINE = 128;       // bytes of a row that one step of the products takes
 constexpr int CE_MAX_D = 1 << 22;
 
-// One product C[m][n] = sum_k A[m][k] B[n][k] of bfloat16 parts. An operand lies
+// One product C[m][n] = sum_k A[m][k] B[n][k]. An operand lies
 // in memory as [row][k] or, where the epilogue takes it transposed, as [k][row];
-// rows of memory start on 16 bytes and can be read in whole groups of 8 elements.
+// rows of memory start on 16 bytes and can be read in whole groups of 16 bytes.
 struct CeGemm {
-  const uint16_t *A, *B;
+  const void *A, *B;
   int64_t lda, ldb;          // strides of memory's rows, elements, at most CE_MAX_D
   int64_t plane_a, plane_b;  // distance of a float32 operand's three parts
   int M, N, K;               // rows of A and B, depth
-  int parts;                 // 1: bfloat16 operands; 6: products of float32's parts
+  int parts;                 // 1: whole operands; 6: products of float32's bfloat16 parts
   int splits;                // workgroups that share one tile's depth
+  bool f32;                  // float32 operands as they are
 };
 
 struct CeStatsOut {
@@ -327,7 +328,7 @@ struct CeDzOut {
   const float* stats;        // [N][2]
   const float* grad_loss;    // [N] or nullptr
   int v0, V;
-  uint16_t* dz;              // [planes][N][ldz], zeros behind the piece's last token
+  void* dz;                  // [parts][N][ldz] bfloat16, or [N][ldz] float; zeros behind the last token
   int64_t ldz, plane_dz;
 };
 struct CeAccOut {
@@ -342,21 +343,22 @@ struct CeMatOut {
   int vec;                   // rows of four can be stored at once
 };
 
-// Rows as the products take them: [planes][rows][ld] bfloat16, zeros from cols to ld.
+// Rows as the products take them: [planes][rows][ld] bfloat16, or [rows][ld] float
+// (planes 0); zeros from cols to ld.
 struct CePack {
   const void* src;           // [rows][cols], float32 or bfloat16
   int64_t stride;
   int bf16;
   int rows, cols;
   int planes;
-  uint16_t* dst;
+  void* dst;
   int64_t ld, plane;
 };
 
-// Tile shapes by the rows of B: see linear_ce.hip.
-int ce_tile_m(int rows_b);
-int ce_tile_n(int rows_b);
-int ce_tiles_per_cu(int rows_b);   // workgroups of that shape a CU holds at once
+struct CeTile {
+  int bm, bn, per_cu;   // per_cu: workgroups that a CU holds at once, by LDS
+};
+CeTile ce_tile(int64_t M, int64_t N, bool f32);
 
 int launch_ce_pack(const CePack& p, hipStream_t s);
 int launch_ce_stats(const CeGemm& g, const CeStatsOut& o, hipStream_t s);

@@ -132,25 +132,34 @@ constexpr int64_t CE_PIECE_BYTES = 128ll << 20, CE_PIECE_MOST = 1024ll << 20;
 constexpr int64_t CE_PIECE_STEP = 256;    // a multiple of every tile height
 constexpr int64_t CE_CUS = 256;
 
+// Up to here states of float32 take the float32 matrix instructions (linear_ce.hip).
+constexpr int64_t CE_F32_STATES = 384;
+
+// float32 in three parts of bfloat16: planes 3; as it is: planes 0; bfloat16: 1.
 struct CeShape {
-  int64_t N, D, V, kp;   // kp: row length of packed operands, a multiple of CE_BK
+  int64_t N, D, V, kp;   // kp: row length of packed operands, whole steps of depth
   int planes;
+  bool f32() const { return planes == 0; }
+  int es() const { return f32() ? 4 : 2; }                   // bytes of an element of an operand
+  int64_t row_bytes(int64_t n) const { return n * (planes == 3 ? 6 : es()); }
+  int64_t depth() const { return sv::CE_LINE / es(); }
+  int64_t per16() const { return 16 / es(); }
 };
 bool ce_shape(int32_t N, int32_t D, int32_t V, sv_dtype dtype, CeShape* s) {
   if (N < 1 || D < 1 || V < 1 || !known(dtype)) return false;
   if (N > CE_MAX_ROWS || D > sv::CE_MAX_D || V >= INT32_MAX - 1024) return false;
-  *s = CeShape{N, D, V, round_up(D, sv::CE_BK), dtype == SV_BF16 ? 1 : 3};
+  *s = CeShape{N, D, V, 0, dtype == SV_BF16 ? 1 : N <= CE_F32_STATES ? 0 : 3};
+  s->kp = round_up(D, s->depth());
   // workgroups of the products over the vocabulary and of dh, and of its sums
-  const int64_t bm = sv::ce_tile_m(N), bn = sv::ce_tile_n(N);
-  return ceil_div(V, bm) * ceil_div(N, bn) < MAX_WORKGROUPS &&
-         ceil_div(D, bm) * ceil_div(N, bn) < MAX_WORKGROUPS && ceil_div(D, 4) * N / 256 < MAX_WORKGROUPS;
+  const sv::CeTile t = sv::ce_tile(V, N, s->f32()), h = sv::ce_tile(D, N, s->f32());
+  return ceil_div(V, t.bm) * ceil_div(N, t.bn) < MAX_WORKGROUPS &&
+         ceil_div(D, h.bm) * ceil_div(N, h.bn) < MAX_WORKGROUPS && ceil_div(D, 4) * N / 256 < MAX_WORKGROUPS;
 }
 
 // Tokens of a piece whose operands take `bytes` a token.
 int64_t piece_rows(const CeShape& s, int64_t bytes) {
-  const int64_t tn = ceil_div(s.N, sv::ce_tile_n((int)s.N)), bm = sv::ce_tile_m((int)s.N);
-  const int64_t per_cu = sv::ce_tiles_per_cu((int)s.N);
-  int64_t round = round_up(ceil_div(CE_CUS * per_cu, tn) * bm, CE_PIECE_STEP);
+  const sv::CeTile t = sv::ce_tile(s.V, s.N, s.f32());
+  const int64_t round = round_up(ceil_div(CE_CUS * t.per_cu, ceil_div(s.N, t.bn)) * t.bm, CE_PIECE_STEP);
   int64_t rows = CE_PIECE_BYTES / bytes / round * round;
   if (rows < round) rows = round;
   const int64_t most = CE_PIECE_MOST / bytes / CE_PIECE_STEP * CE_PIECE_STEP;
@@ -168,11 +177,11 @@ struct CeForward {
 CeForward ce_forward(const CeShape& s) {
   CeForward f;
   Carver c;
-  f.piece = piece_rows(s, s.planes * s.kp * 2);
-  f.partial = c.take((size_t)(ceil_div(s.V, sv::ce_tile_m((int)s.N)) * s.N) * sizeof(sv::MaxSum));
+  f.piece = piece_rows(s, s.row_bytes(s.kp));
+  f.partial = c.take((size_t)(ceil_div(s.V, sv::ce_tile(s.V, s.N, s.f32()).bm) * s.N) * sizeof(sv::MaxSum));
   f.zlabel = c.take((size_t)s.N * sizeof(float));
-  f.hidden = c.take((size_t)(s.planes * s.N * s.kp) * 2);
-  f.weight = c.take((size_t)(s.planes * f.piece * s.kp) * 2);
+  f.hidden = c.take((size_t)(s.N * s.row_bytes(s.kp)));
+  f.weight = c.take((size_t)(f.piece * s.row_bytes(s.kp)));
   f.total = c.off;
   return f;
 }
@@ -185,48 +194,50 @@ struct CeBackward {
 CeBackward ce_backward(const CeShape& s, bool want_h) {
   CeBackward b;
   Carver c;
-  b.piece = piece_rows(s, s.planes * (s.N > s.kp ? s.N : s.kp) * 2);
+  b.piece = piece_rows(s, s.row_bytes(s.N > s.kp ? s.N : s.kp));
   b.acc_ld = round_up(s.D, 4);
-  // dh has few tiles and a long depth: its depth is split until every CU has one
-  const int64_t tiles = ceil_div(s.D, sv::ce_tile_m((int)s.N)) * ceil_div(s.N, sv::ce_tile_n((int)s.N));
-  int64_t splits = ceil_div(CE_CUS * sv::ce_tiles_per_cu((int)s.N), tiles);
-  if (tiles >= CE_CUS) splits = 1;
-  const int64_t steps = b.piece / sv::CE_BK * (s.planes == 1 ? 1 : 6);
+  // dh has few tiles and a long depth: its depth is split until every CU has its fill
+  const sv::CeTile t = sv::ce_tile(s.D, s.N, s.f32());
+  const int64_t tiles = ceil_div(s.D, t.bm) * ceil_div(s.N, t.bn);
+  int64_t splits = tiles >= CE_CUS ? 1 : ceil_div(CE_CUS * t.per_cu, tiles);
+  const int64_t steps = b.piece / s.depth() * (s.planes == 3 ? 6 : 1);
   if (splits > steps / 4) splits = steps / 4;
   const int64_t fit = CE_PIECE_BYTES / (s.N * b.acc_ld * 4);
   if (splits > fit) splits = fit;
   b.splits = splits < 1 ? 1 : (int)splits;
-  b.hidden = c.take((size_t)(s.planes * s.N * s.kp) * 2);
-  b.weight = c.take((size_t)(s.planes * b.piece * s.kp) * 2);
-  b.dz = c.take((size_t)(s.planes * s.N * b.piece) * 2);
+  b.hidden = c.take((size_t)(s.N * s.row_bytes(s.kp)));
+  b.weight = c.take((size_t)(b.piece * s.row_bytes(s.kp)));
+  b.dz = c.take((size_t)(s.N * s.row_bytes(b.piece)));
   b.acc = c.take(want_h ? (size_t)(b.splits * s.N * b.acc_ld) * 4 : 0);
   b.total = c.off;
   return b;
 }
 
-// A matrix as the products take it: bfloat16 (parts), rows on 16 bytes, read in
-// groups of 8. Used as it is where it has that form, else packed.
+// A matrix as the products take it: rows on 16 bytes, read in whole groups of 16 bytes.
+// Used as it is where it has that form, else packed.
 struct Operand {
-  const uint16_t* p;
+  const void* p;
   int64_t ld, plane;
   int64_t cols;
 };
 bool ce_direct(const void* p, int64_t stride, const CeShape& s) {
-  return s.planes == 1 && s.D % 8 == 0 && aligned(p, 16) && stride % 8 == 0 && stride <= sv::CE_MAX_D;
+  return s.planes != 3 && s.D % s.per16() == 0 && aligned(p, 16) && stride % s.per16() == 0 &&
+         stride <= sv::CE_MAX_D;
 }
 int ce_operand(const void* src, int64_t stride, int64_t row0, int64_t rows, const CeShape& s,
-               uint16_t* room, hipStream_t st, Operand* out) {
+               void* room, hipStream_t st, Operand* out) {
   const char* at = (const char*)src + row0 * stride * (s.planes == 1 ? 2 : 4);
   if (ce_direct(src, stride, s)) {
-    *out = Operand{(const uint16_t*)at, stride, 0, s.D};
+    *out = Operand{at, stride, 0, s.D};
     return 0;
   }
-  sv::CePack p{at, stride, s.planes == 1, (int)rows, (int)s.D, s.planes, room, s.kp, rows * s.kp};
+  const sv::CePack p{at, stride, s.planes == 1, (int)rows, (int)s.D, s.planes, room, s.kp, rows * s.kp};
   *out = Operand{room, s.kp, p.plane, s.kp};
   return sv::launch_ce_pack(p, st);
 }
-sv::CeGemm ce_gemm(const Operand& a, int64_t M, const Operand& b, int64_t N, int64_t K, int planes) {
-  return sv::CeGemm{a.p, b.p, a.ld, b.ld, a.plane, b.plane, (int)M, (int)N, (int)K, planes == 1 ? 1 : 6, 1};
+sv::CeGemm ce_gemm(const Operand& a, int64_t M, const Operand& b, int64_t N, int64_t K, const CeShape& s) {
+  return sv::CeGemm{a.p, b.p, a.ld, b.ld, a.plane, b.plane, (int)M, (int)N, (int)K,
+                    s.planes == 3 ? 6 : 1, 1, s.f32()};
 }
 // Depth of the logits' product: what both operands have in whole groups.
 int64_t ce_depth(const Operand& a, const Operand& b) { return a.cols < b.cols ? a.cols : b.cols; }
@@ -337,14 +348,14 @@ int spec_verify_linear_ce(const void* hidden, int64_t hidden_stride, const void*
   sv::MaxSum* partial = (sv::MaxSum*)(ws + f.partial);
   float* zlabel = (float*)(ws + f.zlabel);
   Operand h, w;
-  if (ce_operand(hidden, hidden_stride, 0, N, s, (uint16_t*)(ws + f.hidden), st, &h)) return SV_EHIP;
-  const int bm = sv::ce_tile_m(N);
+  if (ce_operand(hidden, hidden_stride, 0, N, s, ws + f.hidden, st, &h)) return SV_EHIP;
+  const int bm = sv::ce_tile(V, N, s.f32()).bm;
   const int64_t piece = ce_direct(weight, weight_stride, s) ? V : f.piece;
   for (int64_t v0 = 0; v0 < V; v0 += piece) {
     const int64_t rows = V - v0 < piece ? V - v0 : piece;
-    if (ce_operand(weight, weight_stride, v0, rows, s, (uint16_t*)(ws + f.weight), st, &w)) return SV_EHIP;
+    if (ce_operand(weight, weight_stride, v0, rows, s, ws + f.weight, st, &w)) return SV_EHIP;
     const sv::CeStatsOut o{labels, (int)v0, V, partial + v0 / bm * N, zlabel};
-    if (sv::launch_ce_stats(ce_gemm(w, rows, h, N, ce_depth(w, h), s.planes), o, st)) return SV_EHIP;
+    if (sv::launch_ce_stats(ce_gemm(w, rows, h, N, ce_depth(w, h), s), o, st)) return SV_EHIP;
   }
   return sv::launch_ce_join(partial, zlabel, labels, (int)ceil_div(V, bm), N, V, out_loss, out_stats, st)
              ? SV_EHIP : SV_OK;
@@ -377,26 +388,26 @@ int spec_verify_linear_ce_backward(const void* hidden, int64_t hidden_stride, co
   char* ws = (char*)workspace;
   const int bf16 = dtype == SV_BF16;
   const size_t es = size_of(dtype);
-  uint16_t* dz = (uint16_t*)(ws + b.dz);
+  void* dz = ws + b.dz;
   float* acc = (float*)(ws + b.acc);
   Operand h, w;
-  if (ce_operand(hidden, hidden_stride, 0, N, s, (uint16_t*)(ws + b.hidden), st, &h)) return SV_EHIP;
+  if (ce_operand(hidden, hidden_stride, 0, N, s, ws + b.hidden, st, &h)) return SV_EHIP;
   const int mat_vec = aligned(out_grad_weight, 4 * es) && grad_weight_stride % 4 == 0;
   for (int64_t v0 = 0; v0 < V; v0 += b.piece) {
     const int64_t rows = V - v0 < b.piece ? V - v0 : b.piece;
-    const int64_t ldz = round_up(rows, sv::CE_BK);
-    if (ce_operand(weight, weight_stride, v0, rows, s, (uint16_t*)(ws + b.weight), st, &w)) return SV_EHIP;
+    const int64_t ldz = round_up(rows, s.depth());
+    if (ce_operand(weight, weight_stride, v0, rows, s, ws + b.weight, st, &w)) return SV_EHIP;
     const sv::CeDzOut o{labels, stats, grad_loss, (int)v0, V, dz, ldz, N * ldz};
-    if (sv::launch_ce_dz(ce_gemm(w, rows, h, N, ce_depth(w, h), s.planes), o, st)) return SV_EHIP;
+    if (sv::launch_ce_dz(ce_gemm(w, rows, h, N, ce_depth(w, h), s), o, st)) return SV_EHIP;
     const Operand z{dz, ldz, N * ldz, ldz};
     if (out_grad_hidden) {
-      sv::CeGemm g = ce_gemm(w, D, z, N, rows, s.planes);
+      sv::CeGemm g = ce_gemm(w, D, z, N, rows, s);
       g.splits = b.splits;
       const sv::CeAccOut ao{acc, b.acc_ld, N * b.acc_ld, v0 > 0};
       if (sv::launch_ce_acc(g, ao, st)) return SV_EHIP;
     }
     if (out_grad_weight) {
-      const sv::CeGemm g = ce_gemm(h, D, z, rows, N, s.planes);
+      const sv::CeGemm g = ce_gemm(h, D, z, rows, N, s);
       const sv::CeMatOut mo{(char*)out_grad_weight + v0 * grad_weight_stride * es, grad_weight_stride, bf16,
                             mat_vec};
       if (sv::launch_ce_mat(g, mo, st)) return SV_EHIP;
