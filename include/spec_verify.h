@@ -385,9 +385,10 @@ int spec_verify_distill_backward(const void* logits, int64_t logits_stride, sv_d
  *   gradient.
  *   out_loss  [N] float; out_stats [N][2] float: the row's largest logit m, and
  *             log sum_v exp(z_nv - m), also for the rows left out.
- * bfloat16 products are exact and summed in float32. float32 operands are taken as
- * three bfloat16 parts each, whose products down to 2^-24 of the largest are
- * summed in float32.
+ * bfloat16 products are exact and summed in float32. float32 products are made by the
+ * float32 matrix instructions for up to 384 states; for more, operands are taken as
+ * three bfloat16 parts each, whose products down to 2^-24 of the largest are summed
+ * in float32.
  * Inputs are finite; NaN or infinities make the rows (and with them the
  * gradients) they meet NaN.
  * Limits: 1 <= N <= 2^22, 1 <= D <= 2^22, 1 <= V < 2^31 - 1024, and 2^23 tiles of

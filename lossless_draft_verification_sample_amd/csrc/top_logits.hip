@@ -6,16 +6,20 @@
 // the upper half, the complement of its id in the lower, so that keys are
 // unique and the larger key is the larger logit, or the lower id among equals.
 // A workgroup streams its part of a row, four 16-byte groups a thread at a time (a
-// stretch). The first stretch gives a threshold: with one maximum a thread, the k-th
-// largest of the 256 maxima is at most the k-th largest logit, and few logits exceed
-// it while k is well below 256; beyond k = 64 the maxima of the 1024 groups serve. A thread only notes a group with a logit above the threshold;
-// the noted groups are read again, their logits tested and listed as candidates in
-// LDS when 512 have come together, and at the end. (Listing each logit on the spot took more
-// instructions than the sum, because nearly every 64 groups hold one.) When the list
-// grows it is cut to its k largest by a radix selection (8 bits a level, from the top,
-// ending as soon as a bin's border is the cut), and the threshold rises to the k-th
-// value. Ids rise along the stream, so an equal logit that comes later never replaces
-// a listed one and the test is strict. Rising or equal logits only mean more cuts.
+// stretch). The first six stretches (the lead) give a threshold: with one maximum a
+// thread, the k-th largest of the 256 maxima is at most the k-th largest logit, and
+// few logits exceed it while k is well below 256; beyond k = 64 each of a thread's four
+// positions has its own. Groups of the lead whose maximum exceeds the threshold are
+// noted, and in the later stretches those that hold a logit above it; the noted groups are
+// read again, their logits tested and listed as candidates in LDS when 512 have come
+// together, and at the end. (Listing each logit on the spot took more instructions than
+// the sum, because nearly every 64 groups hold one: 190 us for 1152 rows of 151,936 in
+// bfloat16.) When the list grows it is cut to its k largest, by a search of the k-th
+// value that every wave makes for itself, or, from 1024 entries on, by a radix selection
+// (8 bits a level, from the top, ending as soon as a bin's border is the cut), and the
+// threshold rises to the k-th value. Ids rise along the stream, so an equal logit that
+// comes later never replaces a listed one and the test is strict. Rising or equal logits
+// only mean more cuts.
 //
 // Bound: the read of the row. Rows are split over `parts` workgroups when there
 // are few of them; the second kernel joins their lists and sums.
@@ -27,11 +31,14 @@ namespace sv {
 namespace {
 
 constexpr int TOP_NOTES = 1536;
+constexpr int TOP_LEAD = 6;                              // stretches of the lead ...
+constexpr int TOP_LEAD_K = 512;                          // ... for k up to here; else one
 constexpr int TOP_FEW = 64;                              // k up to here: maxima of threads, else of groups
 constexpr int TOP_AHEAD = 4;                             // groups a thread in a stretch
 constexpr int TOP_STRETCH = TOP_AHEAD * TOP_THREADS;     // groups; most that one can note
 
 static_assert(TOP_THREADS == 256, "one bin of a digit a thread");
+static_assert(TOP_LEAD * TOP_STRETCH * 4 <= TOP_CAP * 8, "the lead's maxima take the list's place");
 static_assert(TOP_NOTES >= TOP_STRETCH + TOP_THREADS, "a stretch's notes next to those waiting");
 
 struct TopLds {
@@ -310,28 +317,100 @@ __global__ __launch_bounds__(TOP_THREADS, 5) void top_scan_kernel(TopArgs a) {
       nxt[i] = j < v1 ? row.vec(j) : (vu32x4)(lowest);
     }
   };
+  // The lead: only the sum, the groups' maxima (kept in the list's place) and, per
+  // thread and position in a stretch, the maximum over the lead's stretches.
+  uint32_t* maxima = (uint32_t*)L.buf;
+  const int lead = v0 + (a.K <= TOP_LEAD_K ? TOP_LEAD : 1) * TOP_STRETCH;
+  float best[TOP_AHEAD];
+#pragma unroll
+  for (int i = 0; i < TOP_AHEAD; ++i) best[i] = -INFINITY;
   fetch(v0);
-  if (part == 0 && row.head) singles(row.head, 0);
-  for (int b = v0; b < v1; b += TOP_STRETCH) {
+  int b = v0;
+  for (int at = tid; b < v1 && b < lead; b += TOP_STRETCH, at += TOP_STRETCH) {
 #pragma unroll
     for (int i = 0; i < TOP_AHEAD; ++i) cur[i] = nxt[i];
     fetch(b + TOP_STRETCH);
-    if (b == v0) {   // the notes are not in use yet: room for the maxima
-      float vm = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < TOP_AHEAD; ++i) {
-        float z[EPV];
-        unpack(cur[i], z);
-        const float zm = Running::largest(z);
-        if (a.K > TOP_FEW) L.noted[i * TOP_THREADS + tid] = f32_key(zm);
-        vm = fmaxf(vm, zm);
-      }
-      if (a.K <= TOP_FEW) L.noted[tid] = f32_key(vm);
-      __syncthreads();
-      if (a.K <= TOP_FEW) tau = threshold<TOP_THREADS>(L.noted, a.K, BF16);
-      else tau = threshold<TOP_STRETCH>(L.noted, a.K, BF16);
-      __syncthreads();
+    for (int i = 0; i < TOP_AHEAD; ++i) {
+      float z[EPV];
+      unpack(cur[i], z);
+      const float vm = Running::largest(z);
+      maxima[at + i * TOP_THREADS] = f32_key(vm);
+      best[i] = fmaxf(best[i], vm);
+      run.add(z, vm, a.c);
     }
+  }
+  if (v0 < v1) {
+    const bool few = a.K <= TOP_FEW;
+    if (few) {
+      L.noted[tid] = f32_key(Running::largest(best));
+    } else {
+#pragma unroll
+      for (int i = 0; i < TOP_AHEAD; ++i) L.noted[i * TOP_THREADS + tid] = f32_key(best[i]);
+    }
+    __syncthreads();
+    tau = few ? threshold<TOP_THREADS>(L.noted, a.K, BF16) : threshold<TOP_STRETCH>(L.noted, a.K, BF16);
+    __syncthreads();
+    const uint32_t key = f32_key(tau);
+    for (int at = tid, j = v0 + tid; j - tid < b; j += TOP_THREADS, at += TOP_THREADS)
+      if (maxima[at] > key) {   // this thread's own
+        const int n = atomicAdd(&L.notes[note_slot], 1);
+        if (n < TOP_NOTES) L.noted[n] = (uint32_t)j;
+      }
+    noted = close(L.notes, note_slot);
+    if (noted > TOP_NOTES) {   // many equal logits: the lead once more, a stretch at a time
+      noted = 0;
+      b = v0;
+      fetch(v0);
+    }
+  }
+  const int summed = min(lead, v1);
+  if (part == 0 && row.head) singles(row.head, 0);
+  while (true) {
+    if (noted > TOP_NOTES - TOP_STRETCH || (b >= v1 && noted > 0)) {
+      // the noted groups, one a thread at a time
+      auto load = [&](int n, int* at) {
+        *at = n < noted ? (int)L.noted[n] : -1;
+        return *at >= 0 ? row.vec(*at) : (vu32x4)(lowest);
+      };
+      // Notes come in no order, so that after a cut among them a logit equal to the
+      // k-th may still have a lower id: until all are listed, equal ones pass.
+      const float strict = tau;
+      float higher = -INFINITY;
+      int at, at2;
+      vu32x4 w = load(tid, &at);
+      for (int k = 0; k < noted; k += TOP_THREADS) {
+        const vu32x4 w2 = load(k + TOP_THREADS + tid, &at2);
+        if (listed > TOP_CAP - TOP_STEP) {   // more than K: room for all of it
+          higher = fmaxf(higher, cut(L, listed, a.K, BF16, a.V));
+          listed = a.K;
+          tau = fmaxf(strict, below(higher));
+        }
+        float z[EPV];
+        unpack(w, z);
+        offer(z, row.head + at * EPV);
+        w = w2;
+        at = at2;
+      }
+      noted = 0;
+      tau = fmaxf(strict, higher);
+      // a higher threshold for what follows, or room for the row's last elements
+      if (listed > a.K && (b < v1 ? listed > 2 * a.K : listed > TOP_CAP - EPV)) {
+        float t;
+        if (listed <= TOP_THIN) {
+          listed = thin(L, listed, a.K, BF16, &t);
+        } else {
+          t = cut(L, listed, a.K, BF16, a.V);
+          listed = a.K;
+        }
+        tau = fmaxf(tau, t);
+      }
+    }
+    if (b >= v1) break;
+#pragma unroll
+    for (int i = 0; i < TOP_AHEAD; ++i) cur[i] = nxt[i];
+    fetch(b + TOP_STRETCH);
+    const bool again = b < summed;
 #pragma unroll
     for (int i = 0; i < TOP_AHEAD; ++i) {
       float z[EPV];
@@ -339,47 +418,10 @@ __global__ __launch_bounds__(TOP_THREADS, 5) void top_scan_kernel(TopArgs a) {
       const float vm = Running::largest(z);
       if (vm > tau)
         L.noted[noted + atomicAdd(&L.notes[note_slot], 1)] = (uint32_t)(b + i * TOP_THREADS + tid);
-      run.add(z, vm, a.c);
+      if (!again) run.add(z, vm, a.c);
     }
     noted += close(L.notes, note_slot);
-    if (noted <= TOP_NOTES - TOP_STRETCH && b + TOP_STRETCH < v1) continue;
-    // the noted groups, one a thread at a time
-    auto load = [&](int n, int* at) {
-      *at = n < noted ? (int)L.noted[n] : -1;
-      return *at >= 0 ? row.vec(*at) : (vu32x4)(lowest);
-    };
-    // Notes come in no order, so that after a cut among them a logit equal to the
-    // k-th may still have a lower id: until all are listed, equal ones pass.
-    const float strict = tau;
-    float higher = -INFINITY;
-    int at, at2;
-    vu32x4 w = load(tid, &at);
-    for (int k = 0; k < noted; k += TOP_THREADS) {
-      const vu32x4 w2 = load(k + TOP_THREADS + tid, &at2);
-      if (listed > TOP_CAP - TOP_STEP) {   // more than K: room for all of it
-        higher = fmaxf(higher, cut(L, listed, a.K, BF16, a.V));
-        listed = a.K;
-        tau = fmaxf(strict, below(higher));
-      }
-      float z[EPV];
-      unpack(w, z);
-      offer(z, row.head + at * EPV);
-      w = w2;
-      at = at2;
-    }
-    noted = 0;
-    tau = fmaxf(strict, higher);
-    // a higher threshold for what follows, or room for the row's last elements
-    if (listed > a.K && (b + TOP_STRETCH < v1 ? listed > 2 * a.K : listed > TOP_CAP - EPV)) {
-      float t;
-      if (listed <= TOP_THIN) {
-        listed = thin(L, listed, a.K, BF16, &t);
-      } else {
-        t = cut(L, listed, a.K, BF16, a.V);
-        listed = a.K;
-      }
-      tau = fmaxf(tau, t);
-    }
+    b += TOP_STRETCH;
   }
   if (part == a.parts - 1 && row.tail()) singles(row.tail(), row.tail0());
 
