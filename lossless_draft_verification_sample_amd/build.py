@@ -2,7 +2,8 @@
 
     python -m lossless_draft_verification_sample_amd.build [-v]
 
-- libspecverify.so: the verifier behind include/spec_verify.h.
+- libspecverify.so: the verifier and the drafter's training calls behind
+  include/spec_verify.h.
 - libspecverify_bench.so: the same kernels and entry points, plus HIP event
   pairs around every launch and the two calls that read them
   (csrc/sv_bench_timing.h). Only bench.py loads it, for per-kernel times.
@@ -25,7 +26,10 @@ OBJ_DIR = os.path.join(ROOT, "_build")
 LIB_NAME = "libspecverify.so"
 BENCH_LIB_NAME = "libspecverify_bench.so"
 KERNEL_SOURCES = ["row_stats.hip", "verify.hip", "overlap.hip", "greedy.hip", "commit.hip",
-                  "top_logits.hip", "distill.hip", "linear_ce.hip", "train_api.cpp"]
+                  # the drafter's training calls; in a folder of their own, so that the digest
+                  # of the verification path's sources stays what its counters were taken on
+                  "training/top_logits.hip", "training/distill.hip", "training/linear_ce.hip",
+                  "training/train_api.cpp"]
 API_SOURCE = "api.cpp"
 # HBM read-bandwidth calibration (bench.py --read-ceiling); not on the path
 CALIB_LIB_NAME = "libsvcalib.so"

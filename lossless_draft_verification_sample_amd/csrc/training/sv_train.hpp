@@ -6,7 +6,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "sv_common.hpp"
+#include "../sv_common.hpp"
 
 namespace sv {
 

@@ -6,7 +6,7 @@
 #include <math.h>
 #include <stdint.h>
 
-#include "../../include/spec_verify.h"
+#include "../../../include/spec_verify.h"
 #include "sv_train.hpp"
 
 static_assert(SV_MAX_TOP == sv::TOP_MAX_K && SV_MAX_TOP == sv::DIS_MAX_K, "kept logits per row");
