@@ -339,6 +339,9 @@ def spec_verify_commit(tokens, num_accepted, kv_len, slots=None, gamma_b=None, o
 # ------------------------------------------------------- training the drafter
 
 
+_INT32_MAX = 2 ** 31 - 1
+
+
 def _matrix(t, name, device=None, dtype=None, cols=None):
     """(pointer, row stride) of a tensor whose last dimension is consecutive and
     whose leading dimensions are rows at one stride."""
@@ -354,6 +357,8 @@ def _matrix(t, name, device=None, dtype=None, cols=None):
     width = shape[-1]
     if cols is not None and width != cols:
         raise ValueError(f"{name} must have rows of {cols}, got {tuple(shape)}")
+    if width > _INT32_MAX or t.numel() // width > _INT32_MAX:
+        raise ValueError(f"{name} must have at most {_INT32_MAX} rows and columns, got {tuple(shape)}")
     if t.is_contiguous():
         return t.data_ptr(), width
     steps = t.stride()
@@ -411,6 +416,8 @@ def _on(device, stream):
     import contextlib
     with torch.cuda.device(device):
         handle, strm = _stream(stream)
+    if strm.device != device:
+        raise ValueError(f"the stream is one of {strm.device}, the tensors are on {device}")
     ctx = contextlib.ExitStack()
     ctx.enter_context(torch.cuda.device(device))
     ctx.enter_context(torch.cuda.stream(strm))
@@ -451,11 +458,11 @@ def spec_verify_top_logits(logits, k, temperature=1.0, want_lse=True, workspace=
     ptr, stride = _matrix(logits, "logits")
     dt, dev, lead, V = _dtype_code(logits), logits.device, tuple(logits.shape[:-1]), logits.shape[-1]
     R, k = logits.numel() // V, int(k)
+    if not 1 <= k <= SV_MAX_TOP:
+        raise SpecVerifyError(SV_EINVAL, "spec_verify_top_logits")
     ctx, handle = _on(dev, stream)
     with ctx:
         if out is None:
-            if k < 1:
-                raise SpecVerifyError(SV_EINVAL, "spec_verify_top_logits")
             out = TopLogitsOut(
                 torch.empty((*lead, k), dtype=torch.int32, device=dev),
                 torch.empty((*lead, k), dtype=torch.float32, device=dev),
@@ -484,6 +491,8 @@ def _distill_inputs(logits, teacher_ids, teacher_logits, teacher_lse):
     if teacher_ids.dim() < 1 or tuple(teacher_ids.shape[:-1]) != lead:
         raise ValueError(f"teacher_ids must be {lead} rows of kept ids, got {tuple(teacher_ids.shape)}")
     K = int(teacher_ids.shape[-1])
+    if not 1 <= K <= SV_MAX_TOP:
+        raise SpecVerifyError(SV_EINVAL, "spec_verify_distill")
     return (ptr, stride, dt, logits.numel() // V, V,
             _vector(teacher_ids, "teacher_ids", torch.int32, (*lead, K), dev),
             _vector(teacher_logits, "teacher_logits", torch.float32, (*lead, K), dev),

@@ -255,7 +255,7 @@ struct Held {
 
 constexpr int TOP_THREADS = 256;
 constexpr int TOP_STEP = TOP_THREADS * 8;   // most candidates one group a thread can add
-constexpr int TOP_CAP = 3072;               // candidates held in LDS
+constexpr int TOP_CAP = 12 * TOP_THREADS;    // candidates held in LDS
 constexpr int TOP_MAX_K = 1024;
 constexpr int TOP_THIN = 1024;              // candidates that are thinned without a cut
 

@@ -55,9 +55,11 @@ int64_t row_parts(int64_t R, int64_t bytes, int64_t total, int64_t least, int64_
   return p > 1 && bytes - bytes / p >= gain ? p : 1;
 }
 
-// Top logits: a workgroup alone takes 7 bytes a nanosecond and 6 us besides, the join
-// 5 to 8 us. 9 rows of 151,936 in bfloat16: 16 parts 16.3 us, 8 parts 18.1, 4 parts 21.4, one
-// about 50. 331 rows of 50,257 in float32: one part 55.5 us, two 52.8, five 59.
+// Top logits: a workgroup alone takes 8 bytes a nanosecond and 5 us besides, the join
+// 5 to 12 us, more with more kept. 9 rows of 151,936 in bfloat16, 32 kept: 16 parts 16.6
+// us, 8 parts 17.8, 4 parts 19.4; 100 rows, 64 kept: one part 44, four 26, eight 28; 400 rows:
+// one 52, two 45, three 44, four 49. 331 rows of 50,257 in float32, 200 kept: one 48, two and
+// three 46, four 55. 9 rows of 32,000, 32 kept: one 12.9, two 13.5, four 12.9.
 struct TopLayout {
   int parts;
   size_t keys, sums, total;

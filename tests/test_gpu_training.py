@@ -129,6 +129,32 @@ def test_top_logits_orders_and_ties(dtype, R):
         _check_top(t, _host(t), K)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_top_logits_orders_and_ties_of_long_rows(dtype):
+    """Rows that go on long after the threshold's first stretches, one workgroup to a
+    row and several: orders and ties that fill what is noted and listed."""
+    import torch
+    V, rng = 100003, np.random.default_rng(8)
+    ramp = np.linspace(-40, 40, V).astype(np.float32)
+    late = np.arange(V) > 70000
+    z = np.stack([
+        np.full(V, -2.5, np.float32), ramp, ramp[::-1],
+        np.where(late, 3.0, rng.standard_normal(V)).astype(np.float32),      # ties behind the start
+        np.where(late, ramp, 39.0).astype(np.float32),                       # ties first
+        np.where(np.arange(V) % 9 == 0, 5.0, -1.0).astype(np.float32),       # a tie in every group
+        np.where(late, rng.standard_normal(V), -np.inf).astype(np.float32),  # nothing at the start
+    ])
+    t = _dev(z, dtype)
+    wide = t.repeat(100, 1)
+    assert wide.shape[0] > 640   # at 2 workgroups a row and less
+    for K in (1, 64, 65, 512, 513, 1024):
+        few = _check_top(t, _host(t), K)
+        many = _sv().spec_verify_top_logits(wide, K)
+        torch.cuda.synchronize()
+        assert torch.equal(many.ids, few.ids.repeat(100, 1)) and torch.equal(many.values, few.values.repeat(100, 1))
+        assert ((many.lse - few.lse.repeat(100)).abs() <= 2 * _sum_tol(V) + 4 * U * 60).all()
+
+
 def test_top_logits_nan_is_no_candidate():
     rng = np.random.default_rng(6)
     z = (rng.standard_normal((4, 9000)) * 3).astype(np.float32)
@@ -242,12 +268,13 @@ def test_distill(dtype, R, V, K, pad, shift, T, lse, weighted):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("copies", [1, 200])
-def test_distill_edges(dtype, copies):
+@pytest.mark.parametrize("copies,V", [(1, 9001), (200, 9001), (1, 20011), (80, 20011), (12, 82001)])
+def test_distill_edges(dtype, copies, V):
     """Masked tokens, empty slots, repeated ids, rows that leave nothing; copies
-    gives both one workgroup and several to a row."""
+    gives both one workgroup and several to a row, the longer rows are held in registers
+    (the longest in bfloat16)."""
     rng = np.random.default_rng(9)
-    V, K = 9001, 6
+    K = 6
     z = (rng.standard_normal((8, V)) * 3).astype(np.float32)
     low = np.float32(-3.3895313892515355e38)
     ids = rng.integers(0, V, (8, K))
@@ -268,13 +295,12 @@ def test_distill_edges(dtype, copies):
     assert np.all(_host(a.loss)[3 * copies: 4 * copies] == 0) and not b.grad[3 * copies: 4 * copies].any()
 
 
-@pytest.mark.parametrize("copies", [1, 300])
-def test_distill_impossible_tokens(copies):
+@pytest.mark.parametrize("copies,V", [(1, 9001), (300, 9001), (1, 20011), (150, 20011)])
+def test_distill_impossible_tokens(copies, V):
     """A kept token the student rules out: loss +inf, a finite gradient; a row of -inf
     with a filled slot: loss +inf, no gradient; NaN stays in its row."""
     import torch
     rng = np.random.default_rng(10)
-    V = 9001
     z = (rng.standard_normal((4, V)) * 3).astype(np.float32)
     ids = np.array([[5, 6], [5, 6], [5, 6], [5, 6]], np.int32)
     values = np.ones((4, 2), np.float32)
@@ -493,6 +519,61 @@ def test_linear_ce_gradient_against_differences():
         move = eps * max(_host(h if x is w else w).__abs__().max() * np.sqrt(D), 1e-3)
         tol = N * move ** 3 / 3 + 2 * N * 2e-5
         assert abs(slope - want) <= tol, (slope, want, tol)
+
+
+# ---------------------------------------------------------------- offsets beyond 32 bits
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_further_apart_than_32_bits(dtype):
+    """Three rows 2^32 + 24 bytes apart, and gradients that are as far apart."""
+    import torch
+    sv, rng = _sv(), np.random.default_rng(40)
+    dt = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+    step, R, V, K, D = ((1 << 32) + 24) // dt.itemsize, 3, 20003, 40, 72
+
+    def far(near):
+        flat = torch.empty(2 * step + near.shape[1], dtype=dt, device="cuda:0")
+        t = flat.as_strided(near.shape, (step, 1))
+        t.copy_(near)
+        return t
+
+    z, _ = _rows(rng, R, V, dtype)
+    zf = far(z)
+    a, b = sv.spec_verify_top_logits(z, K), sv.spec_verify_top_logits(zf, K)
+    ids, vals = _teacher(rng, _host(z), K)
+    args = (_dev(ids), _dev(vals))
+    c = sv.spec_verify_distill(z, *args, want_grad=True)
+    d = sv.spec_verify_distill(zf, *args, out=sv.DistillOut(
+        torch.empty_like(c.loss), torch.empty_like(c.stats), far(torch.zeros_like(z))))
+    torch.cuda.synchronize()
+    assert torch.equal(a.ids, b.ids) and torch.equal(a.values, b.values)
+    # rows that start elsewhere in a group of 16 bytes are summed in another order
+    assert ((a.lse - b.lse).abs() <= 2 * _sum_tol(V) + 4 * U * a.lse.abs()).all()
+    ref = ot.distill(_host(z), ids, vals)
+    lt, gt = _distill_tol(_host(z), ids, vals, 1.0, ref, dtype, None)
+    assert np.all(np.abs(_host(d.loss) - ref[0]) <= lt) and np.all(np.abs(_host(d.grad) - ref[1]) <= gt)
+    del zf, b, d
+    h, w, y = _head(rng, R, D, 3, dtype)
+    y[:] = [2, 0, 1]
+    hf, wf = far(h), far(w)
+    e = sv.spec_verify_linear_ce(hf, wf, _dev(y))
+    out = sv.LinearCeGrads(far(torch.zeros_like(h)), far(torch.zeros_like(w)))
+    f = sv.spec_verify_linear_ce_backward(hf, wf, _dev(y), e.stats, out=out)
+    torch.cuda.synchronize()
+    loss, gh, gw, zz, dz = ot.linear_ce(_host(h), _host(w), y)
+    tol = _ce_tol(_host(h), _host(w), zz, dz, np.ones(R), loss, dtype)
+    for got, want, t in ((e.loss, loss, tol[0]), (f.hidden, gh, tol[1]), (f.weight, gw, tol[2])):
+        assert np.all(np.abs(_host(got) - want) <= t)
+
+
+def test_more_rows_than_an_int32_are_refused():
+    """2^32 + 5 rows of one column must not pass as five."""
+    import torch
+    t = torch.empty(((1 << 32) + 5, 1), dtype=torch.bfloat16, device="cuda:0")
+    with pytest.raises(ValueError):
+        _sv().spec_verify_top_logits(t, 1)
+    with pytest.raises(ValueError):
+        _sv().spec_verify_linear_ce(t, t[:4], torch.zeros(5, dtype=torch.int32, device="cuda:0"))
 
 
 # ---------------------------------------------------------------- together, streams, graphs
