@@ -411,8 +411,9 @@ _CURRENT = _Current()
 def _on(device, stream):
     """(context that makes the device and the call's stream current, stream handle)."""
     torch = _torch()
+    # torch's own handle of the current stream: a Stream object around it costs 2 us a call
     if stream is None and torch.cuda.current_device() == device.index:
-        return _CURRENT, torch.cuda.current_stream(device).cuda_stream
+        return _CURRENT, torch._C._cuda_getCurrentRawStream(device.index)
     import contextlib
     with torch.cuda.device(device):
         handle, strm = _stream(stream)
@@ -463,17 +464,19 @@ def spec_verify_top_logits(logits, k, temperature=1.0, want_lse=True, workspace=
     ctx, handle = _on(dev, stream)
     with ctx:
         if out is None:
-            out = TopLogitsOut(
-                torch.empty((*lead, k), dtype=torch.int32, device=dev),
-                torch.empty((*lead, k), dtype=torch.float32, device=dev),
-                torch.empty(lead, dtype=torch.float32, device=dev) if want_lse else None)
+            ids = torch.empty((*lead, k), dtype=torch.int32, device=dev)
+            values = torch.empty((*lead, k), dtype=torch.float32, device=dev)
+            lse = values.new_empty(lead) if want_lse else None
+            out = TopLogitsOut(ids, values, lse)
+            outs = ids.data_ptr(), values.data_ptr(), lse.data_ptr() if want_lse else None
+        else:
+            outs = (_vector(out.ids, "out.ids", torch.int32, (*lead, k), dev),
+                    _vector(out.values, "out.values", torch.float32, (*lead, k), dev),
+                    _vector(out.lse, "out.lse", torch.float32, lead, dev))
         ws, ws_bytes, keep = _space(
             workspace, lib.spec_verify_top_logits_workspace_bytes(R, V, k, dt), dev)
         rc = lib.spec_verify_top_logits(
-            ptr, stride, dt, R, V, k, float(temperature),
-            _vector(out.ids, "out.ids", torch.int32, (*lead, k), dev),
-            _vector(out.values, "out.values", torch.float32, (*lead, k), dev),
-            _vector(out.lse, "out.lse", torch.float32, lead, dev), ws, ws_bytes, handle)
+            ptr, stride, dt, R, V, k, float(temperature), *outs, ws, ws_bytes, handle)
     del keep
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_verify_top_logits")
@@ -488,6 +491,8 @@ def _distill_inputs(logits, teacher_ids, teacher_logits, teacher_lse):
     torch = _torch()
     ptr, stride = _matrix(logits, "logits")
     dt, dev, lead, V = _dtype_code(logits), logits.device, tuple(logits.shape[:-1]), logits.shape[-1]
+    if teacher_ids is None or teacher_logits is None:
+        raise ValueError("teacher_ids and teacher_logits must be device tensors")
     if teacher_ids.dim() < 1 or tuple(teacher_ids.shape[:-1]) != lead:
         raise ValueError(f"teacher_ids must be {lead} rows of kept ids, got {tuple(teacher_ids.shape)}")
     K = int(teacher_ids.shape[-1])
@@ -499,11 +504,23 @@ def _distill_inputs(logits, teacher_ids, teacher_logits, teacher_lse):
             _vector(teacher_lse, "teacher_lse", torch.float32, lead, dev), K), dev, lead
 
 
+def _loss_out(out, like, lead, dev):
+    """Loss and statistics of rows `lead`, new ones (float32, as `like`) when out is
+    None, and their pointers."""
+    if out is None:
+        loss, stats = like.new_empty(lead), like.new_empty((*lead, 2))
+        return loss, stats, (loss.data_ptr(), stats.data_ptr())
+    f32 = _torch().float32
+    return out.loss, out.stats, (_vector(out.loss, "out.loss", f32, lead, dev),
+                                 _vector(out.stats, "out.stats", f32, (*lead, 2), dev))
+
+
 def _grad_out(t, like, name):
     """A gradient's tensor, its pointer and row stride; a new one when None."""
     if t is None:
-        t = _torch().empty(like.shape, dtype=like.dtype, device=like.device)
-    elif tuple(t.shape) != tuple(like.shape):
+        t = _torch().empty_like(like, memory_format=_torch().contiguous_format)
+        return t, t.data_ptr(), like.shape[-1]
+    if tuple(t.shape) != tuple(like.shape):
         raise ValueError(f"{name} must have shape {tuple(like.shape)}, got {tuple(t.shape)}")
     return (t, *_matrix(t, name, like.device, like.dtype))
 
@@ -527,25 +544,20 @@ def spec_verify_distill(logits, teacher_ids, teacher_logits, temperature=1.0, te
     args, dev, lead = _distill_inputs(logits, teacher_ids, teacher_logits, teacher_lse)
     ctx, handle = _on(dev, stream)
     with ctx:
-        if out is None:
-            out = DistillOut(torch.empty(lead, dtype=torch.float32, device=dev),
-                             torch.empty((*lead, 2), dtype=torch.float32, device=dev), None)
-        grad, gptr, gstride = out.grad, None, 0
+        grad, gptr, gstride = out and out.grad, None, 0
+        loss, stats, outs = _loss_out(out, teacher_logits, lead, dev)
         if want_grad or grad is not None:
             grad, gptr, gstride = _grad_out(grad, logits, "out.grad")
-            out = out._replace(grad=grad)
         ws, ws_bytes, keep = _space(
             workspace, lib.spec_verify_distill_workspace_bytes(args[3], args[4], args[2]), dev)
         rc = lib.spec_verify_distill(
             *args, float(temperature),
-            _vector(row_weight, "row_weight", torch.float32, lead, dev),
-            _vector(out.loss, "out.loss", torch.float32, lead, dev),
-            _vector(out.stats, "out.stats", torch.float32, (*lead, 2), dev), gptr, gstride,
+            _vector(row_weight, "row_weight", torch.float32, lead, dev), *outs, gptr, gstride,
             ws, ws_bytes, handle)
     del keep
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_verify_distill")
-    return out
+    return DistillOut(loss, stats, grad)
 
 
 def spec_verify_distill_backward(logits, teacher_ids, teacher_logits, stats, grad_loss=None,
@@ -609,8 +621,8 @@ def spec_verify_linear_ce(hidden, weight, labels, workspace=None, out=None, stre
     ctx, handle = _on(dev, stream)
     with ctx:
         if out is None:
-            out = LinearCeOut(torch.empty(lead, dtype=torch.float32, device=dev),
-                              torch.empty((*lead, 2), dtype=torch.float32, device=dev))
+            loss = torch.empty(lead, dtype=torch.float32, device=dev)
+            out = LinearCeOut(loss, loss.new_empty((*lead, 2)))
         ws, ws_bytes, keep = _space(
             workspace, lib.spec_verify_linear_ce_workspace_bytes(N, D, V, args[4]), dev)
         rc = lib.spec_verify_linear_ce(

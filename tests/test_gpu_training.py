@@ -700,6 +700,8 @@ def test_binding_refusals_on_device_tensors():
         (sv.SpecVerifyError, lambda: sv.spec_verify_top_logits(z, 0)),
         (sv.SpecVerifyError, lambda: sv.spec_verify_top_logits(z, 3, temperature=0.0)),
         (ValueError, lambda: sv.spec_verify_distill(z, ids[:3], vals)),
+        (ValueError, lambda: sv.spec_verify_distill(z, ids, None)),
+        (ValueError, lambda: sv.spec_verify_distill(z, None, vals)),
         (ValueError, lambda: sv.spec_verify_distill(z, ids, vals[:, :2])),
         (TypeError, lambda: sv.spec_verify_distill(z, ids.long(), vals)),
         (ValueError, lambda: sv.spec_verify_distill(z, ids, vals, row_weight=vals)),
