@@ -392,8 +392,8 @@ int spec_verify_distill_backward(const void* logits, int64_t logits_stride, sv_d
  * Inputs are finite; NaN or infinities make the rows (and with them the
  * gradients) they meet NaN.
  * Limits: 1 <= N <= 2^22, 1 <= D <= 2^22, 1 <= V < 2^31 - 1024, and 2^23 tiles of
- * 256 x 256 in N x V and N x D (64 x 32 up to 32 rows, 128 x 64 up to 128); SV_ESIZE
- * beyond. bfloat16 matrices with D a multiple of 8, rows on 16 bytes and strides of at
+ * 256 x 256 in N x V and N x D (64 x 32 up to 32 rows, 128 x 64 up to 128, 256 x 128 in
+ * float32); SV_ESIZE beyond. bfloat16 matrices with D a multiple of 8, rows on 16 bytes and strides of at
  * most 2^22 are read in place, others are copied into the workspace first. */
 size_t spec_verify_linear_ce_workspace_bytes(int32_t N, int32_t D, int32_t V, sv_dtype dtype);
 int spec_verify_linear_ce(const void* hidden, int64_t hidden_stride, const void* weight,

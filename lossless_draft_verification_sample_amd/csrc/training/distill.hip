@@ -176,7 +176,7 @@ __device__ void row_grad(const DistillArgs& a, DisLds& L, const Row<Elem>& row, 
     if (id >= lo && id < hi) L.zid[k] = to_f32(row.p + id);
   }
   __syncthreads();
-  // the output row has its own alignment: whole groups where both agree
+  // the output row has its own alignment; a store takes any
   const bool same = (((uintptr_t)out ^ (uintptr_t)row.p) & 15u) == 0;
   auto single = [&](int v) {
     float z[1] = {to_f32(row.p + v)};
@@ -190,12 +190,9 @@ __device__ void row_grad(const DistillArgs& a, DisLds& L, const Row<Elem>& row, 
     unpack(row.vec(j), z);
     d.apply(z, a.c);
     Elem* o = out + row.head + (int64_t)j * EPV;
-    if (same) {
-      __builtin_nontemporal_store(pack(z), (vu32x4*)o);
-    } else {
-#pragma unroll
-      for (int i = 0; i < EPV; ++i) put(o + i, z[i]);
-    }
+    const vu32x4 w = pack(z);
+    if (same) __builtin_nontemporal_store(w, (vu32x4*)o);
+    else __builtin_memcpy(o, &w, 16);
   }
   __syncthreads();   // orders the dense writes before the slots'
   if (d.none) return;
@@ -405,12 +402,9 @@ __global__ __launch_bounds__(HOLD_THREADS, 2 * HOLD_PER_CU[SIZE]) void distill_h
         d.apply(z, a.c);
         if (j < row.nvec) {
           Elem* o = out + row.head + (int64_t)j * EPV;
-          if (same) {
-            __builtin_nontemporal_store(pack(z), (vu32x4*)o);
-          } else {
-#pragma unroll
-            for (int e = 0; e < EPV; ++e) put(o + e, z[e]);
-          }
+          const vu32x4 g = pack(z);
+          if (same) __builtin_nontemporal_store(g, (vu32x4*)o);
+          else __builtin_memcpy(o, &g, 16);
         }
       }
       if (more && i * HOLD_THREADS < after.nvec) h.load_group(after, i);
@@ -453,8 +447,10 @@ int distill(const DistillArgs& a, bool backward, hipStream_t st) {
       hipLaunchKernelGGL((distill_hold_kernel<Elem, 0>), grid, held, 0, st, a);
     else if (a.hold == 1)
       hipLaunchKernelGGL((distill_hold_kernel<Elem, 1>), grid, held, 0, st, a);
-    else
+    else if (a.hold == 2)
       hipLaunchKernelGGL((distill_hold_kernel<Elem, 2>), grid, held, 0, st, a);
+    else
+      hipLaunchKernelGGL((distill_hold_kernel<Elem, 3>), grid, held, 0, st, a);
   } else if (!backward && a.parts == 1) {
     hipLaunchKernelGGL(distill_row_kernel<Elem>, rows, block, 0, st, a);
   } else {

@@ -15,9 +15,9 @@
 //         the read of W, 4 bytes an element;
 //   many  split into three bfloat16 parts x = x1 + x2 + x3 (each the rounding of what
 //         the parts before leave: 24 bits in all); a product sums the six part products
-//         down to 2^-24 of the largest, small ones first. Six bfloat16 products take
-//         6/2500 of a second per PFLOP against 1/157 for the float32 instructions, but
-//         the parts have to be written first, 6 bytes an element.
+//         down to 2^-24 of the largest. Six bfloat16 products take 6/2500 of a second
+//         per PFLOP against 1/157 for the float32 instructions, but the parts have to be
+//         written first, 6 bytes an element.
 
 #include "sv_train.hpp"
 
@@ -42,13 +42,6 @@ constexpr int RSRC_WORD3 = 0x00027000;
 // A tile's own offsets stay below it: 255 rows of at most 2^22 bfloat16, or 127 of
 // as many float elements.
 constexpr uint32_t BEYOND = 0x80000000u;
-
-// Part products of float32 operands, in the order in which they are summed.
-__device__ __forceinline__ void part_pair(int i, int* pa, int* pb) {
-  // (3,1) (1,3) (2,2) (2,1) (1,2) (1,1)
-  *pa = (0x001102 >> (4 * i)) & 15;
-  *pb = (0x010120 >> (4 * i)) & 15;
-}
 
 template <int BM, int BN, int WM, int WN>
 struct Tile {
@@ -107,11 +100,11 @@ __device__ __forceinline__ void copy_to_lds(uint64_t base, uint32_t byte_off, ui
 }
 
 // One operand of a tile, of bfloat16 (uint16_t) or float elements: how ROWS rows by one
-// step of depth (CE_LINE bytes of a row) get from memory into LDS, and its fragments
+// step of depth (LINE bytes of a row) get from memory into LDS, and its fragments
 // from there: per lane 16 bytes of depth of one row.
-//   plain       memory [row][k]: LDS row of 8 groups of 16 bytes; slot s of row r
-//               holds group s ^ (r & 7), so that a fragment's 16 rows spread over
-//               the banks.
+//   plain       memory [row][k]: LDS row of 8 (LINE 128) or 4 (64) groups of 16 bytes;
+//               slot s of row r holds group s ^ spread(r), so that a fragment's 16
+//               rows spread over the banks.
 //   transposed  memory [k][row]: LDS as in memory. bfloat16: a fragment is made by the
 //               transposing LDS read, which gives lane i of 16 the i-th of 16 columns of
 //               4 consecutive k; blocks of 16 columns (32 bytes) are permuted by
@@ -120,25 +113,27 @@ __device__ __forceinline__ void copy_to_lds(uint64_t base, uint32_t byte_off, ui
 //               each; blocks of 16 columns (64 bytes) are permuted by bits 2 and 3 of k.
 // Groups behind the depth, or (transposed) behind the last row, are loaded from
 // beyond the buffer resource's range, which reads as zero.
-template <typename E, bool TRANS, int ROWS, int FRAGS, int LOADS, int THREADS>
+template <typename E, bool TRANS, int ROWS, int LINE, int FRAGS, int LOADS, int THREADS>
 struct Side {
   static constexpr int ES = sizeof(E);
   static constexpr int EPG = 16 / ES;                           // elements of a group
-  static constexpr int DEPTH = CE_LINE / ES;                    // elements of a step
-  static constexpr int GROUPS = TRANS ? ROWS / EPG : 8;         // of a line of LDS
+  static constexpr int DEPTH = LINE / ES;                       // elements of a step
+  static constexpr int PARTS = LINE / 64;                       // fragments of a row's step
+  static constexpr int GROUPS = TRANS ? ROWS / EPG : LINE / 16; // of a line of LDS
   static constexpr int BLOCK = 16 / EPG;                        // groups of 16 columns
   static constexpr int READS = !TRANS ? 1 : ES == 2 ? 2 : 4;    // LDS reads a fragment
   typedef typename Frag<E>::type F;
   uint32_t off[LOADS];              // of this thread's loads from the tile's first row, bytes
-  uint32_t at[TRANS ? FRAGS : 2];   // in LDS, bytes. transposed: per fragment; plain: per half of the depth
+  uint32_t at[TRANS ? FRAGS : PARTS];   // in LDS, bytes. transposed: per fragment; plain: per part of the depth
 
   static __device__ __forceinline__ int line(int i, int tid) { return (i * THREADS + tid) / GROUPS; }
   static __device__ __forceinline__ int twist(int k) {
     return (ES == 2 ? (k & 3) | ((k >> 3) & 1) << 2 : (k >> 2) & 3) & (GROUPS / BLOCK - 1);
   }
+  static __device__ __forceinline__ int spread(int row) { return LINE == 128 ? row & 7 : (row >> 1) & 3; }
   static __device__ __forceinline__ int group(int i, int tid) {
     const int slot = (i * THREADS + tid) % GROUPS, l = line(i, tid);
-    if (!TRANS) return slot ^ (l & 7);
+    if (!TRANS) return slot ^ spread(l);
     return (slot / BLOCK ^ twist(l)) * BLOCK + slot % BLOCK;
   }
 
@@ -160,8 +155,8 @@ struct Side {
         at[i] = (uint32_t)(k * ROWS + ((wave_row / 16 + i) ^ f) * 16 + in) * ES;
     } else {
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk)
-        at[kk] = (uint32_t)((wave_row + fr) * CE_LINE + ((kk * 4 + fk) ^ (fr & 7)) * 16);
+      for (int kk = 0; kk < PARTS; ++kk)
+        at[kk] = (uint32_t)((wave_row + fr) * LINE + ((kk * 4 + fk) ^ spread(fr)) * 16);
     }
   }
   // Loads the tile's depth k.. of the operand that begins at p (the tile's first
@@ -183,7 +178,7 @@ struct Side {
   __device__ __forceinline__ F frag(const char* lds, int i, int kk) const {
 #if defined(__HIP_DEVICE_COMPILE__)
     if constexpr (!TRANS) {
-      return *(const F*)(lds + at[kk] + i * 16 * CE_LINE);
+      return *(const F*)(lds + at[kk] + i * 16 * LINE);
     } else if constexpr (ES == 2) {
       const char* p = lds + at[i] + kk * 32 * ROWS * ES;
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
@@ -225,32 +220,25 @@ __global__ __launch_bounds__(WM* WN* WAVE, WM* WN == 8 ? 2 : 1) void ce_gemm_ker
   tile_of(blockIdx.x, tiles_m, tiles_n, &tm, &tn);
   const int m0 = tm * BM, n0 = tn * BN;
 
-  Side<E, Epi::TRANS_A, BM, T::MI, T::LA, T::THREADS> sa;
-  Side<E, Epi::TRANS_B, BN, T::NI, T::LB, T::THREADS> sb;
+  Side<E, Epi::TRANS_A, BM, CE_LINE, T::MI, T::LA, T::THREADS> sa;
+  Side<E, Epi::TRANS_B, BN, CE_LINE, T::NI, T::LB, T::THREADS> sb;
   sa.init(m0, g.M, g.lda, wm * T::TM, lane);
   sb.init(n0, g.N, g.ldb, wn * T::TN, lane);
   const E* pa = (const E*)g.A + (Epi::TRANS_A ? (int64_t)m0 : m0 * g.lda);
   const E* pb = (const E*)g.B + (Epi::TRANS_B ? (int64_t)n0 : n0 * g.ldb);
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(lds_void*)lds);
 
-  // steps of this split; next_*: what is to be loaded next
+  // steps of this split; next_k: what is to be loaded next
   constexpr int DEPTH = decltype(sa)::DEPTH;
-  const int steps_k = (g.K + DEPTH - 1) / DEPTH;
-  const int total = steps_k * g.parts;
+  const int total = (g.K + DEPTH - 1) / DEPTH;
   const int per = (total + g.splits - 1) / g.splits;
   const int first = min(total, (int)blockIdx.y * per), last = min(total, first + per);
-  int next_pair = first / steps_k, next_k = (first - next_pair * steps_k) * DEPTH;
+  int next_k = first * DEPTH;
   auto issue = [&](int stage) {
-    int ia = 0, ib = 0;
-    if (g.parts > 1) part_pair(next_pair, &ia, &ib);
     const uint32_t la = lds0 + stage * T::STAGE + wave * WAVE * 16;
-    sa.load(pa + ia * g.plane_a, g.lda, next_k, g.K, la, wave);
-    sb.load(pb + ib * g.plane_b, g.ldb, next_k, g.K, la + BM * CE_LINE, wave);
+    sa.load(pa, g.lda, next_k, g.K, la, wave);
+    sb.load(pb, g.ldb, next_k, g.K, la + BM * CE_LINE, wave);
     next_k += DEPTH;
-    if (next_k >= g.K) {
-      next_k = 0;
-      ++next_pair;
-    }
   };
 
   f32x4 acc[T::MI][T::NI];
@@ -301,6 +289,107 @@ __global__ __launch_bounds__(WM* WN* WAVE, WM* WN == 8 ? 2 : 1) void ce_gemm_ker
         }
       }
     }
+  };
+  if (first < last) issue(0);
+  int s = first;
+  for (; s + 1 < last; s += 2) {
+    step(s, 0);
+    step(s + 1, 1);
+  }
+  if (s < last) step(s, 0);
+  __syncthreads();
+  Epi::template run<T>(ea, g, acc, m0 + wm * T::TM, n0 + wn * T::TN, tm, wm, wn, lane, lds);
+}
+
+// float32 operands in three bfloat16 parts: a step takes 32 of depth of all six, so that
+// 96 matrix instructions share 24 fragments (one pair of parts at a time, over the whole
+// depth, they share 12 each, and LDS bounds it). Parts are numbered from the largest; the
+// order within a step is by B's part, so that the first products need few fragments.
+// A step of 512 states of 1,024 over 32,000 tokens takes 773 us, one pair at a time 882.
+// The lower tile is for dh and dW of up to 128 columns (3,000 states of 64, 32,000 tokens:
+// 1,150 us, in the higher one 1,911).
+template <int BM, int BN, int WM, int WN, typename Epi>
+__global__ __launch_bounds__(WM* WN* WAVE, 2) void ce_split_kernel(CeGemm g, int tiles_m, int tiles_n,
+                                                                   typename Epi::Args ea) {
+  constexpr int LINE = 64;
+  using T = Tile<BM, BN, WM, WN>;
+  constexpr int PLANE_A = BM * LINE, PLANE_B = BN * LINE, STAGE = 3 * (PLANE_A + PLANE_B);
+  __shared__ __align__(16) char lds[2 * STAGE];
+  const int lane = threadIdx.x & (WAVE - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+  const int wm = wave / T::WAVES_N, wn = wave % T::WAVES_N;
+  int tm, tn;
+  tile_of(blockIdx.x, tiles_m, tiles_n, &tm, &tn);
+  const int m0 = tm * BM, n0 = tn * BN;
+
+  Side<uint16_t, Epi::TRANS_A, BM, LINE, T::MI, PLANE_A / 16 / T::THREADS, T::THREADS> sa;
+  Side<uint16_t, Epi::TRANS_B, BN, LINE, T::NI, PLANE_B / 16 / T::THREADS, T::THREADS> sb;
+  sa.init(m0, g.M, g.lda, wm * T::TM, lane);
+  sb.init(n0, g.N, g.ldb, wn * T::TN, lane);
+  const uint16_t* pa = (const uint16_t*)g.A + (Epi::TRANS_A ? (int64_t)m0 : m0 * g.lda);
+  const uint16_t* pb = (const uint16_t*)g.B + (Epi::TRANS_B ? (int64_t)n0 : n0 * g.ldb);
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(lds_void*)lds);
+
+  constexpr int DEPTH = decltype(sa)::DEPTH;
+  const int total = (g.K + DEPTH - 1) / DEPTH;
+  const int per = (total + g.splits - 1) / g.splits;
+  const int first = min(total, (int)blockIdx.y * per), last = min(total, first + per);
+  int next_k = first * DEPTH;
+  auto issue = [&](int stage) {
+    const uint32_t la = lds0 + stage * STAGE + wave * WAVE * 16;
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+      sa.load(pa + p * g.plane_a, g.lda, next_k, g.K, la + p * PLANE_A, wave);
+      sb.load(pb + p * g.plane_b, g.ldb, next_k, g.K, la + 3 * PLANE_A + p * PLANE_B, wave);
+    }
+    next_k += DEPTH;
+  };
+
+  f32x4 acc[T::MI][T::NI];
+#pragma unroll
+  for (int i = 0; i < T::MI; ++i)
+#pragma unroll
+    for (int j = 0; j < T::NI; ++j) acc[i][j] = (f32x4)(0.0f);
+
+  auto step = [&](int s, int stage) {
+    // this stage has arrived for every wave, and every wave is done with the other
+    __builtin_amdgcn_s_waitcnt(WAIT_VM0);
+    __syncthreads();
+    if (s + 1 < last) issue(stage ^ 1);
+    const char* la = lds + stage * STAGE;
+    const char* lb = la + 3 * PLANE_A;
+    bf16x8 fb[3][T::NI];
+#pragma unroll
+    for (int i = 0; i < T::MI; ++i) {
+      bf16x8 fa[3];
+#pragma unroll
+      for (int p = 0; p < 3; ++p) fa[p] = sa.frag(la + p * PLANE_A, i, 0);
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        if (i == 0) {
+#pragma unroll
+          for (int j = 0; j < T::NI; ++j) fb[q][j] = sb.frag(lb + q * PLANE_B, j, 0);
+        }
+#pragma unroll
+        for (int p = 2 - q; p >= 0; --p)
+#pragma unroll
+          for (int j = 0; j < T::NI; ++j) acc[i][j] = multiply(fa[p], fb[q][j], acc[i][j]);
+      }
+    }
+    // Order of issue: what the first products need, then each group of matrix
+    // instructions with the reads that the group after the next needs.
+    constexpr int MFMA = 0x008, DS_READ = 0x100, N = T::NI;
+    constexpr int RA = decltype(sa)::READS * 3, RB = decltype(sb)::READS * N;
+    __builtin_amdgcn_sched_group_barrier(DS_READ, RA + 2 * RB, 0);
+    __builtin_amdgcn_sched_group_barrier(MFMA, 3 * N, 0);
+    __builtin_amdgcn_sched_group_barrier(DS_READ, RB, 0);
+    __builtin_amdgcn_sched_group_barrier(MFMA, 2 * N, 0);
+#pragma unroll
+    for (int i = 1; i < T::MI; ++i) {
+      __builtin_amdgcn_sched_group_barrier(DS_READ, RA, 0);
+      __builtin_amdgcn_sched_group_barrier(MFMA, 6 * N, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(MFMA, N, 0);
   };
   if (first < last) issue(0);
   int s = first;
@@ -466,10 +555,12 @@ struct EpiMat {
       for (int i = 0; i < T::MI; ++i) {
         const int r = mw + 16 * i + 4 * fk;
         const f32x4 v = acc[i][j];
+        // four columns at once, whatever their alignment
         if (o.bf16) {
           uint16_t* p = (uint16_t*)o.out + (int64_t)n * o.ld + r;
-          if (o.vec && r + 3 < g.M) {
-            *(uint2*)p = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+          if (r + 3 < g.M) {
+            const uint2 w = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+            __builtin_memcpy(p, &w, 8);
           } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -477,8 +568,8 @@ struct EpiMat {
           }
         } else {
           float* p = (float*)o.out + (int64_t)n * o.ld + r;
-          if (o.vec && r + 3 < g.M) {
-            *(f32x4*)p = v;
+          if (r + 3 < g.M) {
+            __builtin_memcpy(p, &v, 16);
           } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -598,15 +689,20 @@ __global__ __launch_bounds__(256) void ce_sum_kernel(const float* acc, int split
     }
 }
 
-template <typename Epi, typename EpiF32>
+template <typename Epi, typename EpiSplit, typename EpiF32>
 int gemm(const CeGemm& g, const typename Epi::Args& ea, hipStream_t st) {
-  const CeTile t = ce_tile(g.M, g.N, g.f32);
+  const CeTile t = g.tile;
   const int tiles_m = (g.M + t.bm - 1) / t.bm;
   const int tiles_n = (g.N + t.bn - 1) / t.bn;
   const dim3 grid((uint32_t)tiles_m * (uint32_t)tiles_n, (uint32_t)g.splits);
 #define CE_LAUNCH(E, BM, BN, WM, WN, EPI) \
   hipLaunchKernelGGL((ce_gemm_kernel<E, BM, BN, WM, WN, EPI>), grid, dim3(WM * WN * WAVE), 0, st, g, tiles_m, tiles_n, ea)
-  if (g.f32) {
+  if (g.planes == 3) {
+    if (t.bm == 64)
+      hipLaunchKernelGGL((ce_split_kernel<64, 128, 2, 2, EpiSplit>), grid, dim3(256), 0, st, g, tiles_m, tiles_n, ea);
+    else
+      hipLaunchKernelGGL((ce_split_kernel<256, 128, 4, 2, EpiSplit>), grid, dim3(512), 0, st, g, tiles_m, tiles_n, ea);
+  } else if (g.planes == 0) {
     if (t.bn == 32) CE_LAUNCH(float, 64, 32, 4, 1, EpiF32);
     else CE_LAUNCH(float, 128, 64, 2, 2, EpiF32);
   } else if (t.bn == 32) {
@@ -622,27 +718,28 @@ int gemm(const CeGemm& g, const typename Epi::Args& ea, hipStream_t st) {
 
 }  // namespace
 
-// Tiles by the rows of B (states, or tokens for dW). Few rows leave the read of A as
+// Tiles of bfloat16 and of float32 as it is, by the rows of B (states, or tokens for dW). Few rows leave the read of A as
 // the bound, and many small workgroups in flight keep it busy: logits of 151,936
 // tokens of 1,024 at 17 rows take 52 us in 64 x 32, 55 in 128 x 32, 59 in 256 x 32; at
 // 64 rows 69 us in 128 x 64, 78 in 128 x 128; at 128 rows of 2,048 187 us in 128 x 64, 193 in
 // 128 x 128, 204 in 256 x 128. From there on products bound it, and the largest tile
 // reads LDS least: 1,300 TFLOP/s in 256 x 256, 930 in 256 x 128, 910 to 1,010 in 128 x 128.
 // dh and dW of less than 128 columns (the rows of A) take the smaller tile too.
-CeTile ce_tile(int64_t M, int64_t N, bool f32) {
+CeTile ce_tile(int64_t M, int64_t N, int planes) {
+  if (planes == 3) return M <= 128 ? CeTile{64, 128, 2} : CeTile{256, 128, 1};
   if (N <= 32) return CeTile{64, 32, 6};
-  if (N <= 128 || M <= 128 || f32) return CeTile{128, 64, 3};
+  if (N <= 128 || M <= 128 || planes == 0) return CeTile{128, 64, 3};
   return CeTile{256, 256, 1};
 }
 
 int launch_ce_stats(const CeGemm& g, const CeStatsOut& o, hipStream_t st) {
-  return gemm<EpiStats, EpiStats>(g, o, st);
+  return gemm<EpiStats, EpiStats, EpiStats>(g, o, st);
 }
 int launch_ce_dz(const CeGemm& g, const CeDzOut& o, hipStream_t st) {
-  return g.parts == 1 ? gemm<EpiDz<1>, EpiDz<0>>(g, o, st) : gemm<EpiDz<3>, EpiDz<0>>(g, o, st);
+  return gemm<EpiDz<1>, EpiDz<3>, EpiDz<0>>(g, o, st);
 }
-int launch_ce_acc(const CeGemm& g, const CeAccOut& o, hipStream_t st) { return gemm<EpiAcc, EpiAcc>(g, o, st); }
-int launch_ce_mat(const CeGemm& g, const CeMatOut& o, hipStream_t st) { return gemm<EpiMat, EpiMat>(g, o, st); }
+int launch_ce_acc(const CeGemm& g, const CeAccOut& o, hipStream_t st) { return gemm<EpiAcc, EpiAcc, EpiAcc>(g, o, st); }
+int launch_ce_mat(const CeGemm& g, const CeMatOut& o, hipStream_t st) { return gemm<EpiMat, EpiMat, EpiMat>(g, o, st); }
 
 int launch_ce_pack(const CePack& p, hipStream_t st) {
   const int64_t blocks = (p.ld / 4 * p.rows + 255) / 256;

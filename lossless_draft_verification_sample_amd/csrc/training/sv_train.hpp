@@ -191,16 +191,20 @@ struct Running {
 // thread: 152 of 256 registers at NV = 38, so one workgroup fills a CU and walks
 // over rows r, r + grid, ... . A group's registers take the next row's group as
 // soon as the row's last pass over it is done, so that the next row arrives while
-// this one is finished.
+// this one is finished. NV = 20 leaves two workgroups a CU short of registers (33
+// spilled), but rows that need it are slower one a CU (2000 rows of 40,000 in float32, with
+// the gradient: 145 us, one a CU 160); those that 16 hold are faster there (4096 rows of 50,257
+// in bfloat16: 222 us, in 20 230; 500 of 32,000 in float32: 30 and 36).
 constexpr int HOLD_THREADS = 512;
-constexpr int HOLD_NV[3] = {10, 20, 38};
+constexpr int HOLD_SIZES = 4;
+constexpr int HOLD_NV[HOLD_SIZES] = {10, 16, 20, 38};
 // Workgroups a CU holds at once, by their registers.
-constexpr int HOLD_PER_CU[3] = {2, 2, 1};
+constexpr int HOLD_PER_CU[HOLD_SIZES] = {2, 2, 2, 1};
 constexpr int HOLD_CUS = 256;
 
 // Index into HOLD_NV for rows of V logits of es bytes, or -1: too long.
 inline int hold_size(int64_t V, int es) {
-  for (int i = 0; i < 3; ++i)
+  for (int i = 0; i < HOLD_SIZES; ++i)
     if (V * es <= (int64_t)HOLD_NV[i] * HOLD_THREADS * 16) return i;
   return -1;
 }
@@ -304,6 +308,11 @@ int launch_distill_backward(const DistillArgs& a, int bf16, hipStream_t s);
 constexpr int CE_LINE = 128;       // bytes of a row that one step of the products takes
 constexpr int CE_MAX_D = 1 << 22;
 
+struct CeTile {
+  int bm, bn, per_cu;   // per_cu: workgroups that a CU holds at once, by LDS
+};
+CeTile ce_tile(int64_t M, int64_t N, int planes);
+
 // One product C[m][n] = sum_k A[m][k] B[n][k]. An operand lies
 // in memory as [row][k] or, where the epilogue takes it transposed, as [k][row];
 // rows of memory start on 16 bytes and can be read in whole groups of 16 bytes.
@@ -312,9 +321,9 @@ struct CeGemm {
   int64_t lda, ldb;          // strides of memory's rows, elements, at most CE_MAX_D
   int64_t plane_a, plane_b;  // distance of a float32 operand's three parts
   int M, N, K;               // rows of A and B, depth
-  int parts;                 // 1: whole operands; 6: products of float32's bfloat16 parts
+  int planes;                // 1: bfloat16 operands; 3: float32 in bfloat16 parts; 0: float32 as it is
   int splits;                // workgroups that share one tile's depth
-  bool f32;                  // float32 operands as they are
+  CeTile tile;
 };
 
 struct CeStatsOut {
@@ -340,7 +349,6 @@ struct CeMatOut {
   void* out;                 // [N][M], row stride ld, float32 or bfloat16
   int64_t ld;
   int bf16;
-  int vec;                   // rows of four can be stored at once
 };
 
 // Rows as the products take them: [planes][rows][ld] bfloat16, or [rows][ld] float
@@ -354,11 +362,6 @@ struct CePack {
   void* dst;
   int64_t ld, plane;
 };
-
-struct CeTile {
-  int bm, bn, per_cu;   // per_cu: workgroups that a CU holds at once, by LDS
-};
-CeTile ce_tile(int64_t M, int64_t N, bool f32);
 
 int launch_ce_pack(const CePack& p, hipStream_t s);
 int launch_ce_stats(const CeGemm& g, const CeStatsOut& o, hipStream_t s);

@@ -137,6 +137,10 @@ constexpr int64_t CE_CUS = 256;
 // Up to here states of float32 take the float32 matrix instructions (linear_ce.hip).
 constexpr int64_t CE_F32_STATES = 384;
 
+// Up to here states dW is bound by its writes, which many small tiles serve better (dW of
+// 151,936 tokens of 1,408 at 128 states 332 us with its dz, in 256 x 256 365; at 200 399 and 396).
+constexpr int64_t CE_SHORT_DEPTH = 128;
+
 // float32 in three parts of bfloat16: planes 3; as it is: planes 0; bfloat16: 1.
 struct CeShape {
   int64_t N, D, V, kp;   // kp: row length of packed operands, whole steps of depth
@@ -153,14 +157,14 @@ bool ce_shape(int32_t N, int32_t D, int32_t V, sv_dtype dtype, CeShape* s) {
   *s = CeShape{N, D, V, 0, dtype == SV_BF16 ? 1 : N <= CE_F32_STATES ? 0 : 3};
   s->kp = round_up(D, s->depth());
   // workgroups of the products over the vocabulary and of dh, and of its sums
-  const sv::CeTile t = sv::ce_tile(V, N, s->f32()), h = sv::ce_tile(D, N, s->f32());
+  const sv::CeTile t = sv::ce_tile(V, N, s->planes), h = sv::ce_tile(D, N, s->planes);
   return ceil_div(V, t.bm) * ceil_div(N, t.bn) < MAX_WORKGROUPS &&
          ceil_div(D, h.bm) * ceil_div(N, h.bn) < MAX_WORKGROUPS && ceil_div(D, 4) * N / 256 < MAX_WORKGROUPS;
 }
 
 // Tokens of a piece whose operands take `bytes` a token.
 int64_t piece_rows(const CeShape& s, int64_t bytes) {
-  const sv::CeTile t = sv::ce_tile(s.V, s.N, s.f32());
+  const sv::CeTile t = sv::ce_tile(s.V, s.N, s.planes);
   const int64_t round = round_up(ceil_div(CE_CUS * t.per_cu, ceil_div(s.N, t.bn)) * t.bm, CE_PIECE_STEP);
   int64_t rows = CE_PIECE_BYTES / bytes / round * round;
   if (rows < round) rows = round;
@@ -180,12 +184,38 @@ CeForward ce_forward(const CeShape& s) {
   CeForward f;
   Carver c;
   f.piece = piece_rows(s, s.row_bytes(s.kp));
-  f.partial = c.take((size_t)(ceil_div(s.V, sv::ce_tile(s.V, s.N, s.f32()).bm) * s.N) * sizeof(sv::MaxSum));
+  f.partial = c.take((size_t)(ceil_div(s.V, sv::ce_tile(s.V, s.N, s.planes).bm) * s.N) * sizeof(sv::MaxSum));
   f.zlabel = c.take((size_t)s.N * sizeof(float));
   f.hidden = c.take((size_t)(s.N * s.row_bytes(s.kp)));
   f.weight = c.take((size_t)(f.piece * s.row_bytes(s.kp)));
   f.total = c.off;
   return f;
+}
+
+// dh has few tiles and a long depth, a piece of the vocabulary: workgroups that share a
+// tile's depth. The fewest microseconds of a piece: rounds of workgroups over the CUs, and
+// the sums that every split reads and writes. As many splits as give each CU its fill
+// take a round too many instead: 622 states of 2,048 over 151,936 tokens 2,466 us a step
+// instead of 2,259, 2,742 of 384 2,572 instead of 2,284.
+int dh_splits(const CeShape& s, int64_t piece, int64_t ld) {
+  const sv::CeTile t = sv::ce_tile(s.D, s.N, s.planes);
+  const int64_t tiles = ceil_div(s.D, t.bm) * ceil_div(s.N, t.bn), places = CE_CUS * t.per_cu;
+  const int64_t steps = piece / s.depth() * (s.planes == 3 ? 2 : 1);
+  const double rate = s.planes == 1 ? 1200e6 : s.planes == 3 ? 180e6 : 120e6;   // flop a us
+  const double tile_us = 2.0 * t.bm * t.bn * piece / (rate / places);
+  const double sum_us = 2.0 * s.N * ld * 4 / 5e6;   // at 5 TB/s
+  int64_t most = steps / 4, fit = CE_PIECE_BYTES / (s.N * ld * 4);
+  if (most > fit) most = fit;
+  int best = 1;
+  double least = INFINITY;
+  for (int64_t n = 1; n <= most || n == 1; ++n) {
+    const double us = (double)ceil_div(tiles * n, places) / n * tile_us + n * sum_us;
+    if (us < least) {
+      least = us;
+      best = (int)n;
+    }
+  }
+  return best;
 }
 
 struct CeBackward {
@@ -198,15 +228,7 @@ CeBackward ce_backward(const CeShape& s, bool want_h) {
   Carver c;
   b.piece = piece_rows(s, s.row_bytes(s.N > s.kp ? s.N : s.kp));
   b.acc_ld = round_up(s.D, 4);
-  // dh has few tiles and a long depth: its depth is split until every CU has its fill
-  const sv::CeTile t = sv::ce_tile(s.D, s.N, s.f32());
-  const int64_t tiles = ceil_div(s.D, t.bm) * ceil_div(s.N, t.bn);
-  int64_t splits = tiles >= CE_CUS ? 1 : ceil_div(CE_CUS * t.per_cu, tiles);
-  const int64_t steps = b.piece / s.depth() * (s.planes == 3 ? 6 : 1);
-  if (splits > steps / 4) splits = steps / 4;
-  const int64_t fit = CE_PIECE_BYTES / (s.N * b.acc_ld * 4);
-  if (splits > fit) splits = fit;
-  b.splits = splits < 1 ? 1 : (int)splits;
+  b.splits = dh_splits(s, b.piece, b.acc_ld);
   b.hidden = c.take((size_t)(s.N * s.row_bytes(s.kp)));
   b.weight = c.take((size_t)(b.piece * s.row_bytes(s.kp)));
   b.dz = c.take((size_t)(s.N * s.row_bytes(b.piece)));
@@ -238,8 +260,8 @@ int ce_operand(const void* src, int64_t stride, int64_t row0, int64_t rows, cons
   return sv::launch_ce_pack(p, st);
 }
 sv::CeGemm ce_gemm(const Operand& a, int64_t M, const Operand& b, int64_t N, int64_t K, const CeShape& s) {
-  return sv::CeGemm{a.p, b.p, a.ld, b.ld, a.plane, b.plane, (int)M, (int)N, (int)K,
-                    s.planes == 3 ? 6 : 1, 1, s.f32()};
+  return sv::CeGemm{a.p, b.p, a.ld, b.ld, a.plane, b.plane, (int)M, (int)N, (int)K, s.planes, 1,
+                    sv::ce_tile(M, N, s.planes)};
 }
 // Depth of the logits' product: what both operands have in whole groups.
 int64_t ce_depth(const Operand& a, const Operand& b) { return a.cols < b.cols ? a.cols : b.cols; }
@@ -351,15 +373,17 @@ int spec_verify_linear_ce(const void* hidden, int64_t hidden_stride, const void*
   float* zlabel = (float*)(ws + f.zlabel);
   Operand h, w;
   if (ce_operand(hidden, hidden_stride, 0, N, s, ws + f.hidden, st, &h)) return SV_EHIP;
-  const int bm = sv::ce_tile(V, N, s.f32()).bm;
+  const sv::CeTile tile = sv::ce_tile(V, N, s.planes);   // of every piece: partial has a row a tile
   const int64_t piece = ce_direct(weight, weight_stride, s) ? V : f.piece;
   for (int64_t v0 = 0; v0 < V; v0 += piece) {
     const int64_t rows = V - v0 < piece ? V - v0 : piece;
     if (ce_operand(weight, weight_stride, v0, rows, s, ws + f.weight, st, &w)) return SV_EHIP;
-    const sv::CeStatsOut o{labels, (int)v0, V, partial + v0 / bm * N, zlabel};
-    if (sv::launch_ce_stats(ce_gemm(w, rows, h, N, ce_depth(w, h), s), o, st)) return SV_EHIP;
+    const sv::CeStatsOut o{labels, (int)v0, V, partial + v0 / tile.bm * N, zlabel};
+    sv::CeGemm g = ce_gemm(w, rows, h, N, ce_depth(w, h), s);
+    g.tile = tile;
+    if (sv::launch_ce_stats(g, o, st)) return SV_EHIP;
   }
-  return sv::launch_ce_join(partial, zlabel, labels, (int)ceil_div(V, bm), N, V, out_loss, out_stats, st)
+  return sv::launch_ce_join(partial, zlabel, labels, (int)ceil_div(V, tile.bm), N, V, out_loss, out_stats, st)
              ? SV_EHIP : SV_OK;
 }
 
@@ -394,7 +418,6 @@ int spec_verify_linear_ce_backward(const void* hidden, int64_t hidden_stride, co
   float* acc = (float*)(ws + b.acc);
   Operand h, w;
   if (ce_operand(hidden, hidden_stride, 0, N, s, ws + b.hidden, st, &h)) return SV_EHIP;
-  const int mat_vec = aligned(out_grad_weight, 4 * es) && grad_weight_stride % 4 == 0;
   for (int64_t v0 = 0; v0 < V; v0 += b.piece) {
     const int64_t rows = V - v0 < b.piece ? V - v0 : b.piece;
     const int64_t ldz = round_up(rows, s.depth());
@@ -409,9 +432,9 @@ int spec_verify_linear_ce_backward(const void* hidden, int64_t hidden_stride, co
       if (sv::launch_ce_acc(g, ao, st)) return SV_EHIP;
     }
     if (out_grad_weight) {
-      const sv::CeGemm g = ce_gemm(h, D, z, rows, N, s);
-      const sv::CeMatOut mo{(char*)out_grad_weight + v0 * grad_weight_stride * es, grad_weight_stride, bf16,
-                            mat_vec};
+      sv::CeGemm g = ce_gemm(h, D, z, rows, N, s);
+      if (N <= CE_SHORT_DEPTH && s.planes == 1) g.tile = sv::ce_tile(D, 128, s.planes);
+      const sv::CeMatOut mo{(char*)out_grad_weight + v0 * grad_weight_stride * es, grad_weight_stride, bf16};
       if (sv::launch_ce_mat(g, mo, st)) return SV_EHIP;
     }
   }

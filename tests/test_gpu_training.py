@@ -458,6 +458,23 @@ def test_linear_ce_several_pieces(dtype):
     _check_ce(h, w, y, np.full(N, 1 / N, np.float32), dtype)
 
 
+@pytest.mark.parametrize("N,D,V", [(385, 65, 129), (450, 200, 100), (400, 300, 1003), (700, 129, 257), (385, 7, 64)])
+def test_linear_ce_float32_in_parts(N, D, V):
+    """float32 with more states than the float32 instructions take, around its tiles."""
+    rng = np.random.default_rng(N + D + V)
+    h, w, y = _head(rng, N, D, V, "f32")
+    _check_ce(h, w, y, rng.uniform(0.2, 2.0, N).astype(np.float32) / N, "f32")
+
+
+def test_linear_ce_float32_short_last_piece():
+    """A last piece of 100 tokens: lower than a tile of the pieces before it."""
+    rng = np.random.default_rng(26)
+    N, D, V = 385, 4000, 16384 + 100
+    h, w, y = _head(rng, N, D, V, "f32")
+    y[:4] = [V - 1, 16384, 16383, V - 36]
+    _check_ce(h, w, y, np.full(N, 1 / N, np.float32), "f32")
+
+
 def test_linear_ce_labels():
     """Left-out rows of every kind, the same label everywhere, no weights."""
     rng = np.random.default_rng(22)
