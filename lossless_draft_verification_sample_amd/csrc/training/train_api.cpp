@@ -127,7 +127,7 @@ int distill_args(const void* logits, int64_t logits_stride, sv_dtype dtype, int3
 
 constexpr int64_t CE_MAX_ROWS = 1 << 22;
 // Bytes of a piece's operands in the workspace. A piece is a whole number of
-// rounds of tiles over the CUs (ce_round_rows); as many rounds as stay within
+// rounds of tiles over the CUs (piece_rows); as many rounds as stay within
 // CE_PIECE_BYTES, half of what the last-level cache holds, and at least one unless
 // that takes more than CE_PIECE_MOST.
 constexpr int64_t CE_PIECE_BYTES = 128ll << 20, CE_PIECE_MOST = 1024ll << 20;
@@ -162,10 +162,13 @@ bool ce_shape(int32_t N, int32_t D, int32_t V, sv_dtype dtype, CeShape* s) {
          ceil_div(D, h.bm) * ceil_div(N, h.bn) < MAX_WORKGROUPS && ceil_div(D, 4) * N / 256 < MAX_WORKGROUPS;
 }
 
-// Tokens of a piece whose operands take `bytes` a token.
+// Tokens of a piece whose operands take `bytes` a token. Rounds do not exceed the CUs: with
+// three columns of tiles, 85 rows of them make one (86 would take a second one for two
+// tiles: 622 states of 2,048 over 151,936 tokens 2,251 us a step instead of 2,014).
 int64_t piece_rows(const CeShape& s, int64_t bytes) {
   const sv::CeTile t = sv::ce_tile(s.V, s.N, s.planes);
-  const int64_t round = round_up(ceil_div(CE_CUS * t.per_cu, ceil_div(s.N, t.bn)) * t.bm, CE_PIECE_STEP);
+  int64_t round = CE_CUS * t.per_cu / ceil_div(s.N, t.bn) * t.bm / CE_PIECE_STEP * CE_PIECE_STEP;
+  if (round < CE_PIECE_STEP) round = CE_PIECE_STEP;
   int64_t rows = CE_PIECE_BYTES / bytes / round * round;
   if (rows < round) rows = round;
   const int64_t most = CE_PIECE_MOST / bytes / CE_PIECE_STEP * CE_PIECE_STEP;
