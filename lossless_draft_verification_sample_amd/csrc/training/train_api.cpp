@@ -209,16 +209,22 @@ int dh_splits(const CeShape& s, int64_t piece, int64_t ld) {
   const double sum_us = 2.0 * s.N * ld * 4 / 5e6;   // at 5 TB/s
   int64_t most = steps / 4, fit = CE_PIECE_BYTES / (s.N * ld * 4);
   if (most > fit) most = fit;
-  int best = 1;
+  int64_t best = 1;
   double least = INFINITY;
-  for (int64_t n = 1; n <= most || n == 1; ++n) {
+  auto offer = [&](int64_t n) {
+    n = n > most ? most : n;
+    n = n < 1 ? 1 : n;
     const double us = (double)ceil_div(tiles * n, places) / n * tile_us + n * sum_us;
     if (us < least) {
       least = us;
-      best = (int)n;
+      best = n;
     }
-  }
-  return best;
+  };
+  // the most splits of so many rounds, and where the sums weigh as much as the product
+  const int64_t rounds = ceil_div(tiles, places);
+  for (int64_t r = rounds; r < rounds + 8; ++r) offer(r * places / tiles);
+  offer((int64_t)sqrt(tile_us / sum_us));
+  return (int)best;
 }
 
 struct CeBackward {
