@@ -407,8 +407,8 @@ int spec_verify_linear_ce(const void* hidden, int64_t hidden_stride, const void*
  *   out_grad_hidden [N][D] = dz weight,  out_grad_weight [V][D] = dz^T hidden,
  * both of dtype, with row strides >= D; either may be NULL (then not computed),
  * not both. grad_loss [N] float, or NULL (1).
- * For bfloat16, dz is rounded to bfloat16 before its products, which are summed
- * in float32. Outputs must not overlap inputs. Elements behind D are left as
+ * For bfloat16, dz is taken as two bfloat16 parts, which hold it to 2^-16, and its
+ * products are summed in float32. Outputs must not overlap inputs. Elements behind D are left as
  * they are. */
 size_t spec_verify_linear_ce_backward_workspace_bytes(int32_t N, int32_t D, int32_t V,
                                                       sv_dtype dtype, int want_grad_hidden,

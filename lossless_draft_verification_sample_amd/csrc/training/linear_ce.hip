@@ -4,11 +4,18 @@
 //          maximum and sum of exp over the tile's tokens; a second kernel joins
 //          the tiles of a state;
 //   dz     the same product again: dz = g (exp(z - m - logsum) - [v = y]),
-//          rounded to bfloat16, as [state][token] of a piece of the vocabulary;
+//          as [state][token] of a piece of the vocabulary;
 //   acc    A = W^T of the piece, B = dz: adds to dh in float32;
 //   mat    A = h^T, B = dz^T: rows of dW, complete after one product.
 // The last two read their transposed operands from W, h and dz as they lie in
 // memory; the transposition happens in the read from LDS.
+//
+// dz of bfloat16 matrices is float32 taken as two bfloat16 parts, dz = d1 + d2, which hold it
+// to 2^-16: the gradients' own rounding is the only one to bfloat16 that they show. In one
+// part, half the work, their error against 64 bits is 2.4e-3 instead of the 1.66e-3 of
+// that rounding (4,096 states of 4,096 over 151,936 tokens). A step of the product takes both
+// parts of a stretch of depth, so that the matrix instructions of two products share the
+// fragments of W or h.
 //
 // float32 operands, by the number of states (CE_F32_STATES):
 //   few   as they are, with the float32 matrix instructions: what bounds these calls is
@@ -48,9 +55,6 @@ struct Tile {
   static constexpr int WAVES_M = WM, WAVES_N = WN, THREADS = WM * WN * WAVE;
   static constexpr int TM = BM / WM, TN = BN / WN;   // a wave's tile
   static constexpr int MI = TM / 16, NI = TN / 16;
-  static constexpr int LA = BM * 8 / THREADS, LB = BN * 8 / THREADS;   // 16-byte loads a thread
-  static constexpr int STAGE = (BM + BN) * CE_LINE;   // bytes
-  static_assert(LA * THREADS == BM * 8 && LB * THREADS == BN * 8, "whole rounds of loads");
 };
 
 // Sixteen bytes of depth of one row.
@@ -113,8 +117,10 @@ __device__ __forceinline__ void copy_to_lds(uint64_t base, uint32_t byte_off, ui
 //               each; blocks of 16 columns (64 bytes) are permuted by bits 2 and 3 of k.
 // Groups behind the depth, or (transposed) behind the last row, are loaded from
 // beyond the buffer resource's range, which reads as zero.
-template <typename E, bool TRANS, int ROWS, int LINE, int FRAGS, int LOADS, int THREADS>
+template <typename E, bool TRANS, int ROWS, int LINE, int FRAGS, int THREADS>
 struct Side {
+  static constexpr int LOADS = ROWS * LINE / 16 / THREADS;      // 16-byte loads a thread
+  static_assert(LOADS * THREADS * 16 == ROWS * LINE, "whole rounds of loads");
   static constexpr int ES = sizeof(E);
   static constexpr int EPG = 16 / ES;                           // elements of a group
   static constexpr int DEPTH = LINE / ES;                       // elements of a step
@@ -208,11 +214,15 @@ __device__ __forceinline__ f32x4 multiply(const f32x4& a, const f32x4& b, f32x4 
   return c;
 }
 
-template <typename E, int BM, int BN, int WM, int WN, typename Epi>
+// LINE: bytes of a row that one step takes. Where B is dz in two parts, a step takes both.
+template <typename E, int BM, int BN, int WM, int WN, int LINE, typename Epi>
 __global__ __launch_bounds__(WM* WN* WAVE, WM* WN == 8 ? 2 : 1) void ce_gemm_kernel(
     CeGemm g, int tiles_m, int tiles_n, typename Epi::Args ea) {
   using T = Tile<BM, BN, WM, WN>;
-  __shared__ __align__(16) char lds[2 * T::STAGE];
+  constexpr int PB = Epi::OF_DZ && sizeof(E) == 2 ? 2 : 1;   // parts of B
+  constexpr int PLANE_A = BM * LINE, PLANE_B = BN * LINE, STAGE = PLANE_A + PB * PLANE_B;
+  constexpr int KK = LINE / 64;                              // fragments of a row's step
+  __shared__ __align__(16) char lds[2 * STAGE];
   const int tid = threadIdx.x, lane = tid & (WAVE - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
   const int wm = wave / WN, wn = wave % WN;
@@ -220,8 +230,8 @@ __global__ __launch_bounds__(WM* WN* WAVE, WM* WN == 8 ? 2 : 1) void ce_gemm_ker
   tile_of(blockIdx.x, tiles_m, tiles_n, &tm, &tn);
   const int m0 = tm * BM, n0 = tn * BN;
 
-  Side<E, Epi::TRANS_A, BM, CE_LINE, T::MI, T::LA, T::THREADS> sa;
-  Side<E, Epi::TRANS_B, BN, CE_LINE, T::NI, T::LB, T::THREADS> sb;
+  Side<E, Epi::TRANS_A, BM, LINE, T::MI, T::THREADS> sa;
+  Side<E, Epi::TRANS_B, BN, LINE, T::NI, T::THREADS> sb;
   sa.init(m0, g.M, g.lda, wm * T::TM, lane);
   sb.init(n0, g.N, g.ldb, wn * T::TN, lane);
   const E* pa = (const E*)g.A + (Epi::TRANS_A ? (int64_t)m0 : m0 * g.lda);
@@ -235,9 +245,11 @@ __global__ __launch_bounds__(WM* WN* WAVE, WM* WN == 8 ? 2 : 1) void ce_gemm_ker
   const int first = min(total, (int)blockIdx.y * per), last = min(total, first + per);
   int next_k = first * DEPTH;
   auto issue = [&](int stage) {
-    const uint32_t la = lds0 + stage * T::STAGE + wave * WAVE * 16;
+    const uint32_t la = lds0 + stage * STAGE + wave * WAVE * 16;
     sa.load(pa, g.lda, next_k, g.K, la, wave);
-    sb.load(pb, g.ldb, next_k, g.K, la + BM * CE_LINE, wave);
+#pragma unroll
+    for (int q = 0; q < PB; ++q)
+      sb.load(pb + q * g.plane_b, g.ldb, next_k, g.K, la + PLANE_A + q * PLANE_B, wave);
     next_k += DEPTH;
   };
 
@@ -252,40 +264,44 @@ __global__ __launch_bounds__(WM* WN* WAVE, WM* WN == 8 ? 2 : 1) void ce_gemm_ker
     __builtin_amdgcn_s_waitcnt(WAIT_VM0);
     __syncthreads();
     if (s + 1 < last) issue(stage ^ 1);
-    const char* la = lds + stage * T::STAGE;
-    const char* lb = la + BM * CE_LINE;
+    const char* la = lds + stage * STAGE;
+    const char* lb = la + PLANE_A;
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      typename Frag<E>::type fa[T::MI], fb[T::NI];
+    for (int kk = 0; kk < KK; ++kk) {
+      typename Frag<E>::type fa[T::MI], fb[PB][T::NI];
 #pragma unroll
-      for (int j = 0; j < T::NI; ++j) fb[j] = sb.frag(lb, j, kk);
+      for (int q = 0; q < PB; ++q)
+#pragma unroll
+        for (int j = 0; j < T::NI; ++j) fb[q][j] = sb.frag(lb + q * PLANE_B, j, kk);
 #pragma unroll
       for (int i = 0; i < T::MI; ++i) fa[i] = sa.frag(la, i, kk);
 #pragma unroll
       for (int i = 0; i < T::MI; ++i)
 #pragma unroll
-        for (int j = 0; j < T::NI; ++j) acc[i][j] = multiply(fa[i], fb[j], acc[i][j]);
+        for (int q = 0; q < PB; ++q)
+#pragma unroll
+          for (int j = 0; j < T::NI; ++j) acc[i][j] = multiply(fa[i], fb[q][j], acc[i][j]);
     }
     // Order of issue: all of B's fragments and two of A's, then each row of
     // matrix instructions with the fragment reads that the row after the next needs.
-    constexpr int MFMA = 0x008, DS_READ = 0x100;
-    constexpr int RA = decltype(sa)::READS, RB = decltype(sb)::READS;
+    constexpr int MFMA = 0x008, DS_READ = 0x100, ROW = T::NI * PB;
+    constexpr int RA = decltype(sa)::READS, RB = decltype(sb)::READS * PB;
     if constexpr (T::MI > 2 && sizeof(E) == 2) {
       __builtin_amdgcn_sched_group_barrier(DS_READ, RB * T::NI + 2 * RA, 0);
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
+      for (int kk = 0; kk < KK; ++kk) {
 #pragma unroll
         for (int i = 0; i < T::MI - 2; ++i) {
-          __builtin_amdgcn_sched_group_barrier(MFMA, T::NI, 0);
+          __builtin_amdgcn_sched_group_barrier(MFMA, ROW, 0);
           __builtin_amdgcn_sched_group_barrier(DS_READ, RA, 0);
         }
-        if (kk == 0) {
-          __builtin_amdgcn_sched_group_barrier(MFMA, T::NI, 0);
+        if (kk + 1 < KK) {
+          __builtin_amdgcn_sched_group_barrier(MFMA, ROW, 0);
           __builtin_amdgcn_sched_group_barrier(DS_READ, RB * T::NI, 0);
-          __builtin_amdgcn_sched_group_barrier(MFMA, T::NI, 0);
+          __builtin_amdgcn_sched_group_barrier(MFMA, ROW, 0);
           __builtin_amdgcn_sched_group_barrier(DS_READ, 2 * RA, 0);
         } else {
-          __builtin_amdgcn_sched_group_barrier(MFMA, 2 * T::NI, 0);
+          __builtin_amdgcn_sched_group_barrier(MFMA, 2 * ROW, 0);
         }
       }
     }
@@ -322,8 +338,8 @@ __global__ __launch_bounds__(WM* WN* WAVE, 2) void ce_split_kernel(CeGemm g, int
   tile_of(blockIdx.x, tiles_m, tiles_n, &tm, &tn);
   const int m0 = tm * BM, n0 = tn * BN;
 
-  Side<uint16_t, Epi::TRANS_A, BM, LINE, T::MI, PLANE_A / 16 / T::THREADS, T::THREADS> sa;
-  Side<uint16_t, Epi::TRANS_B, BN, LINE, T::NI, PLANE_B / 16 / T::THREADS, T::THREADS> sb;
+  Side<uint16_t, Epi::TRANS_A, BM, LINE, T::MI, T::THREADS> sa;
+  Side<uint16_t, Epi::TRANS_B, BN, LINE, T::NI, T::THREADS> sb;
   sa.init(m0, g.M, g.lda, wm * T::TM, lane);
   sb.init(n0, g.N, g.ldb, wn * T::TN, lane);
   const uint16_t* pa = (const uint16_t*)g.A + (Epi::TRANS_A ? (int64_t)m0 : m0 * g.lda);
@@ -407,7 +423,7 @@ __global__ __launch_bounds__(WM* WN* WAVE, 2) void ce_split_kernel(CeGemm g, int
 
 struct EpiStats {
   typedef CeStatsOut Args;
-  static constexpr bool TRANS_A = false, TRANS_B = false;
+  static constexpr bool TRANS_A = false, TRANS_B = false, OF_DZ = false;
   template <typename T, typename Acc>
   static __device__ __forceinline__ void run(const Args& o, const CeGemm& g, Acc& acc, int mw, int nw,
                                              int tm, int wm, int wn, int lane, char* lds) {
@@ -465,11 +481,12 @@ __device__ __forceinline__ void split3(float x, uint16_t (&p)[3]) {
   }
 }
 
-// PARTS: 1 writes dz rounded to bfloat16, 3 its three parts, 0 float32.
+// PARTS: bfloat16 parts that dz is written in (each the rounding of what the parts before
+// leave), or 0: float32.
 template <int PARTS>
 struct EpiDz {
   typedef CeDzOut Args;
-  static constexpr bool TRANS_A = false, TRANS_B = false;
+  static constexpr bool TRANS_A = false, TRANS_B = false, OF_DZ = false;
   template <typename T, typename Acc>
   static __device__ __forceinline__ void run(const Args& o, const CeGemm& g, Acc& acc, int mw, int nw,
                                              int, int, int, int lane, char*) {
@@ -517,7 +534,7 @@ struct EpiDz {
 
 struct EpiAcc {
   typedef CeAccOut Args;
-  static constexpr bool TRANS_A = true, TRANS_B = false;
+  static constexpr bool TRANS_A = true, TRANS_B = false, OF_DZ = true;
   template <typename T, typename Acc>
   static __device__ __forceinline__ void run(const Args& o, const CeGemm& g, Acc& acc, int mw, int nw,
                                              int, int, int, int lane, char*) {
@@ -542,7 +559,7 @@ struct EpiAcc {
 
 struct EpiMat {
   typedef CeMatOut Args;
-  static constexpr bool TRANS_A = true, TRANS_B = true;
+  static constexpr bool TRANS_A = true, TRANS_B = true, OF_DZ = true;
   template <typename T, typename Acc>
   static __device__ __forceinline__ void run(const Args& o, const CeGemm& g, Acc& acc, int mw, int nw,
                                              int, int, int, int lane, char*) {
@@ -695,22 +712,24 @@ int gemm(const CeGemm& g, const typename Epi::Args& ea, hipStream_t st) {
   const int tiles_m = (g.M + t.bm - 1) / t.bm;
   const int tiles_n = (g.N + t.bn - 1) / t.bn;
   const dim3 grid((uint32_t)tiles_m * (uint32_t)tiles_n, (uint32_t)g.splits);
-#define CE_LAUNCH(E, BM, BN, WM, WN, EPI) \
-  hipLaunchKernelGGL((ce_gemm_kernel<E, BM, BN, WM, WN, EPI>), grid, dim3(WM * WN * WAVE), 0, st, g, tiles_m, tiles_n, ea)
+  // both parts of dz at a depth of 64 do not fit LDS twice in the largest tile
+  constexpr int WIDE = Epi::OF_DZ ? CE_LINE / 2 : CE_LINE;
+#define CE_LAUNCH(E, BM, BN, WM, WN, LINE, EPI) \
+  hipLaunchKernelGGL((ce_gemm_kernel<E, BM, BN, WM, WN, LINE, EPI>), grid, dim3(WM * WN * WAVE), 0, st, g, tiles_m, tiles_n, ea)
   if (g.planes == 3) {
     if (t.bm == 64)
       hipLaunchKernelGGL((ce_split_kernel<64, 128, 2, 2, EpiSplit>), grid, dim3(256), 0, st, g, tiles_m, tiles_n, ea);
     else
       hipLaunchKernelGGL((ce_split_kernel<256, 128, 4, 2, EpiSplit>), grid, dim3(512), 0, st, g, tiles_m, tiles_n, ea);
   } else if (g.planes == 0) {
-    if (t.bn == 32) CE_LAUNCH(float, 64, 32, 4, 1, EpiF32);
-    else CE_LAUNCH(float, 128, 64, 2, 2, EpiF32);
+    if (t.bn == 32) CE_LAUNCH(float, 64, 32, 4, 1, CE_LINE, EpiF32);
+    else CE_LAUNCH(float, 128, 64, 2, 2, CE_LINE, EpiF32);
   } else if (t.bn == 32) {
-    CE_LAUNCH(uint16_t, 64, 32, 4, 1, Epi);
+    CE_LAUNCH(uint16_t, 64, 32, 4, 1, CE_LINE, Epi);
   } else if (t.bn == 64) {
-    CE_LAUNCH(uint16_t, 128, 64, 2, 2, Epi);
+    CE_LAUNCH(uint16_t, 128, 64, 2, 2, CE_LINE, Epi);
   } else {
-    CE_LAUNCH(uint16_t, 256, 256, 2, 4, Epi);
+    CE_LAUNCH(uint16_t, 256, 256, 2, 4, WIDE, Epi);
   }
 #undef CE_LAUNCH
   return hipGetLastError() == hipSuccess ? 0 : -1;
@@ -736,7 +755,7 @@ int launch_ce_stats(const CeGemm& g, const CeStatsOut& o, hipStream_t st) {
   return gemm<EpiStats, EpiStats, EpiStats>(g, o, st);
 }
 int launch_ce_dz(const CeGemm& g, const CeDzOut& o, hipStream_t st) {
-  return gemm<EpiDz<1>, EpiDz<3>, EpiDz<0>>(g, o, st);
+  return gemm<EpiDz<2>, EpiDz<3>, EpiDz<0>>(g, o, st);
 }
 int launch_ce_acc(const CeGemm& g, const CeAccOut& o, hipStream_t st) { return gemm<EpiAcc, EpiAcc, EpiAcc>(g, o, st); }
 int launch_ce_mat(const CeGemm& g, const CeMatOut& o, hipStream_t st) { return gemm<EpiMat, EpiMat, EpiMat>(g, o, st); }

@@ -305,7 +305,7 @@ int launch_distill_backward(const DistillArgs& a, int bf16, hipStream_t s);
 
 // ------------------------------------------------------------ linear cross entropy
 
-constexpr int CE_LINE = 128;       // bytes of a row that one step of the products takes
+constexpr int CE_LINE = 128;       // most bytes of a row that one step of the products takes
 constexpr int CE_MAX_D = 1 << 22;
 
 struct CeTile {
@@ -319,9 +319,9 @@ CeTile ce_tile(int64_t M, int64_t N, int planes);
 struct CeGemm {
   const void *A, *B;
   int64_t lda, ldb;          // strides of memory's rows, elements, at most CE_MAX_D
-  int64_t plane_a, plane_b;  // distance of a float32 operand's three parts
+  int64_t plane_a, plane_b;  // distance of an operand's parts: three of float32, two of dz of bfloat16
   int M, N, K;               // rows of A and B, depth
-  int planes;                // 1: bfloat16 operands; 3: float32 in bfloat16 parts; 0: float32 as it is
+  int planes;                // 1: bfloat16 operands (dz in two parts); 3: float32 in bfloat16 parts; 0: float32 as it is
   int splits;                // workgroups that share one tile's depth
   CeTile tile;
 };

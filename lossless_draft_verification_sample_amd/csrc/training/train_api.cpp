@@ -129,7 +129,9 @@ constexpr int64_t CE_MAX_ROWS = 1 << 22;
 // Bytes of a piece's operands in the workspace. A piece is a whole number of
 // rounds of tiles over the CUs (piece_rows); as many rounds as stay within
 // CE_PIECE_BYTES, half of what the last-level cache holds, and at least one unless
-// that takes more than CE_PIECE_MOST.
+// that takes more than CE_PIECE_MOST. dz of bfloat16 takes twice that, a part each: pieces
+// of half the length make more sums of dh (8,192 states of 1,024 over 32,000 tokens 4,512 us a
+// step instead of 3,386, 2,742 of 384 over 151,936 3,517 instead of 2,945).
 constexpr int64_t CE_PIECE_BYTES = 128ll << 20, CE_PIECE_MOST = 1024ll << 20;
 constexpr int64_t CE_PIECE_STEP = 256;    // a multiple of every tile height
 constexpr int64_t CE_CUS = 256;
@@ -137,8 +139,8 @@ constexpr int64_t CE_CUS = 256;
 // Up to here states of float32 take the float32 matrix instructions (linear_ce.hip).
 constexpr int64_t CE_F32_STATES = 384;
 
-// Up to here states dW is bound by its writes, which many small tiles serve better (dW of
-// 151,936 tokens of 1,408 at 128 states 332 us with its dz, in 256 x 256 365; at 200 399 and 396).
+// Up to here states dW is bound by its writes, which many small tiles serve better (a step of
+// 151,936 tokens of 1,408 at 128 states 756 us, with dW in 256 x 256 774; at 200 881 and 827).
 constexpr int64_t CE_SHORT_DEPTH = 128;
 
 // float32 in three parts of bfloat16: planes 3; as it is: planes 0; bfloat16: 1.
@@ -148,6 +150,7 @@ struct CeShape {
   bool f32() const { return planes == 0; }
   int es() const { return f32() ? 4 : 2; }                   // bytes of an element of an operand
   int64_t row_bytes(int64_t n) const { return n * (planes == 3 ? 6 : es()); }
+  int64_t dz_bytes(int64_t n) const { return n * (planes == 3 ? 6 : 4); }   // bfloat16: two parts
   int64_t depth() const { return sv::CE_LINE / es(); }
   int64_t per16() const { return 16 / es(); }
 };
@@ -203,9 +206,9 @@ CeForward ce_forward(const CeShape& s) {
 int dh_splits(const CeShape& s, int64_t piece, int64_t ld) {
   const sv::CeTile t = sv::ce_tile(s.D, s.N, s.planes);
   const int64_t tiles = ceil_div(s.D, t.bm) * ceil_div(s.N, t.bn), places = CE_CUS * t.per_cu;
-  const int64_t steps = piece / s.depth() * (s.planes == 3 ? 2 : 1);
+  const int64_t steps = piece / s.depth() * (s.planes == 3 || t.bm == 256 ? 2 : 1);
   const double rate = s.planes == 1 ? 1200e6 : s.planes == 3 ? 180e6 : 120e6;   // flop a us
-  const double tile_us = 2.0 * t.bm * t.bn * piece / (rate / places);
+  const double tile_us = 2.0 * t.bm * t.bn * piece * (s.planes == 1 ? 2 : 1) / (rate / places);
   const double sum_us = 2.0 * s.N * ld * 4 / 5e6;   // at 5 TB/s
   int64_t most = steps / 4, fit = CE_PIECE_BYTES / (s.N * ld * 4);
   if (most > fit) most = fit;
@@ -240,7 +243,7 @@ CeBackward ce_backward(const CeShape& s, bool want_h) {
   b.splits = dh_splits(s, b.piece, b.acc_ld);
   b.hidden = c.take((size_t)(s.N * s.row_bytes(s.kp)));
   b.weight = c.take((size_t)(b.piece * s.row_bytes(s.kp)));
-  b.dz = c.take((size_t)(s.N * s.row_bytes(b.piece)));
+  b.dz = c.take((size_t)s.dz_bytes(s.N * b.piece));
   b.acc = c.take(want_h ? (size_t)(b.splits * s.N * b.acc_ld) * 4 : 0);
   b.total = c.off;
   return b;
