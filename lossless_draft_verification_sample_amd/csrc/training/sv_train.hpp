@@ -124,10 +124,12 @@ __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 // multiply-add, one exp2 and one addition. The reference is next to m c when it is
 // set, and set again only when a logit lies 2^30 above it (float32 holds sums of
 // 2^31 such terms): a reference that followed every new maximum would be moved in
-// nearly every step, since one lane of the 64 is enough. The fused product is exact,
-// whatever the size of z c. Where m or m c passes 2^100 (rows of the type's lowest
-// value, temperatures next to 0) m c may not be representable: there ref is +inf as a
-// mark and the sum is kept relative to m.
+// nearly every step, since one lane of the 64 is enough. The fused product rounds z c - ref
+// once. From 2^24 on (masks of -1e9 and below, temperatures next to 0) a float next to m c
+// may lie more than 1 from it, from 2^32 on so far that exp2 of the difference is 0 or
+// infinite: there ref is +inf as a mark and the sum is kept relative to m.
+constexpr float REF_RANGE = 0x1p24f;
+
 struct Running {
   float m = -INFINITY;        // largest logit
   float limit = -INFINITY;    // a larger one sets a new reference
@@ -142,7 +144,7 @@ struct Running {
   __device__ __forceinline__ void raise(float vm, float c) {
     float t = set(c).s;
     t *= fast_exp2((m - vm) * c);   // m = -inf: t is 0
-    if (fabsf(vm) < 0x1p100f && fabsf(vm * c) < 0x1p100f) {
+    if (fabsf(vm * c) < REF_RANGE) {
       ref = rintf(vm * c);
       limit = vm + 30.0f / c;
       s = t * fast_exp2(__builtin_fmaf(vm, c, -ref));

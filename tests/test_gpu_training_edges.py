@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 
 from oracle import training as ot
-from tests.test_gpu_training import HALF, U, _dev, _head, _host, _sum_tol, _sv
+from tests.test_gpu_training import HALF, U, _dev, _distill_tol, _head, _host, _lse_tol, _sum_tol, _sv
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +60,103 @@ def test_linear_ce_gradients_keep_dz_beyond_bfloat16(N, D, V, pad):
                               _gradient_tol(hh, ww, z, dz, np.where(used, g, 0.0))):
         far = np.abs(_host(got) - want) - tol
         assert np.all(far <= 0), (far.max(), np.argwhere(far > 0)[:4], (far > 0).mean())
+
+
+# ---------------------------------------------------------------- finite masks
+
+
+def _masked(rng, V, fill):
+    """Rows with a block of `fill` first, in the middle, last, and everywhere."""
+    z = (rng.standard_normal((5, V)) * 3).astype(np.float32)
+    z[0, : V // 2] = fill
+    z[1, V // 3: V // 2] = fill
+    z[2, V // 2:] = fill
+    z[3] = fill
+    z[4] = np.where(rng.random(V) < 0.9, fill, z[4])
+    return z
+
+
+MASKS = (-1e9, -1e10, -6e10, -1e12, -1e15, -1e20, -1e25, -1e30, 1e10, 1e20)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("copies,V,T", [
+    (1, 9001, 1.0), (120, 9001, 0.7), (1, 50003, 0.8), (20, 50003, 1.0), (1, 160001, 1.0)])
+def test_top_logits_of_finite_masks(dtype, copies, V, T):
+    """One workgroup to a row and several; masks of every size that the exponents'
+    reference may be taken at."""
+    import torch
+    rng = np.random.default_rng(V + copies)
+    z = np.concatenate([_masked(rng, V, f) for f in MASKS])
+    t = _dev(z, dtype)
+    want = ot.top_logits(_host(t), 5, T)
+    out = _sv().spec_verify_top_logits(t.repeat(copies, 1), 5, temperature=T)
+    torch.cuda.synchronize()
+    tol = _lse_tol(V, want[2])
+    for k in range(0, len(z) * copies, len(z)):
+        assert np.array_equal(out.ids[k: k + len(z)].cpu().numpy(), want[0])
+        far = np.abs(_host(out.lse[k: k + len(z)]) - want[2])
+        assert np.all(far <= tol), (np.argwhere(~(far <= tol)).ravel(), far)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1e-5, 1e-8, 1e-9, 1e-20, 1e-30])
+def test_top_logits_at_small_temperatures(dtype, T):
+    import torch
+    rng = np.random.default_rng(3)
+    z = np.concatenate([(rng.standard_normal((4, 20011)) * s) for s in (1.0, 10.0, 60.0, T, 30 * T)]).astype(np.float32)
+    t = _dev(z, dtype)
+    T = float(np.float32(T))
+    lse = ot.top_logits(_host(t), 1, T)[2]
+    for copies in (1, 80):
+        out = _sv().spec_verify_top_logits(t.repeat(copies, 1), 1, temperature=T)
+        torch.cuda.synchronize()
+        far = np.abs(_host(out.lse).reshape(copies, -1) - lse)
+        assert np.all(far <= _lse_tol(20011, lse)), far.max(0)
+
+
+def _distill_case(rng, z, T, K=6):
+    """Kept tokens among the row's, the rest of the teacher near them."""
+    ids = np.stack([rng.choice(z.shape[1], K, replace=False) for _ in z]).astype(np.int32)
+    return ids, (rng.standard_normal(ids.shape) * 2 * min(T, 1.0)).astype(np.float32)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("copies,V", [(1, 9001), (120, 9001), (1, 30011), (20, 30011), (3, 82001), (1, 160001)])
+def test_distill_loss_of_finite_masks(dtype, copies, V):
+    """Streamed, split and (with the gradient) held rows."""
+    import torch
+    sv, rng = _sv(), np.random.default_rng(V + copies)
+    for T in (1.0, 0.7):
+        z = np.concatenate([_masked(rng, V, f) for f in MASKS])
+        t = _dev(z, dtype)
+        z = _host(t)
+        ids, values = _distill_case(rng, z, T)
+        ref = ot.distill(z, ids, values, T)
+        tol = _distill_tol(z, ids, values, T, ref, dtype, None)[0]
+        args = t.repeat(copies, 1), _dev(ids).repeat(copies, 1), _dev(values).repeat(copies, 1)
+        for out in (sv.spec_verify_distill(*args, temperature=T),
+                    sv.spec_verify_distill(*args, temperature=T, want_grad=True)):
+            torch.cuda.synchronize()
+            far = np.abs(_host(out.loss).reshape(copies, -1) - ref[0])
+            assert np.all(far <= tol), (np.argwhere(~(far <= tol))[:5], far.max(0))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1e-5, 1e-8, 1e-9, 1e-20])
+def test_distill_loss_at_small_temperatures(dtype, T):
+    import torch
+    sv, rng = _sv(), np.random.default_rng(4)
+    z = np.concatenate([(rng.standard_normal((4, 20011)) * s) for s in (1.0, 60.0, T, 30 * T)]).astype(np.float32)
+    t = _dev(z, dtype)
+    z, T = _host(t), float(np.float32(T))
+    ids, values = _distill_case(rng, z, T)
+    ref = ot.distill(z, ids, values, T)
+    tol = _distill_tol(z, ids, values, T, ref, dtype, None)[0]
+    for copies in (1, 40):
+        args = t.repeat(copies, 1), _dev(ids).repeat(copies, 1), _dev(values).repeat(copies, 1)
+        for out in (sv.spec_verify_distill(*args, temperature=T),
+                    sv.spec_verify_distill(*args, temperature=T, want_grad=True)):
+            torch.cuda.synchronize()
+            far = np.abs(_host(out.loss).reshape(copies, -1) - ref[0])
+            assert np.all(far <= tol), (np.argwhere(~(far <= tol))[:5], far.max(0))
