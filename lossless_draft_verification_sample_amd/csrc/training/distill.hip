@@ -128,7 +128,7 @@ __device__ MaxSum row_set(const DistillArgs& a, DisLds& L, const Row<Elem>& row,
 
 // The dense part of a row's gradient, w / T P q_v, as scale exp2(z c - ref): ref is the
 // whole number next to (m / T + logsum) log2 e, and what the rounding leaves is in the
-// scale (beyond 2^100, see Running: relative to m).
+// scale (from REF_RANGE on, see Running: relative to m).
 struct Density {
   float g, scale, ref, m;
   bool none;   // nothing to learn from: no teacher mass, or a row that rules out every token
@@ -137,7 +137,7 @@ struct Density {
     g = weight * a.inv_t;
     none = P == 0.0f || m == -INFINITY;
     const float ls2 = logsum * LOG2E;
-    if (fabsf(m) < 0x1p100f && fabsf(m * a.c) < 0x1p100f) {
+    if (fabsf(m * a.c) < REF_RANGE) {
       ref = rintf(__builtin_fmaf(m, a.c, ls2));
       scale = g * P * fast_exp2(__builtin_fmaf(-m, a.c, ref) - ls2);
     } else {

@@ -160,3 +160,30 @@ def test_distill_loss_at_small_temperatures(dtype, T):
             torch.cuda.synchronize()
             far = np.abs(_host(out.loss).reshape(copies, -1) - ref[0])
             assert np.all(far <= tol), (np.argwhere(~(far <= tol))[:5], far.max(0))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("copies,V,T", [
+    (1, 9001, 1.0), (120, 9001, 0.7), (1, 30011, 1.0), (20, 30011, 0.7), (1, 30011, 1e-5), (1, 30011, 1e-9),
+    (3, 82001, 1.0), (1, 160001, 1.0), (120, 9001, 1e-9)])
+def test_distill_gradient_of_finite_masks_and_small_temperatures(dtype, copies, V, T):
+    """With the loss, and alone from its statistics."""
+    import torch
+    sv, rng = _sv(), np.random.default_rng(V + copies)
+    T = float(np.float32(T))
+    z = np.concatenate([_masked(rng, V, f) for f in MASKS] + [np.float32(T) * _masked(rng, V, -50.0)])
+    t = _dev(z, dtype)
+    z = _host(t)
+    ids, values = _distill_case(rng, z, T)
+    w = np.full(len(z), T, np.float32)   # a gradient of ordinary size
+    ref = ot.distill(z, ids, values, T, None, w)
+    tol = _distill_tol(z, ids, values, T, ref, dtype, w)[1]
+    args = t.repeat(copies, 1), _dev(ids).repeat(copies, 1), _dev(values).repeat(copies, 1)
+    dw = _dev(w).repeat(copies)
+    a = sv.spec_verify_distill(*args, temperature=T, row_weight=dw, want_grad=True)
+    b = sv.spec_verify_distill_backward(*args, a.stats, dw, temperature=T)
+    torch.cuda.synchronize()
+    for grad in (a.grad, b):
+        for k in range(copies):
+            far = np.abs(_host(grad[k * len(z): (k + 1) * len(z)]) - ref[1])
+            assert np.all(far <= tol), (k, np.argwhere(~(far <= tol))[:5], np.nanmax(far - tol))
