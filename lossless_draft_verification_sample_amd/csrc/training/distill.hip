@@ -34,11 +34,17 @@ __device__ __forceinline__ bool filled(const DistillArgs& a, int32_t id, float t
   return id >= 0 && id < a.V && t / a.temperature != -INFINITY;
 }
 
+// A row of -inf. One of NaN, or of NaN and -inf, has the largest logit -inf too (NaN do not
+// count in a maximum), but a sum of NaN.
+__device__ __forceinline__ bool rules_out_all(float m, double logsum) {
+  return m == -INFINITY && logsum == -INFINITY;
+}
+
 // The loss's terms p (log p - log q) are differences of logarithms that nearly agree
 // for the tokens that count, and there are few of them: they are made in float64.
 // log q of a kept token with logit z, of a row with these statistics.
 __device__ __forceinline__ double log_q(const DistillArgs& a, float z, float m, double logsum) {
-  return m == -INFINITY ? (double)-INFINITY : ((double)z - (double)m) * a.inv_t64 - logsum;
+  return rules_out_all(m, logsum) ? (double)-INFINITY : ((double)z - (double)m) * a.inv_t64 - logsum;
 }
 
 // Teacher's masses of row r into LDS (an empty slot: id -1, mass 0); returns P.
@@ -135,7 +141,7 @@ struct Density {
   __device__ __forceinline__ Density(const DistillArgs& a, float P, float weight, float m_, float logsum) {
     m = m_;
     g = weight * a.inv_t;
-    none = P == 0.0f || m == -INFINITY;
+    none = P == 0.0f || rules_out_all(m, logsum);
     const float ls2 = logsum * LOG2E;
     if (fabsf(m * a.c) < REF_RANGE) {
       ref = rintf(__builtin_fmaf(m, a.c, ls2));

@@ -187,3 +187,33 @@ def test_distill_gradient_of_finite_masks_and_small_temperatures(dtype, copies, 
         for k in range(copies):
             far = np.abs(_host(grad[k * len(z): (k + 1) * len(z)]) - ref[1])
             assert np.all(far <= tol), (k, np.argwhere(~(far <= tol))[:5], np.nanmax(far - tol))
+
+
+# ---------------------------------------------------------------- rows of NaN, teachers of the lowest value
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("copies,V", [(1, 9001), (300, 9001), (1, 20011), (150, 20011), (3, 82001), (1, 160001)])
+def test_distill_rows_of_nan_are_not_empty_rows(dtype, copies, V):
+    """NaN makes a row's loss and gradient NaN also where no other logit is above -inf."""
+    import torch
+    sv = _sv()
+    z = np.full((5, V), -np.inf, np.float32)
+    z[0] = np.nan
+    z[1, V // 2] = np.nan                     # NaN among -inf
+    z[2, 0] = z[2, V - 1] = np.nan
+    ids = np.array([[5, 6]] * 5, np.int32)
+    ids[4] = -1                               # nothing kept: 0 whatever the row holds
+    z[4] = np.nan
+    args = [_dev(np.repeat(x, copies, 0)) for x in (z, ids, np.ones((5, 2), np.float32))]
+    args[0] = args[0].to({"bf16": torch.bfloat16, "f32": torch.float32}[dtype])
+    only = sv.spec_verify_distill(*args)
+    both = sv.spec_verify_distill(*args, want_grad=True)
+    alone = sv.spec_verify_distill_backward(*args, both.stats)
+    torch.cuda.synchronize()
+    for loss in (only.loss, both.loss):
+        x = loss.reshape(5, copies)
+        assert x[:3].isnan().all() and bool((x[3] == np.inf).all()) and not x[4].any()
+    for grad in (both.grad, alone):
+        x = grad.reshape(5, copies, V)
+        assert x[:3].isnan().all() and not x[3:].any()
