@@ -48,7 +48,9 @@ __device__ __forceinline__ double log_q(const DistillArgs& a, float z, float m, 
 }
 
 // Teacher's masses of row r into LDS (an empty slot: id -1, mass 0); returns P.
-// log p_k, which the loss needs besides, comes back through L.lp.
+// log p_k, which the loss needs besides, comes back through L.lp: the distance to the
+// largest logit less the log of the sum, which would be lost in their sum where the
+// logits are large (a teacher row of one far value).
 __device__ float teacher(const DistillArgs& a, DisLds& L, int64_t r) {
   const int tid = threadIdx.x;
   float tm = -INFINITY;
@@ -62,6 +64,7 @@ __device__ float teacher(const DistillArgs& a, DisLds& L, int64_t r) {
   }
   double lse;
   if (a.tlse) {
+    tm = 0.0f;
     lse = a.tlse[r];
   } else {
     tm = block_max<DIS_THREADS>(tm, L.red);
@@ -69,11 +72,11 @@ __device__ float teacher(const DistillArgs& a, DisLds& L, int64_t r) {
     for (int k = tid; k < a.K; k += DIS_THREADS)
       if (L.id[k] >= 0) s += exp(((double)L.p[k] - (double)tm) * a.inv_t64);
     s = block_sum<DIS_THREADS>(s, L.red64);
-    lse = (double)tm * a.inv_t64 + log(s);
+    lse = log(s);
   }
   float P = 0.0f;
   for (int k = tid; k < a.K; k += DIS_THREADS) {
-    const double lp = (double)L.p[k] * a.inv_t64 - lse;
+    const double lp = ((double)L.p[k] - (double)tm) * a.inv_t64 - lse;
     L.lp[k] = lp;
     L.p[k] = L.id[k] >= 0 ? (float)exp(lp) : 0.0f;
     P += L.p[k];
@@ -350,12 +353,13 @@ __global__ __launch_bounds__(HOLD_THREADS, 2 * HOLD_PER_CU[SIZE]) void distill_h
     const float m = sum.m;
     const double logsum = log_of(sum);
 
-    double lse;
+    double lse;   // log p_k: as teacher()'s
+    float tm = 0.0f;
     if (a.tlse) {
       lse = a.tlse[r];
     } else {
-      float tm = -INFINITY;
       double ts = 0.0;
+      tm = -INFINITY;
 #pragma unroll
       for (int i = 0; i < SLOTS; ++i)
         if (id[i] >= 0) tm = fmaxf(tm, t[i]);
@@ -363,14 +367,14 @@ __global__ __launch_bounds__(HOLD_THREADS, 2 * HOLD_PER_CU[SIZE]) void distill_h
 #pragma unroll
       for (int i = 0; i < SLOTS; ++i)
         if (id[i] >= 0) ts += exp(((double)t[i] - (double)tm) * a.inv_t64);
-      lse = (double)tm * a.inv_t64 + log(block_sum<HOLD_THREADS>(ts, L.red64));
+      lse = log(block_sum<HOLD_THREADS>(ts, L.red64));
     }
     float P = 0.0f;
     double loss = 0.0;
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i) {
       const int k = tid + i * HOLD_THREADS;
-      const double lp = (double)t[i] * a.inv_t64 - lse;
+      const double lp = ((double)t[i] - (double)tm) * a.inv_t64 - lse;
       const double p = id[i] >= 0 ? exp(lp) : 0.0;
       P += (float)p;
       if (!(p == 0.0))   // an empty slot, or a mass that is 0: no part in the loss

@@ -52,13 +52,11 @@ def distill(z, ids, t, temperature=1.0, teacher_lse=None, row_weight=None):
         slots = [k for k in range(K) if 0 <= ids[r, k] < V and t[r, k] > -np.inf]
         if not slots:
             continue
-        if teacher_lse is None:
-            tm, tl = log_sum_exp(t[r, slots])
-            L = tm + tl
-        else:
-            L = float(teacher_lse[r])
+        # the largest and the logarithm of the sum apart: added, they lose the second
+        # where the logits are large
+        tm, tl = log_sum_exp(t[r, slots]) if teacher_lse is None else (0.0, float(teacher_lse[r]))
         for k in slots:
-            log_p = t[r, k] - L
+            log_p = t[r, k] - tm - tl
             p = np.exp(log_p)
             ps[r, k] = p
             pv[r, ids[r, k]] += p

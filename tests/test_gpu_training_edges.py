@@ -217,3 +217,43 @@ def test_distill_rows_of_nan_are_not_empty_rows(dtype, copies, V):
     for grad in (both.grad, alone):
         x = grad.reshape(5, copies, V)
         assert x[:3].isnan().all() and not x[3:].any()
+
+
+# ---------------------------------------------------------------- teachers of the lowest value
+
+
+def _check_far_teacher(copies, V, values, T, want_p):
+    """Loss and gradients of student rows against teachers with these exact masses."""
+    import torch
+    sv, rng = _sv(), np.random.default_rng(6)
+    R = len(values)
+    z = (rng.standard_normal((R, V)) * 3).astype(np.float32)
+    ids = np.array([[3, 9, 4000, V - 1]] * R, np.int32)
+    # the same masses from ordinary teacher logits: the exact results, and their bounds
+    with np.errstate(divide="ignore"):
+        near = np.log(np.array(want_p)) * float(np.float32(T))
+    ref = ot.distill(z, ids, near, float(np.float32(T)))
+    assert np.allclose(ref[2], want_p, rtol=1e-14, atol=0)
+    lt, gt = _distill_tol(z.astype(np.float64), ids, near.astype(np.float32), T, ref, "f32", None)
+    args = [_dev(np.repeat(x, copies, 0)) for x in (z, ids, np.array(values, np.float32))]
+    a = sv.spec_verify_distill(*args, temperature=T, want_grad=True)
+    b = sv.spec_verify_distill(*args, temperature=T)
+    g = sv.spec_verify_distill_backward(*args, b.stats, temperature=T)
+    torch.cuda.synchronize()
+    for loss in (a.loss, b.loss):
+        assert np.all(np.abs(_host(loss).reshape(R, copies) - ref[0][:, None]) <= lt[:, None])
+    for grad in (a.grad, g):
+        assert np.all(np.abs(_host(grad).reshape(R, copies, V) - ref[1][:, None]) <= gt[:, None])
+
+
+LOW = -3.3895313892515355e38
+INF = float("inf")
+
+
+@pytest.mark.parametrize("copies,V", [(1, 9001), (300, 9001), (1, 30011), (150, 30011)])
+def test_distill_teachers_of_one_far_value_share_their_mass(copies, V):
+    """Equal teacher logits are a quarter each whatever their size: their log-normaliser
+    is not their value."""
+    far = [-1e10, -1e16, -1e20, LOW, 3e38]
+    _check_far_teacher(copies, V, [[x] * 4 for x in far] + [[-1e20, -INF, -INF, -1e20]], 1.0,
+                       [[0.25] * 4] * len(far) + [[0.5, 0, 0, 0.5]])
