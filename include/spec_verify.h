@@ -344,7 +344,7 @@ int spec_verify_top_logits(const void* logits, int64_t logits_stride, sv_dtype d
  *   logits         [R][V] of dtype: the drafter's (student's) rows.
  *   teacher_ids    [R][K] int32, teacher_logits [R][K] float, contiguous, in any
  *                  order, as spec_verify_top_logits writes them. A slot whose id
- *                  lies outside [0, V) or whose tempered logit is -inf is empty;
+ *                  lies outside [0, V) or whose logit is -inf is empty;
  *                  an id may appear more than once: its masses add up.
  *   teacher_lse    [R] float (spec_verify_top_logits at the same temperature), or
  *                  NULL.

@@ -29,9 +29,10 @@ struct DisLds {
   MaxSum scratch[DIS_THREADS / WAVE];
 };
 
-// A slot is filled when its id is a token and its tempered logit is not -inf.
+// A slot is filled when its id is a token and its logit is not -inf. (Not its tempered
+// logit: that may pass float32's range, but its mass is made in float64.)
 __device__ __forceinline__ bool filled(const DistillArgs& a, int32_t id, float t) {
-  return id >= 0 && id < a.V && t / a.temperature != -INFINITY;
+  return id >= 0 && id < a.V && t != -INFINITY;
 }
 
 // A row of -inf. One of NaN, or of NaN and -inf, has the largest logit -inf too (NaN do not

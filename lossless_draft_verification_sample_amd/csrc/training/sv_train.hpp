@@ -293,7 +293,7 @@ struct DistillArgs {
   const float* weight;       // [R] or nullptr (1): d total / d loss
   int R, V, K;
   int parts;                 // workgroups per row
-  float temperature, inv_t, c;
+  float inv_t, c;            // 1 / T, log2(e) / T
   double inv_t64;
   float* loss;               // [R] or nullptr (backward alone)
   float* stats;              // [R][2]: largest logit, log of the sum; or nullptr

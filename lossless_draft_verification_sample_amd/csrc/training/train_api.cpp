@@ -114,7 +114,6 @@ int distill_args(const void* logits, int64_t logits_stride, sv_dtype dtype, int3
   a->K = K;
   a->parts = distill_parts(R, V, dtype);
   a->hold = grad ? distill_hold(R, V, dtype) : -1;   // the loss alone streams faster
-  a->temperature = temperature;
   a->inv_t = 1.0f / temperature;
   a->inv_t64 = 1.0 / temperature;
   a->c = (float)((double)LOG2E_D / temperature);

@@ -257,3 +257,12 @@ def test_distill_teachers_of_one_far_value_share_their_mass(copies, V):
     far = [-1e10, -1e16, -1e20, LOW, 3e38]
     _check_far_teacher(copies, V, [[x] * 4 for x in far] + [[-1e20, -INF, -INF, -1e20]], 1.0,
                        [[0.25] * 4] * len(far) + [[0.5, 0, 0, 0.5]])
+
+
+@pytest.mark.parametrize("copies,V", [(1, 9001), (300, 9001), (1, 30011), (150, 30011)])
+@pytest.mark.parametrize("T", [0.5, 1e-3])
+def test_distill_teachers_beyond_the_tempered_range(copies, V, T):
+    """A finite teacher logit keeps its slot also where its tempered value passes
+    float32's range; next to an ordinary one it has no mass."""
+    _check_far_teacher(copies, V, [[LOW] * 4, [LOW, T, LOW, T], [-INF, LOW, -INF, LOW]], T,
+                       [[0.25] * 4, [0, 0.5, 0, 0.5], [0, 0.5, 0, 0.5]])
