@@ -181,6 +181,20 @@ int64_t piece_rows(const CeShape& s, int64_t bytes) {
   return rows < all ? rows : all;
 }
 
+// Tokens packed at a time. Heads whose width is whole groups of 16 bytes are read in place, but
+// for odd strides, and do not get room for a long piece that only those would use: one
+// state of 4,096 over 128,256 tokens had a workspace of 768 MB, its logits take 0.5. Odd strides
+// pay for it in launches that do not fill the CUs: 17 states of 4,096 over 151,936 tokens, rows
+// 4,099 apart, 880 us instead of 836, 200 states 1,410 instead of 970, a step of 64 of float32
+// over 32,000 1,882 instead of 1,087. Other widths are packed by every call, which has the whole
+// piece.
+int64_t packed_rows(const CeShape& s, int64_t piece) {
+  if (s.planes == 3 || s.D % s.per16()) return piece;
+  int64_t rows = CE_PIECE_BYTES / s.row_bytes(s.kp) / CE_PIECE_STEP * CE_PIECE_STEP;
+  if (rows < 4 * CE_PIECE_STEP) rows = 4 * CE_PIECE_STEP;
+  return rows < piece ? rows : piece;
+}
+
 struct CeForward {
   int64_t piece;               // tokens a piece where the weight is packed
   size_t partial, zlabel, hidden, weight, total;
@@ -188,7 +202,7 @@ struct CeForward {
 CeForward ce_forward(const CeShape& s) {
   CeForward f;
   Carver c;
-  f.piece = piece_rows(s, s.row_bytes(s.kp));
+  f.piece = packed_rows(s, piece_rows(s, s.row_bytes(s.kp)));
   f.partial = c.take((size_t)(ceil_div(s.V, sv::ce_tile(s.V, s.N, s.planes).bm) * s.N) * sizeof(sv::MaxSum));
   f.zlabel = c.take((size_t)s.N * sizeof(float));
   f.hidden = c.take((size_t)(s.N * s.row_bytes(s.kp)));
@@ -230,7 +244,7 @@ int dh_splits(const CeShape& s, int64_t piece, int64_t ld) {
 }
 
 struct CeBackward {
-  int64_t piece, acc_ld;
+  int64_t piece, packed, acc_ld;   // tokens a piece, and a piece that is packed
   int splits;
   size_t hidden, weight, dz, acc, total;
 };
@@ -238,10 +252,11 @@ CeBackward ce_backward(const CeShape& s, bool want_h) {
   CeBackward b;
   Carver c;
   b.piece = piece_rows(s, s.row_bytes(s.N > s.kp ? s.N : s.kp));
+  b.packed = packed_rows(s, b.piece);
   b.acc_ld = round_up(s.D, 4);
   b.splits = dh_splits(s, b.piece, b.acc_ld);
   b.hidden = c.take((size_t)(s.N * s.row_bytes(s.kp)));
-  b.weight = c.take((size_t)(b.piece * s.row_bytes(s.kp)));
+  b.weight = c.take((size_t)(b.packed * s.row_bytes(s.kp)));
   b.dz = c.take((size_t)s.dz_bytes(s.N * b.piece));
   b.acc = c.take(want_h ? (size_t)(b.splits * s.N * b.acc_ld) * 4 : 0);
   b.total = c.off;
@@ -429,8 +444,9 @@ int spec_verify_linear_ce_backward(const void* hidden, int64_t hidden_stride, co
   float* acc = (float*)(ws + b.acc);
   Operand h, w;
   if (ce_operand(hidden, hidden_stride, 0, N, s, ws + b.hidden, st, &h)) return SV_EHIP;
-  for (int64_t v0 = 0; v0 < V; v0 += b.piece) {
-    const int64_t rows = V - v0 < b.piece ? V - v0 : b.piece;
+  const int64_t piece = ce_direct(weight, weight_stride, s) ? b.piece : b.packed;
+  for (int64_t v0 = 0; v0 < V; v0 += piece) {
+    const int64_t rows = V - v0 < piece ? V - v0 : piece;
     const int64_t ldz = round_up(rows, s.depth());
     if (ce_operand(weight, weight_stride, v0, rows, s, ws + b.weight, st, &w)) return SV_EHIP;
     const sv::CeDzOut o{labels, stats, grad_loss, (int)v0, V, dz, ldz, N * ldz};

@@ -62,6 +62,18 @@ def test_linear_ce_gradients_keep_dz_beyond_bfloat16(N, D, V, pad):
         assert np.all(far <= 0), (far.max(), np.argwhere(far > 0)[:4], (far > 0).mean())
 
 
+@pytest.mark.parametrize("N,D,V,pad,dtype", [(5, 4096, 40003, 3, "bf16"), (40, 2048, 40003, 1, "f32"),
+                                             (150, 4096, 20100, 5, "bf16")])
+def test_linear_ce_wide_heads_at_odd_strides(N, D, V, pad, dtype):
+    """A head that is read in place but for its stride is packed in several pieces, the
+    last of them short."""
+    from tests.test_gpu_training import _check_ce
+    rng = np.random.default_rng(N + D)
+    h, w, y = _head(rng, N, D, V, dtype, pad)
+    y[:4] = [V - 1, 16384, 16383, V - 100]
+    _check_ce(h, w, y, np.full(N, 1 / N, np.float32), dtype)
+
+
 # ---------------------------------------------------------------- finite masks
 
 
