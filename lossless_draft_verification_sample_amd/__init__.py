@@ -337,6 +337,11 @@ def spec_verify_commit(tokens, num_accepted, kv_len, slots=None, gamma_b=None, o
 
 
 # ------------------------------------------------------- training the drafter
+#
+# Autograd records none of these calls: what they return has no graph, whether the
+# inputs require gradients or not, and the gradients are those the *_backward calls and
+# want_grad give. A program that trains through autograd makes the calls in the forward
+# and backward of a torch.autograd.Function of its own.
 
 
 _INT32_MAX = 2 ** 31 - 1
@@ -438,6 +443,15 @@ def _space(workspace, need, device):
     return _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(), workspace
 
 
+def _written(out):
+    """Tells autograd that a caller's outputs were written, as an operation in place would:
+    a backward pass that had saved one of them (logits that were overwritten by their
+    gradient) then raises instead of using what it holds now."""
+    for t in out or ():
+        if t is not None:
+            _torch().autograd.graph.increment_version(t)
+
+
 def spec_verify_top_logits_workspace_bytes(R, V, K, dtype=SV_BF16):
     return int(_lib.load().spec_verify_top_logits_workspace_bytes(int(R), int(V), int(K), int(dtype)))
 
@@ -458,7 +472,7 @@ def spec_verify_top_logits(logits, k, temperature=1.0, want_lse=True, workspace=
     lib = lib or _lib.load()
     ptr, stride = _matrix(logits, "logits")
     dt, dev, lead, V = _dtype_code(logits), logits.device, tuple(logits.shape[:-1]), logits.shape[-1]
-    R, k = logits.numel() // V, int(k)
+    R, k, given = logits.numel() // V, int(k), out is not None
     if not 1 <= k <= SV_MAX_TOP:
         raise SpecVerifyError(SV_EINVAL, "spec_verify_top_logits")
     ctx, handle = _on(dev, stream)
@@ -480,6 +494,8 @@ def spec_verify_top_logits(logits, k, temperature=1.0, want_lse=True, workspace=
     del keep
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_verify_top_logits")
+    if given:
+        _written(out)
     return out
 
 
@@ -535,7 +551,8 @@ def spec_verify_distill(logits, teacher_ids, teacher_logits, temperature=1.0, te
     and teacher_logits [..., K] float32 as spec_verify_top_logits returns them,
     teacher_lse [...] float32 (its lse at the same temperature) or None to
     renormalise over the kept ids; row_weight [...] float32 scales the gradient's
-    rows (not the loss). out: a DistillOut; its grad may be `logits` itself.
+    rows (not the loss). out: a DistillOut; its grad may be `logits` itself. Autograd
+    records nothing here; outputs given by the caller count as changed in place.
     Returns DistillOut(loss [...], stats [..., 2], grad like logits or None);
     stats serve spec_verify_distill_backward.
     """
@@ -557,18 +574,21 @@ def spec_verify_distill(logits, teacher_ids, teacher_logits, temperature=1.0, te
     del keep
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_verify_distill")
+    _written(out)
     return DistillOut(loss, stats, grad)
 
 
 def spec_verify_distill_backward(logits, teacher_ids, teacher_logits, stats, grad_loss=None,
                                  temperature=1.0, teacher_lse=None, out=None, stream=None, lib=None):
     """Gradient of spec_verify_distill's loss from its stats; grad_loss [...]
-    float32 or None (1). out: the gradient's tensor, which may be `logits`.
+    float32 or None (1). out: the gradient's tensor, which may be `logits` (then changed
+    in place, for autograd too).
     Returns the gradient, like logits."""
     torch = _torch()
     lib = lib or _lib.load()
     args, dev, lead = _distill_inputs(logits, teacher_ids, teacher_logits, teacher_lse)
     ctx, handle = _on(dev, stream)
+    given = out is not None
     with ctx:
         out, gptr, gstride = _grad_out(out, logits, "out")
         if stats is None:
@@ -578,6 +598,8 @@ def spec_verify_distill_backward(logits, teacher_ids, teacher_logits, stats, gra
             _vector(grad_loss, "grad_loss", torch.float32, lead, dev), gptr, gstride, handle)
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_verify_distill_backward")
+    if given:
+        _written((out,))
     return out
 
 
@@ -610,7 +632,8 @@ def spec_verify_linear_ce(hidden, weight, labels, workspace=None, out=None, stre
 
     hidden [..., D] and weight [V, D] (bf16 or fp32, rows at one stride each),
     labels [...] int32; rows whose label lies outside [0, V), such as -100, are
-    left out (loss 0).
+    left out (loss 0). Autograd records nothing here: the gradients come from
+    spec_verify_linear_ce_backward.
     Returns LinearCeOut(loss [...], stats [..., 2]), both float32; stats serve
     spec_verify_linear_ce_backward.
     """
@@ -618,6 +641,7 @@ def spec_verify_linear_ce(hidden, weight, labels, workspace=None, out=None, stre
     lib = lib or _lib.load()
     args, N, dev, lead = _ce_inputs(hidden, weight, labels)
     V, D = weight.shape
+    given = out is not None
     ctx, handle = _on(dev, stream)
     with ctx:
         if out is None:
@@ -631,6 +655,8 @@ def spec_verify_linear_ce(hidden, weight, labels, workspace=None, out=None, stre
     del keep
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_verify_linear_ce")
+    if given:
+        _written(out)
     return out
 
 
@@ -664,6 +690,8 @@ def spec_verify_linear_ce_backward(hidden, weight, labels, stats, grad_loss=None
     del keep
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_verify_linear_ce_backward")
+    if out is not None:
+        _written((gh, gw))
     return LinearCeGrads(gh, gw)
 
 

@@ -278,3 +278,46 @@ def test_distill_teachers_beyond_the_tempered_range(copies, V, T):
     float32's range; next to an ordinary one it has no mass."""
     _check_far_teacher(copies, V, [[LOW] * 4, [LOW, T, LOW, T], [-INF, LOW, -INF, LOW]], T,
                        [[0.25] * 4, [0, 0.5, 0, 0.5], [0, 0.5, 0, 0.5]])
+
+
+# ---------------------------------------------------------------- autograd
+
+
+def test_outputs_have_no_graph_and_count_as_changed_in_place():
+    """The calls are not recorded; a tensor they overwrite raises its version, so that a
+    backward pass which saved it refuses to use it."""
+    import torch
+    sv, rng = _sv(), np.random.default_rng(1)
+    ids, values = _dev(np.zeros((4, 3), np.int32)), _dev(np.ones((4, 3), np.float32))
+    x = _dev(rng.standard_normal((4, 700)).astype(np.float32)).requires_grad_()
+    w = _dev(rng.standard_normal((50, 700)).astype(np.float32)).requires_grad_()
+    y = _dev(np.arange(4, dtype=np.int32))
+
+    def saved():
+        z = x.exp()                 # exp keeps its result for the backward pass
+        return z, z.sum()
+
+    z, total = saved()
+    kept = sv.spec_verify_distill(z, ids, values, want_grad=True)
+    assert not (kept.loss.requires_grad or kept.grad.requires_grad)
+    total.backward()                # nothing was overwritten
+    z, total = saved()
+    sv.spec_verify_distill(z, ids, values, out=sv.DistillOut(kept.loss, kept.stats, z.detach()))
+    with pytest.raises(RuntimeError, match="inplace"):
+        total.backward()
+    z, total = saved()
+    sv.spec_verify_distill_backward(z, ids, values, kept.stats, out=z.detach())
+    with pytest.raises(RuntimeError, match="inplace"):
+        total.backward()
+    ce = sv.spec_verify_linear_ce(x, w, y)
+    assert not ce.loss.requires_grad
+    top = sv.spec_verify_top_logits(x, 3)
+    assert not top.values.requires_grad
+    outs = [torch.zeros(4, 700, device="cuda:0"), torch.zeros(50, 700, device="cuda:0")]
+    sv.spec_verify_linear_ce_backward(x, w, y, ce.stats, out=sv.LinearCeGrads(*outs))
+    sv.spec_verify_linear_ce(x, w, y, out=ce)
+    sv.spec_verify_top_logits(x, 3, out=top)
+    torch.cuda.synchronize()
+    assert all(t._version == 1 for t in (*outs, *ce, *top))
+    with torch.inference_mode():
+        sv.spec_verify_linear_ce(x, w, y, out=sv.spec_verify_linear_ce(x, w, y))
