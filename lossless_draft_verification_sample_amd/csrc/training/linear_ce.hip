@@ -96,12 +96,17 @@ __device__ __forceinline__ int thread_again(int wave) {
 // memory operation, and the caller waits for it (WAIT_VM0).
 // In assembly because the compiler, which cannot tell the two halves of LDS apart,
 // else waits for it before the next transposing read (dW 632 instead of 450 us a
-// piece of 16,384 tokens at 4,096 states of 4,096). It has no result register.
+// piece of 16,384 tokens at 4,096 states of 4,096). It has no result register. m0 is
+// no register the compiler allocates (it warns that it cannot keep a value there), but
+// it does place writes of m0 of its own, and the clobber tells it where they end.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void copy_to_lds(uint64_t base, uint32_t byte_off, uint32_t lds) {
   const vs32x4 rsrc = {(int)(uint32_t)base, (int)(uint32_t)(base >> 32), (int)BEYOND, RSRC_WORD3};
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :: "s"(lds), "v"(byte_off), "s"(rsrc) : "memory");
+               :: "s"(lds), "v"(byte_off), "s"(rsrc) : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // One operand of a tile, of bfloat16 (uint16_t) or float elements: how ROWS rows by one
 // step of depth (LINE bytes of a row) get from memory into LDS, and its fragments
