@@ -15,7 +15,6 @@ static_assert(sv::TOP_CAP - sv::TOP_STEP >= sv::TOP_MAX_K, "a cut list leaves ro
 namespace {
 
 constexpr size_t WS_ALIGN = 256;
-constexpr float LOG2E_D = sv::LOG2E;
 
 size_t align_up(size_t x) { return (x + WS_ALIGN - 1) / WS_ALIGN * WS_ALIGN; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -28,6 +27,11 @@ bool workspace_ok(const void* p, size_t have, size_t need) {
   return need == 0 || (p && aligned(p, WS_ALIGN) && have >= need);
 }
 bool temperature_ok(float t) { return t > 0.0f && isnormal(t); }   // 1 / t is finite too
+
+// log2(e) / T, the factor of the kernels' exponents. One float, so that an exponent is one
+// fused product: off by 2^-25 of a logit's distance to the row's largest, which for the
+// tokens that count is within the rounding of the exponent itself.
+float exponent_factor(float temperature) { return (float)(M_LOG2E / temperature); }
 
 // Threads of a launch, 512 a workgroup, are counted in 32 bits.
 constexpr int64_t MAX_WORKGROUPS = 1 << 23;
@@ -116,7 +120,7 @@ int distill_args(const void* logits, int64_t logits_stride, sv_dtype dtype, int3
   a->hold = grad ? distill_hold(R, V, dtype) : -1;   // the loss alone streams faster
   a->inv_t = 1.0f / temperature;
   a->inv_t64 = 1.0 / temperature;
-  a->c = (float)((double)LOG2E_D / temperature);
+  a->c = exponent_factor(temperature);
   a->grad = grad;
   a->grad_stride = grad_stride;
   return SV_OK;
@@ -328,7 +332,7 @@ int spec_verify_top_logits(const void* logits, int64_t logits_stride, sv_dtype d
   a.V = V;
   a.K = K;
   a.parts = L.parts;
-  a.c = (float)((double)LOG2E_D / temperature);
+  a.c = exponent_factor(temperature);
   a.temperature = temperature;
   a.ids = out_ids;
   a.values = out_values;
