@@ -74,6 +74,45 @@ def test_linear_ce_wide_heads_at_odd_strides(N, D, V, pad, dtype):
     _check_ce(h, w, y, np.full(N, 1 / N, np.float32), dtype)
 
 
+@pytest.mark.parametrize("N,D,V,pad,border", [
+    (129, 4096, 65636, 0, 65536), (129, 4095, 65636, 0, 65536),      # in place; packed, forward too
+    (1030, 136, 52324, 0, 52224), (1030, 161, 52324, 0, 52224),      # several splits of dh
+    (1030, 136, 52224 + 129, 3, 52224), (2050, 64, 28772, 0, 28672)])
+def test_linear_ce_large_tiles_over_two_pieces(N, D, V, pad, border):
+    """bfloat16 in the largest tile: dh added up over pieces of the vocabulary, the last of
+    them of few tokens, with labels on both sides of the border. Exact values by float64
+    products on the device; bounds as in _gradient_tol."""
+    import torch
+    sv, rng = _sv(), np.random.default_rng(N + D)
+    h, w, y = _head(rng, N, D, V, "bf16", pad)
+    y[:6] = [border - 1, border, border + 1, V - 1, 0, border]
+    y, g = _dev(y), _dev(rng.uniform(0.2, 2.0, N).astype(np.float32) / N)
+    a = sv.spec_verify_linear_ce(h, w, y)
+    b = sv.spec_verify_linear_ce_backward(h, w, y, a.stats, g)
+    torch.cuda.synchronize()
+    hh, ww = h.double(), w.double()
+    z = torch.mm(hh, ww.t().contiguous())
+    m = z.amax(1)
+    ls = torch.log(torch.exp(z - m[:, None]).sum(1))
+    used = (y >= 0) & (y < V)
+    at = torch.where(used, y, 0).long()[:, None]
+    loss = torch.where(used, m + ls - z.gather(1, at)[:, 0], 0.0)
+    zt = 8 * D ** 0.5 * U * torch.mm(hh.abs(), ww.abs().t().contiguous()).amax(1)
+    rel = 2 * zt + 8 * U * (z.abs().amax(1) + 30) + _sum_tol(V)
+    assert ((a.loss.double() - loss).abs() <= rel + 4 * U * loss.abs()).all()
+    q = torch.exp(z - (m + ls)[:, None])
+    gg = torch.where(used, g.double(), 0.0)[:, None]
+    dz = q.scatter_add(1, at, torch.full((N, 1), -1.0, dtype=torch.float64, device=z.device)) * gg
+    dt = gg * (rel[:, None] * q + 4 * U * (dz != 0)) + 2.0 ** -16 * dz.abs()
+    del z, q
+    for got, x, xt, other in ((b.hidden, dz, dt, ww), (b.weight, dz.t().contiguous(), dt.t().contiguous(), hh)):
+        want = torch.mm(x, other)
+        tol = (torch.mm(xt, other.abs()) + 8 * (2 * x.shape[1]) ** 0.5 * U * torch.mm(x.abs(), other.abs())
+               + HALF["bf16"] * want.abs() + 1e-37)
+        far = (got.double() - want).abs() - tol
+        assert bool((far <= 0).all()), (far.max().item(), torch.nonzero(far > 0)[:4].tolist())
+
+
 # ---------------------------------------------------------------- finite masks
 
 
