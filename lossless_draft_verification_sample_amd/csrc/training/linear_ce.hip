@@ -750,10 +750,11 @@ int gemm(const CeGemm& g, const typename Epi::Args& ea, hipStream_t st) {
 // reads LDS least: 1,300 TFLOP/s in 256 x 256, 930 in 256 x 128, 910 to 1,010 in 128 x 128.
 // dh and dW of less than 128 columns (the rows of A) take the smaller tile too.
 CeTile ce_tile(int64_t M, int64_t N, int planes) {
-  if (planes == 3) return M <= 128 ? CeTile{64, 128, 2} : CeTile{256, 128, 1};
-  if (N <= 32) return CeTile{64, 32, 6};
-  if (N <= 128 || M <= 128 || planes == 0) return CeTile{128, 64, 3};
-  return CeTile{256, 256, 1};
+  if (planes == 3) return M <= 128 ? CeTile{64, 128, 2, 2} : CeTile{256, 128, 1, 1};
+  const bool parts = planes == 1;   // dz in two
+  if (N <= 32) return CeTile{64, 32, 6, parts ? 5 : 6};
+  if (N <= 128 || M <= 128 || planes == 0) return CeTile{128, 64, 3, parts ? 2 : 3};
+  return CeTile{256, 256, 1, 1};
 }
 
 int launch_ce_stats(const CeGemm& g, const CeStatsOut& o, hipStream_t st) {

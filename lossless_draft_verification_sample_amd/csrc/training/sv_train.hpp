@@ -311,7 +311,8 @@ constexpr int CE_LINE = 128;       // most bytes of a row that one step of the p
 constexpr int CE_MAX_D = 1 << 22;
 
 struct CeTile {
-  int bm, bn, per_cu;   // per_cu: workgroups that a CU holds at once, by LDS
+  int bm, bn;
+  int per_cu, per_cu_dz;   // workgroups that a CU holds at once, by LDS; of the products of dz
 };
 CeTile ce_tile(int64_t M, int64_t N, int planes);
 

@@ -170,7 +170,7 @@ bool ce_shape(int32_t N, int32_t D, int32_t V, sv_dtype dtype, CeShape* s) {
 
 // Tokens of a piece whose operands take `bytes` a token. Rounds do not exceed the CUs: with
 // three columns of tiles, 85 rows of them make one (86 would take a second one for two
-// tiles: 622 states of 2,048 over 151,936 tokens 2,251 us a step instead of 2,014).
+// tiles: 622 states of 2,048 over 151,936 tokens 2,734 us a step instead of 2,483).
 int64_t piece_rows(const CeShape& s, int64_t bytes) {
   const sv::CeTile t = sv::ce_tile(s.V, s.N, s.planes);
   int64_t round = CE_CUS * t.per_cu / ceil_div(s.N, t.bn) * t.bm / CE_PIECE_STEP * CE_PIECE_STEP;
@@ -218,11 +218,11 @@ CeForward ce_forward(const CeShape& s) {
 // dh has few tiles and a long depth, a piece of the vocabulary: workgroups that share a
 // tile's depth. The fewest microseconds of a piece: rounds of workgroups over the CUs, and
 // the sums that every split reads and writes. As many splits as give each CU its fill
-// take a round too many instead: 622 states of 2,048 over 151,936 tokens 2,466 us a step
-// instead of 2,259, 2,742 of 384 2,572 instead of 2,284.
+// take a round too many instead: 622 states of 2,048 over 151,936 tokens 2,934 us a step
+// instead of 2,499, 2,742 of 384 3,231 instead of 2,832.
 int dh_splits(const CeShape& s, int64_t piece, int64_t ld) {
   const sv::CeTile t = sv::ce_tile(s.D, s.N, s.planes);
-  const int64_t tiles = ceil_div(s.D, t.bm) * ceil_div(s.N, t.bn), places = CE_CUS * t.per_cu;
+  const int64_t tiles = ceil_div(s.D, t.bm) * ceil_div(s.N, t.bn), places = CE_CUS * t.per_cu_dz;
   const int64_t steps = piece / s.depth() * (s.planes == 3 || t.bm == 256 ? 2 : 1);
   const double rate = s.planes == 1 ? 1200e6 : s.planes == 3 ? 180e6 : 120e6;   // flop a us
   const double tile_us = 2.0 * t.bm * t.bn * piece * (s.planes == 1 ? 2 : 1) / (rate / places);
