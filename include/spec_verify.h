@@ -393,8 +393,11 @@ int spec_verify_distill_backward(const void* logits, int64_t logits_stride, sv_d
  * gradients) they meet NaN.
  * Limits: 1 <= N <= 2^22, 1 <= D <= 2^22, 1 <= V < 2^31 - 1024, and 2^23 tiles of
  * 256 x 256 in N x V and N x D (64 x 32 up to 32 rows, 128 x 64 up to 128, 256 x 128 in
- * float32); SV_ESIZE beyond. bfloat16 matrices with D a multiple of 8, rows on 16 bytes and strides of at
- * most 2^22 are read in place, others are copied into the workspace first. */
+ * float32); SV_ESIZE beyond. Matrices whose rows start on 16 bytes and are whole groups of 16
+ * bytes (D a multiple of 8 in bfloat16, of 4 in float32), at strides of at most 2^22, are read
+ * in place, but for float32 of more than 384 states; others are copied into the workspace
+ * first, the weight a piece at a time. The workspace holds whatever the strides need: for few
+ * states about 128 MB, up to 1 GiB where D is not whole groups of 16 bytes. */
 size_t spec_verify_linear_ce_workspace_bytes(int32_t N, int32_t D, int32_t V, sv_dtype dtype);
 int spec_verify_linear_ce(const void* hidden, int64_t hidden_stride, const void* weight,
                           int64_t weight_stride, sv_dtype dtype, const int32_t* labels, int32_t N,

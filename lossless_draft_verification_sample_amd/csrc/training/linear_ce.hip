@@ -96,7 +96,7 @@ __device__ __forceinline__ int thread_again(int wave) {
 // memory operation, and the caller waits for it (WAIT_VM0).
 // In assembly because the compiler, which cannot tell the two halves of LDS apart,
 // else waits for it before the next transposing read (dW 632 instead of 450 us a
-// piece of 16,384 tokens at 4,096 states of 4,096). It has no result register. m0 is
+// piece of 16,384 tokens at 4,096 states of 4,096, with dz in one part). It has no result register. m0 is
 // no register the compiler allocates (it warns that it cannot keep a value there), but
 // it does place writes of m0 of its own, and the clobber tells it where they end.
 #pragma clang diagnostic push
