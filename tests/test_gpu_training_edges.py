@@ -360,3 +360,45 @@ def test_outputs_have_no_graph_and_count_as_changed_in_place():
     assert all(t._version == 1 for t in (*outs, *ce, *top))
     with torch.inference_mode():
         sv.spec_verify_linear_ce(x, w, y, out=sv.spec_verify_linear_ce(x, w, y))
+
+
+# ---------------------------------------------------------------- two streams, replays of the larger tiles
+
+
+@pytest.mark.parametrize("N,D,V,dtype", [(300, 264, 30000, "bf16"), (20, 100, 30011, "bf16"), (400, 136, 9001, "f32")])
+def test_steps_on_two_streams_and_in_a_graph(N, D, V, dtype):
+    """Steps that run at once on two streams, and a captured one replayed on new inputs with
+    eager steps between: the bits of a step alone."""
+    import torch
+    sv, rng = _sv(), np.random.default_rng(N)
+    sets = []
+    for _ in range(2):
+        h, w, y = _head(rng, N, D, V, dtype)
+        sets.append((h, w, _dev(y)))
+
+    def step(h, w, y):
+        a = sv.spec_verify_linear_ce(h, w, y)
+        return [*a, *sv.spec_verify_linear_ce_backward(h, w, y, a.stats)]
+
+    want = [step(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [[], []]
+    for _ in range(3):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[k].append(step(*sets[k]))
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert all(torch.equal(a, b) for out in got[k] for a, b in zip(out, want[k]))
+    static = [x.clone() for x in sets[0]]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(*static)
+    for turn in (1, 0, 1):
+        for a, b in zip(static, sets[turn]):
+            a.copy_(b)
+        eager = step(*static)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) and torch.equal(a, c) for a, b, c in zip(out, want[turn], eager))
