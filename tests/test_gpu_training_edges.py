@@ -402,3 +402,24 @@ def test_steps_on_two_streams_and_in_a_graph(N, D, V, dtype):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) and torch.equal(a, c) for a, b, c in zip(out, want[turn], eager))
+
+
+def test_top_logits_pass_over_negative_ties():
+    """bfloat16 rows of one negative value take about as long as those of a positive one:
+    once k of them are listed, those that come later are not. (Listed again and again they
+    took twelve times as long.)"""
+    import torch
+    sv, times = _sv(), []
+    for value in (2.5, -2.5):
+        t = torch.full((1152, 151936), value, dtype=torch.bfloat16, device="cuda:0")
+        runs = []
+        for _ in range(7):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            out = sv.spec_verify_top_logits(t, 64)
+            b.record()
+            torch.cuda.synchronize()
+            runs.append(a.elapsed_time(b))
+        times.append(sorted(runs)[3])
+        assert torch.equal(out.ids, torch.arange(64, dtype=torch.int32, device="cuda:0").repeat(1152, 1))
+    assert times[1] < 4 * times[0], times
