@@ -423,6 +423,171 @@ int spec_verify_linear_ce_backward(const void* hidden, int64_t hidden_stride, co
                                    void* out_grad_weight, int64_t grad_weight_stride,
                                    void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------- the verification pass's rows
+ *
+ * What a serving program does to the rows that a verification round reads, before
+ * and after the target model's own layers: rotary positions of queries and keys,
+ * a paged 8-bit cache of keys and values written and read back, attention of a
+ * round's rows over it, and the adjustments of logits that are part of the
+ * sampler and have to be made to the target's and the drafter's rows alike.
+ *
+ * Conventions of these calls
+ *   - A batch has B requests of N rows (N = gamma + 1 in a verification round, 1 for
+ *     plain decoding). Row j of request b stands at position kv_len[b] + j, kv_len as
+ *     in spec_verify_commit. `rows` [B] (device) gives each request's number of
+ *     rows, 0 <= rows[b] <= N (NULL: N). Outputs of rows beyond it are left as
+ *     they were.
+ *   - kv_len, rows and page tables live on the device, so what is wrong in them is only
+ *     seen there. A request whose kv_len or rows is out of range has NaN in all its N rows
+ *     of the outputs, and nothing of it is written to the cache.
+ *   - Sums, softmax statistics and products are float32 or wider whatever the
+ *     inputs' type; results are rounded once.
+ *   - No result depends on the order in which workgroups run.
+ *   - Workspaces as in the training calls: no initialisation, 256-byte aligned,
+ *     nothing kept between calls, separate ones for calls that may run concurrently. */
+
+/* Element strides of a [B][N][heads][D] tensor whose D elements are consecutive. Inputs may
+ * take any strides >= 0; rows and heads of outputs must not overlap. */
+typedef struct {
+  int64_t request, row, head;
+} sv_strides;
+
+/* Rotary positions. The first rotary_dim = R dimensions of every head are turned in pairs:
+ * with a_i = position * freqs[i],
+ *   (x, y) -> (scale (x cos a_i - y sin a_i), scale (y cos a_i + x sin a_i)),
+ * pairs (i, i + R/2), or (2i, 2i + 1) when `interleaved` is not 0; the other
+ * dimensions are copied. `inverse` (not 0) turns by -a_i: the gradient's way back.
+ *   q, k       [B][N][q_heads][head_dim] and [B][N][k_heads][head_dim] of dtype at any
+ *              strides (both may be views of one fused projection); k may be NULL
+ *              with k_heads 0.
+ *   freqs      [R/2] double on the device, radians a position: base^(-2i/R), scaled for long
+ *              contexts as the caller's model does. Angles are made in float64.
+ *   scale      finite; the factor on the rotated dimensions alone that some scalings
+ *              for long contexts carry, else 1.
+ *   kv_len     [B], or NULL (positions from 0); any int32 value is a position.
+ *   out_q, out_k  like q and k at strides of their own; each may be its input
+ *              at the input's strides. Any other overlap is an error of the caller.
+ * Limits: head_dim >= 1, R even, 0 <= R <= head_dim <= 1024, q_heads >= 1; B*N < 2^31 and
+ * q_heads + k_heads <= 2^15 (SV_ESIZE beyond). */
+int spec_verify_rotate(const void* q, sv_strides q_strides, const void* k, sv_strides k_strides,
+                       sv_dtype dtype, int32_t B, int32_t N, int32_t q_heads, int32_t k_heads,
+                       int32_t head_dim, int32_t rotary_dim, int interleaved, int inverse,
+                       const double* freqs, float scale, const int32_t* kv_len,
+                       const int32_t* rows, void* out_q, sv_strides out_q_strides, void* out_k,
+                       sv_strides out_k_strides, void* stream);
+
+/* A paged cache of keys and values in 8 bits (e4m3: no infinities, largest value 448).
+ * Position p of request b lies in page page_table[b][p / page_size], token p % page_size.
+ * A block is 32 consecutive tokens of a page and one head, and has one scale for its keys and
+ * one for its values: value = scale * code.
+ *   k, v              [pages][heads][page_size / 32] blocks of 1024 * ceil(head_dim / 32)
+ *                     bytes. A block is made of bricks of 32 dimensions; within a brick
+ *                     the code of token s and dimension d (both 0..31) is
+ *                       keys:   byte 256 (d / 8) + 16 (4 (s / 8) + s % 4) + 8 (s / 4 % 2) + d % 8
+ *                       values: byte 256 (s / 8) + 16 (d % 16) + 8 (d / 16) + s % 8,
+ *                     the order in which a wavefront takes an operand of its matrix
+ *                     instruction, 16 consecutive bytes a lane.
+ *   k_scale, v_scale  [pages][heads][page_size / 32] float.
+ *   page_size         a power of two from 32 to 65536.
+ * Fresh memory needs no initialisation: what no call has written is never used. */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int32_t pages, heads, page_size, head_dim;
+} sv_cache;
+
+/* Bytes of k (and of v); 0 when a size is out of range. */
+size_t spec_verify_cache_bytes(int32_t pages, int32_t heads, int32_t page_size, int32_t head_dim);
+
+/* Writes the keys and values of a batch's rows, positions kv_len[b] .. kv_len[b] + rows[b] - 1.
+ * The scale of a block is the smallest power of two 2^e, e >= -126, with max |x| <= 448 * 2^e
+ * over what it holds up to its last new row (1 if that is all zero): the new rows, and the
+ * rows before kv_len[b] in the same block, whose codes are taken over, at the new
+ * scale, rounded to nearest even as the new ones. So the scale is a function of what the block
+ * holds: a proposal that was rejected leaves no trace in it once its slot is
+ * rewritten, and writing the same rows again changes nothing. NaN and infinities are stored as
+ * NaN and left out of the scale; numbers that would round to 2^128 (from 248 * 2^120 on), which
+ * float32 does not hold, are stored as 240 * 2^120. Slots behind the last new row keep their bytes.
+ *   k, v        [B][N][cache heads][head_dim] of dtype at any strides.
+ *   page_table  [B][table_width] int32. A row whose page lies outside [0, pages) is not written.
+ *               A block may be written through one request only: requests that share pages
+ *               must own the block they write into.
+ * A request is out of range (nothing written) when kv_len[b] < 0, rows[b] is not in 0..N, or
+ * kv_len[b] + rows[b] > table_width * page_size.
+ * Limits: 1 <= head_dim <= 256, table_width * page_size <= 2^30, 2^31 workgroup threads
+ * (SV_ESIZE beyond). */
+int spec_verify_cache_write(const sv_cache* cache, const int32_t* page_table, int32_t table_width,
+                            const int32_t* kv_len, const int32_t* rows, const void* k,
+                            sv_strides k_strides, const void* v, sv_strides v_strides,
+                            sv_dtype dtype, int32_t B, int32_t N, void* stream);
+
+/* Reads positions first[b] .. first[b] + rows[b] - 1 (first NULL: from 0) back: scale * code,
+ * rounded once to dtype. out_k, out_v [B][N][heads][head_dim]; either may be NULL, not both.
+ * Positions in a page outside [0, pages) read as NaN; a request is out of range as in
+ * spec_verify_cache_write. */
+int spec_verify_cache_read(const sv_cache* cache, const int32_t* page_table, int32_t table_width,
+                           const int32_t* first, const int32_t* rows, void* out_k,
+                           sv_strides k_strides, void* out_v, sv_strides v_strides, sv_dtype dtype,
+                           int32_t B, int32_t N, void* stream);
+
+/* Attention of a round's rows over the cache, which already holds them (call
+ * spec_verify_cache_write first). Query head h reads cache head h / (q_heads / heads). Row j
+ * of request b, at p = kv_len[b] + j, sees positions max(0, p - window + 1) .. p (window 0: all
+ * up to p):
+ *   out = sum_t softmax_t(scale q . k_t) v_t,   out_lse = log sum_t exp(scale q . k_t).
+ *   q        [B][N][q_heads][head_dim] of dtype at any strides; scale finite.
+ *   out      like q, of dtype, at its strides; out_lse [B][N][q_heads] float, or NULL.
+ * bfloat16: products of q and k are exact, probabilities enter their product with v as two
+ * bfloat16 parts (2^-17); float32: q and the probabilities as three.
+ * NaN in a position that a row does not see does not reach it. A row that sees a position in a
+ * page outside [0, pages) is NaN; pages that no row of the request sees (all before its window)
+ * are not read. Requests out of range as in spec_verify_cache_write.
+ * Limits: 1 <= N <= 64, q_heads a multiple of the cache's heads, head_dim <= 256, window >= 0;
+ * B * N * q_heads < 2^31 (SV_ESIZE beyond). The workspace holds the parts of requests that
+ * several workgroups share; `tokens` is table_width * page_size. */
+#define SV_MAX_ROWS 64
+size_t spec_verify_attention_workspace_bytes(int32_t B, int32_t N, int32_t q_heads, int32_t heads,
+                                             int32_t head_dim, int64_t tokens, sv_dtype dtype);
+int spec_verify_attention(const void* q, sv_strides q_strides, sv_dtype dtype, int32_t B, int32_t N,
+                          int32_t q_heads, const sv_cache* cache, const int32_t* page_table,
+                          int32_t table_width, const int32_t* kv_len, const int32_t* rows,
+                          float scale, int32_t window, void* out, sv_strides out_strides,
+                          float* out_lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Adjusts the logits of a batch's rows before they are compared or drawn from. For row j of
+ * request b let c_v be how often token v occurs in history[b] and in tokens[b][0 .. j-1]
+ * (the proposals before row j), and seen_v whether c_v > 0 or v occurs in prompt[b]. In float32:
+ *   z1 = seen_v ? (z > 0 ? z / repetition[b] : z * repetition[b]) : z
+ *   z2 = c_v > 0 ? z1 - (frequency[b] * c_v + presence[b]) : z1
+ *   z3 = z2 + bias_v                                 (tokens with a bias)
+ *   out = bit v of allowed[b][j] is set ? z3 : -inf
+ * rounded once to dtype; a logit that none of these touches keeps its bits.
+ *   logits, out  [B][N][V] of dtype, rows of V at strides >= V elements (request and row; `head`
+ *                is not used). out may be logits itself at the same strides; any other overlap is
+ *                an error of the caller.
+ *   tokens       [B][n_tokens] int32, n_tokens >= N - 1, or NULL with n_tokens 0 (no proposals).
+ *   history, prompt  [B][n_history], [B][n_prompt] int32, or NULL with 0.
+ *                Ids outside [0, V), such as -1, are padding in all lists.
+ *   repetition, frequency, presence  [B] float, or NULL (1, 0, 0). They are taken as
+ *                they are: a repetition of 0 divides by it.
+ *   bias_ids, bias  [B][n_bias] int32 and float, or NULL with 0; the last entry of an id that
+ *                occurs more than once counts.
+ *   allowed      [B][N][ceil(V / 32)] words, token v at bit v % 32 of word v / 32, or NULL. A row
+ *                without a set bit becomes all -inf (SV_FLAG_EMPTY in the verifier).
+ * A request whose rows[b] is not in 0..N has NaN in all its rows.
+ * Limits: V < 2^31 - 2^16, n_history, n_prompt and n_bias < 2^24, B * N * ceil(V / 4096) < 2^23
+ * (SV_ESIZE beyond). */
+int spec_verify_adjust_logits(const void* logits, sv_strides strides, sv_dtype dtype, int32_t B,
+                              int32_t N, int32_t V, const int32_t* rows, const int32_t* tokens,
+                              int32_t n_tokens, const int32_t* history, int32_t n_history,
+                              const int32_t* prompt, int32_t n_prompt, const float* repetition,
+                              const float* frequency, const float* presence,
+                              const int32_t* bias_ids, const float* bias, int32_t n_bias,
+                              const uint32_t* allowed, void* out, sv_strides out_strides,
+                              void* stream);
+
 /* Static description of a status code. */
 const char* spec_verify_strerror(int status);
 

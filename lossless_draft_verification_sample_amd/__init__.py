@@ -1,5 +1,5 @@
-"""Lossless speculative-sampling verifier for AMD MI355X (gfx950), and the
-losses its drafter is trained with.
+"""Lossless speculative-sampling verifier for AMD MI355X (gfx950), the losses its
+drafter is trained with, and the operators that make and shape the rows it reads.
 
 Thin Python binding over the C interface of include/spec_verify.h. The
 functions below only marshal arguments (device pointers of torch tensors, the
@@ -28,11 +28,14 @@ from ._lib import (  # noqa: F401
     SV_FLAG_TOKEN_RANGE,
     SV_MAX_BANNED,
     SV_MAX_HISTORY,
+    SV_MAX_ROWS,
     SV_MAX_TOP,
     SV_NOALLOC_SCRATCH_BYTES,
     SV_OK,
+    SvCache,
     SvRequests,
     SvSampler,
+    SvStrides,
 )
 
 SampleOut = namedtuple("SampleOut",
@@ -44,6 +47,13 @@ TopLogitsOut = namedtuple("TopLogitsOut", "ids values lse")
 DistillOut = namedtuple("DistillOut", "loss stats grad")
 LinearCeOut = namedtuple("LinearCeOut", "loss stats")
 LinearCeGrads = namedtuple("LinearCeGrads", "hidden weight")
+RotateOut = namedtuple("RotateOut", "q k")
+CacheRows = namedtuple("CacheRows", "k v")
+AttentionOut = namedtuple("AttentionOut", "out lse")
+# A paged 8-bit cache (see sv_cache in include/spec_verify.h): k, v [pages, heads,
+# page_size / 32, ceil(head_dim / 32), 1024] float8_e4m3fn, k_scale, v_scale [pages, heads,
+# page_size / 32] float32. kv_cache() makes one.
+KVCache = namedtuple("KVCache", "k v k_scale v_scale page_size head_dim")
 # Per-request settings of a mixed batch (see sv_requests in include/spec_verify.h):
 # gamma [B] int32, target / draft [B, 12] uint8 sv_sampler records (sampler_array),
 # banned_draft [B, m] int32, history [B, H] int32, penalty / penalty_draft [B]
@@ -693,6 +703,338 @@ def spec_verify_linear_ce_backward(hidden, weight, labels, stats, grad_loss=None
     if out is not None:
         _written((gh, gw))
     return LinearCeGrads(gh, gw)
+
+
+# ------------------------------------------- the verification pass's rows
+#
+# Row j of request b stands at position kv_len[b] + j. Autograd records none of these
+# calls; outputs and caches given by the caller count as changed in place.
+
+
+def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, original=None, low=1.0,
+                       high=4.0, fast=32.0, slow=1.0, device="cuda"):
+    """(freqs, scale) of spec_verify_rotate for a head's `rotary_dim` rotated dimensions:
+    freqs [rotary_dim / 2] float64, radians a position, and the factor on rotated values.
+
+    f_i = base^(-2i / rotary_dim), scaled for contexts `factor` times as long as the model was
+    trained for:
+      None      as they are.
+      "linear"  f_i / factor: positions are interpolated.
+      "base"    the base raised to base * factor^(R / (R - 2)), which leaves the fastest
+                pair as it is and divides the slowest by factor.
+      "smooth"  by wavelength w = 2 pi / f_i against the trained context `original`: w < original / high
+                as it is, w > original / low divided by factor, between them
+                f_i ((1 - s) / factor + s), s = (original / w - low) / (high - low).
+      "ramp"    by the pair's index between those that turn `fast` and `slow` times over `original`
+                positions: f_i (1 - r + r / factor), r rising from 0 to 1, and scale
+                0.1 log(factor) + 1 (Peng et al. 2023, "YaRN", sections 3.2 to 3.4).
+    """
+    import math
+    torch = _torch()
+    R = int(rotary_dim)
+    if R < 0 or R % 2:
+        raise ValueError(f"rotary_dim must be even, got {rotary_dim}")
+    if not base > 0 or not factor >= 1:
+        raise ValueError("base must be positive, factor at least 1")
+    if scaling in ("smooth", "ramp") and not (original and original > 0):
+        raise ValueError(f"scaling {scaling!r} needs the trained context, original")
+    if scaling == "base" and R > 2:
+        base = base * factor ** (R / (R - 2))
+    freqs = [float(base) ** (-2.0 * i / R) for i in range(R // 2)]
+    scale = 1.0
+    if scaling == "linear":
+        freqs = [f / factor for f in freqs]
+    elif scaling == "smooth":
+        if not high > low:
+            raise ValueError("high must exceed low")
+        share = [min(1.0, max(0.0, (original * f / (2 * math.pi) - low) / (high - low))) for f in freqs]
+        freqs = [f * ((1 - s) / factor + s) for f, s in zip(freqs, share)]
+    elif scaling == "ramp":
+        def index(turns):   # of the pair that turns so often
+            return R * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))
+        first, last = max(0, math.floor(index(fast))), min(R - 1, math.ceil(index(slow)))
+        width = max(last - first, 0.001)
+        ramp = [min(1.0, max(0.0, (i - first) / width)) for i in range(R // 2)]
+        freqs = [f * (1 - r + r / factor) for f, r in zip(freqs, ramp)]
+        scale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "base"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return torch.tensor(freqs, dtype=torch.float64, device=device), scale
+
+
+def _rows4(t, name, device=None, dtype=None, shape=None):
+    """(pointer, strides) of a [B, N, heads, D] tensor with consecutive D."""
+    if not _torch().is_tensor(t) or not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    size = t.shape
+    if len(size) != 4 or t.numel() == 0:
+        raise ValueError(f"{name} must be [B, N, heads, D], none of them 0, got {tuple(size)}")
+    if shape is not None and tuple(size) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(size)}")
+    step = t.stride()
+    if size[3] > 1 and step[3] != 1:
+        raise ValueError(f"{name} must have consecutive elements in a head")
+    return t.data_ptr(), SvStrides(step[0], step[1], step[2])
+
+
+def _out4(t, like, name):
+    """An output like `like`, its pointer and strides; a new contiguous one when None."""
+    if t is None:
+        t = _torch().empty_like(like, memory_format=_torch().contiguous_format)
+    return (t, *_rows4(t, name, like.device, like.dtype, like.shape))
+
+
+_NO_STRIDES = SvStrides(0, 0, 0)
+
+
+def spec_verify_rotate(q, k, kv_len, freqs, interleaved=False, scale=1.0, inverse=False, rows=None,
+                       out=None, stream=None, lib=None):
+    """Rotary positions of queries and keys (see include/spec_verify.h).
+
+    q [B, N, q_heads, D] and k [B, N, k_heads, D] or None (bf16 or fp32, any strides with
+    consecutive D), kv_len [B] int32 or None (positions from 0), freqs [R/2] float64 (see
+    rotary_frequencies): the first R dimensions of a head are turned. inverse turns
+    back: with it, gradients of the outputs become gradients of the inputs. rows [B] int32 or None.
+    out: a RotateOut, whose tensors may be q and k themselves.
+    Returns RotateOut(q, k)."""
+    torch = _torch()
+    lib = lib or _lib.load()
+    qp, qs = _rows4(q, "q")
+    dt, dev, (B, N, qh, D) = _dtype_code(q), q.device, q.shape
+    kp, ks, kh = None, _NO_STRIDES, 0
+    if k is not None:
+        kh = k.shape[2] if k.dim() == 4 else 0
+        kp, ks = _rows4(k, "k", dev, q.dtype, (B, N, kh, D))
+    if freqs is None or freqs.dim() != 1:
+        raise ValueError("freqs must be [R/2] float64")
+    R = 2 * freqs.shape[0]
+    ctx, handle = _on(dev, stream)
+    with ctx:
+        oq, oqp, oqs = _out4(out and out.q, q, "out.q")
+        ok, okp, oks = (None, None, _NO_STRIDES) if k is None else _out4(out and out.k, k, "out.k")
+        rc = lib.spec_verify_rotate(
+            qp, qs, kp, ks, dt, B, N, qh, kh, D, R, int(bool(interleaved)), int(bool(inverse)),
+            _vector(freqs, "freqs", torch.float64, freqs.shape, dev), float(scale),
+            _vector(kv_len, "kv_len", torch.int32, (B,), dev),
+            _vector(rows, "rows", torch.int32, (B,), dev), oqp, oqs, okp, oks, handle)
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_verify_rotate")
+    _written(out)
+    return RotateOut(oq, ok)
+
+
+def spec_verify_cache_bytes(pages, heads, page_size, head_dim):
+    return int(_lib.load().spec_verify_cache_bytes(int(pages), int(heads), int(page_size), int(head_dim)))
+
+
+def kv_cache(pages, heads, page_size, head_dim, device="cuda"):
+    """An empty KVCache of this many pages (a power of two of tokens each, 32 or more)."""
+    torch = _torch()
+    if spec_verify_cache_bytes(pages, heads, page_size, head_dim) == 0:
+        raise SpecVerifyError(SV_EINVAL, "kv_cache")
+    per = page_size // 32
+    k, v = (torch.empty((pages, heads, per, -(-head_dim // 32), 1024), dtype=torch.float8_e4m3fn,
+                        device=device) for _ in range(2))
+    ks, vs = (torch.empty((pages, heads, per), dtype=torch.float32, device=device) for _ in range(2))
+    return KVCache(k, v, ks, vs, page_size, head_dim)
+
+
+def _cache(cache, device):
+    """sv_cache of a KVCache, and (heads, head_dim)."""
+    torch = _torch()
+    shape, D, page = cache.k.shape, int(cache.head_dim), int(cache.page_size)
+    if len(shape) != 5 or shape[2] * 32 != page or shape[3] != -(-D // 32) or shape[4] != 1024:
+        raise ValueError(f"cache.k must be [pages, heads, {page} / 32, ceil({D} / 32), 1024], got {tuple(shape)}")
+    small = shape[:3]
+    return SvCache(_vector(cache.k, "cache.k", torch.float8_e4m3fn, shape, device),
+                   _vector(cache.v, "cache.v", torch.float8_e4m3fn, shape, device),
+                   _vector(cache.k_scale, "cache.k_scale", torch.float32, small, device),
+                   _vector(cache.v_scale, "cache.v_scale", torch.float32, small, device),
+                   shape[0], shape[1], page, D)
+
+
+def _table(page_table, B, device):
+    if page_table is None or page_table.dim() != 2:
+        raise ValueError("page_table must be [B, width] int32")
+    width = page_table.shape[1]
+    return _vector(page_table, "page_table", _torch().int32, (B, width), device), width
+
+
+def spec_verify_cache_write(cache, page_table, kv_len, k, v, rows=None, stream=None, lib=None):
+    """Quantises the rows k, v [B, N, heads, D] (bf16 or fp32, any strides with consecutive D)
+    into the cache at positions kv_len[b] .. (see include/spec_verify.h).
+
+    cache: a KVCache; page_table [B, width] int32, kv_len [B] int32, rows [B] int32 or None."""
+    torch = _torch()
+    lib = lib or _lib.load()
+    kp, ks = _rows4(k, "k")
+    dt, dev, (B, N, heads, D) = _dtype_code(k), k.device, k.shape
+    vp, vs = _rows4(v, "v", dev, k.dtype, k.shape)
+    c = _cache(cache, dev)
+    if (heads, D) != (c.heads, c.head_dim):
+        raise ValueError(f"k must have {c.heads} heads of {c.head_dim}, got {tuple(k.shape)}")
+    table, width = _table(page_table, B, dev)
+    if kv_len is None:
+        raise ValueError("kv_len must be [B] int32")
+    ctx, handle = _on(dev, stream)
+    with ctx:
+        rc = lib.spec_verify_cache_write(
+            c, table, width, _vector(kv_len, "kv_len", torch.int32, (B,), dev),
+            _vector(rows, "rows", torch.int32, (B,), dev), kp, ks, vp, vs, dt, B, N, handle)
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_verify_cache_write")
+    _written(cache[:4])
+
+
+def spec_verify_cache_read(cache, page_table, first, N, dtype=None, rows=None, out=None, stream=None,
+                           lib=None):
+    """Rows first[b] .. first[b] + N - 1 of every request as values (see
+    include/spec_verify.h).
+
+    first [B] int32 or None (from position 0), rows [B] int32 or None; dtype of new outputs
+    (torch.bfloat16 when None). out: a CacheRows of [B, N, heads, D] tensors, either may be None.
+    Returns CacheRows(k, v)."""
+    torch = _torch()
+    lib = lib or _lib.load()
+    dev = cache.k.device
+    if not cache.k.is_cuda:
+        raise ValueError("cache must be on a device")
+    c = _cache(cache, dev)
+    if page_table is None:
+        raise ValueError("page_table must be [B, width] int32")
+    B = page_table.shape[0]
+    table, width = _table(page_table, B, dev)
+    shape = (B, int(N), c.heads, c.head_dim)
+    ctx, handle = _on(dev, stream)
+    with ctx:
+        if out is None:
+            given = None
+            out = CacheRows(*(torch.empty(shape, dtype=dtype or torch.bfloat16, device=dev)
+                              for _ in range(2)))
+        else:
+            given = out
+        one = out.k if out.k is not None else out.v
+        if one is None:
+            raise ValueError("out must have k or v")
+        kp, ks = (None, _NO_STRIDES) if out.k is None else _rows4(out.k, "out.k", dev, one.dtype, shape)
+        vp, vs = (None, _NO_STRIDES) if out.v is None else _rows4(out.v, "out.v", dev, one.dtype, shape)
+        rc = lib.spec_verify_cache_read(
+            c, table, width, _vector(first, "first", torch.int32, (B,), dev),
+            _vector(rows, "rows", torch.int32, (B,), dev), kp, ks, vp, vs, _dtype_code(one), B, int(N),
+            handle)
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_verify_cache_read")
+    _written(given)
+    return out
+
+
+def spec_verify_attention_workspace_bytes(B, N, q_heads, heads, head_dim, tokens, dtype=SV_BF16):
+    return int(_lib.load().spec_verify_attention_workspace_bytes(
+        int(B), int(N), int(q_heads), int(heads), int(head_dim), int(tokens), int(dtype)))
+
+
+def spec_verify_attention(q, cache, page_table, kv_len, scale=None, window=0, rows=None, want_lse=False,
+                          workspace=None, out=None, stream=None, lib=None):
+    """Attention of a round's rows over the 8-bit cache, which holds them already (see
+    include/spec_verify.h).
+
+    q [B, N, q_heads, D] (bf16 or fp32, any strides with consecutive D), N up to SV_MAX_ROWS, q_heads
+    a multiple of the cache's heads; page_table [B, width] int32, kv_len [B] int32: tokens
+    before the rows; scale of the scores (None: D^-1/2); window: how many positions a row sees, its
+    own included (0: all); rows [B] int32 or None. out: an AttentionOut; its lse may be None.
+    Returns AttentionOut(out like q, lse [B, N, q_heads] float32 or None)."""
+    torch = _torch()
+    lib = lib or _lib.load()
+    qp, qs = _rows4(q, "q")
+    dt, dev, (B, N, qh, D) = _dtype_code(q), q.device, q.shape
+    c = _cache(cache, dev)
+    if D != c.head_dim:
+        raise ValueError(f"q must have heads of {c.head_dim}, got {tuple(q.shape)}")
+    table, width = _table(page_table, B, dev)
+    if kv_len is None:
+        raise ValueError("kv_len must be [B] int32")
+    ctx, handle = _on(dev, stream)
+    with ctx:
+        o, op, os_ = _out4(out and out.out, q, "out.out")
+        lse = out.lse if out is not None else None
+        if out is None and want_lse:
+            lse = torch.empty((B, N, qh), dtype=torch.float32, device=dev)
+        ws, ws_bytes, keep = _space(
+            workspace, lib.spec_verify_attention_workspace_bytes(B, N, qh, c.heads, D, width * c.page_size, dt), dev)
+        rc = lib.spec_verify_attention(
+            qp, qs, dt, B, N, qh, c, table, width, _vector(kv_len, "kv_len", torch.int32, (B,), dev),
+            _vector(rows, "rows", torch.int32, (B,), dev), D ** -0.5 if scale is None else float(scale),
+            int(window), op, os_, _vector(lse, "out.lse", torch.float32, (B, N, qh), dev), ws, ws_bytes, handle)
+    del keep
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_verify_attention")
+    _written(out)
+    return AttentionOut(o, lse)
+
+
+def _rows3(t, name, device=None, dtype=None, shape=None):
+    """(pointer, strides) of a [B, N, V] tensor with consecutive V."""
+    if not _torch().is_tensor(t) or not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [B, N, V], got {tuple(t.shape)}")
+    ptr, s = _rows4(t.unsqueeze(2), name, device, dtype, shape and (shape[0], shape[1], 1, shape[2]))
+    return ptr, SvStrides(s.request, s.row, 0)
+
+
+def _id_list(t, name, B, device):
+    """(pointer, width) of a [B, n] int32 list, or of none."""
+    if t is None or (t.dim() == 2 and t.shape[1] == 0):
+        return None, 0
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [B, n] int32")
+    return _vector(t, name, _torch().int32, (B, t.shape[1]), device), t.shape[1]
+
+
+def spec_verify_adjust_logits(logits, tokens=None, history=None, prompt=None, repetition=None,
+                              frequency=None, presence=None, bias_ids=None, bias=None, allowed=None,
+                              rows=None, out=None, stream=None, lib=None):
+    """Penalties, biases and a grammar's mask on a batch's logits (see include/spec_verify.h),
+    before they are verified or drawn from: the target rows [B, gamma+1, V] and the
+    drafter's [B, gamma, V] alike.
+
+    logits [B, N, V] bf16 or fp32 (any strides with consecutive V), tokens [B, >= N - 1] int32: the
+    proposals, of which row j counts those before it; history, prompt [B, n] int32 (-1: padding);
+    repetition, frequency, presence [B] float32; bias_ids [B, n] int32 with bias [B, n]
+    float32; allowed [B, N, ceil(V / 32)] int32, token v at bit v % 32 of word v / 32; rows [B] int32. All
+    but logits may be None. out: a tensor like logits, or logits itself.
+    Returns the adjusted logits."""
+    torch = _torch()
+    lib = lib or _lib.load()
+    zp, zs = _rows3(logits, "logits")
+    dt, dev, (B, N, V) = _dtype_code(logits), logits.device, logits.shape
+    tp, nt = _id_list(tokens, "tokens", B, dev)
+    hp, nh = _id_list(history, "history", B, dev)
+    pp, np_ = _id_list(prompt, "prompt", B, dev)
+    bp, nb = _id_list(bias_ids, "bias_ids", B, dev)
+    if (bias is None) != (bias_ids is None):
+        raise ValueError("bias_ids and bias come together")
+    f32, given = torch.float32, out is not None
+    weight = _vector(bias, "bias", f32, (B, nb), dev) if nb else None
+    ctx, handle = _on(dev, stream)
+    with ctx:
+        if out is None:
+            out = torch.empty_like(logits, memory_format=torch.contiguous_format)
+        op, os_ = _rows3(out, "out", dev, logits.dtype, (B, N, V))
+        rc = lib.spec_verify_adjust_logits(
+            zp, zs, dt, B, N, V, _vector(rows, "rows", torch.int32, (B,), dev), tp, nt, hp, nh, pp, np_,
+            _vector(repetition, "repetition", f32, (B,), dev), _vector(frequency, "frequency", f32, (B,), dev),
+            _vector(presence, "presence", f32, (B,), dev), bp, weight, nb,
+            _vector(allowed, "allowed", torch.int32, (B, N, -(-V // 32)), dev), op, os_, handle)
+    if rc != SV_OK:
+        raise SpecVerifyError(rc, "spec_verify_adjust_logits")
+    if given:
+        _written((out,))
+    return out
 
 
 def bench_profile_start(max_launches_per_kernel):

@@ -36,6 +36,7 @@ SV_FLAG_BAD_PARAM = 32
 SV_MAX_BANNED = 2048
 SV_MAX_HISTORY = 1984
 SV_MAX_TOP = 1024
+SV_MAX_ROWS = 64
 
 # kernel indices of sv_bench_profile_stop (csrc/sv_bench_timing.h)
 SV_K_ROW_STATS = 0
@@ -60,6 +61,18 @@ class SvRequests(ctypes.Structure):
                 ("n_banned_draft", ctypes.c_int32), ("history", ctypes.c_void_p),
                 ("n_history", ctypes.c_int32), ("penalty", ctypes.c_void_p),
                 ("penalty_draft", ctypes.c_void_p)]
+
+
+class SvStrides(ctypes.Structure):
+    """sv_strides: element strides of a [B][N][heads][D] tensor."""
+    _fields_ = [("request", ctypes.c_int64), ("row", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class SvCache(ctypes.Structure):
+    """sv_cache: device pointers (as integers) and sizes of a paged 8-bit cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
 _c = ctypes
@@ -98,6 +111,20 @@ SIGNATURES = {
     "spec_verify_linear_ce_backward_workspace_bytes": (_size, [_i32, _i32, _i32, _int, _int, _int]),
     "spec_verify_linear_ce_backward": (_int, [_vp, _i64, _vp, _i64, _int, _vp, _vp, _vp, _i32, _i32,
                                               _i32, _vp, _i64, _vp, _i64, _vp, _size, _vp]),
+    "spec_verify_rotate": (_int, [_vp, SvStrides, _vp, SvStrides, _int, _i32, _i32, _i32, _i32, _i32,
+                                  _i32, _int, _int, _vp, _f32, _vp, _vp, _vp, SvStrides, _vp,
+                                  SvStrides, _vp]),
+    "spec_verify_cache_bytes": (_size, [_i32, _i32, _i32, _i32]),
+    "spec_verify_cache_write": (_int, [_c.POINTER(SvCache), _vp, _i32, _vp, _vp, _vp, SvStrides, _vp,
+                                       SvStrides, _int, _i32, _i32, _vp]),
+    "spec_verify_cache_read": (_int, [_c.POINTER(SvCache), _vp, _i32, _vp, _vp, _vp, SvStrides, _vp,
+                                      SvStrides, _int, _i32, _i32, _vp]),
+    "spec_verify_attention_workspace_bytes": (_size, [_i32, _i32, _i32, _i32, _i32, _i64, _int]),
+    "spec_verify_attention": (_int, [_vp, SvStrides, _int, _i32, _i32, _i32, _c.POINTER(SvCache), _vp,
+                                     _i32, _vp, _vp, _f32, _i32, _vp, SvStrides, _vp, _vp, _size, _vp]),
+    "spec_verify_adjust_logits": (_int, [_vp, SvStrides, _int, _i32, _i32, _i32, _vp, _vp, _i32, _vp,
+                                         _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp,
+                                         SvStrides, _vp]),
     "spec_verify_strerror": (_c.c_char_p, [_c.c_int]),
 }
 BENCH_SIGNATURES = {

@@ -29,7 +29,10 @@ KERNEL_SOURCES = ["row_stats.hip", "verify.hip", "overlap.hip", "greedy.hip", "c
                   # the drafter's training calls; in a folder of their own, so that the digest
                   # of the verification path's sources stays what its counters were taken on
                   "training/top_logits.hip", "training/distill.hip", "training/linear_ce.hip",
-                  "training/train_api.cpp"]
+                  "training/train_api.cpp",
+                  # the verification pass's rows
+                  "serving/rotate.hip", "serving/cache_rows.hip", "serving/attend.hip",
+                  "serving/attend_f32.hip", "serving/adjust.hip", "serving/serve_api.cpp"]
 API_SOURCE = "api.cpp"
 # HBM read-bandwidth calibration (bench.py --read-ceiling); not on the path
 CALIB_LIB_NAME = "libsvcalib.so"

@@ -1,0 +1,300 @@
+// Host side of the calls for the verification pass's rows (include/spec_verify.h):
+// argument checks before anything touches the device, how work is cut into
+// workgroups, workspace carving and the launches on the caller's stream.
+
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "../../../include/spec_verify.h"
+#include "sv_serve.hpp"
+
+namespace {
+
+constexpr size_t WS_ALIGN = 256;
+// Threads of a launch, 256 a workgroup, are counted in 32 bits.
+constexpr int64_t MAX_WORKGROUPS = 1 << 23;
+constexpr int64_t MAX_TOKENS = 1 << 30;
+constexpr int MAX_PAGE = 65536;
+constexpr int CUS = 256;
+
+size_t align_up(size_t x) { return (x + WS_ALIGN - 1) / WS_ALIGN * WS_ALIGN; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+bool known(sv_dtype t) { return t == SV_F32 || t == SV_BF16; }
+size_t size_of(sv_dtype t) { return t == SV_BF16 ? 2 : 4; }
+bool aligned(const void* p, size_t to) { return (uintptr_t)p % to == 0; }
+
+// Inputs: strides of dimensions of one entry do not matter, others are not negative.
+bool readable(sv_strides s, int64_t B, int64_t N, int64_t H) {
+  return (B <= 1 || s.request >= 0) && (N <= 1 || s.row >= 0) && (H <= 1 || s.head >= 0);
+}
+// Outputs: no two rows or heads overlap, with the dimensions in any order.
+bool writable(sv_strides s, int64_t B, int64_t N, int64_t H, int64_t width) {
+  int64_t step[3] = {s.request, s.row, s.head}, size[3] = {B, N, H};
+  for (int i = 0; i < 3; ++i)
+    if (size[i] <= 1) step[i] = INT64_MAX;      // never stepped over
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2; ++j)
+      if (step[j] > step[j + 1]) {
+        const int64_t a = step[j], b = size[j];
+        step[j] = step[j + 1];
+        size[j] = size[j + 1];
+        step[j + 1] = a;
+        size[j + 1] = b;
+      }
+  int64_t extent = width;                       // elements from the first to the last, and one
+  for (int i = 0; i < 3; ++i) {
+    if (size[i] <= 1) continue;
+    if (step[i] < extent || step[i] > INT64_MAX / 4 / size[i]) return false;
+    extent += step[i] * (size[i] - 1);
+  }
+  return true;
+}
+sv::Strides strides_of(sv_strides s) { return sv::Strides{s.request, s.row, s.head}; }
+bool same(sv_strides a, sv_strides b, int64_t B, int64_t N, int64_t H) {
+  return (B <= 1 || a.request == b.request) && (N <= 1 || a.row == b.row) && (H <= 1 || a.head == b.head);
+}
+// In place only at the same strides.
+bool place_ok(const void* in, sv_strides is, const void* out, sv_strides os, int64_t B, int64_t N, int64_t H) {
+  return in != out || same(is, os, B, N, H);
+}
+
+// ---------------------------------------------------------------- the cache
+
+bool cache_shape(int64_t pages, int64_t heads, int64_t page, int64_t D) {
+  return pages >= 1 && heads >= 1 && D >= 1 && D <= sv::CACHE_MAX_D && page >= sv::CACHE_BLOCK && page <= MAX_PAGE &&
+         (page & (page - 1)) == 0;
+}
+int log2_of(int x) { return 31 - __builtin_clz((unsigned)x); }
+
+int cache_of(const sv_cache* c, bool k, bool v, sv::Cache* out) {
+  if (!c || (k && (!c->k || !c->k_scale)) || (v && (!c->v || !c->v_scale))) return SV_EINVAL;
+  if (!cache_shape(c->pages, c->heads, c->page_size, c->head_dim)) return SV_EINVAL;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)) return SV_EINVAL;
+  *out = sv::Cache{(uint8_t*)c->k, (uint8_t*)c->v, c->k_scale, c->v_scale, c->pages, c->heads,
+                   log2_of(c->page_size / sv::CACHE_BLOCK), (int)ceil_div(c->head_dim, 32), c->head_dim};
+  return SV_OK;
+}
+
+int batch_of(const int32_t* table, int32_t width, const int32_t* first, const int32_t* rows, int32_t B, int32_t N,
+             int32_t page, sv::Batch* out) {
+  if (!table || width < 1 || B < 1 || N < 1) return SV_EINVAL;
+  if (!aligned(table, 4) || !aligned(first, 4) || !aligned(rows, 4)) return SV_EINVAL;
+  if ((int64_t)width * page > MAX_TOKENS || N > MAX_TOKENS) return SV_ESIZE;
+  *out = sv::Batch{table, width, first, rows, B, N, width * page};
+  return SV_OK;
+}
+
+int cache_rows(const sv_cache* cache, const int32_t* table, int32_t width, const int32_t* first,
+               const int32_t* rows, const void* k, sv_strides ks, const void* v, sv_strides vs, sv_dtype dtype,
+               int32_t B, int32_t N, bool write, sv::CacheRowsArgs* a) {
+  if (write ? !k || !v : !k && !v) return SV_EINVAL;
+  if (!known(dtype)) return SV_EDTYPE;
+  int rc = cache_of(cache, k, v, &a->c);
+  if (rc == SV_OK) rc = batch_of(table, width, first, rows, B, N, cache->page_size, &a->t);
+  if (rc != SV_OK) return rc;
+  const int64_t H = a->c.heads, D = a->c.D;
+  for (int i = 0; i < 2; ++i) {
+    const void* p = i ? v : k;
+    const sv_strides s = i ? vs : ks;
+    if (!p) continue;
+    if (!aligned(p, size_of(dtype))) return SV_EINVAL;
+    if (write ? !readable(s, B, N, H) : !writable(s, B, N, H, D)) return SV_EINVAL;
+  }
+  a->k = (void*)k;
+  a->v = (void*)v;
+  a->ks = strides_of(ks);
+  a->vs = strides_of(vs);
+  a->which = (k ? 1 : 0) | (v ? 2 : 0);
+  a->bf16 = dtype == SV_BF16;
+  // rows that start at a block's last token touch one block more
+  a->blocks = (int)ceil_div((int64_t)N + sv::CACHE_BLOCK - 1, sv::CACHE_BLOCK);
+  if ((double)B * a->blocks * H * 2 >= MAX_WORKGROUPS) return SV_ESIZE;
+  return SV_OK;
+}
+
+// ---------------------------------------------------------------- attention
+
+// Tiles of 16 columns: as few sets as the LDS that holds their queries allows (60 KB, so that
+// two workgroups fit a CU with room to spare), then as few waves side by side as the
+// registers allow, so that the others share out the tokens.
+bool attend_shape(int64_t B, int64_t N, int64_t qh, int64_t heads, int64_t D, int64_t tokens, sv_dtype dtype,
+                  sv::AttendShape* s) {
+  if (B < 1 || N < 1 || N > SV_MAX_ROWS || qh < 1 || heads < 1 || qh % heads || D < 1 || D > sv::CACHE_MAX_D ||
+      tokens < 1 || tokens > MAX_TOKENS || !known(dtype) || (double)B * N * qh >= 2147483648.0)
+    return false;
+  const int64_t bricks = ceil_div(D, 32), parts = dtype == SV_BF16 ? 1 : 3;
+  const int64_t cols = N * (qh / heads), tiles = ceil_div(cols, 16);
+  const int64_t most = 60 / (bricks * parts), nt_most = bricks <= 4 ? 4 : 2;
+  for (int64_t sets = 1;; ++sets) {
+    const int64_t t = ceil_div(tiles, sets);
+    for (int64_t across = 1; across <= 4; across *= 2) {
+      const int64_t nt = ceil_div(t, across);
+      if (nt > nt_most || nt * across > most) continue;
+      const int64_t units = B * heads * sets;
+      const int64_t cols_set = 16 * nt * across;
+      if ((double)units * cols_set / 4 >= MAX_WORKGROUPS) return false;
+      s->cols = (int)cols;
+      s->nt = (int)nt;
+      s->across = (int)across;
+      s->sets = (int)sets;
+      s->cols_set = (int)cols_set;
+      const int64_t q = nt * across * bricks * parts * 1024, sums = 8 * nt * 1024;
+      s->lds = (int)(q > sums ? q : sums);
+      // a workgroup takes four blocks at least
+      const int64_t blocks = units * (ceil_div(tokens, sv::CACHE_BLOCK) + 1);
+      const int64_t full = CUS * (nt == 1 ? 4 : 2);
+      s->grid = (int)(ceil_div(blocks, 4) < full ? ceil_div(blocks, 4) : full);
+      return true;
+    }
+  }
+}
+struct AttendSpace {
+  size_t record, partial, total;
+};
+AttendSpace attend_space(const sv::AttendShape& s, int64_t B, int64_t heads, int64_t D) {
+  AttendSpace w;
+  w.record = 0;
+  w.partial = align_up((size_t)(B * heads * s.sets) * 2 * sizeof(int32_t));
+  w.total = w.partial + align_up((size_t)s.grid * 2 * s.cols_set * (D + 2) * sizeof(float));
+  return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+int spec_verify_rotate(const void* q, sv_strides q_strides, const void* k, sv_strides k_strides,
+                       sv_dtype dtype, int32_t B, int32_t N, int32_t q_heads, int32_t k_heads,
+                       int32_t head_dim, int32_t rotary_dim, int interleaved, int inverse,
+                       const double* freqs, float scale, const int32_t* kv_len,
+                       const int32_t* rows, void* out_q, sv_strides out_q_strides, void* out_k,
+                       sv_strides out_k_strides, void* stream) {
+  if (!q || !out_q || (k_heads > 0 && (!k || !out_k)) || (rotary_dim > 0 && !freqs)) return SV_EINVAL;
+  if (!known(dtype)) return SV_EDTYPE;
+  if (B < 1 || N < 1 || q_heads < 1 || k_heads < 0 || head_dim < 1 || head_dim > 1024 || rotary_dim < 0 ||
+      rotary_dim % 2 || rotary_dim > head_dim || !isfinite(scale))
+    return SV_EINVAL;
+  if ((int64_t)q_heads + k_heads > 1 << 15 || (double)B * N >= 2147483648.0) return SV_ESIZE;
+  const size_t es = size_of(dtype);
+  if (!aligned(q, es) || !aligned(out_q, es) || !aligned(freqs, 8) || !aligned(kv_len, 4) || !aligned(rows, 4) ||
+      !readable(q_strides, B, N, q_heads) || !writable(out_q_strides, B, N, q_heads, head_dim) ||
+      !place_ok(q, q_strides, out_q, out_q_strides, B, N, q_heads))
+    return SV_EINVAL;
+  if (k_heads > 0 &&
+      (!aligned(k, es) || !aligned(out_k, es) || !readable(k_strides, B, N, k_heads) ||
+       !writable(out_k_strides, B, N, k_heads, head_dim) || !place_ok(k, k_strides, out_k, out_k_strides, B, N, k_heads)))
+    return SV_EINVAL;
+  const sv::RotateArgs a{q, k, out_q, out_k, strides_of(q_strides), strides_of(k_strides), strides_of(out_q_strides),
+                         strides_of(out_k_strides), B, N, q_heads, k_heads, head_dim, rotary_dim, freqs, scale,
+                         interleaved != 0, inverse != 0, dtype == SV_BF16, kv_len, rows};
+  return sv::launch_rotate(a, (hipStream_t)stream) ? SV_EHIP : SV_OK;
+}
+
+size_t spec_verify_cache_bytes(int32_t pages, int32_t heads, int32_t page_size, int32_t head_dim) {
+  if (!cache_shape(pages, heads, page_size, head_dim)) return 0;
+  const double all = (double)pages * heads * page_size * ceil_div(head_dim, 32) * 32;
+  if (all >= 9e18) return 0;
+  return (size_t)pages * heads * page_size * ceil_div(head_dim, 32) * 32;
+}
+
+int spec_verify_cache_write(const sv_cache* cache, const int32_t* page_table, int32_t table_width,
+                            const int32_t* kv_len, const int32_t* rows, const void* k,
+                            sv_strides k_strides, const void* v, sv_strides v_strides,
+                            sv_dtype dtype, int32_t B, int32_t N, void* stream) {
+  sv::CacheRowsArgs a;
+  if (!kv_len) return SV_EINVAL;
+  const int rc = cache_rows(cache, page_table, table_width, kv_len, rows, k, k_strides, v, v_strides, dtype, B, N,
+                            true, &a);
+  if (rc != SV_OK) return rc;
+  return sv::launch_cache_write(a, (hipStream_t)stream) ? SV_EHIP : SV_OK;
+}
+
+int spec_verify_cache_read(const sv_cache* cache, const int32_t* page_table, int32_t table_width,
+                           const int32_t* first, const int32_t* rows, void* out_k,
+                           sv_strides k_strides, void* out_v, sv_strides v_strides, sv_dtype dtype,
+                           int32_t B, int32_t N, void* stream) {
+  sv::CacheRowsArgs a;
+  const int rc = cache_rows(cache, page_table, table_width, first, rows, out_k, k_strides, out_v, v_strides, dtype, B,
+                            N, false, &a);
+  if (rc != SV_OK) return rc;
+  return sv::launch_cache_read(a, (hipStream_t)stream) ? SV_EHIP : SV_OK;
+}
+
+size_t spec_verify_attention_workspace_bytes(int32_t B, int32_t N, int32_t q_heads, int32_t heads,
+                                             int32_t head_dim, int64_t tokens, sv_dtype dtype) {
+  sv::AttendShape s;
+  if (!attend_shape(B, N, q_heads, heads, head_dim, tokens, dtype, &s)) return 0;
+  return attend_space(s, B, heads, head_dim).total;
+}
+
+int spec_verify_attention(const void* q, sv_strides q_strides, sv_dtype dtype, int32_t B, int32_t N,
+                          int32_t q_heads, const sv_cache* cache, const int32_t* page_table,
+                          int32_t table_width, const int32_t* kv_len, const int32_t* rows,
+                          float scale, int32_t window, void* out, sv_strides out_strides,
+                          float* out_lse, void* workspace, size_t workspace_bytes, void* stream) {
+  sv::AttendArgs a;
+  if (!q || !out || !kv_len) return SV_EINVAL;
+  if (!known(dtype)) return SV_EDTYPE;
+  int rc = cache_of(cache, true, true, &a.c);
+  if (rc == SV_OK) rc = batch_of(page_table, table_width, kv_len, rows, B, N, cache->page_size, &a.t);
+  if (rc != SV_OK) return rc;
+  if (N > SV_MAX_ROWS || q_heads < 1 || q_heads % a.c.heads || window < 0 || !isfinite(scale)) return SV_EINVAL;
+  const size_t es = size_of(dtype);
+  if (!aligned(q, es) || !aligned(out, es) || !aligned(out_lse, 4) || !readable(q_strides, B, N, q_heads) ||
+      !writable(out_strides, B, N, q_heads, a.c.D) || q == out)
+    return SV_EINVAL;
+  if (!attend_shape(B, N, q_heads, a.c.heads, a.c.D, a.t.capacity, dtype, &a.s)) return SV_ESIZE;
+  const AttendSpace w = attend_space(a.s, B, a.c.heads, a.c.D);
+  if (!workspace || !aligned(workspace, WS_ALIGN) || workspace_bytes < w.total) return SV_EWORKSPACE;
+  a.q = q;
+  a.out = out;
+  a.qs = strides_of(q_strides);
+  a.os = strides_of(out_strides);
+  a.lse = out_lse;
+  a.qh = q_heads;
+  a.group = q_heads / a.c.heads;
+  a.window = window;
+  a.bf16 = dtype == SV_BF16;
+  a.scale2 = (float)((double)scale * M_LOG2E);
+  a.record = (int32_t*)((char*)workspace + w.record);
+  a.partial = (float*)((char*)workspace + w.partial);
+  return sv::launch_attend(a, (hipStream_t)stream) ? SV_EHIP : SV_OK;
+}
+
+int spec_verify_adjust_logits(const void* logits, sv_strides strides, sv_dtype dtype, int32_t B,
+                              int32_t N, int32_t V, const int32_t* rows, const int32_t* tokens,
+                              int32_t n_tokens, const int32_t* history, int32_t n_history,
+                              const int32_t* prompt, int32_t n_prompt, const float* repetition,
+                              const float* frequency, const float* presence,
+                              const int32_t* bias_ids, const float* bias, int32_t n_bias,
+                              const uint32_t* allowed, void* out, sv_strides out_strides,
+                              void* stream) {
+  if (!logits || !out) return SV_EINVAL;
+  if (!known(dtype)) return SV_EDTYPE;
+  if (B < 1 || N < 1 || V < 1 || n_tokens < 0 || n_history < 0 || n_prompt < 0 || n_bias < 0) return SV_EINVAL;
+  if ((n_tokens > 0) != (tokens != nullptr) || (n_history > 0) != (history != nullptr) ||
+      (n_prompt > 0) != (prompt != nullptr) || (n_bias > 0) != (bias_ids != nullptr) ||
+      (n_bias > 0) != (bias != nullptr) || (tokens && n_tokens < N - 1))
+    return SV_EINVAL;
+  const size_t es = size_of(dtype);
+  const void* words[] = {rows, tokens, history, prompt, repetition, frequency, presence, bias_ids, bias, allowed};
+  for (const void* p : words)
+    if (!aligned(p, 4)) return SV_EINVAL;
+  strides.head = out_strides.head = 0;
+  if (!aligned(logits, es) || !aligned(out, es) || !readable(strides, B, N, 1) || !writable(out_strides, B, N, 1, V) ||
+      !place_ok(logits, strides, out, out_strides, B, N, 1))
+    return SV_EINVAL;
+  if (V >= INT32_MAX - 65536 || n_history >= 1 << 24 || n_prompt >= 1 << 24 || n_bias >= 1 << 24) return SV_ESIZE;
+  const int64_t chunks = ceil_div(V, sv::ADJ_CHUNK);
+  if ((double)chunks * B * N >= MAX_WORKGROUPS) return SV_ESIZE;
+  // rows of a request in one workgroup, which counts the lists once, unless that leaves CUs idle
+  int64_t groups = ceil_div(8 * CUS, chunks * B);
+  if (groups > N) groups = N;
+  const sv::AdjustArgs a{logits, out, strides_of(strides), strides_of(out_strides), B, N, V, dtype == SV_BF16,
+                         rows, tokens, history, prompt, bias_ids, n_tokens, n_history, n_prompt, n_bias,
+                         repetition, frequency, presence, bias, allowed, (int)chunks, (int)groups};
+  return sv::launch_adjust(a, (hipStream_t)stream) ? SV_EHIP : SV_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,606 @@
+"""The kernels for the verification pass's rows against their float64 forms
+(oracle/serving.py).
+
+Tolerances count roundings. U = 2^-24 is half a step of float32, H half a step of the
+outputs' type.
+  rotate: the angle's fraction of a turn is one float32 (2 pi 2^-26 of a radian), sine
+    and cosine within 2 U each, their factor one rounding, two products and a sum: 8 U (|x| + |y|);
+    plus float64 angles of t turns, off by 2 t 2^-52 turns; plus H of the result.
+  cache: bytes, scales and values are equal, bfloat16 values too: a code times a power of two.
+  attention: a score's products are summed in float32, off by (D + 8) U of sum |q k| scale, which
+    counts twice in a probability's ratio to their sum; base-2 exponents round at |t| U, twice; a
+    probability enters in parts (2^-17 for bfloat16, U for float32); sums of 32 tokens in a matrix
+    instruction, then a block after the other: (64 + tokens / 16) U of sum p |v|; plus H.
+  adjust: float32 operations, at most six roundings of what they pass through; plus H.
+"""
+
+import numpy as np
+import pytest
+
+from oracle import serving as os_
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+HALF = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a HIP device"
+    import lossless_draft_verification_sample_amd._lib as L
+    L.load()
+
+
+def _sv():
+    import lossless_draft_verification_sample_amd as sv
+    return sv
+
+
+def _type(dtype):
+    import torch
+    return {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
+
+
+def _dev(a, dtype=None):
+    import torch
+    t = torch.from_numpy(np.ascontiguousarray(a)).to("cuda:0")
+    return t if dtype is None else t.to(_type(dtype))
+
+
+def _ints(a):
+    return _dev(np.asarray(a, dtype=np.int32))
+
+
+def _host(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _rows(rng, shape, dtype, how="plain", size=1.0):
+    """[B, N, heads, D] on the device and its float64 values. how: plain, fused (cut from a wider
+    row, one element in), heads_first (heads before rows in memory)."""
+    B, N, H, D = shape
+    if how == "heads_first":
+        t = _dev((rng.standard_normal((B, H, N, D)) * size).astype(np.float32), dtype).transpose(1, 2)
+    elif how == "fused":
+        t = _dev((rng.standard_normal((B, N, H * D + 7)) * size).astype(np.float32), dtype)
+        t = t[..., 1: 1 + H * D].unflatten(-1, (H, D))
+    else:
+        t = _dev((rng.standard_normal(shape) * size).astype(np.float32), dtype)
+    assert tuple(t.shape) == tuple(shape)
+    return t, _host(t)
+
+
+# ---------------------------------------------------------------- rotary positions
+
+def _rotate_tol(x, D, R, inter, positions, freqs, scale, dtype, want):
+    lo, hi = (slice(0, R, 2), slice(1, R, 2)) if inter else (slice(0, R // 2), slice(R // 2, R))
+    both = np.abs(x[..., lo]) + np.abs(x[..., hi])
+    turns = np.abs(np.asarray(positions, float)[:, None] * np.asarray(freqs)[None] / (2 * np.pi))
+    tol = np.zeros_like(x)
+    t = both * abs(scale) * (8 * U + 2 * np.pi * 2 * turns * 2.0 ** -52)[:, None]
+    tol[..., lo], tol[..., hi] = t, t
+    tol[..., :R] += HALF[dtype] * (np.abs(want[..., :R]) + t.max(initial=0))
+    return tol
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("B,N,Hq,Hk,D,R,how", [
+    (1, 1, 1, 0, 2, 2, "plain"), (2, 3, 4, 2, 128, 128, "plain"), (3, 5, 2, 1, 96, 48, "fused"),
+    (2, 1, 3, 3, 7, 6, "fused"), (1, 9, 8, 2, 64, 32, "heads_first"), (2, 2, 1, 1, 1024, 1024, "plain"),
+    (1, 2, 2, 1, 10, 0, "plain"), (1, 700, 2, 2, 80, 20, "plain"), (2, 33, 5, 1, 12, 4, "fused"),
+])
+def test_rotate(dtype, inter, B, N, Hq, Hk, D, R, how):
+    import torch
+    rng = np.random.default_rng(B * 100 + N + D + R)
+    q, qx = _rows(rng, (B, N, Hq, D), dtype, how)
+    k, kx = _rows(rng, (B, N, Hk, D), dtype, how) if Hk else (None, None)
+    first = np.array([0, 131071, 2 ** 31 - 5000][:B], dtype=np.int32)
+    freqs = 10000.0 ** (-2.0 * np.arange(R // 2) / max(R, 1))
+    scale = 1.25
+    for inverse in (False, True):
+        out = _sv().spec_verify_rotate(q, k, _ints(first), _dev(freqs), inter, scale, inverse)
+        torch.cuda.synchronize()
+        for got, x in ((out.q, qx), (out.k, kx)):
+            if x is None:
+                assert got is None
+                continue
+            for b in range(B):
+                at = first[b].astype(np.int64) + np.arange(N)
+                want = os_.rotate(x[b], at, freqs, inter, scale, inverse)
+                tol = _rotate_tol(x[b], D, R, inter, at, freqs, scale, dtype, want)
+                far = np.abs(_host(got[b]) - want)
+                assert np.all(far <= tol), (inverse, b, (far - tol).max())
+    # in place, and from position 0
+    at0 = _sv().spec_verify_rotate(q, k, None, _dev(freqs), inter)
+    both = (q.clone(), None if k is None else k.clone())
+    _sv().spec_verify_rotate(*both, None, _dev(freqs), inter, out=_sv().RotateOut(*both))
+    for a, c in zip(at0, both):
+        assert a is None or torch.equal(a, c)
+
+
+def test_rotate_rows_and_gradient():
+    """Rows behind rows[b] stay; a request with rows out of range is NaN; the inverse is the
+    gradient of the sum of products with any weights."""
+    import torch
+    rng = np.random.default_rng(8)
+    q, qx = _rows(rng, (4, 5, 3, 16), "f32")
+    k, kx = _rows(rng, (4, 5, 1, 16), "f32")
+    f = _dev(10000.0 ** (-np.arange(8) / 8.0))
+    at, rows = _ints([3, 4, 5, 6]), _ints([5, 2, 0, 6])
+    full = _sv().spec_verify_rotate(q, k, at, f)
+    out = _sv().RotateOut(torch.full_like(q, 7.0), torch.full_like(k, 7.0))
+    _sv().spec_verify_rotate(q, k, at, f, rows=rows, out=out)
+    for got, want in zip(out, full):
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1, :2], want[1, :2])
+        assert (got[1, 2:] == 7).all() and (got[2] == 7).all() and torch.isnan(got[3]).all()
+    w = torch.randn_like(q)
+    back = _sv().spec_verify_rotate(w, None, at, f, inverse=True).q
+    step = torch.randn_like(q)
+    ahead = _sv().spec_verify_rotate(step, None, at, f).q
+    # sum w R(step) = sum R^-1(w) step: rotation is linear, so this is its gradient exactly
+    a, b = (w.double() * ahead.double()).sum(), (back.double() * step.double()).sum()
+    size = (w.double().abs().amax() * step.double().abs().sum()).item()
+    assert abs(a - b).item() <= 2 * 10 * U * 2 * size
+
+
+# ---------------------------------------------------------------- the cache
+
+def _cache(rng, pages, H, page, D, fill="random"):
+    """A cache whose unwritten bytes are anything (NaN codes among them), scales NaN."""
+    import torch
+    sv = _sv()
+    c = sv.kv_cache(pages, H, page, D)
+    for t in (c.k, c.v):
+        t.view(torch.uint8).copy_(torch.from_numpy(rng.integers(0, 256, t.shape).astype(np.uint8)))
+    for t in (c.k_scale, c.v_scale):
+        t.fill_(float("nan"))
+    return c
+
+
+def _mirror(cache):
+    """The same cache for the oracle: (keys, values)."""
+    import torch
+    return tuple(os_.Cache(codes.view(torch.uint8).cpu().numpy().copy(), scale.cpu().numpy().copy(), cache.head_dim, v)
+                 for codes, scale, v in ((cache.k, cache.k_scale, False), (cache.v, cache.v_scale, True)))
+
+
+def _same_cache(cache, mirror):
+    import torch
+    for codes, scale, m in ((cache.k, cache.k_scale, mirror[0]), (cache.v, cache.v_scale, mirror[1])):
+        a, b = codes.view(torch.uint8).cpu().numpy(), m.codes
+        nan = ((a & 127) == 127) & ((b & 127) == 127)
+        assert np.array_equal(np.where(nan, 0, a), np.where(nan, 0, b))
+        assert np.array_equal(scale.cpu().numpy(), m.scale, equal_nan=True)
+
+
+def _tables(rng, B, width, pages):
+    assert pages >= B * width
+    return rng.permutation(pages)[: B * width].reshape(B, width).astype(np.int32)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("H,D,page,how", [
+    (1, 1, 32, "plain"), (2, 128, 64, "plain"), (3, 80, 32, "fused"), (2, 31, 128, "heads_first"),
+    (1, 256, 32, "plain"), (5, 40, 256, "fused"), (2, 96, 64, "heads_first"), (1, 225, 32, "plain"),
+])
+def test_cache_write_and_read(dtype, H, D, page, how):
+    """Rounds of rows from one token to many, ends inside blocks and pages, then a round that
+    goes back over rejected rows; bytes, scales and values as the float64 form has them."""
+    import torch
+    rng = np.random.default_rng(H * 1000 + D + page)
+    B, top = 4, 200
+    width = -(-top // page)
+    table = _tables(rng, B, width, B * width + 2)
+    cache = _cache(rng, B * width + 2, H, page, D)
+    mirror = _mirror(cache)
+    at = np.array([0, 0, 0, 0])
+    for N, rows in ((1, None), (9, [9, 0, 3, 1]), (70, [70, 33, 31, 32]), (64, [64, 1, 2, 64]), (5, [5, 5, 5, 5])):
+        at = np.maximum(at - 2, 0)
+        k, kx = _rows(rng, (B, N, H, D), dtype, how, 2.0 ** rng.integers(-20, 20))
+        v, vx = _rows(rng, (B, N, H, D), dtype, how, 2.0 ** rng.integers(-3, 3))
+        _sv().spec_verify_cache_write(cache, _dev(table), _ints(at), k, v, None if rows is None else _ints(rows))
+        count = [N] * B if rows is None else rows
+        for b in range(B):
+            mirror[0].write(table[b], at[b], kx[b, : count[b]])
+            mirror[1].write(table[b], at[b], vx[b, : count[b]])
+        torch.cuda.synchronize()
+        _same_cache(cache, mirror)
+        at = at + np.array(count)
+    held = int(at.max())
+    for dt in ("bf16", "f32"):
+        out = _sv().spec_verify_cache_read(cache, _dev(table), None, held, _type(dt), rows=_ints(at))
+        start = np.minimum(at, 13)
+        part = _sv().spec_verify_cache_read(cache, _dev(table), _ints(start), held, _type(dt), rows=_ints(at - start))
+        for got, late, m in zip(out, part, mirror):
+            for b in range(B):
+                want = m.read(table[b], 0, at[b])
+                assert np.array_equal(_host(got[b, : at[b]]), want)
+                assert np.array_equal(_host(late[b, : at[b] - start[b]]), want[start[b]:])
+
+
+def test_cache_values_that_are_not_numbers():
+    """NaN and infinities are stored as NaN and do not count in the scale; zeros have scale 1; the
+    largest and smallest float32 values keep to the definition."""
+    import torch
+    rng = np.random.default_rng(9)
+    cases = [np.array([np.nan, np.inf, -np.inf, 3.0]), np.zeros(4), np.array([-0.0, 0, 0, 0]),
+             np.array([np.nan] * 4), np.array([3.4e38, -1e38, 1, 0]), np.array([1e-45, -1e-42, 0, 1e-44]),
+             np.array([448.0, 449, 1, 2.0 ** -9]), np.array([447.9, 13.5, 14.5, 2.0 ** -10])]
+    B = len(cases)
+    x = np.zeros((B, 2, 1, 4), np.float32)
+    with np.errstate(over="ignore"):
+        x[:, 0, 0] = cases
+        x[:, 1, 0] = np.array(cases)[:, ::-1]
+    cache = _cache(rng, B, 1, 32, 4)
+    mirror = _mirror(cache)
+    table = np.arange(B, dtype=np.int32)[:, None]
+    t = _dev(x)
+    _sv().spec_verify_cache_write(cache, _dev(table), _ints([0] * B), t, t)
+    for b in range(B):
+        for m in mirror:
+            m.write(table[b], 0, _host(t)[b])
+    torch.cuda.synchronize()
+    _same_cache(cache, mirror)
+    got = _sv().spec_verify_cache_read(cache, _dev(table), None, 2, torch.float32)
+    for b in range(B):
+        for g, m in zip(got, mirror):
+            assert np.array_equal(_host(g[b]), m.read(table[b], 0, 2), equal_nan=True)
+    # a later round over a block that holds NaN keeps it
+    y = _dev(np.full((B, 1, 1, 4), 2.0, np.float32))
+    _sv().spec_verify_cache_write(cache, _dev(table), _ints([2] * B), y, y)
+    for b in range(B):
+        for m in mirror:
+            m.write(table[b], 2, _host(y)[b])
+    torch.cuda.synchronize()
+    _same_cache(cache, mirror)
+
+
+def test_cache_requests_and_pages_out_of_range():
+    """Nothing is written for them, they read as NaN, their neighbours are untouched."""
+    import torch
+    rng = np.random.default_rng(10)
+    B, H, D, page = 6, 2, 24, 32
+    table = _tables(rng, B, 2, 2 * B)
+    table[3, 1], table[4, 0] = -1, 2 * B
+    at, rows = [-1, 0, 60, 30, 0, 5], [4, 5, 4, 4, 4, -2]
+    cache = _cache(rng, 2 * B, H, page, D)
+    at[1], rows[1] = 61, 4                               # beyond the table's 64 tokens
+    mirror = _mirror(cache)
+    k, kx = _rows(rng, (B, 4, H, D), "bf16")
+    _sv().spec_verify_cache_write(cache, _dev(table), _ints(at), k, k, _ints(rows))
+    for m in mirror:
+        m.write(table[2], 60, kx[2])
+        m.write(table[3], 30, kx[3])
+    torch.cuda.synchronize()
+    _same_cache(cache, mirror)
+    out = _sv().CacheRows(torch.full((B, 4, H, D), 5.0, device="cuda"), torch.full((B, 4, H, D), 5.0, device="cuda"))
+    _sv().spec_verify_cache_read(cache, _dev(table), _ints(at), 4, rows=_ints(rows), out=out)
+    for g, m in zip(out, mirror):
+        g = _host(g)
+        assert np.isnan(g[[0, 1, 4, 5]]).all()
+        assert np.array_equal(g[2], m.read(table[2], 60, 4)) and np.array_equal(g[3], m.read(table[3], 30, 4), equal_nan=True)
+        assert np.isnan(g[3, 2:]).all() and not np.isnan(g[3, :2]).any()
+    # one of the two alone, rows behind the last one stay
+    one = torch.full((B, 4, H, D), 5.0, device="cuda")
+    _sv().spec_verify_cache_read(cache, _dev(table), _ints([60] * B), 4, rows=_ints([2] * B), out=_sv().CacheRows(None, one))
+    assert (one[:, 2:] == 5).all() and np.array_equal(_host(one[2, :2]), mirror[1].read(table[2], 60, 2))
+
+
+# ---------------------------------------------------------------- attention
+
+def _filled(rng, lens, H, D, page, dtype="bf16", size=1.0):
+    """A cache holding lens[b] tokens of each request: (cache, table, values of keys and of values)."""
+    B, top = len(lens), max(max(lens), 1)
+    width = -(-top // page)
+    table = _tables(rng, B, width, B * width + 3)
+    cache = _cache(rng, B * width + 3, H, page, D)
+    k, kx = _rows(rng, (B, top, H, D), dtype, size=size)
+    v, vx = _rows(rng, (B, top, H, D), dtype)
+    _sv().spec_verify_cache_write(cache, _dev(table), _ints([0] * B), k, v, _ints(lens))
+    keys, vals = (_host(t) for t in _sv().spec_verify_cache_read(cache, _dev(table), None, top, _type("f32")))
+    return cache, table, keys, vals
+
+
+def _attend_tol(q, want, lse, size, reach, tokens, D, dtype):
+    """(of out, of lse)"""
+    parts = 2.0 ** -17 if dtype == "bf16" else U
+    score = (D + 8) * U * reach + 2 * U * (reach + 30) * 1.5
+    near = 2 * score[..., None] + parts + (64 + tokens / 16) * U
+    return size * near + HALF[dtype] * (np.abs(want) + size * near), score + (70 + tokens / 16) * U + U * np.abs(lse)
+
+
+def _check_attend(rng, lens, rows, N, qh, H, D, page, dtype, window=0, how="plain", scale=None, size=1.0, lens_after=None):
+    """lens: tokens before the rows."""
+    import torch
+    B = len(lens)
+    count = [N] * B if rows is None else rows
+    cache, table, keys, vals = _filled(rng, [a + n for a, n in zip(lens, count)], H, D, page, size=size)
+    q, qx = _rows(rng, (B, N, qh, D), dtype, how)
+    s = D ** -0.5 if scale is None else scale
+    out = _sv().AttentionOut(torch.full((B, N, qh, D), 9.0, dtype=_type(dtype), device="cuda"),
+                             torch.full((B, N, qh), 9.0, device="cuda"))
+    got = _sv().spec_verify_attention(q, cache, _dev(table), _ints(lens), scale, window,
+                                      None if rows is None else _ints(rows), out=out)
+    torch.cuda.synchronize()
+    for b in range(B):
+        n, t = count[b], lens[b] + count[b]
+        if n:
+            want, lse, sizes, reach = os_.attention(qx[b, :n], keys[b, :t], vals[b, :t], lens[b], s, window)
+            tol, ltol = _attend_tol(qx, want, lse, sizes, reach, t, D, dtype)
+            far, lfar = np.abs(_host(got.out[b, :n]) - want), np.abs(_host(got.lse[b, :n]) - lse)
+            assert np.all(far <= tol), (b, n, t, (far / tol).max())
+            assert np.all(lfar <= ltol), (b, n, t, (lfar / ltol).max())
+        assert (got.out[b, n:] == 9).all() and (got.lse[b, n:] == 9).all()
+    return cache, table, q, got
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("qh,H,D", [(1, 1, 1), (4, 1, 64), (8, 2, 128), (6, 6, 80), (3, 3, 31), (16, 2, 96), (2, 1, 256),
+                                    (5, 1, 160), (2, 2, 200), (8, 1, 32), (7, 1, 224)])
+def test_attention_heads(dtype, qh, H, D):
+    rng = np.random.default_rng(qh * 100 + H + D)
+    _check_attend(rng, [0, 31, 200], None, 3, qh, H, D, 32, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,qh,H,D", [(1, 8, 8, 128), (9, 8, 2, 128), (9, 16, 2, 64), (17, 4, 1, 128), (33, 4, 1, 96),
+                                      (64, 8, 1, 128), (64, 8, 1, 256), (64, 3, 3, 64), (16, 4, 1, 256), (64, 16, 2, 33)])
+def test_attention_rows(dtype, N, qh, H, D):
+    """One tile of columns to many sets of them; requests without rows among others."""
+    rng = np.random.default_rng(N * 100 + qh + D)
+    _check_attend(rng, [0, 40, 300, 5, 77], [N, (N + 1) // 2, N, 0, 1], N, qh, H, D, 64, dtype, how="fused")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("window", [1, 2, 31, 32, 33, 100, 100000, 2 ** 31 - 1])
+def test_attention_window(dtype, window):
+    rng = np.random.default_rng(window % 1000)
+    _check_attend(rng, [0, 1, 63, 64, 500, 95], [5, 5, 5, 1, 5, 4], 5, 4, 2, 64, 32, dtype, window, how="heads_first")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("page", [32, 128, 1024])
+def test_attention_lengths(dtype, page):
+    """Lengths around the borders of blocks and pages, and long ones that many workgroups share."""
+    rng = np.random.default_rng(page)
+    _check_attend(rng, [0, 1, 30, 31, 32, 33, 63, 64, 65, 127, 128, 5000, 20011], None, 2, 4, 2, 64, page, dtype)
+    _check_attend(rng, [30011], None, 1, 2, 1, 128, page, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B", [64, 65, 300])
+def test_attention_many_requests(dtype, B):
+    rng = np.random.default_rng(B)
+    lens = [int(x) for x in rng.integers(0, 90, B)]
+    rows = [int(x) for x in rng.integers(0, 4, B)]
+    lens[3], rows[3], rows[-1] = 2000, 3, 3
+    _check_attend(rng, lens, rows, 3, 4, 2, 40, 32, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale,size", [(0.0, 1.0), (-0.5, 1.0), (3.0, 4.0), (1e-6, 1.0)])
+def test_attention_scales_and_sharp_scores(dtype, scale, size):
+    """Scores that are all equal, turned round, far apart (each block moves the reference), or tiny."""
+    rng = np.random.default_rng(int(size * 10))
+    _check_attend(rng, [3, 100, 700], None, 4, 4, 1, 64, 32, dtype, scale=scale, size=size)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_rising_scores(dtype):
+    """Scores that rise all along by far more than the reference's slack, and fall again."""
+    import torch
+    rng = np.random.default_rng(5)
+    D, T = 32, 999
+    cache, table, _, _ = _filled(rng, [T], 1, D, 32)
+    ramp = np.concatenate([np.linspace(-200, 200, 600), np.linspace(200, -200, 399)]).astype(np.float32)
+    k = np.zeros((1, T, 1, D), np.float32)
+    k[0, :, 0, 0] = ramp
+    v, vx = _rows(rng, (1, T, 1, D), "f32")
+    _sv().spec_verify_cache_write(cache, _dev(table), _ints([0]), _dev(k), v)
+    keys, vals = (_host(t) for t in _sv().spec_verify_cache_read(cache, _dev(table), None, T, _type("f32")))
+    q = np.zeros((1, 2, 3, D), np.float32)
+    q[0, :, :, 0] = [[1, -1, 0.25], [5, 0.01, 1]]
+    qt = _dev(q, dtype)
+    got = _sv().spec_verify_attention(qt, cache, _dev(table), _ints([T - 2]), 1.0, want_lse=True)
+    want, lse, sizes, reach = os_.attention(_host(qt)[0], keys[0], vals[0], T - 2, 1.0)
+    tol, ltol = _attend_tol(q, want, lse, sizes, reach, T, D, dtype)
+    assert np.all(np.abs(_host(got.out[0]) - want) <= tol) and np.all(np.abs(_host(got.lse[0]) - lse) <= ltol)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [70, 3000])
+def test_attention_nan_reaches_only_rows_that_see_it(dtype, T):
+    """NaN keys and values at one position: rows before it are as without it."""
+    import torch
+    rng = np.random.default_rng(T)
+    N, H, D = 6, 2, 64
+    cache, table, keys, vals = _filled(rng, [T], H, D, 32)
+    q, qx = _rows(rng, (1, N, 4, D), dtype)
+    clean = _sv().spec_verify_attention(q, cache, _dev(table), _ints([T - N])).out
+    for at in (T - 3, T - 1):
+        for name in ("k", "v"):
+            one = {"k": _dev(keys[:, at: at + 1]).float(), "v": _dev(vals[:, at: at + 1]).float()}
+            good = {n: x.clone() for n, x in one.items()}
+            one[name][0, 0, 1, 5] = float("nan")
+            _sv().spec_verify_cache_write(cache, _dev(table), _ints([at]), one["k"], one["v"])
+            got = _sv().spec_verify_attention(q, cache, _dev(table), _ints([T - N])).out
+            _sv().spec_verify_cache_write(cache, _dev(table), _ints([at]), good["k"], good["v"])
+            row = at - (T - N)
+            # writing a position of a block again may move its scale, so compare within tolerance
+            far = (got[0, :row].double() - clean[0, :row].double()).abs().amax().item() if row else 0.0
+            assert far <= 2.0 ** -3, (at, name)          # a code's step of values near 4, at most
+            hit = torch.isnan(got[0, row:])
+            assert hit[:, 2:].any(-1).all() and not hit[:, :2].any()
+            if name == "v":
+                assert hit[:, 2:, 5].all() and hit.sum() == hit[:, 2:, 5].sum()
+            else:
+                assert hit[:, 2:].all()
+    # and outside the window on the other side
+    bad = _dev(np.full((1, 1, H, D), np.nan, np.float32))
+    _sv().spec_verify_cache_write(cache, _dev(table), _ints([T - N - 5]), bad, bad)
+    # (writing position T - N - 5 ends the block's content there; write the rest again)
+    rest = slice(T - N - 4, T)
+    _sv().spec_verify_cache_write(cache, _dev(table), _ints([T - N - 4]), _dev(keys[:, rest]).float(), _dev(vals[:, rest]).float())
+    got = _sv().spec_verify_attention(q, cache, _dev(table), _ints([T - N]), window=7).out
+    assert torch.isnan(got[0, :2]).all() and not torch.isnan(got[0, 2:]).any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_requests_and_pages_out_of_range(dtype):
+    """Bad requests and rows that see an unknown page are NaN, the others as without them; pages
+    before every row's window may be unknown."""
+    import torch
+    rng = np.random.default_rng(12)
+    B, N, H, D, T = 7, 3, 2, 48, 130
+    cache, table, keys, vals = _filled(rng, [T + N] * B, H, D, 32)
+    q, qx = _rows(rng, (B, N, 4, D), dtype)
+    clean = _sv().spec_verify_attention(q, cache, _dev(table), _ints([T] * B), want_lse=True)
+    low = _sv().spec_verify_attention(q, cache, _dev(table), _ints([T] * B), window=40)
+    bad = table.copy()
+    bad[1, 0], bad[2, 2], bad[6, 0] = -1, 10 ** 6, -1
+    lens, rows = [T, T, T, -1, T, 2 ** 31 - 1, T], [N, N, N, N, N + 1, N, N]
+    got = _sv().spec_verify_attention(q, cache, _dev(bad), _ints(lens), rows=_ints(rows), want_lse=True)
+    assert torch.isnan(got.out[1:]).all() and torch.isnan(got.lse[1:]).all()
+    assert torch.equal(got.out[0], clean.out[0]) and torch.equal(got.lse[0], clean.lse[0])
+    got = _sv().spec_verify_attention(q, cache, _dev(bad), _ints([T] * B), window=40)
+    for b in (0, 1, 3, 4, 5, 6):
+        assert torch.equal(got.out[b], low.out[b])       # page 0 lies before the windows
+    assert torch.isnan(got.out[2]).all()                 # page 2 (64 ..) does not: 93 .. is seen
+    late = np.array([T] * B, dtype=np.int32)
+    bad = table.copy()
+    bad[:, 4] = -7                                       # positions 128 ..: the rows themselves
+    late[:] = 126                                        # rows 126, 127 do not see it, 128 does
+    got = _sv().spec_verify_attention(q, cache, _dev(bad), _ints(late)).out
+    want = _sv().spec_verify_attention(q, cache, _dev(table), _ints(late)).out
+    assert torch.equal(got[:, :2], want[:, :2]) and torch.isnan(got[:, 2]).all()
+
+
+def test_cache_and_attention_beyond_32_bits():
+    """Pages further than 2^31 bytes into the cache, rows further apart than 2^31 elements."""
+    import torch
+    rng = np.random.default_rng(13)
+    H, D, page = 1, 128, 32
+    pages = 2 ** 31 // (page * D) + 40
+    cache = _sv().kv_cache(pages, H, page, D)
+    far = np.array([[pages - 1, 3], [5, pages - 7]], dtype=np.int32)
+    near = np.array([[0, 1], [2, 4]], dtype=np.int32)
+    apart = torch.zeros(2 ** 31 + 60 * D, dtype=torch.bfloat16, device="cuda")
+    k, kx = _rows(rng, (2, 50, H, D), "bf16")
+    wide = apart.as_strided((2, 50, H, D), (2 ** 31, D, D, 1))
+    wide.copy_(k)
+    _sv().spec_verify_cache_write(cache, _dev(far), _ints([0, 0]), wide, wide)
+    _sv().spec_verify_cache_write(cache, _dev(near), _ints([0, 0]), k, k)
+    a, b = (_sv().spec_verify_cache_read(cache, _dev(t), None, 50).k for t in (far, near))
+    assert torch.equal(a, b) and (a.double() - k.double()).abs().amax().item() <= 2.0 ** -4 * 5
+    q = wide[:, -3:]
+    x, y = (_sv().spec_verify_attention(p, cache, _dev(t), _ints([47, 47])).out
+            for p, t in ((q, far), (k[:, -3:].contiguous(), near)))
+    assert torch.equal(x, y)
+    f = _dev(10000.0 ** (-np.arange(D // 2) / (D / 2.0)))
+    assert torch.equal(_sv().spec_verify_rotate(wide, None, None, f).q, _sv().spec_verify_rotate(k, None, None, f).q)
+    _sv().spec_verify_rotate(wide, None, None, f, out=_sv().RotateOut(wide, None))
+    assert torch.equal(wide, _sv().spec_verify_rotate(k, None, None, f).q)
+
+
+# ---------------------------------------------------------------- logits
+
+def _words(rng, B, N, V, share):
+    ok = rng.random((B, N, -(-V // 32) * 32)) < share
+    bits = (ok.reshape(B, N, -1, 32).astype(np.uint64) << np.arange(32, dtype=np.uint64)).sum(-1)
+    return ok[..., :V], bits.astype(np.uint32).view(np.int32)
+
+
+def _check_adjust(rng, B, N, V, dtype, nh=0, np_=0, nb=0, share=None, pen=True, rows=None, pad=0, in_place=False, tokens=True,
+                  special=False):
+    import torch
+    z = rng.standard_normal((B, N, V + pad)).astype(np.float32) * 3
+    if special:
+        z[..., ::7], z[..., 1::11], z[..., 2::13] = -np.inf, np.inf, np.nan
+    t = _dev(z, dtype)[..., pad // 2: pad // 2 + V]
+    x = _host(t)
+    lists = {n: rng.integers(-3, min(V, 40) + 5, (B, c)).astype(np.int32) if c else None for n, c in (("history", nh), ("prompt", np_))}
+    prop = rng.integers(-1, V + 1, (B, max(N - 1, 1))).astype(np.int32) if tokens else None
+    vals = {n: (rng.uniform(lo, hi, B)).astype(np.float32) if pen else None
+            for n, lo, hi in (("repetition", 0.7, 2.0), ("frequency", -0.5, 1.0), ("presence", -0.5, 1.0))}
+    bids = rng.integers(-2, V + 2, (B, nb)).astype(np.int32) if nb else None
+    bias = (rng.standard_normal((B, nb)) * 4).astype(np.float32) if nb else None
+    ok, words = _words(rng, B, N, V, share) if share is not None else (None, None)
+    dev = lambda a: None if a is None else _dev(a)  # noqa: E731
+    out = t if in_place else torch.full((B, N, V), 3.0, dtype=t.dtype, device="cuda")
+    _sv().spec_verify_adjust_logits(t, dev(prop), dev(lists["history"]), dev(lists["prompt"]),
+                                    *(dev(vals[n]) for n in ("repetition", "frequency", "presence")), dev(bids), dev(bias),
+                                    dev(words), None if rows is None else _ints(rows), out)
+    torch.cuda.synchronize()
+    got = _host(out)
+    for b in range(B):
+        n = N if rows is None else rows[b]
+        if not 0 <= n <= N:
+            assert np.isnan(got[b]).all()
+            continue
+        p = {m: float(v[b]) if v is not None else d for (m, v), d in zip(vals.items(), (1.0, 0.0, 0.0))}
+        for j in range(n):
+            with np.errstate(invalid="ignore"):
+                want = os_.adjust(x[b, j], j, prop[b] if tokens and pen else (), lists["history"][b] if nh and pen else (),
+                                  lists["prompt"][b] if np_ and pen else (), **p,
+                                  bias=[] if bids is None else zip(bids[b], bias[b].astype(float)),
+                                  allowed=None if ok is None else ok[b, j])
+                size = np.abs(x[b, j]) * 2 + 3 * (nh + N + 1) + (0 if bias is None else np.abs(bias[b]).max())
+                # what nothing touches keeps its value
+                same = (want == x[b, j]) | (np.isnan(want) & np.isnan(x[b, j])) | np.isinf(want)
+                tol = np.where(same, 0.0, HALF[dtype] * np.abs(want) + 6 * U * size * (1 + HALF[dtype]))
+                far = np.abs(got[b, j] - want)
+            fine = (got[b, j] == want) | (np.isnan(got[b, j]) & np.isnan(want)) | (far <= tol)
+            assert fine.all(), (b, j, np.flatnonzero(~fine)[:5], got[b, j][~fine][:5], want[~fine][:5])
+        assert np.array_equal(got[b, n:], x[b, n:] if in_place else np.full_like(got[b, n:], 3.0), equal_nan=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("B,N,V,nh,np_,nb,share,pad", [
+    (1, 1, 1, 3, 0, 0, None, 0), (2, 3, 31, 5, 4, 3, 0.5, 1), (1, 9, 4096, 0, 0, 0, 0.5, 0), (3, 2, 4097, 100, 0, 9, 0.9, 3),
+    (2, 5, 8191, 0, 30, 0, None, 8), (2, 4, 50257, 300, 200, 40, 0.1, 47), (1, 9, 32000, 20, 0, 0, None, 0),
+    (5, 17, 1000, 50, 50, 2, 0.5, 5), (2, 2, 100, 20000, 9000, 1500, None, 0), (40, 9, 9001, 20, 5, 3, 0.5, 0),
+])
+def test_adjust(dtype, in_place, B, N, V, nh, np_, nb, share, pad):
+    rng = np.random.default_rng(B * 100 + V + nh)
+    _check_adjust(rng, B, N, V, dtype, nh, np_, nb, share, pad=pad, in_place=in_place)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_adjust_parts_alone_and_rows(dtype):
+    rng = np.random.default_rng(77)
+    for in_place in (False, True):
+        _check_adjust(rng, 2, 3, 5000, dtype, pen=False, tokens=False, in_place=in_place)       # nothing: a copy
+        _check_adjust(rng, 2, 3, 5000, dtype, pen=False, nb=70, in_place=in_place)
+        _check_adjust(rng, 2, 3, 5000, dtype, pen=False, share=0.3, in_place=in_place)
+        _check_adjust(rng, 2, 3, 5000, dtype, pen=False, share=0.0, in_place=in_place)          # rows without a token
+        _check_adjust(rng, 2, 3, 5000, dtype, pen=False, share=1.0, in_place=in_place)
+        _check_adjust(rng, 2, 3, 5000, dtype, nh=9, tokens=False, in_place=in_place)
+        _check_adjust(rng, 5, 3, 5000, dtype, nh=9, nb=4, share=0.5, rows=[3, 0, 2, 4, -1], in_place=in_place)
+        _check_adjust(rng, 2, 3, 5000, dtype, nh=200, np_=3, nb=60, share=0.7, special=True, in_place=in_place)
+
+
+def test_adjust_long_histories_count_exactly():
+    import torch
+    ids = np.full((1, 300000), 7, np.int32)
+    ids[0, :5] = 9
+    z = _dev(np.zeros((1, 1, 64), np.float32))
+    got = _host(_sv().spec_verify_adjust_logits(z, history=_dev(ids), frequency=_dev(np.array([2.0 ** -10], np.float32))))
+    assert got[0, 0, 7] == -299995 * 2.0 ** -10 and got[0, 0, 9] == -5 * 2.0 ** -10 and np.count_nonzero(got) == 2
+
+
+def test_adjust_rows_further_apart_than_32_bits():
+    import torch
+    V = 40000
+    far = torch.zeros(2 ** 31 + V, dtype=torch.bfloat16, device="cuda")
+    z = far.as_strided((1, 2, V), (0, 2 ** 31, 1))
+    z.copy_(torch.randn(1, 2, V, device="cuda"))
+    near = z.clone(memory_format=torch.contiguous_format)
+    ids = _ints([[5, 6, 39999]])
+    kw = dict(bias_ids=ids, bias=_dev(np.ones((1, 3), np.float32)))
+    want = _sv().spec_verify_adjust_logits(near, **kw)
+    assert torch.equal(_sv().spec_verify_adjust_logits(z, **kw), want)
+    assert torch.equal(_sv().spec_verify_adjust_logits(z, **kw, out=z), want) and torch.equal(z, want)

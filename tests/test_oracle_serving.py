@@ -1,0 +1,116 @@
+"""The float64 forms of oracle/serving.py against independent statements of the
+same things, on the CPU."""
+
+import numpy as np
+import pytest
+
+from oracle import serving as os_
+
+
+def test_codes_are_torchs_e4m3():
+    import torch
+    every = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy()
+    assert np.array_equal(every, os_.TABLE, equal_nan=True)
+    rng = np.random.default_rng(1)
+    x = np.concatenate([rng.uniform(-448, 448, 4000), rng.standard_normal(4000) * 2.0 ** rng.integers(-12, 6, 4000),
+                        (os_.TABLE[:126] + os_.TABLE[1:127]) / 2, [0.0, -0.0, 448, -448, 2.0 ** -10, np.nan]])
+    x = x.astype(np.float32)
+    want = torch.from_numpy(x).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    got = os_.encode(x)
+    nan = np.isnan(x)
+    assert np.array_equal(got[~nan], want[~nan]) and np.all(got[nan] & 127 == 127)
+
+
+@pytest.mark.parametrize("values", [False, True])
+def test_a_brick_has_a_place_for_every_token_and_dimension(values):
+    s, d = np.meshgrid(np.arange(32), np.arange(32), indexing="ij")
+    assert sorted(os_.place(s, d, values).ravel()) == list(range(1024))
+
+
+def test_block_scale():
+    for amax in (448.0, 448.0001, 1.0, 1.75, 1.7500001, 1e-30, 3e38, 1e-45):
+        s = os_.block_scale(np.array([amax, -amax / 3, np.nan, np.inf]))
+        assert 448 * s >= amax and (448 * s / 2 < amax or s == 2.0 ** -126)
+        assert np.log2(s) == np.rint(np.log2(s))
+    assert os_.block_scale(np.zeros(3)) == 1.0
+
+
+@pytest.mark.parametrize("values", [False, True])
+def test_cache_content_decides_the_scale(values):
+    """Writing in pieces is writing the values that the pieces' codes stand for; writing again
+    changes nothing; a rejected outlier leaves no trace once its slot is rewritten."""
+    rng = np.random.default_rng(2)
+    D, H = 40, 2
+    codes = rng.integers(0, 256, (3, H, 2, 2, 1024)).astype(np.uint8)
+    c = os_.Cache(codes, np.full((3, H, 2), np.nan, np.float32), D, values)
+    table, x = [2, 0], rng.standard_normal((70, H, D))
+    c.write(table, 0, x)
+    got = c.read(table, 0, 70)
+    assert np.abs(got - x).max() <= 2.0 ** -4 * np.abs(x).max()
+    before, scales = c.codes.copy(), c.scale.copy()
+    c.write(table, 0, x)
+    assert np.array_equal(before, c.codes) and np.array_equal(scales, c.scale, equal_nan=True)
+    big = x[65:70] * 1000
+    c.write(table, 65, big)
+    assert np.abs(c.read(table, 65, 5) - big).max() <= 2.0 ** -4 * np.abs(big).max()
+    assert c.scale[0, 0, 0] > scales[0, 0, 0]
+    c.write(table, 65, x[65:70])
+    assert c.scale[0, 0, 0] <= scales[0, 0, 0]
+    assert np.isnan(c.read([7], 0, 1)).all()
+
+
+def test_rotation_is_a_rotation_and_goes_back():
+    rng = np.random.default_rng(3)
+    x, f = rng.standard_normal((5, 3, 10)), [1.0, 0.3, 0.01]
+    for inter in (False, True):
+        y = os_.rotate(x, np.arange(7, 12), f, inter)
+        assert np.allclose((y ** 2).sum(-1), (x ** 2).sum(-1)) and np.array_equal(y[..., 6:], x[..., 6:])
+        assert np.allclose(os_.rotate(y, np.arange(7, 12), f, inter, inverse=True), x)
+        # scores depend on distances alone
+        a, b = os_.rotate(x[:1], [100], f, inter), os_.rotate(x[1:2], [90], f, inter)
+        c, d = os_.rotate(x[:1], [12], f, inter), os_.rotate(x[1:2], [2], f, inter)
+        assert np.allclose((a * b).sum(-1), (c * d).sum(-1))
+
+
+def test_rotary_frequencies():
+    import lossless_draft_verification_sample_amd as sv
+    plain, one = sv.rotary_frequencies(64, device="cpu")
+    assert one == 1.0 and np.allclose(plain.numpy(), 10000.0 ** (-np.arange(32) / 32), rtol=1e-15)
+    linear, _ = sv.rotary_frequencies(64, scaling="linear", factor=4.0, device="cpu")
+    assert np.allclose(linear, plain / 4)
+    base, _ = sv.rotary_frequencies(64, scaling="base", factor=4.0, device="cpu")
+    assert base[0] == plain[0] and np.isclose(base[-1], plain[-1] / 4)
+    smooth, _ = sv.rotary_frequencies(64, scaling="smooth", factor=8.0, original=8192, device="cpu")
+    wave = 2 * np.pi / plain.numpy()
+    assert np.array_equal(smooth[wave < 2048], plain[wave < 2048])
+    assert np.allclose(smooth[wave > 8192], plain[wave > 8192] / 8)
+    assert (smooth[:-1] > smooth[1:]).all()
+    ramp, scale = sv.rotary_frequencies(64, scaling="ramp", factor=8.0, original=4096, device="cpu")
+    turns = 4096 / wave
+    assert np.allclose(ramp[turns > 40], plain[turns > 40]) and np.allclose(ramp[turns < 0.7], plain[turns < 0.7] / 8)
+    assert np.isclose(scale, 0.1 * np.log(8.0) + 1)
+    assert sv.rotary_frequencies(0, device="cpu")[0].numel() == 0
+    for bad in (dict(rotary_dim=7), dict(rotary_dim=8, factor=0.5), dict(rotary_dim=8, scaling="no"),
+                dict(rotary_dim=8, scaling="smooth"), dict(rotary_dim=8, base=0.0)):
+        with pytest.raises(ValueError):
+            sv.rotary_frequencies(**bad, device="cpu")
+
+
+def test_attention_by_a_loop_over_tokens():
+    rng = np.random.default_rng(4)
+    q, k, v = rng.standard_normal((3, 4, 6)), rng.standard_normal((9, 2, 6)), rng.standard_normal((9, 2, 6))
+    for window in (0, 1, 4, 100):
+        out, lse, _, _ = os_.attention(q, k, v, 6, 0.4, window)
+        for j in range(3):
+            for h in range(4):
+                seen = [t for t in range(9) if t <= 6 + j and (not window or 6 + j - t < window)]
+                w = [np.exp(0.4 * sum(q[j, h, d] * k[t, h // 2, d] for d in range(6))) for t in seen]
+                want = sum(a * v[t, h // 2] for a, t in zip(w, seen)) / sum(w)
+                assert np.allclose(out[j, h], want) and np.isclose(lse[j, h], np.log(sum(w)))
+
+
+def test_adjust_by_hand():
+    z = np.array([2.0, -2.0, 0.0, 1.0, -np.inf, 3.0])
+    got = os_.adjust(z, 2, tokens=[1, 9, 3], history=[0, 0, -1, 4], prompt=[5], repetition=2.0, frequency=0.25,
+                     presence=0.5, bias=[(3, 7.0), (3, 1.0), (99, 5.0)], allowed=[1, 1, 0, 1, 1, 1])
+    assert np.array_equal(got, [2 / 2 - 1.0, -2 * 2 - 0.75, -np.inf, 2.0, -np.inf, 1.5])
