@@ -487,7 +487,7 @@ int spec_verify_rotate(const void* q, sv_strides q_strides, const void* k, sv_st
  *                       values: byte 256 (s / 8) + 16 (d % 16) + 8 (d / 16) + s % 8,
  *                     the order in which a wavefront takes an operand of its matrix
  *                     instruction, 16 consecutive bytes a lane.
- *   k_scale, v_scale  [pages][heads][page_size / 32] float.
+ *   k_scale, v_scale  [pages][heads][page_size / 32] float, not negative.
  *   page_size         a power of two from 32 to 65536.
  * Fresh memory needs no initialisation: what no call has written is never used. */
 typedef struct {

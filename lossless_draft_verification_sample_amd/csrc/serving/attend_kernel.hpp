@@ -27,11 +27,21 @@
 
 #include <math.h>
 
+#include <type_traits>
+
 #include "sv_serve.hpp"
+
+// What no kernel writes while it runs, read through the scalar cache.
+#define SCALAR __attribute__((address_space(4)))
+#define GLOBAL __attribute__((address_space(1)))
 
 namespace sv {
 
 constexpr float AT_SLACK = 16.0f;      // how far a score may pass the reference (base 2)
+constexpr float AT_FAR = 65536.0f;     // 2^AT_SLACK
+// The reference of a column that has seen no token: finite, so that a masked score's weight is 0,
+// and lower than any that a score of float32 products can become and stay finite.
+constexpr float AT_NONE = -3.40282346638528859812e38f;
 constexpr int AT_LEAST = 4;            // blocks of a workgroup at least: one a wave
 
 __device__ __forceinline__ float at_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -90,6 +100,24 @@ __device__ __forceinline__ Reach reach_of(const AttendArgs& a, int b) {
   return r;
 }
 
+// The first lane's value, which the compiler then keeps in scalar registers: a quotient is made
+// in vector registers, and loads from an address there do not go through the scalar cache.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  return (int64_t)((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v));
+}
+__device__ __forceinline__ float uniform(float v) { return __int_as_float(uniform(__float_as_int(v))); }
+// A uniform address that stays in scalar registers, with nothing of a lane's added to it ahead of
+// its loop.
+template <typename P>
+__device__ __forceinline__ P scalar(P p) {
+  asm volatile("" : "+s"(p));
+  return p;
+}
+__device__ __forceinline__ Reach uniform(Reach r) {
+  return Reach{uniform(r.first), uniform(r.rows), uniform(r.block0), uniform(r.blocks), uniform((int)r.bad) != 0};
+}
+
 __device__ __forceinline__ int64_t wave_sum64(int64_t v) {
 #pragma unroll
   for (int off = WAVE / 2; off; off >>= 1) v += __shfl_xor(v, off, WAVE);
@@ -111,33 +139,35 @@ __device__ __forceinline__ sbf16x8 ones8(uint32_t lo, uint32_t hi) {
   return __builtin_bit_cast(sbf16x8, w);
 }
 
-constexpr int at_waves_per_simd(int bricks, int nt) {
-  // registers of a lane: sums, a block's codes, scores and parts, the rest
-  const int need = 8 * bricks * nt + 8 * bricks + 16 * nt + 56;
-  return need <= 128 ? 4 : need <= 168 ? 3 : need <= 256 ? 2 : 1;
+// The kernel's arguments, loaded again: what only the end of a segment needs does not take
+// scalar registers from the loop.
+__device__ __forceinline__ const AttendArgs& fresh_args() {
+  const SCALAR AttendArgs* p = (const SCALAR AttendArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const AttendArgs*)p;
 }
 
 template <int BRICKS, int NT, bool F32>
-__global__ __launch_bounds__(AT_THREADS, at_waves_per_simd(BRICKS, NT)) void attend_kernel(AttendArgs a) {
+__global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT)) void attend_kernel(AttendArgs a) {
   constexpr int QP = F32 ? 3 : 1, PP = F32 ? 3 : 2, DT = 2 * BRICKS;
   extern __shared__ char lds[];
-  __shared__ float stat[AT_WAVES][NT * 16][2];
+  __shared__ float stat[AT_WAVES][NT * 16][2], total[AT_WAVES * NT * 16][2];
   const int tid = threadIdx.x, lane = tid % WAVE, wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
   const int col16 = lane & 15, quad = lane >> 4;
-  const int across = a.s.across, along = AT_WAVES / across;
-  const int side = wave % across, turn = wave / across;
+  const int across = a.s.across, along = uniform(AT_WAVES / across);
+  const int turn = uniform(wave / across), side = wave - turn * across;
   const int U = a.c.heads * a.s.sets;
 
   // the blocks of all requests, and this workgroup's share of them
   int64_t T = 0;
   for (int b = lane; b < a.t.B; b += WAVE) T += (int64_t)reach_of(a, b).blocks * U;
-  T = wave_sum64(T);
+  T = uniform(wave_sum64(T));
   int64_t W = T / AT_LEAST;
   W = W < 1 ? 1 : W > (int64_t)gridDim.x ? (int64_t)gridDim.x : W;
   const int64_t wg = blockIdx.x;
   if (wg >= W || T == 0) return;
-  int64_t x = T * wg / W;
-  const int64_t x1 = T * (wg + 1) / W;
+  int64_t x = uniform(T * wg / W);
+  const int64_t x1 = uniform(T * (wg + 1) / W);
   if (x >= x1) return;
   // the request of block x
   int64_t before = 0;      // blocks of the requests before b
@@ -159,43 +189,48 @@ __global__ __launch_bounds__(AT_THREADS, at_waves_per_simd(BRICKS, NT)) void att
     }
     before += __shfl(upto, WAVE - 1, WAVE);
   }
-  b = __builtin_amdgcn_readfirstlane(b);
+  b = uniform(b);
+  before = uniform(before);
 
   while (x < x1) {
     // a segment: this workgroup's blocks of one unit
-    Reach r = reach_of(a, b);
+    Reach r = uniform(reach_of(a, b));
     while ((int64_t)r.blocks * U <= x - before) {      // also requests without blocks
       before += (int64_t)r.blocks * U;
-      r = reach_of(a, ++b);
+      r = uniform(reach_of(a, ++b));
     }
-    const int unit = (int)((x - before) / r.blocks);
+    const int unit = uniform((int)((x - before) / r.blocks));
     const int64_t unit0 = before + (int64_t)unit * r.blocks;
     const int i0 = (int)(x - unit0);
     const int i1 = (int)((x1 < unit0 + r.blocks ? x1 : unit0 + r.blocks) - unit0);
-    const int h = unit / a.s.sets, set = unit % a.s.sets;
+    const int h = uniform(unit / a.s.sets), set = unit - h * a.s.sets;
     const int col0 = (set * across + side) * NT * 16;   // this wave's first column
-    const int C = a.s.cols;
 
     // queries into LDS, in the order of the B operand: [part][tile][brick][lane] 16 bytes
     {
+      const AttendArgs& z = fresh_args();
       const int tiles = across * NT;
       for (int i = tid; i < tiles * BRICKS * WAVE; i += AT_THREADS) {
         const int l = i % WAVE, c = i / WAVE % BRICKS, t = i / WAVE / BRICKS;
-        const int col = set * a.s.cols_set + t * 16 + (l & 15), d = 32 * c + 8 * (l >> 4);
+        const int col = set * z.s.cols_set + t * 16 + (l & 15), d = 32 * c + 8 * (l >> 4);
         float y[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] = 0.0f;
-        if (col < C && d < a.c.D) {
-          const int j = col / a.group, g = col % a.group;
-          const int64_t at = b * a.qs.b + j * a.qs.n + (int64_t)(h * a.group + g) * a.qs.h + d;
-          if (d + 8 <= a.c.D) {
-            if constexpr (F32) load8((const float*)a.q + at, y);
-            else load8((const uint16_t*)a.q + at, y);
+        if (col < z.s.cols && d < z.c.D) {
+          const int j = col / z.group, g = col % z.group;
+          const int64_t from = b * z.qs.b + j * z.qs.n + (int64_t)(h * z.group + g) * z.qs.h + d;
+          if (d + 8 <= z.c.D) {
+            if constexpr (F32) load8((const float*)z.q + from, y);
+            else load8((const uint16_t*)z.q + from, y);
           } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              if (d + e < a.c.D) y[e] = F32 ? elem((const float*)a.q + at + e) : elem((const uint16_t*)a.q + at + e);
+              if (d + e < z.c.D) y[e] = F32 ? elem((const float*)z.q + from + e) : elem((const uint16_t*)z.q + from + e);
           }
+        }
+        if (z.scale2 < 0.0f) {      // so that a score's factor is never negative
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = -y[e];
         }
         sbf16x8 p[QP];
         split8<QP>(y, p);
@@ -206,14 +241,15 @@ __global__ __launch_bounds__(AT_THREADS, at_waves_per_simd(BRICKS, NT)) void att
     __syncthreads();
 
     sf32x4 O[NT][DT];
-    float l[NT], sub[NT], thr[NT];
+    float l[NT], sub[NT];                                // sub: the column's reference
+    bool settled = false;                                // every column has one
     int last[NT];                                        // the last position a column sees
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
       for (int i = 0; i < DT; ++i) O[t][i] = sf32x4{0, 0, 0, 0};
-      l[t] = sub[t] = 0.0f;
-      thr[t] = -INFINITY;
+      l[t] = 0.0f;
+      sub[t] = AT_NONE;
       last[t] = r.first + (col0 + t * 16 + col16) / a.group;
     }
     const int end = r.first + r.rows;
@@ -221,39 +257,53 @@ __global__ __launch_bounds__(AT_THREADS, at_waves_per_simd(BRICKS, NT)) void att
     const sbf16x8* qf = (const sbf16x8*)lds + side * NT * BRICKS * WAVE + lane;
     const int q_part = across * NT * BRICKS * WAVE;
 
-    su32x4 kraw[BRICKS], vraw[BRICKS];
+    // Where block i lies: its page is asked for two blocks ahead, its scales one ahead, both
+    // through the scalar cache, so that no load waits for an address.
+    const SCALAR int32_t* table = (const SCALAR int32_t*)a.t.table + (r.bad ? 0 : (int64_t)b * a.t.width);
+    auto page_of = [&](int i) {
+      i = i < i1 ? i : i1 - 1;
+      const SCALAR int32_t* p = scalar(table + (r.bad ? 0 : (r.block0 + i) >> a.c.per_log2));
+      return uniform(*p);
+    };
+    const float scale2 = fabsf(a.scale2);
+    int page_next = 0;
+    int64_t at = 0;
     float ks = 0, vs = 0, ks_next = 0, vs_next = 0;
     bool lost = false, lost_next = false;
-    // asks for a block's keys; where it lies is kept for its values
-    int64_t at_next = 0;
     auto locate = [&](int i) {
-      const int blk = r.block0 + i;
-      int page = r.bad ? -1 : a.t.table[(int64_t)b * a.t.width + (blk >> a.c.per_log2)];
-      page = __builtin_amdgcn_readfirstlane(page);
-      lost_next = (uint32_t)page >= (uint32_t)a.c.pages;
-      if (lost_next) page = 0;
-      at_next = (((int64_t)page * a.c.heads + h) << a.c.per_log2) + (blk & ((1 << a.c.per_log2) - 1));
-      ks_next = a.c.ks[at_next];
-      vs_next = lost_next ? 1.0f : a.c.vs[at_next];
+      lost_next = r.bad || (uint32_t)page_next >= (uint32_t)a.c.pages;
+      const int page = lost_next ? 0 : page_next, in_page = (r.block0 + i) & ((1 << a.c.per_log2) - 1);
+      at = uniform((((int64_t)page * a.c.heads + h) << a.c.per_log2) + in_page);
+      ks_next = uniform(*scalar((const SCALAR float*)a.c.ks + at));
+      vs_next = uniform(*scalar((const SCALAR float*)a.c.vs + at));
     };
+    su32x4 kraw[BRICKS], vraw[BRICKS];
     auto load = [&](const uint8_t* base, su32x4 (&raw)[BRICKS]) {
-      const su32x4* p = (const su32x4*)(base + at_next * (BRICKS * BRICK)) + lane;
+      const GLOBAL uint8_t* p = scalar((const GLOBAL uint8_t*)base + at * (BRICKS * BRICK));
 #pragma unroll
-      for (int c = 0; c < BRICKS; ++c) raw[c] = p[c * WAVE];
+      for (int c = 0; c < BRICKS; ++c) raw[c] = *(const GLOBAL su32x4*)(p + (uint32_t)(lane * 16) + c * BRICK);
     };
     int i = i0 + turn;
     if (i < i1) {
+      page_next = page_of(i);
       locate(i);
+      page_next = page_of(i + along);
       load(a.c.k, kraw);
       load(a.c.v, vraw);
     }
+
     for (; i < i1; i += along) {
+      // the queries are read from LDS for every block, not kept in registers that the sums need
+      if constexpr (NT * BRICKS * QP > 8) asm volatile("" ::: "memory");
       const int t0 = (r.block0 + i) * CACHE_BLOCK;
-      ks = ks_next * a.scale2;
+      ks = ks_next * scale2;
       vs = vs_next;
       lost = lost_next;
       const bool more = i + along < i1;
-      if (more) locate(i + along);
+      if (more) {
+        locate(i + along);
+        page_next = page_of(i + 2 * along);
+      }
 
       sf32x4 S[NT][2];
 #pragma unroll
@@ -273,80 +323,97 @@ __global__ __launch_bounds__(AT_THREADS, at_waves_per_simd(BRICKS, NT)) void att
       }
       if (more) load(a.c.k, kraw);
 
-      // whether some row does not see some token here, or the page is unknown
+      // some row does not see some token here, or the page is unknown
       const bool edge = t0 + CACHE_BLOCK - 1 > r.first || t0 < open0 || lost;
-      float p[NT][8], most[NT];
-      bool moved = false;
+      if (edge) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) p[t][e] = S[t][e >> 2][e & 3] * ks;
-        if (edge) {
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const int pos = t0 + 8 * quad + e;
-            if (lost) p[t][e] = NAN;
-            if (pos > last[t] || (a.window && pos <= last[t] - a.window)) p[t][e] = -INFINITY;
+            float x = lost ? NAN : S[t][e >> 2][e & 3] * ks;
+            if (pos > last[t] || (a.window && pos <= last[t] - a.window)) x = -INFINITY;
+            S[t][e >> 2][e & 3] = x;
           }
-        }
-        most[t] = fmaxf(fmaxf(fmaxf(p[t][0], p[t][1]), fmaxf(p[t][2], p[t][3])),
-                        fmaxf(fmaxf(p[t][4], p[t][5]), fmaxf(p[t][6], p[t][7])));
-        moved |= most[t] > thr[t];
-      }
-      if (__any(moved)) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          float m = most[t];
-          m = fmaxf(m, __shfl_xor(m, 16, WAVE));
-          m = fmaxf(m, __shfl_xor(m, 32, WAVE));
-          if (m > thr[t]) {
-            const float f = thr[t] == -INFINITY ? 1.0f : at_exp2(sub[t] - m);
-#pragma unroll
-            for (int k = 0; k < DT; ++k) O[t][k] *= f;
-            l[t] *= f;
-            sub[t] = m;
-            thr[t] = m + AT_SLACK;
-          }
-        }
-      }
-      // values of tokens that no row sees may be anything, and NaN times 0 is NaN
-      uint32_t nan0[BRICKS], nan1[BRICKS], nan2[BRICKS], nan3[BRICKS];
-      bool some_nan = false;
-      if (edge) {
+        ks = 1.0f;
+        // values of tokens that no row sees may be anything, and NaN times 0 is NaN
         const int left = end - (t0 + 8 * quad);
         const uint32_t m0 = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
         const uint32_t m1 = left >= 8 ? ~0u : left <= 4 ? 0u : (1u << (8 * (left - 4))) - 1u;
 #pragma unroll
         for (int c = 0; c < BRICKS; ++c) {
-          vraw[c][0] &= m0;
-          vraw[c][1] &= m1;
-          vraw[c][2] &= m0;
-          vraw[c][3] &= m1;
-          nan0[c] = nan_codes(vraw[c][0]);
-          nan1[c] = nan_codes(vraw[c][1]);
-          nan2[c] = nan_codes(vraw[c][2]);
-          nan3[c] = nan_codes(vraw[c][3]);
-          some_nan |= (nan0[c] | nan1[c] | nan2[c] | nan3[c]) != 0;
-          vraw[c][0] &= ~(nan0[c] * 255u);
-          vraw[c][1] &= ~(nan1[c] * 255u);
-          vraw[c][2] &= ~(nan2[c] * 255u);
-          vraw[c][3] &= ~(nan3[c] * 255u);
+          vraw[c] &= su32x4{m0, m1, m0, m1};
+          su32x4 nan;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) nan[e] = nan_codes(vraw[c][e]);
+          if (__any((nan[0] | nan[1] | nan[2] | nan[3]) != 0)) {
+            // NaN values that some row sees, and maybe not all: taken out of the product, and a
+            // product of their places with the rows' sight says whose sums are NaN
+            vraw[c] &= ~(nan * 255u);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              float one[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) one[e] = S[t][e >> 2][e & 3] != -INFINITY ? 1.0f : 0.0f;
+              sbf16x8 seen[1];
+              split8<1>(one, seen);
+              const sf32x4 zero{0, 0, 0, 0};
+              const sf32x4 n0 = mma(ones8(nan[0], nan[1]), seen[0], zero);
+              const sf32x4 n1 = mma(ones8(nan[2], nan[3]), seen[0], zero);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if (n0[e] > 0.0f) O[t][2 * c][e] = NAN;
+                if (n1[e] > 0.0f) O[t][2 * c + 1][e] = NAN;
+              }
+            }
+          }
         }
-        some_nan = __any(some_nan);
       }
+
+      // Weights, and where a column has no reference yet, or a score exceeds it by more than the
+      // slack, its reference first.
+      float w[NT][8];
+      for (bool move = !settled;;) {
+        if (move) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const sf32x4 x = S[t][0], y = S[t][1];
+            float m = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])));
+            m *= ks;
+            m = fmaxf(m, __shfl_xor(m, 16, WAVE));
+            m = fmaxf(m, __shfl_xor(m, 32, WAVE));
+            const bool none = sub[t] == AT_NONE;
+            if (m > sub[t] + AT_SLACK || (none && m > -INFINITY)) {
+              const float f = none ? 1.0f : at_exp2(sub[t] - m);
+#pragma unroll
+              for (int k = 0; k < DT; ++k) O[t][k] *= f;
+              l[t] *= f;
+              sub[t] = m;
+            }
+          }
+        }
+        float most = 0.0f;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            w[t][e] = at_exp2(__builtin_fmaf(S[t][e >> 2][e & 3], ks, -sub[t]));
+            most = fmaxf(most, w[t][e]);
+          }
+        if (move || !__any(most > AT_FAR)) break;
+        move = true;
+      }
+      if (!edge) settled = true;
+
       sbf16x8 pf[NT][PP];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        float w[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const bool seen = p[t][e] != -INFINITY;
-          w[e] = at_exp2(p[t][e] - sub[t]);
-          l[t] += w[e];
-          w[e] = edge && !seen ? 0.0f : w[e] * vs;
-          p[t][e] = seen ? 1.0f : 0.0f;
+          l[t] += w[t][e];
+          w[t][e] *= vs;
         }
-        split8<PP>(w, pf[t]);
+        split8<PP>(w[t], pf[t]);
       }
 #pragma unroll
       for (int c = 0; c < BRICKS; ++c) {
@@ -360,80 +427,60 @@ __global__ __launch_bounds__(AT_THREADS, at_waves_per_simd(BRICKS, NT)) void att
           }
         }
       }
-      if (some_nan) {
-        // how many NaN values each column sees of each dimension
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          sbf16x8 seen[1];
-          split8<1>(p[t], seen);
-#pragma unroll
-          for (int c = 0; c < BRICKS; ++c) {
-            const sf32x4 zero{0, 0, 0, 0};
-            const sf32x4 n0 = mma(ones8(nan0[c], nan1[c]), seen[0], zero);
-            const sf32x4 n1 = mma(ones8(nan2[c], nan3[c]), seen[0], zero);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if (n0[e] > 0.0f) O[t][2 * c][e] = NAN;
-              if (n1[e] > 0.0f) O[t][2 * c + 1][e] = NAN;
-            }
-          }
-        }
-      }
       if (more) load(a.c.v, vraw);
     }
 
     // the waves' parts joined, in the order of the waves
+    const AttendArgs& z = fresh_args();
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       l[t] += __shfl_xor(l[t], 16, WAVE);
       l[t] += __shfl_xor(l[t], 32, WAVE);
       if (quad == 0) {
-        stat[wave][t * 16 + col16][0] = thr[t] == -INFINITY && l[t] == 0.0f ? -INFINITY : sub[t];
+        // -inf: it saw nothing
+        stat[wave][t * 16 + col16][0] = sub[t] == AT_NONE && l[t] == 0.0f ? -INFINITY : sub[t];
         stat[wave][t * 16 + col16][1] = l[t];
       }
     }
     __syncthreads();       // the queries are free too
-    float f[NT][AT_WAVES], M[NT], L[NT];
+    const bool all = i0 == 0 && i1 == r.blocks;
+    float* part = z.partial + (wg * 2 + (i0 == 0 ? 1 : 0)) * ((int64_t)z.s.cols_set * (z.c.D + 2));
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      M[t] = -INFINITY;
+      float M = -INFINITY, L = 0.0f;
       bool nan = false;
       for (int k = 0; k < along; ++k) {
         const float m = stat[k * across + side][t * 16 + col16][0];
-        M[t] = fmaxf(M[t], m);
+        M = fmaxf(M, m);
         nan |= m != m;
       }
-      if (nan) M[t] = NAN;
-      L[t] = 0.0f;
+      if (nan) M = NAN;
+      for (int k = 0; k < along; ++k) {
+        const float m = stat[k * across + side][t * 16 + col16][0];
+        if (m != -INFINITY) L += at_exp2(m - M) * stat[k * across + side][t * 16 + col16][1];
+      }
+      const float mine = stat[wave][t * 16 + col16][0];
+      const float f = at_exp2(mine - M);
 #pragma unroll
-      for (int k = 0; k < AT_WAVES; ++k) {
-        f[t][k] = -1.0f;
-        if (k < along) {
-          const float m = stat[k * across + side][t * 16 + col16][0];
-          f[t][k] = m == -INFINITY ? -1.0f : at_exp2(m - M[t]);    // -1: it saw nothing
-          if (m != -INFINITY) L[t] += f[t][k] * stat[k * across + side][t * 16 + col16][1];
+      for (int k = 0; k < DT; ++k) O[t][k] = mine == -INFINITY ? sf32x4{0, 0, 0, 0} : O[t][k] * f;
+      if (turn == 0 && quad == 0) {
+        const int col = (side * NT + t) * 16 + col16;
+        total[col][0] = M;
+        total[col][1] = L;
+        if (!all) {
+          float* ml = part + (int64_t)z.s.cols_set * z.c.D;
+          ml[2 * col] = M;
+          ml[2 * col + 1] = L;
         }
       }
     }
-    const bool all = i0 == 0 && i1 == r.blocks;
-    const int64_t unit_id = ((int64_t)b * a.c.heads + h) * a.s.sets + set;
-    float* part = a.partial + (wg * 2 + (i0 == 0 ? 1 : 0)) * ((int64_t)a.s.cols_set * (a.c.D + 2));
     if (i0 == 0 && tid == 0) {
-      const int64_t y = unit0 + r.blocks - 1;
-      a.record[2 * unit_id] = (int32_t)wg;
-      a.record[2 * unit_id + 1] = (int32_t)(((y + 1) * W + T - 1) / T - 1 - wg) + 1;
+      const int64_t unit_id = ((int64_t)b * z.c.heads + h) * z.s.sets + set, y = unit0 + r.blocks - 1;
+      z.record[2 * unit_id] = (int32_t)wg;
+      z.record[2 * unit_id + 1] = (int32_t)(((y + 1) * W + T - 1) / T - 1 - wg) + 1;
     }
-    if (!all && turn == 0 && quad == 0) {
-      float* ml = part + (int64_t)a.s.cols_set * a.c.D;
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int col = (side * NT + t) * 16 + col16;
-        ml[2 * col] = M[t];
-        ml[2 * col + 1] = L[t];
-      }
-    }
-    sf32x4* sums = (sf32x4*)lds;                 // [wave][tile of a dimension's 16][NT][lane]
-    constexpr int CH = 2;                        // tiles of dimensions a round
+    sf32x4* sums = (sf32x4*)lds;                 // [wave][16 dimensions of CH][NT][lane]
+    constexpr int CH = 2;                        // groups of 16 dimensions a round
 #pragma unroll
     for (int d0 = 0; d0 < DT; d0 += CH) {
 #pragma unroll
@@ -441,34 +488,25 @@ __global__ __launch_bounds__(AT_THREADS, at_waves_per_simd(BRICKS, NT)) void att
 #pragma unroll
         for (int t = 0; t < NT; ++t) sums[((wave * CH + k) * NT + t) * WAVE + lane] = O[t][d0 + k];
       __syncthreads();
-#pragma unroll
-      for (int kt = 0; kt < CH * NT; ++kt) {
-        if (kt % along != turn) continue;
-        const int k = kt / NT, t = kt % NT;
-        sf32x4 o{0, 0, 0, 0};
-#pragma unroll
-        for (int n = 0; n < AT_WAVES; ++n)
-          if (n < along) {
-            const sf32x4 y = sums[(((n * across + side) * CH + k) * NT + t) * WAVE + lane];
-            if (!(f[t][n] < 0.0f)) o += y * f[t][n];
-          }
-        const int d = 16 * (d0 + k) + 4 * quad, in_set = (side * NT + t) * 16 + col16;
-        const int col = set * a.s.cols_set + in_set;
+      for (int n = tid; n < across * CH * NT * WAVE; n += AT_THREADS) {
+        sf32x4 o = sums[n];
+        for (int k = 1; k < along; ++k) o += sums[k * across * CH * NT * WAVE + n];
+        const int ln = n % WAVE, t = n / WAVE % NT, k = n / WAVE / NT % CH, sd = n / WAVE / NT / CH;
+        const int d = 16 * (d0 + k) + 4 * (ln >> 4), in_set = (sd * NT + t) * 16 + (ln & 15);
+        const int col = set * z.s.cols_set + in_set;
         if (!all) {
           for (int e = 0; e < 4; ++e)
-            if (d + e < a.c.D) part[(int64_t)in_set * a.c.D + d + e] = o[e];
-        } else if (col < C && col / a.group < r.rows) {
-          const int j = col / a.group, g = col % a.group;
-          const int64_t at = b * a.os.b + j * a.os.n + (int64_t)(h * a.group + g) * a.os.h + d;
-          const float inv = 1.0f / L[t];
+            if (d + e < z.c.D) part[(int64_t)in_set * z.c.D + d + e] = o[e];
+        } else if (col < z.s.cols && col / z.group < r.rows) {
+          const int j = col / z.group, head = h * z.group + col % z.group;
+          const int64_t to = b * z.os.b + j * z.os.n + (int64_t)head * z.os.h + d;
+          const float M = total[in_set][0], L = total[in_set][1], inv = 1.0f / L;
           for (int e = 0; e < 4; ++e)
-            if (d + e < a.c.D) {
-              if constexpr (F32) put((float*)a.out + at + e, o[e] * inv);
-              else put((uint16_t*)a.out + at + e, o[e] * inv);
+            if (d + e < z.c.D) {
+              if constexpr (F32) put((float*)z.out + to + e, o[e] * inv);
+              else put((uint16_t*)z.out + to + e, o[e] * inv);
             }
-          if (a.lse && d0 + k == 0 && quad == 0)
-            a.lse[((int64_t)b * a.t.N + j) * a.qh + h * a.group + g] =
-                (M[t] + __log2f(L[t])) * 0.69314718055994530942f;
+          if (z.lse && d == 0) z.lse[((int64_t)b * z.t.N + j) * z.qh + head] = (M + __log2f(L)) * 0.69314718055994530942f;
         }
       }
       __syncthreads();

@@ -164,6 +164,12 @@ struct AttendShape {
   int grid;           // workgroups at most
   int lds;            // bytes of LDS
 };
+// Workgroups of a CU, which is waves of a SIMD: by the registers of a lane (sums, a block's
+// codes, scores and parts, the rest).
+constexpr int attend_per_cu(int bricks, int nt) {
+  const int need = 8 * bricks * nt + 8 * bricks + 22 * nt + 40;
+  return need <= 128 ? 4 : need <= 168 ? 3 : need <= 256 ? 2 : 1;
+}
 struct AttendArgs {
   Cache c;
   Batch t;
