@@ -442,7 +442,9 @@ int spec_verify_linear_ce_backward(const void* hidden, int64_t hidden_stride, co
  *     of the outputs, and nothing of it is written to the cache.
  *   - Sums, softmax statistics and products are float32 or wider whatever the
  *     inputs' type; results are rounded once.
- *   - No result depends on the order in which workgroups run.
+ *   - No result depends on the order in which workgroups run. (How attention shares out a
+ *     request's tokens follows from the lengths of the whole batch: in another batch its sums may
+ *     be in another order.)
  *   - Workspaces as in the training calls: no initialisation, 256-byte aligned,
  *     nothing kept between calls, separate ones for calls that may run concurrently. */
 
@@ -544,7 +546,8 @@ int spec_verify_cache_read(const sv_cache* cache, const int32_t* page_table, int
  * NaN in a position that a row does not see does not reach it. A row that sees a position in a
  * page outside [0, pages) is NaN; pages that no row of the request sees (all before its window)
  * are not read. Requests out of range as in spec_verify_cache_write.
- * Limits: 1 <= N <= 64, q_heads a multiple of the cache's heads, head_dim <= 256, window >= 0;
+ * Limits: 1 <= N <= 64, q_heads a multiple of the cache's heads (at most 4096 of them to one, SV_ESIZE
+ * beyond), head_dim <= 256, window >= 0;
  * B * N * q_heads < 2^31 (SV_ESIZE beyond). The workspace holds the parts of requests that
  * several workgroups share; `tokens` is table_width * page_size. */
 #define SV_MAX_ROWS 64

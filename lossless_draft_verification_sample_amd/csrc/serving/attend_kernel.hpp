@@ -43,6 +43,8 @@ constexpr float AT_FAR = 65536.0f;     // 2^AT_SLACK
 // and lower than any that a score of float32 products can become and stay finite.
 constexpr float AT_NONE = -3.40282346638528859812e38f;
 constexpr int AT_LEAST = 4;            // blocks of a workgroup at least: one a wave
+// What starting and ending a unit costs, in blocks: it counts in the workgroups' shares.
+constexpr int AT_START = 8;
 
 __device__ __forceinline__ float at_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -139,6 +141,28 @@ __device__ __forceinline__ sbf16x8 ones8(uint32_t lo, uint32_t hi) {
   return __builtin_bit_cast(sbf16x8, w);
 }
 
+// The row of a column, by the reciprocal of the query heads that share a cache head.
+__device__ __forceinline__ int row_of(const AttendArgs& a, int col) {
+  return a.group == 1 ? col : (int)__umulhi((uint32_t)col, a.group_inv);
+}
+
+// Up to 4 of 4 values, `left` of them in the row.
+__device__ __forceinline__ void put4(float* p, sf32x4 x, int left) {
+  if (left >= 4) {
+    *(su32x4_any*)p = __builtin_bit_cast(su32x4, x);
+  } else {
+    for (int e = 0; e < left; ++e) p[e] = x[e];
+  }
+}
+__device__ __forceinline__ void put4(uint16_t* p, sf32x4 x, int left) {
+  const su32x2 w{round_bf16x2(x[0], x[1]), round_bf16x2(x[2], x[3])};
+  if (left >= 4) {
+    *(su32x2_any*)p = w;
+  } else {
+    for (int e = 0; e < left; ++e) p[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+  }
+}
+
 // The kernel's arguments, loaded again: what only the end of a segment needs does not take
 // scalar registers from the loop.
 __device__ __forceinline__ const AttendArgs& fresh_args() {
@@ -159,8 +183,9 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT)) void attend_
   const int U = a.c.heads * a.s.sets;
 
   // the blocks of all requests, and this workgroup's share of them
+  auto cost = [&](const Reach& r) { return r.blocks ? (int64_t)(r.blocks + AT_START) * U : 0; };
   int64_t T = 0;
-  for (int b = lane; b < a.t.B; b += WAVE) T += (int64_t)reach_of(a, b).blocks * U;
+  for (int b = lane; b < a.t.B; b += WAVE) T += cost(reach_of(a, b));
   T = uniform(wave_sum64(T));
   int64_t W = T / AT_LEAST;
   W = W < 1 ? 1 : W > (int64_t)gridDim.x ? (int64_t)gridDim.x : W;
@@ -168,12 +193,11 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT)) void attend_
   if (wg >= W || T == 0) return;
   int64_t x = uniform(T * wg / W);
   const int64_t x1 = uniform(T * (wg + 1) / W);
-  if (x >= x1) return;
-  // the request of block x
-  int64_t before = 0;      // blocks of the requests before b
+  // the request of x
+  int64_t before = 0;      // cost of the requests before b
   int b = 0;
   for (int b0 = 0; b0 < a.t.B; b0 += WAVE) {
-    const int64_t mine = b0 + lane < a.t.B ? (int64_t)reach_of(a, b0 + lane).blocks * U : 0;
+    const int64_t mine = b0 + lane < a.t.B ? cost(reach_of(a, b0 + lane)) : 0;
     int64_t upto = mine;
 #pragma unroll
     for (int off = 1; off < WAVE; off <<= 1) {
@@ -192,50 +216,109 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT)) void attend_
   b = uniform(b);
   before = uniform(before);
 
-  while (x < x1) {
-    // a segment: this workgroup's blocks of one unit
-    Reach r = uniform(reach_of(a, b));
-    while ((int64_t)r.blocks * U <= x - before) {      // also requests without blocks
-      before += (int64_t)r.blocks * U;
-      r = uniform(reach_of(a, ++b));
+  // A segment: this workgroup's blocks i0 .. i1 - 1 of one unit.
+  Reach r = uniform(reach_of(a, b));
+  int h = 0, set = 0, i0 = 0, i1 = 0;
+  int64_t unit1 = 0;       // where the unit ends
+  auto next = [&]() {      // the one at x or after it; false: there is none
+    for (; x < x1;) {
+      while (cost(r) <= x - before) {                  // also requests without blocks
+        before += cost(r);
+        r = uniform(reach_of(a, ++b));
+      }
+      const int n = r.blocks + AT_START, unit = uniform((int)((x - before) / n));
+      h = uniform(unit / a.s.sets);
+      set = unit - h * a.s.sets;
+      unit1 = before + (int64_t)(unit + 1) * n;
+      const int64_t stop = x1 < unit1 ? x1 : unit1, zero = unit1 - r.blocks;
+      i0 = (int)(x > zero ? x - zero : 0);
+      i1 = (int)(stop - zero);
+      x = stop;
+      if (i1 > i0) return true;                        // not only a unit's start
     }
-    const int unit = uniform((int)((x - before) / r.blocks));
-    const int64_t unit0 = before + (int64_t)unit * r.blocks;
-    const int i0 = (int)(x - unit0);
-    const int i1 = (int)((x1 < unit0 + r.blocks ? x1 : unit0 + r.blocks) - unit0);
-    const int h = uniform(unit / a.s.sets), set = unit - h * a.s.sets;
-    const int col0 = (set * across + side) * NT * 16;   // this wave's first column
+    return false;
+  };
 
-    // queries into LDS, in the order of the B operand: [part][tile][brick][lane] 16 bytes
+  // Where block i lies: its page is asked for two blocks ahead, its scales one ahead, both
+  // through the scalar cache, so that no load waits for an address.
+  auto page_of = [&](int i) {
+    i = i < i1 ? i : i1 - 1;
+    const int64_t at = r.bad ? 0 : (int64_t)b * a.t.width + ((r.block0 + i) >> a.c.per_log2);
+    return uniform(*scalar((const SCALAR int32_t*)a.t.table + at));
+  };
+  const float scale2 = fabsf(a.scale2);
+  int page_next = 0;
+  int64_t at = 0;
+  float ks = 0, vs = 0, ks_next = 0, vs_next = 0;
+  bool lost = false, lost_next = false;
+  auto locate = [&](int i) {
+    lost_next = r.bad || (uint32_t)page_next >= (uint32_t)a.c.pages;
+    const int page = lost_next ? 0 : page_next, in_page = (r.block0 + i) & ((1 << a.c.per_log2) - 1);
+    at = uniform((((int64_t)page * a.c.heads + h) << a.c.per_log2) + in_page);
+    ks_next = uniform(*scalar((const SCALAR float*)a.c.ks + at));
+    vs_next = uniform(*scalar((const SCALAR float*)a.c.vs + at));
+  };
+  su32x4 kraw[BRICKS], vraw[BRICKS];
+  auto load = [&](const uint8_t* base, su32x4 (&raw)[BRICKS]) {
+    const GLOBAL uint8_t* p = scalar((const GLOBAL uint8_t*)base + at * (BRICKS * BRICK));
+#pragma unroll
+    for (int c = 0; c < BRICKS; ++c) raw[c] = *(const GLOBAL su32x4*)(p + (uint32_t)(lane * 16) + c * BRICK);
+  };
+  int i = 0;
+  auto start = [&]() {     // the wave's first block of a segment
+    i = i0 + turn;
+    if (i < i1) {
+      page_next = page_of(i);
+      locate(i);
+      page_next = page_of(i + along);
+      load(a.c.k, kraw);
+      load(a.c.v, vraw);
+    }
+  };
+
+  if (!next()) return;
+  start();
+  for (;;) {
+    // queries into LDS, in the order of the B operand: [part][tile][brick][lane] 16 bytes; the
+    // loads of four go out together
     {
       const AttendArgs& z = fresh_args();
-      const int tiles = across * NT;
-      for (int i = tid; i < tiles * BRICKS * WAVE; i += AT_THREADS) {
-        const int l = i % WAVE, c = i / WAVE % BRICKS, t = i / WAVE / BRICKS;
-        const int col = set * z.s.cols_set + t * 16 + (l & 15), d = 32 * c + 8 * (l >> 4);
-        float y[8];
+      const int items = across * NT * BRICKS * WAVE;
+      for (int n0 = tid; n0 < items; n0 += 4 * AT_THREADS) {
+        float y[4][8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = 0.0f;
-        if (col < z.s.cols && d < z.c.D) {
-          const int j = col / z.group, g = col % z.group;
-          const int64_t from = b * z.qs.b + j * z.qs.n + (int64_t)(h * z.group + g) * z.qs.h + d;
-          if (d + 8 <= z.c.D) {
-            if constexpr (F32) load8((const float*)z.q + from, y);
-            else load8((const uint16_t*)z.q + from, y);
-          } else {
+        for (int k = 0; k < 4; ++k) {
+          const int n = n0 + k * AT_THREADS, l = n % WAVE, c = n / WAVE % BRICKS, t = n / WAVE / BRICKS;
+          const int col = set * z.s.cols_set + t * 16 + (l & 15), d = 32 * c + 8 * (l >> 4);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (d + e < z.c.D) y[e] = F32 ? elem((const float*)z.q + from + e) : elem((const uint16_t*)z.q + from + e);
+          for (int e = 0; e < 8; ++e) y[k][e] = 0.0f;
+          if (n < items && col < z.s.cols && d < z.c.D) {
+            const int j = row_of(z, col), g = col - j * z.group;
+            const int64_t from = b * z.qs.b + j * z.qs.n + (int64_t)(h * z.group + g) * z.qs.h + d;
+            if (d + 8 <= z.c.D) {
+              if constexpr (F32) load8((const float*)z.q + from, y[k]);
+              else load8((const uint16_t*)z.q + from, y[k]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (d + e < z.c.D)
+                  y[k][e] = F32 ? elem((const float*)z.q + from + e) : elem((const uint16_t*)z.q + from + e);
+            }
           }
         }
-        if (z.scale2 < 0.0f) {      // so that a score's factor is never negative
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = -y[e];
+        for (int k = 0; k < 4; ++k) {
+          const int n = n0 + k * AT_THREADS;
+          if (n >= items) break;
+          if (z.scale2 < 0.0f) {      // so that a score's factor is never negative
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[k][e] = -y[k][e];
+          }
+          sbf16x8 p[QP];
+          split8<QP>(y[k], p);
+#pragma unroll
+          for (int m = 0; m < QP; ++m) ((sbf16x8*)lds)[m * items + n] = p[m];
         }
-        sbf16x8 p[QP];
-        split8<QP>(y, p);
-#pragma unroll
-        for (int n = 0; n < QP; ++n) ((sbf16x8*)lds)[n * tiles * BRICKS * WAVE + i] = p[n];
       }
     }
     __syncthreads();
@@ -244,53 +327,19 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT)) void attend_
     float l[NT], sub[NT];                                // sub: the column's reference
     bool settled = false;                                // every column has one
     int last[NT];                                        // the last position a column sees
+    const int col0 = (set * across + side) * NT * 16;    // this wave's first column
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
-      for (int i = 0; i < DT; ++i) O[t][i] = sf32x4{0, 0, 0, 0};
+      for (int k = 0; k < DT; ++k) O[t][k] = sf32x4{0, 0, 0, 0};
       l[t] = 0.0f;
       sub[t] = AT_NONE;
-      last[t] = r.first + (col0 + t * 16 + col16) / a.group;
+      last[t] = r.first + row_of(a, col0 + t * 16 + col16);
     }
     const int end = r.first + r.rows;
     const int open0 = a.window ? end - a.window : 0;     // from here to r.first all rows see all
     const sbf16x8* qf = (const sbf16x8*)lds + side * NT * BRICKS * WAVE + lane;
     const int q_part = across * NT * BRICKS * WAVE;
-
-    // Where block i lies: its page is asked for two blocks ahead, its scales one ahead, both
-    // through the scalar cache, so that no load waits for an address.
-    const SCALAR int32_t* table = (const SCALAR int32_t*)a.t.table + (r.bad ? 0 : (int64_t)b * a.t.width);
-    auto page_of = [&](int i) {
-      i = i < i1 ? i : i1 - 1;
-      const SCALAR int32_t* p = scalar(table + (r.bad ? 0 : (r.block0 + i) >> a.c.per_log2));
-      return uniform(*p);
-    };
-    const float scale2 = fabsf(a.scale2);
-    int page_next = 0;
-    int64_t at = 0;
-    float ks = 0, vs = 0, ks_next = 0, vs_next = 0;
-    bool lost = false, lost_next = false;
-    auto locate = [&](int i) {
-      lost_next = r.bad || (uint32_t)page_next >= (uint32_t)a.c.pages;
-      const int page = lost_next ? 0 : page_next, in_page = (r.block0 + i) & ((1 << a.c.per_log2) - 1);
-      at = uniform((((int64_t)page * a.c.heads + h) << a.c.per_log2) + in_page);
-      ks_next = uniform(*scalar((const SCALAR float*)a.c.ks + at));
-      vs_next = uniform(*scalar((const SCALAR float*)a.c.vs + at));
-    };
-    su32x4 kraw[BRICKS], vraw[BRICKS];
-    auto load = [&](const uint8_t* base, su32x4 (&raw)[BRICKS]) {
-      const GLOBAL uint8_t* p = scalar((const GLOBAL uint8_t*)base + at * (BRICKS * BRICK));
-#pragma unroll
-      for (int c = 0; c < BRICKS; ++c) raw[c] = *(const GLOBAL su32x4*)(p + (uint32_t)(lane * 16) + c * BRICK);
-    };
-    int i = i0 + turn;
-    if (i < i1) {
-      page_next = page_of(i);
-      locate(i);
-      page_next = page_of(i + along);
-      load(a.c.k, kraw);
-      load(a.c.v, vraw);
-    }
 
     for (; i < i1; i += along) {
       // the queries are read from LDS for every block, not kept in registers that the sums need
@@ -430,6 +479,18 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT)) void attend_
       if (more) load(a.c.v, vraw);
     }
 
+    // The next segment's first block is asked for before this one's end is dealt with.
+    const bool whole = i0 == 0 && i1 == r.blocks;
+    const int slot = i0 == 0, was_b = b, was_h = h, was_set = set, was_rows = r.rows;
+    if (i0 == 0 && tid == 0) {
+      const AttendArgs& z = fresh_args();
+      const int64_t unit_id = ((int64_t)b * z.c.heads + h) * z.s.sets + set;
+      z.record[2 * unit_id] = (int32_t)wg;
+      z.record[2 * unit_id + 1] = (int32_t)((unit1 * W + T - 1) / T - 1 - wg) + 1;
+    }
+    const bool more_segments = next();
+    if (more_segments) start();
+
     // the waves' parts joined, in the order of the waves
     const AttendArgs& z = fresh_args();
 #pragma unroll
@@ -443,22 +504,19 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT)) void attend_
       }
     }
     __syncthreads();       // the queries are free too
-    const bool all = i0 == 0 && i1 == r.blocks;
-    float* part = z.partial + (wg * 2 + (i0 == 0 ? 1 : 0)) * ((int64_t)z.s.cols_set * (z.c.D + 2));
+    float* part = z.partial + (wg * 2 + slot) * ((int64_t)z.s.cols_set * (BRICKS * 32 + 2));
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      float M = -INFINITY, L = 0.0f;
-      bool nan = false;
-      for (int k = 0; k < along; ++k) {
-        const float m = stat[k * across + side][t * 16 + col16][0];
-        M = fmaxf(M, m);
-        nan |= m != m;
+      float ms[AT_WAVES], ls[AT_WAVES], M = -INFINITY, L = 0.0f;
+#pragma unroll
+      for (int k = 0; k < AT_WAVES; ++k) {
+        const int from = k < along ? k * across + side : wave;
+        ms[k] = k < along ? stat[from][t * 16 + col16][0] : -INFINITY;
+        ls[k] = stat[from][t * 16 + col16][1];
+        M = M != M || ms[k] != ms[k] ? NAN : fmaxf(M, ms[k]);
       }
-      if (nan) M = NAN;
-      for (int k = 0; k < along; ++k) {
-        const float m = stat[k * across + side][t * 16 + col16][0];
-        if (m != -INFINITY) L += at_exp2(m - M) * stat[k * across + side][t * 16 + col16][1];
-      }
+#pragma unroll
+      for (int k = 0; k < AT_WAVES; ++k) L += ms[k] == -INFINITY ? 0.0f : at_exp2(ms[k] - M) * ls[k];
       const float mine = stat[wave][t * 16 + col16][0];
       const float f = at_exp2(mine - M);
 #pragma unroll
@@ -467,20 +525,15 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT)) void attend_
         const int col = (side * NT + t) * 16 + col16;
         total[col][0] = M;
         total[col][1] = L;
-        if (!all) {
-          float* ml = part + (int64_t)z.s.cols_set * z.c.D;
+        if (!whole) {
+          float* ml = part + (int64_t)z.s.cols_set * (BRICKS * 32);
           ml[2 * col] = M;
           ml[2 * col + 1] = L;
         }
       }
     }
-    if (i0 == 0 && tid == 0) {
-      const int64_t unit_id = ((int64_t)b * z.c.heads + h) * z.s.sets + set, y = unit0 + r.blocks - 1;
-      z.record[2 * unit_id] = (int32_t)wg;
-      z.record[2 * unit_id + 1] = (int32_t)(((y + 1) * W + T - 1) / T - 1 - wg) + 1;
-    }
     sf32x4* sums = (sf32x4*)lds;                 // [wave][16 dimensions of CH][NT][lane]
-    constexpr int CH = 2;                        // groups of 16 dimensions a round
+    constexpr int CH = attend_round(BRICKS, NT);
 #pragma unroll
     for (int d0 = 0; d0 < DT; d0 += CH) {
 #pragma unroll
@@ -493,25 +546,23 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT)) void attend_
         for (int k = 1; k < along; ++k) o += sums[k * across * CH * NT * WAVE + n];
         const int ln = n % WAVE, t = n / WAVE % NT, k = n / WAVE / NT % CH, sd = n / WAVE / NT / CH;
         const int d = 16 * (d0 + k) + 4 * (ln >> 4), in_set = (sd * NT + t) * 16 + (ln & 15);
-        const int col = set * z.s.cols_set + in_set;
-        if (!all) {
-          for (int e = 0; e < 4; ++e)
-            if (d + e < z.c.D) part[(int64_t)in_set * z.c.D + d + e] = o[e];
-        } else if (col < z.s.cols && col / z.group < r.rows) {
-          const int j = col / z.group, head = h * z.group + col % z.group;
-          const int64_t to = b * z.os.b + j * z.os.n + (int64_t)head * z.os.h + d;
-          const float M = total[in_set][0], L = total[in_set][1], inv = 1.0f / L;
-          for (int e = 0; e < 4; ++e)
-            if (d + e < z.c.D) {
-              if constexpr (F32) put((float*)z.out + to + e, o[e] * inv);
-              else put((uint16_t*)z.out + to + e, o[e] * inv);
-            }
-          if (z.lse && d == 0) z.lse[((int64_t)b * z.t.N + j) * z.qh + head] = (M + __log2f(L)) * 0.69314718055994530942f;
+        const int col = was_set * z.s.cols_set + in_set, j = row_of(z, col);
+        if (!whole) {
+          *(sf32x4*)(part + (int64_t)in_set * (BRICKS * 32) + d) = o;
+        } else if (col < z.s.cols && j < was_rows) {
+          const int head = was_h * z.group + col - j * z.group;
+          const int64_t to = was_b * z.os.b + j * z.os.n + (int64_t)head * z.os.h + d;
+          const float M = total[in_set][0], L = total[in_set][1];
+          o *= 1.0f / L;
+          if constexpr (F32) put4((float*)z.out + to, o, z.c.D - d);
+          else put4((uint16_t*)z.out + to, o, z.c.D - d);
+          if (z.lse && d == 0)
+            z.lse[((int64_t)was_b * z.t.N + j) * z.qh + head] = (M + __log2f(L)) * 0.69314718055994530942f;
         }
       }
       __syncthreads();
     }
-    x = unit0 + i1;
+    if (!more_segments) break;
   }
 }
 

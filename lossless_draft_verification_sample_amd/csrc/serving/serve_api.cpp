@@ -16,6 +16,7 @@ constexpr size_t WS_ALIGN = 256;
 constexpr int64_t MAX_WORKGROUPS = 1 << 23;
 constexpr int64_t MAX_TOKENS = 1 << 30;
 constexpr int MAX_PAGE = 65536;
+constexpr int MAX_GROUP = 4096;    // query heads that share a cache head
 constexpr int CUS = 256;
 
 size_t align_up(size_t x) { return (x + WS_ALIGN - 1) / WS_ALIGN * WS_ALIGN; }
@@ -121,7 +122,7 @@ int cache_rows(const sv_cache* cache, const int32_t* table, int32_t width, const
 bool attend_shape(int64_t B, int64_t N, int64_t qh, int64_t heads, int64_t D, int64_t tokens, sv_dtype dtype,
                   sv::AttendShape* s) {
   if (B < 1 || N < 1 || N > SV_MAX_ROWS || qh < 1 || heads < 1 || qh % heads || D < 1 || D > sv::CACHE_MAX_D ||
-      tokens < 1 || tokens > MAX_TOKENS || !known(dtype) || (double)B * N * qh >= 2147483648.0)
+      qh / heads > MAX_GROUP || tokens < 1 || tokens > MAX_TOKENS || !known(dtype) || (double)B * N * qh >= 2147483648.0)
     return false;
   const int64_t bricks = ceil_div(D, 32), parts = dtype == SV_BF16 ? 1 : 3;
   const int64_t cols = N * (qh / heads), tiles = ceil_div(cols, 16);
@@ -133,13 +134,13 @@ bool attend_shape(int64_t B, int64_t N, int64_t qh, int64_t heads, int64_t D, in
       if (nt > nt_most || nt * across > most) continue;
       const int64_t units = B * heads * sets;
       const int64_t cols_set = 16 * nt * across;
-      if ((double)units * cols_set / 4 >= MAX_WORKGROUPS) return false;
+      if ((double)units * cols_set >= MAX_WORKGROUPS) return false;
       s->cols = (int)cols;
       s->nt = (int)nt;
       s->across = (int)across;
       s->sets = (int)sets;
       s->cols_set = (int)cols_set;
-      const int64_t q = nt * across * bricks * parts * 1024, sums = 8 * nt * 1024;
+      const int64_t q = nt * across * bricks * parts * 1024, sums = 4096 * nt * sv::attend_round((int)bricks, (int)nt);
       s->lds = (int)(q > sums ? q : sums);
       // a workgroup takes four blocks at least
       const int64_t blocks = units * (ceil_div(tokens, sv::CACHE_BLOCK) + 1);
@@ -156,7 +157,7 @@ AttendSpace attend_space(const sv::AttendShape& s, int64_t B, int64_t heads, int
   AttendSpace w;
   w.record = 0;
   w.partial = align_up((size_t)(B * heads * s.sets) * 2 * sizeof(int32_t));
-  w.total = w.partial + align_up((size_t)s.grid * 2 * s.cols_set * (D + 2) * sizeof(float));
+  w.total = w.partial + align_up((size_t)s.grid * 2 * s.cols_set * (ceil_div(D, 32) * 32 + 2) * sizeof(float));
   return w;
 }
 
@@ -254,9 +255,15 @@ int spec_verify_attention(const void* q, sv_strides q_strides, sv_dtype dtype, i
   a.lse = out_lse;
   a.qh = q_heads;
   a.group = q_heads / a.c.heads;
+  // exact for columns below 2^32 / group: there are 64 * group of them and a set's filling
+  a.group_inv = (uint32_t)((0x100000000ull + a.group - 1) / a.group);
   a.window = window;
   a.bf16 = dtype == SV_BF16;
   a.scale2 = (float)((double)scale * M_LOG2E);
+  // units enough to fill the CUs are joined by a workgroup each, fewer by more
+  const int64_t units = (int64_t)B * a.c.heads * a.s.sets;
+  a.join_cols = a.s.cols_set;
+  while (a.join_cols > 4 && units * ceil_div(a.s.cols_set, a.join_cols) < 4 * CUS) a.join_cols = (a.join_cols + 1) / 2;
   a.record = (int32_t*)((char*)workspace + w.record);
   a.partial = (float*)((char*)workspace + w.partial);
   return sv::launch_attend(a, (hipStream_t)stream) ? SV_EHIP : SV_OK;

@@ -154,6 +154,7 @@ struct CacheRowsArgs {
 int launch_cache_write(const CacheRowsArgs& a, hipStream_t st);
 int launch_cache_read(const CacheRowsArgs& a, hipStream_t st);
 
+constexpr int AT_MAX_COLS = 256;      // of a set: four waves of four tiles
 constexpr int AT_THREADS = 256, AT_WAVES = AT_THREADS / WAVE;
 // How the N * group columns (row, query head) of a cache head are spread: NT tiles of
 // 16 columns a wave, `across` waves of a workgroup side by side (the others share out the
@@ -168,7 +169,13 @@ struct AttendShape {
 // codes, scores and parts, the rest).
 constexpr int attend_per_cu(int bricks, int nt) {
   const int need = 8 * bricks * nt + 8 * bricks + 22 * nt + 40;
-  return need <= 128 ? 4 : need <= 168 ? 3 : need <= 256 ? 2 : 1;
+  return need <= 128 ? 4 : need <= 152 ? 3 : need <= 248 ? 2 : 1;
+}
+// Groups of 16 dimensions that the waves of a workgroup join at a time, in 4 KB of LDS a tile each.
+constexpr int attend_round(int bricks, int nt) {
+  int n = 12 / nt;
+  while (2 * bricks % n) --n;
+  return n;
 }
 struct AttendArgs {
   Cache c;
@@ -178,10 +185,12 @@ struct AttendArgs {
   Strides qs, os;
   float* lse;
   int qh, group, window, bf16;
+  uint32_t group_inv; // 2^32 / group, rounded up: a column's row is the product's upper half
   float scale2;       // scale * log2 e
+  int join_cols;      // columns that a workgroup of the join takes
   AttendShape s;
   int32_t* record;    // [B][heads][sets][2]: the first workgroup of a unit, and how many
-  float* partial;     // [grid][2][cols_set][D + 2]
+  float* partial;     // [grid][2]: [cols_set][bricks * 32] sums, [cols_set][2] references and sums of weights
 };
 int launch_attend(const AttendArgs& a, hipStream_t st);
 

@@ -457,14 +457,16 @@ def test_attention_requests_and_pages_out_of_range(dtype):
     B, N, H, D, T = 7, 3, 2, 48, 130
     cache, table, keys, vals = _filled(rng, [T + N] * B, H, D, 32)
     q, qx = _rows(rng, (B, N, 4, D), dtype)
-    clean = _sv().spec_verify_attention(q, cache, _dev(table), _ints([T] * B), want_lse=True)
     low = _sv().spec_verify_attention(q, cache, _dev(table), _ints([T] * B), window=40)
     bad = table.copy()
     bad[1, 0], bad[2, 2], bad[6, 0] = -1, 10 ** 6, -1
     lens, rows = [T, T, T, -1, T, 2 ** 31 - 1, T], [N, N, N, N, N + 1, N, N]
     got = _sv().spec_verify_attention(q, cache, _dev(bad), _ints(lens), rows=_ints(rows), want_lse=True)
     assert torch.isnan(got.out[1:]).all() and torch.isnan(got.lse[1:]).all()
-    assert torch.equal(got.out[0], clean.out[0]) and torch.equal(got.lse[0], clean.lse[0])
+    # the first request's tokens are shared out as the whole batch's lengths say: not the same bits
+    want, lse, sizes, reach = os_.attention(qx[0], keys[0], vals[0], T, D ** -0.5)
+    tol, ltol = _attend_tol(qx, want, lse, sizes, reach, T + N, D, dtype)
+    assert np.all(np.abs(_host(got.out[0]) - want) <= tol) and np.all(np.abs(_host(got.lse[0]) - lse) <= ltol)
     got = _sv().spec_verify_attention(q, cache, _dev(bad), _ints([T] * B), window=40)
     for b in (0, 1, 3, 4, 5, 6):
         assert torch.equal(got.out[b], low.out[b])       # page 0 lies before the windows
