@@ -541,8 +541,9 @@ int spec_verify_cache_read(const sv_cache* cache, const int32_t* page_table, int
  *   out = sum_t softmax_t(scale q . k_t) v_t,   out_lse = log sum_t exp(scale q . k_t).
  *   q        [B][N][q_heads][head_dim] of dtype at any strides; scale finite.
  *   out      like q, of dtype, at its strides; out_lse [B][N][q_heads] float, or NULL.
- * bfloat16: products of q and k are exact, probabilities enter their product with v as two
- * bfloat16 parts (2^-17); float32: q and the probabilities as three.
+ * bfloat16: products of q and k are exact, probabilities enter their product with v as float16
+ * (off by 2^-12, and 2^-25 of the largest), and blocks whose v_scale lies 2^-60 below another's of
+ * the request lose precision; float32: q and the probabilities as three bfloat16 parts.
  * NaN in a position that a row does not see does not reach it. A row that sees a position in a
  * page outside [0, pages) is NaN; pages that no row of the request sees (all before its window)
  * are not read. Requests out of range as in spec_verify_cache_write.

@@ -4,7 +4,13 @@
 // C = N * group columns. With K a block's keys (32 tokens), Q the columns' queries:
 //   S = K Q            16x16x32 matrix instructions, tokens by columns
 //   P = exp2(c S - r)  c = k_scale * scale * log2 e, r the column's reference
-//   O += V^T (v_scale P)   dimensions by columns, l += sum P
+//   O += V^T P         dimensions by columns, V = v_scale * code; l += sum P
+// Keys become bfloat16, which holds their codes and bfloat16 queries exactly. For bfloat16
+// outputs P becomes float16, off by 2^-12, a sixteenth of the outputs' own step, and V is
+// code * v_scale / 2^e in float16, exact for powers of two within 2^-15 .. 2^7 of 2^e; where a scale
+// lies outside, e is moved and O with it. For float32, P v_scale is taken as three bfloat16 parts.
+// (P in two bfloat16 parts took 1,600 issue cycles of vector instructions a block of three tiles
+// instead of 930, and twice the second product's matrix instructions.)
 // A wave takes whole blocks on its own. Every operand is in place without a shuffle: the
 // cache's bricks hold keys and values in the order of the instruction's A operand, and the
 // tokens of a brick of keys are ordered so that the 8 tokens whose scores a lane gets are the
@@ -16,7 +22,7 @@
 // that about one block a wave is in flight all the time.
 //
 // The reference r is not the running maximum but a score near it, moved only when a score
-// exceeds it by 2^16; so a block costs no reduction over lanes and O is rescaled hardly ever.
+// exceeds it by 8, so that weights stay below 256; so a block costs no reduction over lanes and O is rescaled hardly ever.
 // Float32 holds sums relative to any such reference as exactly as relative to the maximum.
 //
 // Workgroups share out the blocks of all requests evenly, whatever their lengths: with T blocks
@@ -37,8 +43,8 @@
 
 namespace sv {
 
-constexpr float AT_SLACK = 16.0f;      // how far a score may pass the reference (base 2)
-constexpr float AT_FAR = 65536.0f;     // 2^AT_SLACK
+constexpr float AT_SLACK = 8.0f;       // how far a score may pass the reference (base 2)
+constexpr float AT_FAR = 256.0f;       // 2^AT_SLACK
 // The reference of a column that has seen no token: finite, so that a masked score's weight is 0,
 // and lower than any that a score of float32 products can become and stay finite.
 constexpr float AT_NONE = -3.40282346638528859812e38f;
@@ -78,8 +84,26 @@ __device__ __forceinline__ sbf16x8 codes8(uint32_t lo, uint32_t hi) {
   return sbf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+// 8 codes times 2^e as float16: exact for e from -15 to 7.
+__device__ __forceinline__ sf16x8 codes8_half(uint32_t lo, uint32_t hi, float grow) {
+  const sf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, grow, false);
+  const sf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, grow, true);
+  const sf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, grow, false);
+  const sf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, grow, true);
+  return sf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+__device__ __forceinline__ sf16x8 half8(const float (&x)[8]) {
+  sf16x8 h;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h[i] = (_Float16)x[i];
+  return h;
+}
+
 __device__ __forceinline__ sf32x4 mma(sbf16x8 a, sbf16x8 b, sf32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ sf32x4 mma(sf16x8 a, sf16x8 b, sf32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
 // Blocks of a request's units, and the first one.
@@ -172,8 +196,8 @@ __device__ __forceinline__ const AttendArgs& fresh_args() {
 }
 
 template <int BRICKS, int NT, bool F32>
-__global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT)) void attend_kernel(AttendArgs a) {
-  constexpr int QP = F32 ? 3 : 1, PP = F32 ? 3 : 2, DT = 2 * BRICKS;
+__global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT, F32)) void attend_kernel(AttendArgs a) {
+  constexpr int QP = F32 ? 3 : 1, DT = 2 * BRICKS;
   extern __shared__ char lds[];
   __shared__ float stat[AT_WAVES][NT * 16][2], total[AT_WAVES * NT * 16][2];
   const int tid = threadIdx.x, lane = tid % WAVE, wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
@@ -262,7 +286,7 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT)) void attend_
   auto load = [&](const uint8_t* base, su32x4 (&raw)[BRICKS]) {
     const GLOBAL uint8_t* p = scalar((const GLOBAL uint8_t*)base + at * (BRICKS * BRICK));
 #pragma unroll
-    for (int c = 0; c < BRICKS; ++c) raw[c] = *(const GLOBAL su32x4*)(p + (uint32_t)(lane * 16) + c * BRICK);
+    for (int c = 0; c < BRICKS; ++c) raw[c] = __builtin_nontemporal_load((const GLOBAL su32x4*)(p + (uint32_t)(lane * 16) + c * BRICK));
   };
   int i = 0;
   auto start = [&]() {     // the wave's first block of a segment
@@ -326,6 +350,10 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT)) void attend_
     sf32x4 O[NT][DT];
     float l[NT], sub[NT];                                // sub: the column's reference
     bool settled = false;                                // every column has one
+    // What the sums are relative to: 2^(eref - 127), near the scales of the values; the largest yet.
+    int eref = (int)(__float_as_uint(vs_next) >> 23 & 255) + 2;
+    if (F32 || eref <= 2 || eref > 250) eref = 127;
+    int etop = eref;
     int last[NT];                                        // the last position a column sees
     const int col0 = (set * across + side) * NT * 16;    // this wave's first column
 #pragma unroll
@@ -454,25 +482,68 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT)) void attend_
       }
       if (!edge) settled = true;
 
-      sbf16x8 pf[NT][PP];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          l[t] += w[t][e];
-          w[t][e] *= vs;
+        for (int e = 0; e < 8; ++e) l[t] += w[t][e];
+      if constexpr (!F32) {
+        // value = vref * (2^up * code), and rho for what vs has besides a power of two near vref
+        const int ev = (int)(__float_as_uint(vs) >> 23 & 255);
+        int up = 0;
+        float rho = vs;                                  // 0, infinities, NaN
+        if (vs != 0.0f && ev != 255) {
+          if (ev - eref > 7 || ev - eref < -15) {
+            int to = ev + 2;                             // 448 * 2^7 is float16's range above it
+            if (to < etop - 60) to = etop - 60;          // the sums stay finite
+            if (to > 250) to = 250;
+            if (etop < to) etop = to;
+            const float f = ldexpf(1.0f, eref - to);
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int k = 0; k < DT; ++k) O[t][k] *= f;
+            eref = to;
+          }
+          up = ev - eref < -15 ? -15 : ev - eref;
+          rho = ldexpf(vs, 127 - eref - up);
         }
-        split8<PP>(w[t], pf[t]);
-      }
+        if (rho != 1.0f) {
 #pragma unroll
-      for (int c = 0; c < BRICKS; ++c) {
-        const sbf16x8 v0 = codes8(vraw[c][0], vraw[c][1]), v1 = codes8(vraw[c][2], vraw[c][3]);
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[t][e] *= rho;
+        }
+        const float grow = __uint_as_float((uint32_t)(127 + up) << 23);
+        sf16x8 pf[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) pf[t] = half8(w[t]);
+#pragma unroll
+        for (int c = 0; c < BRICKS; ++c) {
+          const sf16x8 v0 = codes8_half(vraw[c][0], vraw[c][1], grow), v1 = codes8_half(vraw[c][2], vraw[c][3], grow);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            O[t][2 * c] = mma(v0, pf[t], O[t][2 * c]);
+            O[t][2 * c + 1] = mma(v1, pf[t], O[t][2 * c + 1]);
+          }
+        }
+      } else {
+        sbf16x8 pf[NT][3];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
-          for (int n = 0; n < PP; ++n) {
-            O[t][2 * c] = mma(v0, pf[t][n], O[t][2 * c]);
-            O[t][2 * c + 1] = mma(v1, pf[t][n], O[t][2 * c + 1]);
+          for (int e = 0; e < 8; ++e) w[t][e] *= vs;
+          split8<3>(w[t], pf[t]);
+        }
+#pragma unroll
+        for (int c = 0; c < BRICKS; ++c) {
+          const sbf16x8 v0 = codes8(vraw[c][0], vraw[c][1]), v1 = codes8(vraw[c][2], vraw[c][3]);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+#pragma unroll
+            for (int n = 0; n < 3; ++n) {
+              O[t][2 * c] = mma(v0, pf[t][n], O[t][2 * c]);
+              O[t][2 * c + 1] = mma(v1, pf[t][n], O[t][2 * c + 1]);
+            }
           }
         }
       }
@@ -518,7 +589,7 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT)) void attend_
 #pragma unroll
       for (int k = 0; k < AT_WAVES; ++k) L += ms[k] == -INFINITY ? 0.0f : at_exp2(ms[k] - M) * ls[k];
       const float mine = stat[wave][t * 16 + col16][0];
-      const float f = at_exp2(mine - M);
+      const float f = at_exp2(mine - M) * ldexpf(1.0f, eref - 127);
 #pragma unroll
       for (int k = 0; k < DT; ++k) O[t][k] = mine == -INFINITY ? sf32x4{0, 0, 0, 0} : O[t][k] * f;
       if (turn == 0 && quad == 0) {

@@ -16,6 +16,8 @@ typedef float sf32x2 __attribute__((ext_vector_type(2)));
 typedef float sf32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 sbf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 sbf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 sf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 sf16x8 __attribute__((ext_vector_type(8)));
 
 // The same at any alignment of their elements: the hardware loads and stores
 // vectors at any address, so no row needs a head of single elements.
@@ -167,8 +169,8 @@ struct AttendShape {
 };
 // Workgroups of a CU, which is waves of a SIMD: by the registers of a lane (sums, a block's
 // codes, scores and parts, the rest).
-constexpr int attend_per_cu(int bricks, int nt) {
-  const int need = 8 * bricks * nt + 8 * bricks + 22 * nt + 40;
+constexpr int attend_per_cu(int bricks, int nt, bool f32) {
+  const int need = 8 * bricks * nt + 8 * bricks + 22 * nt + 40 + (f32 ? 8 : 0);
   return need <= 128 ? 4 : need <= 152 ? 3 : need <= 248 ? 2 : 1;
 }
 // Groups of 16 dimensions that the waves of a workgroup join at a time, in 4 KB of LDS a tile each.

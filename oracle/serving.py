@@ -127,11 +127,12 @@ class Cache:
 
 def attention(q, k, v, first, scale, window=0):
     """q [N, q_heads, D] over k, v [tokens, heads, D], row j at position first + j.
-    Returns out, lse, and for tolerances sum p |v| and the largest sum |q k| scale."""
+    Returns out, lse, and for tolerances sum p |v|, the largest sum |q k| scale, and
+    the largest p times sum |v|."""
     N, qh, D = q.shape
     group = qh // k.shape[1]
     out, lse, size = np.zeros_like(q), np.zeros((N, qh)), np.zeros_like(q)
-    reach = np.zeros((N, qh))
+    reach, most = np.zeros((N, qh)), np.zeros_like(q)
     for j in range(N):
         p = first + j
         low = max(0, p - window + 1) if window else 0
@@ -144,7 +145,8 @@ def attention(q, k, v, first, scale, window=0):
             w /= w.sum()
             out[j, h], size[j, h] = w @ vv, w @ np.abs(vv)
             reach[j, h] = (np.abs(kk) @ np.abs(q[j, h])).max() * abs(scale)
-    return out, lse, size, reach
+            most[j, h] = w.max() * np.abs(vv).sum(0)
+    return out, lse, size, reach, most
 
 
 def adjust(z, j, tokens=(), history=(), prompt=(), repetition=1.0, frequency=0.0, presence=0.0,

@@ -9,7 +9,8 @@ outputs' type.
   cache: bytes, scales and values are equal, bfloat16 values too: a code times a power of two.
   attention: a score's products are summed in float32, off by (D + 8) U of sum |q k| scale, which
     counts twice in a probability's ratio to their sum; base-2 exponents round at |t| U, twice; a
-    probability enters in parts (2^-17 for bfloat16, U for float32); sums of 32 tokens in a matrix
+    probability enters as float16 for bfloat16 (2^-12 of it, 2^-25 of one that is at most the
+    largest, whose weight is at least 1) and in parts of U for float32; sums of 32 tokens in a matrix
     instruction, then a block after the other: (64 + tokens / 16) U of sum p |v|; plus H.
   adjust: float32 operations, at most six roundings of what they pass through; plus H.
 """
@@ -304,12 +305,13 @@ def _filled(rng, lens, H, D, page, dtype="bf16", size=1.0):
     return cache, table, keys, vals
 
 
-def _attend_tol(q, want, lse, size, reach, tokens, D, dtype):
+def _attend_tol(want, lse, size, reach, most, tokens, D, dtype):
     """(of out, of lse)"""
-    parts = 2.0 ** -17 if dtype == "bf16" else U
+    parts = 2.0 ** -12 if dtype == "bf16" else U
     score = (D + 8) * U * reach + 2 * U * (reach + 30) * 1.5
     near = 2 * score[..., None] + parts + (64 + tokens / 16) * U
-    return size * near + HALF[dtype] * (np.abs(want) + size * near), score + (70 + tokens / 16) * U + U * np.abs(lse)
+    far = size * near + (2.0 ** -25 * most if dtype == "bf16" else 0.0)
+    return far + HALF[dtype] * (np.abs(want) + far), score + (70 + tokens / 16) * U + U * np.abs(lse)
 
 
 def _check_attend(rng, lens, rows, N, qh, H, D, page, dtype, window=0, how="plain", scale=None, size=1.0, lens_after=None):
@@ -328,8 +330,8 @@ def _check_attend(rng, lens, rows, N, qh, H, D, page, dtype, window=0, how="plai
     for b in range(B):
         n, t = count[b], lens[b] + count[b]
         if n:
-            want, lse, sizes, reach = os_.attention(qx[b, :n], keys[b, :t], vals[b, :t], lens[b], s, window)
-            tol, ltol = _attend_tol(qx, want, lse, sizes, reach, t, D, dtype)
+            want, lse, sizes, reach, most = os_.attention(qx[b, :n], keys[b, :t], vals[b, :t], lens[b], s, window)
+            tol, ltol = _attend_tol(want, lse, sizes, reach, most, t, D, dtype)
             far, lfar = np.abs(_host(got.out[b, :n]) - want), np.abs(_host(got.lse[b, :n]) - lse)
             assert np.all(far <= tol), (b, n, t, (far / tol).max())
             assert np.all(lfar <= ltol), (b, n, t, (lfar / ltol).max())
@@ -389,6 +391,31 @@ def test_attention_scales_and_sharp_scores(dtype, scale, size):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("spread", ["far", "any", "zero", "down"])
+def test_attention_scales_of_blocks(dtype, spread):
+    """Scales that a caller's own quantisation chose: powers of two far apart, rising and falling, any
+    number, and 0 in some blocks."""
+    rng = np.random.default_rng(21)
+    T, H, D = 900, 2, 64
+    cache, table, keys, vals = _filled(rng, [T], H, D, 32)
+    blocks = -(-T // 32)
+    v = np.asarray({"far": 2.0 ** rng.integers(-25, 25, (blocks, H)), "any": rng.uniform(0.1, 9.0, (blocks, H)),
+                    "zero": rng.integers(0, 2, (blocks, H)) * 0.7,
+                    "down": 2.0 ** (20.0 - 2 * np.arange(blocks))[:, None] * np.ones(H)}[spread], np.float32)
+    k = (rng.uniform(0.001, 0.01, (blocks, H))).astype(np.float32)
+    for t, new in ((cache.k_scale, k), (cache.v_scale, v)):
+        for i in range(blocks):
+            t[int(table[0, i]), :, 0] = _dev(new[i])
+    keys, vals = (_host(t)[0] for t in _sv().spec_verify_cache_read(cache, _dev(table), None, T, _type("f32")))
+    qt = _dev(rng.standard_normal((1, 2, 4, D)).astype(np.float32), dtype)
+    for window in (0, 40):
+        got = _sv().spec_verify_attention(qt, cache, _dev(table), _ints([T - 2]), 1.0, window, want_lse=True)
+        want, lse, sizes, reach, most = os_.attention(_host(qt)[0], keys, vals, T - 2, 1.0, window)
+        tol, ltol = _attend_tol(want, lse, sizes, reach, most, T, D, dtype)
+        assert np.all(np.abs(_host(got.out[0]) - want) <= tol) and np.all(np.abs(_host(got.lse[0]) - lse) <= ltol)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_attention_rising_scores(dtype):
     """Scores that rise all along by far more than the reference's slack, and fall again."""
     import torch
@@ -405,8 +432,8 @@ def test_attention_rising_scores(dtype):
     q[0, :, :, 0] = [[1, -1, 0.25], [5, 0.01, 1]]
     qt = _dev(q, dtype)
     got = _sv().spec_verify_attention(qt, cache, _dev(table), _ints([T - 2]), 1.0, want_lse=True)
-    want, lse, sizes, reach = os_.attention(_host(qt)[0], keys[0], vals[0], T - 2, 1.0)
-    tol, ltol = _attend_tol(q, want, lse, sizes, reach, T, D, dtype)
+    want, lse, sizes, reach, most = os_.attention(_host(qt)[0], keys[0], vals[0], T - 2, 1.0)
+    tol, ltol = _attend_tol(want, lse, sizes, reach, most, T, D, dtype)
     assert np.all(np.abs(_host(got.out[0]) - want) <= tol) and np.all(np.abs(_host(got.lse[0]) - lse) <= ltol)
 
 
@@ -464,8 +491,8 @@ def test_attention_requests_and_pages_out_of_range(dtype):
     got = _sv().spec_verify_attention(q, cache, _dev(bad), _ints(lens), rows=_ints(rows), want_lse=True)
     assert torch.isnan(got.out[1:]).all() and torch.isnan(got.lse[1:]).all()
     # the first request's tokens are shared out as the whole batch's lengths say: not the same bits
-    want, lse, sizes, reach = os_.attention(qx[0], keys[0], vals[0], T, D ** -0.5)
-    tol, ltol = _attend_tol(qx, want, lse, sizes, reach, T + N, D, dtype)
+    want, lse, sizes, reach, most = os_.attention(qx[0], keys[0], vals[0], T, D ** -0.5)
+    tol, ltol = _attend_tol(want, lse, sizes, reach, most, T + N, D, dtype)
     assert np.all(np.abs(_host(got.out[0]) - want) <= tol) and np.all(np.abs(_host(got.lse[0]) - lse) <= ltol)
     got = _sv().spec_verify_attention(q, cache, _dev(bad), _ints([T] * B), window=40)
     for b in (0, 1, 3, 4, 5, 6):

@@ -100,7 +100,7 @@ def test_attention_by_a_loop_over_tokens():
     rng = np.random.default_rng(4)
     q, k, v = rng.standard_normal((3, 4, 6)), rng.standard_normal((9, 2, 6)), rng.standard_normal((9, 2, 6))
     for window in (0, 1, 4, 100):
-        out, lse, _, _ = os_.attention(q, k, v, 6, 0.4, window)
+        out, lse, _, _, _ = os_.attention(q, k, v, 6, 0.4, window)
         for j in range(3):
             for h in range(4):
                 seen = [t for t in range(9) if t <= 6 + j and (not window or 6 + j - t < window)]
