@@ -49,7 +49,9 @@ constexpr float AT_FAR = 256.0f;       // 2^AT_SLACK
 // and lower than any that a score of float32 products can become and stay finite.
 constexpr float AT_NONE = -3.40282346638528859812e38f;
 constexpr int AT_LEAST = 4;            // blocks of a workgroup at least: one a wave
-// What starting and ending a unit costs, in blocks: it counts in the workgroups' shares.
+// What starting and ending a unit costs, in blocks, a tile: it counts in the workgroups' shares.
+// (Ragged batch of 128 requests, three tiles: 8 in all 250 us, 16 231, 24 227, 40 231; one tile: 8
+// 200, 24 203.)
 constexpr int AT_START = 8;
 
 __device__ __forceinline__ float at_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -155,6 +157,15 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
   const uint32_t x = (w & 0x7F7F7F7Fu) ^ 0x7F7F7F7Fu;       // 0 in a byte of NaN
   return (((x + 0x7F7F7F7Fu) >> 7) & 0x01010101u) ^ 0x01010101u;
 }
+__device__ __forceinline__ su32x4 nan_codes(su32x4 w) {
+  return su32x4{nan_codes(w[0]), nan_codes(w[1]), nan_codes(w[2]), nan_codes(w[3])};
+}
+// The bytes of a lane's codes (8 tokens of a dimension, twice) of the first `left` tokens.
+__device__ __forceinline__ su32x4 tokens_before(int left) {
+  const uint32_t lo = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+  const uint32_t hi = left >= 8 ? ~0u : left <= 4 ? 0u : (1u << (8 * (left - 4))) - 1u;
+  return su32x4{lo, hi, lo, hi};
+}
 // 0 / 1 bytes as bfloat16 0.0 / 1.0.
 __device__ __forceinline__ sbf16x8 ones8(uint32_t lo, uint32_t hi) {
   su32x4 w;
@@ -196,8 +207,9 @@ __device__ __forceinline__ const AttendArgs& fresh_args() {
 }
 
 template <int BRICKS, int NT, bool F32>
-__global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT, F32)) void attend_kernel(AttendArgs a) {
+__global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT)) void attend_kernel(AttendArgs a) {
   constexpr int QP = F32 ? 3 : 1, DT = 2 * BRICKS;
+  using VF = std::conditional_t<F32, sbf16x8, sf16x8>;   // values in the second product
   extern __shared__ char lds[];
   __shared__ float stat[AT_WAVES][NT * 16][2], total[AT_WAVES * NT * 16][2];
   const int tid = threadIdx.x, lane = tid % WAVE, wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
@@ -207,7 +219,7 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT, F32)) void at
   const int U = a.c.heads * a.s.sets;
 
   // the blocks of all requests, and this workgroup's share of them
-  auto cost = [&](const Reach& r) { return r.blocks ? (int64_t)(r.blocks + AT_START) * U : 0; };
+  auto cost = [&](const Reach& r) { return r.blocks ? (int64_t)(r.blocks + AT_START * NT) * U : 0; };
   int64_t T = 0;
   for (int b = lane; b < a.t.B; b += WAVE) T += cost(reach_of(a, b));
   T = uniform(wave_sum64(T));
@@ -250,7 +262,7 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT, F32)) void at
         before += cost(r);
         r = uniform(reach_of(a, ++b));
       }
-      const int n = r.blocks + AT_START, unit = uniform((int)((x - before) / n));
+      const int n = r.blocks + AT_START * NT, unit = uniform((int)((x - before) / n));
       h = uniform(unit / a.s.sets);
       set = unit - h * a.s.sets;
       unit1 = before + (int64_t)(unit + 1) * n;
@@ -376,10 +388,67 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT, F32)) void at
       ks = ks_next * scale2;
       vs = vs_next;
       lost = lost_next;
-      const bool more = i + along < i1;
-      if (more) {
+      // some row does not see some token here, or the page is unknown
+      const bool edge = t0 + CACHE_BLOCK - 1 > r.first || t0 < open0 || lost;
+      const int64_t here = at;
+      bool nan_values = false;
+      if (edge) {
+        // values of tokens that no row sees may be anything, and NaN times 0 is NaN
+#pragma unroll
+        for (int c = 0; c < BRICKS; ++c) {
+          vraw[c] &= tokens_before(end - (t0 + 8 * quad));
+          const su32x4 nan = nan_codes(vraw[c]);
+          nan_values |= (nan[0] | nan[1] | nan[2] | nan[3]) != 0;
+          vraw[c] &= ~(nan * 255u);
+        }
+        nan_values = __any(nan_values);
+      }
+      // the codes become numbers first, so that the next block is asked for with the whole of this
+      // one's work ahead
+      sbf16x8 kf[BRICKS][2];
+      VF vf[BRICKS][2];
+#pragma unroll
+      for (int c = 0; c < BRICKS; ++c) {
+        kf[c][0] = codes8(kraw[c][0], kraw[c][1]);
+        kf[c][1] = codes8(kraw[c][2], kraw[c][3]);
+      }
+      int up = 0;
+      float rho = vs;                                    // what v_scale has besides 2^up; 0, infinities, NaN
+      if constexpr (!F32) {
+        const int ev = (int)(__float_as_uint(vs) >> 23 & 255);
+        if (vs != 0.0f && ev != 255) {
+          if (ev - eref > 7 || ev - eref < -15) {
+            int to = ev + 2;                             // 448 * 2^7 is float16's range above it
+            if (to < etop - 60) to = etop - 60;          // the sums stay finite
+            if (to > 250) to = 250;
+            if (etop < to) etop = to;
+            const float f = ldexpf(1.0f, eref - to);
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int k = 0; k < DT; ++k) O[t][k] *= f;
+            eref = to;
+          }
+          up = ev - eref < -15 ? -15 : ev - eref;
+          rho = ldexpf(vs, 127 - eref - up);
+        }
+      }
+      const float grow = __uint_as_float((uint32_t)(127 + up) << 23);
+#pragma unroll
+      for (int c = 0; c < BRICKS; ++c) {
+        if constexpr (F32) {
+          vf[c][0] = codes8(vraw[c][0], vraw[c][1]);
+          vf[c][1] = codes8(vraw[c][2], vraw[c][3]);
+        } else {
+          vf[c][0] = codes8_half(vraw[c][0], vraw[c][1], grow);
+          vf[c][1] = codes8_half(vraw[c][2], vraw[c][3], grow);
+        }
+      }
+      if (i + along < i1) {
         locate(i + along);
         page_next = page_of(i + 2 * along);
+        load(a.c.k, kraw);
+        load(a.c.v, vraw);
       }
 
       sf32x4 S[NT][2];
@@ -387,21 +456,17 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT, F32)) void at
       for (int t = 0; t < NT; ++t) S[t][0] = S[t][1] = sf32x4{0, 0, 0, 0};
 #pragma unroll
       for (int c = 0; c < BRICKS; ++c) {
-        const sbf16x8 k0 = codes8(kraw[c][0], kraw[c][1]), k1 = codes8(kraw[c][2], kraw[c][3]);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
           for (int n = 0; n < QP; ++n) {
             const sbf16x8 q = qf[n * q_part + (t * BRICKS + c) * WAVE];
-            S[t][0] = mma(k0, q, S[t][0]);
-            S[t][1] = mma(k1, q, S[t][1]);
+            S[t][0] = mma(kf[c][0], q, S[t][0]);
+            S[t][1] = mma(kf[c][1], q, S[t][1]);
           }
         }
       }
-      if (more) load(a.c.k, kraw);
 
-      // some row does not see some token here, or the page is unknown
-      const bool edge = t0 + CACHE_BLOCK - 1 > r.first || t0 < open0 || lost;
       if (edge) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -413,20 +478,14 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT, F32)) void at
             S[t][e >> 2][e & 3] = x;
           }
         ks = 1.0f;
-        // values of tokens that no row sees may be anything, and NaN times 0 is NaN
-        const int left = end - (t0 + 8 * quad);
-        const uint32_t m0 = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
-        const uint32_t m1 = left >= 8 ? ~0u : left <= 4 ? 0u : (1u << (8 * (left - 4))) - 1u;
+        if (nan_values) {
+          // NaN values that some row sees, and maybe not all: they were taken out of the product,
+          // and a product of their places with the rows' sight says whose sums are NaN
+          const GLOBAL uint8_t* p = scalar((const GLOBAL uint8_t*)a.c.v + here * (BRICKS * BRICK));
 #pragma unroll
-        for (int c = 0; c < BRICKS; ++c) {
-          vraw[c] &= su32x4{m0, m1, m0, m1};
-          su32x4 nan;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) nan[e] = nan_codes(vraw[c][e]);
-          if (__any((nan[0] | nan[1] | nan[2] | nan[3]) != 0)) {
-            // NaN values that some row sees, and maybe not all: taken out of the product, and a
-            // product of their places with the rows' sight says whose sums are NaN
-            vraw[c] &= ~(nan * 255u);
+          for (int c = 0; c < BRICKS; ++c) {
+            const su32x4 code = *(const GLOBAL su32x4*)(p + (uint32_t)(lane * 16) + c * BRICK);
+            const su32x4 nan = nan_codes(code & tokens_before(end - (t0 + 8 * quad)));
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
               float one[8];
@@ -486,47 +545,7 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT, F32)) void at
       for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int e = 0; e < 8; ++e) l[t] += w[t][e];
-      if constexpr (!F32) {
-        // value = vref * (2^up * code), and rho for what vs has besides a power of two near vref
-        const int ev = (int)(__float_as_uint(vs) >> 23 & 255);
-        int up = 0;
-        float rho = vs;                                  // 0, infinities, NaN
-        if (vs != 0.0f && ev != 255) {
-          if (ev - eref > 7 || ev - eref < -15) {
-            int to = ev + 2;                             // 448 * 2^7 is float16's range above it
-            if (to < etop - 60) to = etop - 60;          // the sums stay finite
-            if (to > 250) to = 250;
-            if (etop < to) etop = to;
-            const float f = ldexpf(1.0f, eref - to);
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-              for (int k = 0; k < DT; ++k) O[t][k] *= f;
-            eref = to;
-          }
-          up = ev - eref < -15 ? -15 : ev - eref;
-          rho = ldexpf(vs, 127 - eref - up);
-        }
-        if (rho != 1.0f) {
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[t][e] *= rho;
-        }
-        const float grow = __uint_as_float((uint32_t)(127 + up) << 23);
-        sf16x8 pf[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) pf[t] = half8(w[t]);
-#pragma unroll
-        for (int c = 0; c < BRICKS; ++c) {
-          const sf16x8 v0 = codes8_half(vraw[c][0], vraw[c][1], grow), v1 = codes8_half(vraw[c][2], vraw[c][3], grow);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            O[t][2 * c] = mma(v0, pf[t], O[t][2 * c]);
-            O[t][2 * c + 1] = mma(v1, pf[t], O[t][2 * c + 1]);
-          }
-        }
-      } else {
+      if constexpr (F32) {
         sbf16x8 pf[NT][3];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -535,19 +554,32 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT, F32)) void at
           split8<3>(w[t], pf[t]);
         }
 #pragma unroll
-        for (int c = 0; c < BRICKS; ++c) {
-          const sbf16x8 v0 = codes8(vraw[c][0], vraw[c][1]), v1 = codes8(vraw[c][2], vraw[c][3]);
+        for (int c = 0; c < BRICKS; ++c)
 #pragma unroll
-          for (int t = 0; t < NT; ++t) {
+          for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int n = 0; n < 3; ++n) {
-              O[t][2 * c] = mma(v0, pf[t][n], O[t][2 * c]);
-              O[t][2 * c + 1] = mma(v1, pf[t][n], O[t][2 * c + 1]);
+              O[t][2 * c] = mma(vf[c][0], pf[t][n], O[t][2 * c]);
+              O[t][2 * c + 1] = mma(vf[c][1], pf[t][n], O[t][2 * c + 1]);
             }
-          }
+      } else {
+        if (rho != 1.0f) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[t][e] *= rho;
         }
+        sf16x8 pf[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) pf[t] = half8(w[t]);
+#pragma unroll
+        for (int c = 0; c < BRICKS; ++c)
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            O[t][2 * c] = mma(vf[c][0], pf[t], O[t][2 * c]);
+            O[t][2 * c + 1] = mma(vf[c][1], pf[t], O[t][2 * c + 1]);
+          }
       }
-      if (more) load(a.c.v, vraw);
     }
 
     // The next segment's first block is asked for before this one's end is dealt with.
@@ -613,8 +645,11 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT, F32)) void at
         for (int t = 0; t < NT; ++t) sums[((wave * CH + k) * NT + t) * WAVE + lane] = O[t][d0 + k];
       __syncthreads();
       for (int n = tid; n < across * CH * NT * WAVE; n += AT_THREADS) {
-        sf32x4 o = sums[n];
-        for (int k = 1; k < along; ++k) o += sums[k * across * CH * NT * WAVE + n];
+        sf32x4 o = sums[n], more[AT_WAVES - 1];
+#pragma unroll
+        for (int k = 1; k < AT_WAVES; ++k) more[k - 1] = sums[(k < along ? k * across * CH * NT * WAVE : 0) + n];
+#pragma unroll
+        for (int k = 1; k < AT_WAVES; ++k) o += k < along ? more[k - 1] : sf32x4{0, 0, 0, 0};
         const int ln = n % WAVE, t = n / WAVE % NT, k = n / WAVE / NT % CH, sd = n / WAVE / NT / CH;
         const int d = 16 * (d0 + k) + 4 * (ln >> 4), in_set = (sd * NT + t) * 16 + (ln & 15);
         const int col = was_set * z.s.cols_set + in_set, j = row_of(z, col);

@@ -144,7 +144,7 @@ bool attend_shape(int64_t B, int64_t N, int64_t qh, int64_t heads, int64_t D, in
       s->lds = (int)(q > sums ? q : sums);
       // a workgroup takes four blocks at least
       const int64_t blocks = units * (ceil_div(tokens, sv::CACHE_BLOCK) + 1);
-      const int64_t full = CUS * sv::attend_per_cu((int)bricks, (int)nt, dtype == SV_F32);
+      const int64_t full = CUS * sv::attend_per_cu((int)bricks, (int)nt);
       s->grid = (int)(ceil_div(blocks, 4) < full ? ceil_div(blocks, 4) : full);
       return true;
     }

@@ -168,10 +168,10 @@ struct AttendShape {
   int lds;            // bytes of LDS
 };
 // Workgroups of a CU, which is waves of a SIMD: by the registers of a lane (sums, a block's
-// codes, scores and parts, the rest).
-constexpr int attend_per_cu(int bricks, int nt, bool f32) {
-  const int need = 8 * bricks * nt + 8 * bricks + 22 * nt + 40 + (f32 ? 8 : 0);
-  return need <= 128 ? 4 : need <= 152 ? 3 : need <= 248 ? 2 : 1;
+// values and the next one's codes, scores and weights, the rest).
+constexpr int attend_per_cu(int bricks, int nt) {
+  const int need = 8 * bricks * nt + 16 * bricks + 22 * nt + 36;
+  return need <= 126 ? 4 : need <= 166 ? 3 : need <= 264 ? 2 : 1;
 }
 // Groups of 16 dimensions that the waves of a workgroup join at a time, in 4 KB of LDS a tile each.
 constexpr int attend_round(int bricks, int nt) {
