@@ -69,9 +69,16 @@ class SpecVerifyError(RuntimeError):
         self.status = status
 
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    """torch, imported when a call first needs it; the import statement takes 0.2 us even then."""
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _dtype_code(t):
@@ -764,27 +771,29 @@ def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, origi
 
 def _rows4(t, name, device=None, dtype=None, shape=None):
     """(pointer, strides) of a [B, N, heads, D] tensor with consecutive D."""
-    if not _torch().is_tensor(t) or not t.is_cuda:
+    if not _TORCH.is_tensor(t) or not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     size = t.shape
-    if len(size) != 4 or t.numel() == 0:
+    if len(size) != 4 or 0 in size:
         raise ValueError(f"{name} must be [B, N, heads, D], none of them 0, got {tuple(size)}")
-    if shape is not None and tuple(size) != tuple(shape):
+    if shape is not None and size != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(size)}")
-    step = t.stride()
-    if size[3] > 1 and step[3] != 1:
+    b, n, h, one = t.stride()
+    if one != 1 and size[3] > 1:
         raise ValueError(f"{name} must have consecutive elements in a head")
-    return t.data_ptr(), SvStrides(step[0], step[1], step[2])
+    return t.data_ptr(), SvStrides(b, n, h)
 
 
 def _out4(t, like, name):
     """An output like `like`, its pointer and strides; a new contiguous one when None."""
     if t is None:
-        t = _torch().empty_like(like, memory_format=_torch().contiguous_format)
+        t = _TORCH.empty_like(like, memory_format=_TORCH.contiguous_format)
+        b, n, h, _ = t.stride()
+        return t, t.data_ptr(), SvStrides(b, n, h)
     return (t, *_rows4(t, name, like.device, like.dtype, like.shape))
 
 
@@ -844,17 +853,20 @@ def kv_cache(pages, heads, page_size, head_dim, device="cuda"):
 
 
 def _cache(cache, device):
-    """sv_cache of a KVCache, and (heads, head_dim)."""
-    torch = _torch()
-    shape, D, page = cache.k.shape, int(cache.head_dim), int(cache.page_size)
+    """sv_cache of a KVCache."""
+    k, v, ks, vs, page, D = cache
+    code, f32 = _TORCH.float8_e4m3fn, _TORCH.float32
+    shape, small = k.shape, ks.shape
     if len(shape) != 5 or shape[2] * 32 != page or shape[3] != -(-D // 32) or shape[4] != 1024:
         raise ValueError(f"cache.k must be [pages, heads, {page} / 32, ceil({D} / 32), 1024], got {tuple(shape)}")
-    small = shape[:3]
-    return SvCache(_vector(cache.k, "cache.k", torch.float8_e4m3fn, shape, device),
-                   _vector(cache.v, "cache.v", torch.float8_e4m3fn, shape, device),
-                   _vector(cache.k_scale, "cache.k_scale", torch.float32, small, device),
-                   _vector(cache.v_scale, "cache.v_scale", torch.float32, small, device),
-                   shape[0], shape[1], page, D)
+    if not (v.shape == shape and small == shape[:3] and vs.shape == small and k.dtype == code and v.dtype == code
+            and ks.dtype == f32 and vs.dtype == f32 and k.device == device and v.device == device
+            and ks.device == device and vs.device == device and k.is_contiguous() and v.is_contiguous()
+            and ks.is_contiguous() and vs.is_contiguous()):
+        for t, name, dtype, size in ((k, "cache.k", code, shape), (v, "cache.v", code, shape),
+                                     (ks, "cache.k_scale", f32, shape[:3]), (vs, "cache.v_scale", f32, shape[:3])):
+            _vector(t, name, dtype, size, device)      # which raises
+    return SvCache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), shape[0], shape[1], page, D)
 
 
 def _table(page_table, B, device):

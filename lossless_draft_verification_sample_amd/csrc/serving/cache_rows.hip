@@ -8,9 +8,12 @@
 // binade either way. Since the scale depends on what the block holds alone, rows
 // that it held before are decoded, and coded again at the new scale with the new ones.
 //
-// Bound by memory. One workgroup takes a block's keys or values: its threads read 8
-// dimensions of two tokens each, the largest value goes through a block reduction, and the
-// codes are put in the block's order in LDS, from where 16 bytes a thread are stored.
+// Bound by memory where prompts are written, by the latency of a chain of reads (lengths, page,
+// block) in a round of few rows. One workgroup takes a block's keys or values. Its threads hold the
+// block's codes, 16 bytes each as they lie; the new rows come 8 dimensions a thread; the largest
+// value goes through a block reduction, for which old codes need no decoding; and the new codes go
+// to their places through LDS. Old codes are made again only where the scale changes, and parts of
+// the block that hold no new row are then the only ones not written.
 
 #include <math.h>
 
@@ -20,7 +23,9 @@ namespace sv {
 namespace {
 
 constexpr int NTH = 256;
-constexpr int MAX_UNITS = CACHE_MAX_D / 32 * 64 / NTH;   // pairs of tokens by 8 dimensions, a thread
+constexpr int MAX_CHUNKS = CACHE_MAX_D / 32 * 64 / NTH;               // 16 bytes of codes, a thread
+constexpr int MAX_UNITS = CACHE_BLOCK * CACHE_MAX_D / 8 / NTH;        // 8 dimensions of a row, a thread
+constexpr int ROW_BYTES = CACHE_MAX_D + 8;
 
 struct Where {
   int b, h, block;
@@ -57,9 +62,27 @@ __device__ __forceinline__ uint32_t code4(const float* x, float inv, float most)
   return __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w, true);
 }
 
+// The bytes of a chunk (16 bytes of a block as they lie, chunk q * 16 + m of a brick) that hold
+// tokens from `from` on and before `to`.
+__device__ __forceinline__ su32x4 bytes_of(bool values, int chunk, int from, int to) {
+  const int m = chunk & 15, q = chunk >> 4 & 3;
+  if (values) return tokens_before(to - 8 * q) & ~tokens_before(from - 8 * q);
+  const int s = 8 * (m >> 2) + (m & 3);       // and s + 4
+  const uint32_t a = s >= from && s < to ? ~0u : 0u, b = s + 4 >= from && s + 4 < to ? ~0u : 0u;
+  return su32x4{a, a, b, b};
+}
+
+// The bytes of a chunk whose dimensions lie within the head.
+__device__ __forceinline__ su32x4 bytes_within(bool values, int chunk, int D) {
+  const int d = 32 * (chunk >> 6), m = chunk & 15, q = chunk >> 4 & 3;
+  if (!values) return tokens_before(D - (d + 8 * q));      // as many bytes as dimensions
+  const uint32_t a = d + m < D ? ~0u : 0u, b = d + 16 + m < D ? ~0u : 0u;
+  return su32x4{a, a, b, b};
+}
+
 template <typename E>
 __global__ __launch_bounds__(NTH) void write_kernel(CacheRowsArgs a) {
-  __shared__ uint8_t block[CACHE_MAX_D / 32 * BRICK];
+  __shared__ __attribute__((aligned(16))) uint8_t fresh[CACHE_BLOCK][ROW_BYTES];   // new codes, row by row
   __shared__ float top[NTH / WAVE];
   const Where w = where(a);
   const Span s = span_of(a.t, w.b);
@@ -68,97 +91,126 @@ __global__ __launch_bounds__(NTH) void write_kernel(CacheRowsArgs a) {
   if (t0 >= end) return;
   const int blk = t0 / CACHE_BLOCK, in_page = blk & ((1 << a.c.per_log2) - 1);
   const int page = a.t.table[(int64_t)w.b * a.t.width + (blk >> a.c.per_log2)];
-  if ((uint32_t)page >= (uint32_t)a.c.pages) return;
-  const int64_t at = (((int64_t)page * a.c.heads + w.h) << a.c.per_log2) + in_page;
-  const int bytes = a.c.bricks * BRICK, tid = threadIdx.x;
-  uint8_t* mem = (w.values ? a.c.v : a.c.k) + at * bytes;
-  float* scale = (w.values ? a.c.vs : a.c.ks) + at;
-  const bool held = t0 < s.first;                     // rows from before
-  const bool whole = !held && t0 + CACHE_BLOCK <= end;
-  float old_scale = 0.0f;
-  if (!whole) {
-    for (int i = tid * 16; i < bytes; i += NTH * 16) *(su32x4*)(block + i) = *(const su32x4*)(mem + i);
-    if (held) old_scale = *scale;
-    __syncthreads();
-  }
+  const int tid = threadIdx.x;
+  // new rows from .. to - 1 of the block; those before `from` are kept
+  const int from = s.first > t0 ? s.first - t0 : 0, to = end - t0 < CACHE_BLOCK ? end - t0 : CACHE_BLOCK;
   const Strides st = w.values ? a.vs : a.ks;
-  const E* rows = (const E*)(w.values ? a.v : a.k) + w.b * st.b + w.h * st.h;
-  const int units = a.c.bricks * 64;
-  float x[MAX_UNITS][2][8];
-  float amax = 0.0f;
+  const E* rows = (const E*)(w.values ? a.v : a.k) + w.b * st.b + w.h * st.h + (t0 - s.first) * st.n;
+  const int per_row = a.c.bricks * 4, units = (to - from) * per_row, chunks = a.c.bricks * 64;
+  float x[MAX_UNITS][8], amax = 0.0f;
 #pragma unroll
   for (int n = 0; n < MAX_UNITS; ++n) {
     const int u = tid + n * NTH;
     if (u >= units) break;
-    // a unit: dimensions 8 d8 .. + 7 of tokens s0 and s0 + 4
-    const int d8 = u % (a.c.bricks * 4), m = u / (a.c.bricks * 4);
-    const int d = d8 * 8, s0 = 8 * (m >> 2) + (m & 3);
+    const int row = u / per_row, d = (u - row * per_row) * 8;
+    const E* p = rows + (from + row) * st.n + d;
+    if (d + 8 <= a.c.D) {
+      load8(p, x[n]);
+    } else {
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int tok = s0 + 4 * half, pos = t0 + tok;
-      float(&y)[8] = x[n][half];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = 0.0f;
-      if (pos >= end) continue;
-      if (pos >= s.first) {
-        const E* p = rows + (pos - s.first) * st.n + d;
-        if (d + 8 <= a.c.D) {
-          load8(p, y);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (d + e < a.c.D) y[e] = elem(p + e);
-        }
-      } else {
-        const uint8_t* brick = block + (d / 32) * BRICK;
-        uint32_t lo = 0, hi = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t c = brick[w.values ? value_byte(tok, d % 32 + e) : key_byte(tok, d % 32 + e)];
-          if (e < 4) lo |= c << (8 * e);
-          else hi |= c << (8 * (e - 4));
-        }
-        codes4(lo, y);
-        codes4(hi, y + 4);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = d + e < a.c.D ? y[e] * old_scale : 0.0f;
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(y[e]) < INFINITY ? fabsf(y[e]) : 0.0f);
+      for (int e = 0; e < 8; ++e) x[n][e] = d + e < a.c.D ? elem(p + e) : 0.0f;
     }
+  }
+  if ((uint32_t)page >= (uint32_t)a.c.pages) return;
+  const int64_t at = (((int64_t)page * a.c.heads + w.h) << a.c.per_log2) + in_page;
+  su32x4* mem = (su32x4*)((w.values ? a.c.v : a.c.k) + at * (a.c.bricks * BRICK));
+  float* scale = (w.values ? a.c.vs : a.c.ks) + at;
+  const bool whole = from == 0 && to == CACHE_BLOCK;
+  su32x4 code[MAX_CHUNKS];
+  float old_scale = 0.0f;
+  if (!whole) {
+#pragma unroll
+    for (int n = 0; n < MAX_CHUNKS; ++n)
+      if (tid + n * NTH < chunks) code[n] = mem[tid + n * NTH];
+    if (a.c.D % 32) {
+#pragma unroll
+      for (int n = 0; n < MAX_CHUNKS; ++n) {
+        const int chunk = tid + n * NTH;
+        if (chunk < chunks) code[n] &= bytes_within(w.values, chunk, a.c.D) | ~bytes_of(w.values, chunk, 0, from);
+      }
+    }
+    if (from) {
+      old_scale = *scale;
+      uint32_t most = 0;     // codes without their sign are in the order of their values
+#pragma unroll
+      for (int n = 0; n < MAX_CHUNKS; ++n) {
+        if (tid + n * NTH >= chunks) break;
+        su32x4 c = code[n] & bytes_of(w.values, tid + n * NTH, 0, from);
+        c &= ~(nan_codes(c) * 255u) & 0x7F7F7F7Fu;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const uint32_t b = c[e / 4] >> (8 * (e & 3)) & 255u;
+          most = b > most ? b : most;
+        }
+      }
+      float y[4];
+      codes4(most, y);
+      amax = fabsf(y[0] * old_scale) < INFINITY ? fabsf(y[0] * old_scale) : 0.0f;
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < MAX_UNITS; ++n) {
+    if (tid + n * NTH >= units) break;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[n][e]) < INFINITY ? fabsf(x[n][e]) : 0.0f);
   }
 #pragma unroll
   for (int off = WAVE / 2; off; off >>= 1) amax = fmaxf(amax, __shfl_xor(amax, off, WAVE));
   if (tid % WAVE == 0) top[tid / WAVE] = amax;
-  __syncthreads();   // also: every old code has been read
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < NTH / WAVE; ++i) amax = fmaxf(amax, top[i]);
   const int ex = amax > 0.0f ? scale_exponent(amax) : 0;
-  const float inv = pow2(-ex), most = ex == 120 ? 240.0f : E4M3_MAX;
+  const float inv = pow2(-ex), most = ex == 120 ? 240.0f : E4M3_MAX, new_scale = pow2(ex);
 #pragma unroll
   for (int n = 0; n < MAX_UNITS; ++n) {
     const int u = tid + n * NTH;
     if (u >= units) break;
-    const int d8 = u % (a.c.bricks * 4), m = u / (a.c.bricks * 4);
-    const int d = d8 * 8, s0 = 8 * (m >> 2) + (m & 3);
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int tok = s0 + 4 * half;
-      if (t0 + tok >= end) continue;
-      uint8_t* brick = block + (d / 32) * BRICK;
-      const uint32_t lo = code4(x[n][half], inv, most), hi = code4(x[n][half] + 4, inv, most);
-      if (w.values) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          brick[value_byte(tok, d % 32 + e)] = (uint8_t)((e < 4 ? lo : hi) >> (8 * (e & 3)));
-      } else {
-        *(su32x2*)(brick + key_byte(tok, d % 32)) = su32x2{lo, hi};
-      }
-    }
+    const int row = u / per_row, d = (u - row * per_row) * 8;
+    *(su32x2*)&fresh[from + row][d] = su32x2{code4(x[n], inv, most), code4(x[n] + 4, inv, most)};
   }
   __syncthreads();
-  for (int i = tid * 16; i < bytes; i += NTH * 16) *(su32x4*)(mem + i) = *(const su32x4*)(block + i);
-  if (tid == 0) *scale = pow2(ex);
+  const bool again = from && old_scale != new_scale;
+#pragma unroll
+  for (int n = 0; n < MAX_CHUNKS; ++n) {
+    const int chunk = tid + n * NTH;
+    if (chunk >= chunks) break;
+    const int c = chunk >> 6, q = chunk >> 4 & 3, m = chunk & 15;
+    const su32x4 now = bytes_of(w.values, chunk, from, to);
+    const bool some = (now[0] | now[1] | now[2] | now[3]) != 0;
+    if (!some && !again) continue;
+    su32x4 out = whole ? su32x4{0, 0, 0, 0} : code[n];
+    if (again) {
+      const su32x4 kept = bytes_of(w.values, chunk, 0, from) & bytes_within(w.values, chunk, a.c.D);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float y[4];
+        codes4(out[e], y);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] *= old_scale;
+        out[e] = (out[e] & ~kept[e]) | (code4(y, inv, most) & kept[e]);
+      }
+    }
+    if (some) {
+      su32x4 in{0, 0, 0, 0};
+      if (w.values) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int tok = 8 * q + e;
+          if (tok < from || tok >= to) continue;
+          in[e >> 2] |= (uint32_t)fresh[tok][32 * c + m] << (8 * (e & 3));
+          in[2 + (e >> 2)] |= (uint32_t)fresh[tok][32 * c + 16 + m] << (8 * (e & 3));
+        }
+      } else {
+        const int tok = 8 * (m >> 2) + (m & 3), d = 32 * c + 8 * q;
+        const su32x2 lo = *(const su32x2*)&fresh[tok][d], hi = *(const su32x2*)&fresh[tok + 4][d];
+        in = su32x4{lo[0], lo[1], hi[0], hi[1]};
+      }
+      out = (out & ~now) | (in & now);
+    }
+    mem[chunk] = out;
+  }
+  if (tid == 0) *scale = new_scale;
 }
 
 template <typename E>

@@ -16,131 +16,188 @@ namespace {
 
 constexpr int NTH = 256;
 constexpr int MAX_R2 = 512;        // R / 2
-constexpr int MAX_ROWS = 8;        // rows of a workgroup
 
-template <typename E>
-struct Side {
-  const E* x;
-  E* y;
-  Strides xs, ys;
-};
-
-template <int W, typename E>
-__device__ __forceinline__ void get(const E* p, float (&x)[W]) {
-  if constexpr (W == 8) {
-    load8(p, x);
-  } else {
-#pragma unroll
-    for (int i = 0; i < W; ++i) x[i] = elem(p + i);
-  }
-}
-template <int W, typename E>
-__device__ __forceinline__ void set(E* p, const float (&x)[W]) {
-  if constexpr (W == 8) {
-    store8(p, x);
-  } else {
-#pragma unroll
-    for (int i = 0; i < W; ++i) put(p + i, x[i]);
-  }
-}
-
-// W pairs a unit; whole units of 8 elements of what is not turned.
-template <typename E, bool INTER, int W>
-__global__ __launch_bounds__(NTH) void rotate_kernel(RotateArgs a, int per_wg) {
-  __shared__ sf32x2 turn[MAX_ROWS * 64 > MAX_R2 ? MAX_ROWS * 64 : MAX_R2];
-  const int R2 = a.R / 2, tid = threadIdx.x;
-  const int64_t total = (int64_t)a.B * a.N, row0 = (int64_t)blockIdx.x * per_wg;
-  for (int i = tid; i < per_wg * R2; i += NTH) {
+// Cosines and sines of this workgroup's rows, times the scale.
+__device__ __forceinline__ void make_turns(const RotateArgs& a, sf32x2* turn, int64_t row0, int rows) {
+  const int R2 = a.R / 2;
+  for (int i = threadIdx.x; i < rows * R2; i += NTH) {
     const int64_t row = row0 + i / R2;
-    if (row >= total) break;
-    const int b = (int)(row / a.N), j = (int)(row % a.N);
+    const int b = (int)(row / a.N), j = (int)(row - (int64_t)b * a.N);
     const double at = (double)((int64_t)(a.first ? a.first[b] : 0) + j);
     // in turns, to [-1/2, 1/2]: exact up to the product's own rounding
     const double t = at * (a.freqs[i % R2] * 0.15915494309189533577);
-    const float r = (float)(t - rint(t));
     float s, c;
-    sincospif(2.0f * r, &s, &c);
+    sincospif(2.0f * (float)(t - rint(t)), &s, &c);
     turn[i] = sf32x2{c * a.scale, (a.inverse ? -s : s) * a.scale};
   }
-  __syncthreads();
-  const int heads = a.qh + a.kh;
-  const int pairs = R2 / W, rest = a.D - a.R, units = pairs + (rest + 7) / 8;
-  for (int r = 0; r < per_wg; ++r) {
-    const int64_t row = row0 + r;
-    if (row >= total) return;
-    const int b = (int)(row / a.N), j = (int)(row % a.N);
-    const int used = a.rows ? a.rows[b] : a.N;
-    const bool bad = used < 0 || used > a.N;
-    if (j >= used && !bad) continue;
-    for (int i = tid; i < heads * units; i += NTH) {
-      const int head = i / units, u = i - head * units;
-      const bool isq = head < a.qh;
-      const int h = isq ? head : head - a.qh;
-      const Strides xs = isq ? a.qs : a.ks, ys = isq ? a.oqs : a.oks;
-      const E* x = (const E*)(isq ? a.q : a.k) + b * xs.b + j * xs.n + h * xs.h;
-      E* y = (E*)(isq ? a.oq : a.ok) + b * ys.b + j * ys.n + h * ys.h;
+}
+
+__device__ __forceinline__ void turn_pair(float& x, float& y, sf32x2 cs) {
+  const float u = __builtin_fmaf(x, cs[0], -(y * cs[1])), v = __builtin_fmaf(y, cs[0], x * cs[1]);
+  x = u;
+  y = v;
+}
+
+// Where a unit of work lies: a head of a row, and what of it.
+template <typename E>
+struct Item {
+  const E* x;
+  E* y;
+  int row, unit;
+  bool bad;
+};
+template <typename E>
+__device__ __forceinline__ bool item_of(const RotateArgs& a, int64_t row0, int rows, int units, int i, Item<E>* it) {
+  const int heads = a.qh + a.kh, per = heads * units, r = i / per, h = (i - r * per) / units;
+  if (r >= rows) return false;
+  it->row = r;
+  it->unit = i - r * per - h * units;
+  const int b = (int)((row0 + r) / a.N), j = (int)(row0 + r - (int64_t)b * a.N);
+  const int used = a.rows ? a.rows[b] : a.N;
+  it->bad = used < 0 || used > a.N;
+  if (j >= used && !it->bad) return false;
+  const bool isq = h < a.qh;
+  const Strides xs = isq ? a.qs : a.ks, ys = isq ? a.oqs : a.oks;
+  const int k = isq ? h : h - a.qh;
+  it->x = (const E*)(isq ? a.q : a.k) + b * xs.b + j * xs.n + k * xs.h;
+  it->y = (E*)(isq ? a.oq : a.ok) + b * ys.b + j * ys.n + k * ys.h;
+  return true;
+}
+
+// 16 bytes of float32, or of bfloat16, as float32.
+__device__ __forceinline__ void open16(const su32x4& w, float (&x)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(w[i]);
+}
+__device__ __forceinline__ void open16(const su32x4& w, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ su32x4 close16(const float (&x)[4]) {
+  return su32x4{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])};
+}
+__device__ __forceinline__ su32x4 close16(const float (&x)[8]) {
+  return su32x4{round_bf16x2(x[0], x[1]), round_bf16x2(x[2], x[3]), round_bf16x2(x[4], x[5]), round_bf16x2(x[6], x[7])};
+}
+
+// R/2 a multiple of the elements of 16 bytes: a unit is two times 16 bytes, of both halves or one
+// after the other, of the rest of a head too where that is whole. Every thread asks for its
+// first MINE units before the angles are made.
+template <typename E, bool INTER>
+__global__ __launch_bounds__(NTH) void rotate_vec_kernel(RotateArgs a, int per_wg) {
+  constexpr int W = 16 / (int)sizeof(E), MINE = 4;
+  __shared__ __attribute__((aligned(16))) sf32x2 turn[MAX_R2];
+  const int R2 = a.R / 2, tid = threadIdx.x;
+  const int64_t total = (int64_t)a.B * a.N, row0 = (int64_t)blockIdx.x * per_wg;
+  const int rows = (int)(total - row0 < per_wg ? total - row0 : per_wg);
+  const int pairs = R2 / W, rest = a.D - a.R;
+  const int copies = a.oq == a.q && a.ok == a.k && !a.rows ? 0 : (rest + 2 * W - 1) / (2 * W);
+  const int units = pairs + copies, items = rows * (a.qh + a.kh) * units;
+  for (int i0 = tid, first = 1; first || i0 - tid < items; i0 += MINE * NTH, first = 0) {
+    su32x4 lo[MINE], hi[MINE];
+    Item<E> it[MINE];
+    bool there[MINE];
+#pragma unroll
+    for (int k = 0; k < MINE; ++k) {
+      there[k] = item_of(a, row0, rows, units, i0 + k * NTH, &it[k]);
+      if (!there[k]) continue;
+      const int u = it[k].unit, d = u < pairs ? (INTER ? 2 * u * W : u * W) : a.R + (u - pairs) * 2 * W;
+      const int d1 = u < pairs && !INTER ? R2 + u * W : d + W;
+      if (d1 + W <= a.D) {
+        lo[k] = *(const su32x4_any*)(it[k].x + d);
+        hi[k] = *(const su32x4_any*)(it[k].x + d1);
+      }
+    }
+    if (first) {
+      make_turns(a, turn, row0, rows);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int k = 0; k < MINE; ++k) {
+      if (!there[k]) continue;
+      const int u = it[k].unit;
       if (u < pairs) {
-        const int p = u * W;
-        float lo[W], hi[W], o0[W], o1[W];
+        float x[W], y[W];
+        open16(lo[k], x);
+        open16(hi[k], y);
+        const sf32x2* cs = turn + it[k].row * R2 + u * W;
         if constexpr (INTER) {
-          float both[2 * W];
-          if constexpr (W == 4) {
-            load8(x + 2 * p, both);
-          } else {
-            get<2 * W>(x + 2 * p, both);
-          }
 #pragma unroll
-          for (int e = 0; e < W; ++e) {
-            lo[e] = both[2 * e];
-            hi[e] = both[2 * e + 1];
+          for (int e = 0; e < W; e += 2) {
+            turn_pair(x[e], x[e + 1], cs[e / 2]);
+            turn_pair(y[e], y[e + 1], cs[W / 2 + e / 2]);
           }
         } else {
-          get<W>(x + p, lo);
-          get<W>(x + R2 + p, hi);
-        }
 #pragma unroll
-        for (int e = 0; e < W; ++e) {
-          const sf32x2 cs = turn[r * R2 + p + e];
-          o0[e] = bad ? NAN : __builtin_fmaf(lo[e], cs[0], -(hi[e] * cs[1]));
-          o1[e] = bad ? NAN : __builtin_fmaf(hi[e], cs[0], lo[e] * cs[1]);
+          for (int e = 0; e < W; ++e) turn_pair(x[e], y[e], cs[e]);
         }
-        if constexpr (INTER) {
-          float both[2 * W];
+        if (it[k].bad) {
 #pragma unroll
-          for (int e = 0; e < W; ++e) {
-            both[2 * e] = o0[e];
-            both[2 * e + 1] = o1[e];
-          }
-          set<2 * W>(y + 2 * p, both);
-        } else {
-          set<W>(y + p, o0);
-          set<W>(y + R2 + p, o1);
+          for (int e = 0; e < W; ++e) x[e] = y[e] = NAN;
         }
+        *(su32x4_any*)(it[k].y + (INTER ? 2 * u * W : u * W)) = close16(x);
+        *(su32x4_any*)(it[k].y + (INTER ? 2 * u * W + W : R2 + u * W)) = close16(y);
       } else {
-        const int d = a.R + (u - pairs) * 8;
-        if (x == y && !bad) continue;
-        for (int e = 0; e < 8 && d + e < a.D; ++e) {
-          if (bad) put(y + d + e, NAN);
-          else y[d + e] = x[d + e];
+        const int d = a.R + (u - pairs) * 2 * W;
+        if (d + 2 * W <= a.D && !it[k].bad) {
+          *(su32x4_any*)(it[k].y + d) = lo[k];
+          *(su32x4_any*)(it[k].y + d + W) = hi[k];
+        } else {
+          for (int e = d; e < d + 2 * W && e < a.D; ++e) {
+            if (it[k].bad) put(it[k].y + e, NAN);
+            else it[k].y[e] = it[k].x[e];
+          }
         }
       }
     }
   }
 }
 
+// Any other R: a pair a unit, then the rest element by element.
+template <typename E, bool INTER>
+__global__ __launch_bounds__(NTH) void rotate_any_kernel(RotateArgs a, int per_wg) {
+  __shared__ sf32x2 turn[MAX_R2];
+  const int R2 = a.R / 2;
+  const int64_t total = (int64_t)a.B * a.N, row0 = (int64_t)blockIdx.x * per_wg;
+  const int rows = (int)(total - row0 < per_wg ? total - row0 : per_wg);
+  make_turns(a, turn, row0, rows);
+  __syncthreads();
+  const int units = R2 + a.D - a.R, items = rows * (a.qh + a.kh) * units;
+  for (int i = threadIdx.x; i < items; i += NTH) {
+    Item<E> it;
+    if (!item_of(a, row0, rows, units, i, &it)) continue;
+    if (it.unit < R2) {
+      const int p = INTER ? 2 * it.unit : it.unit, q = INTER ? p + 1 : R2 + p;
+      float x = elem(it.x + p), y = elem(it.x + q);
+      turn_pair(x, y, turn[it.row * R2 + it.unit]);
+      put(it.y + p, it.bad ? NAN : x);
+      put(it.y + q, it.bad ? NAN : y);
+    } else {
+      const int d = a.R + it.unit - R2;
+      if (it.bad) put(it.y + d, NAN);
+      else it.y[d] = it.x[d];
+    }
+  }
+}
+
 template <typename E, bool INTER>
 int launch(const RotateArgs& a, hipStream_t st) {
+  constexpr int W = 16 / (int)sizeof(E);
   const int R2 = a.R / 2;
-  int per = R2 ? MAX_R2 / R2 : MAX_ROWS;
-  if (per > 4) per = 4;
-  const int64_t total = (int64_t)a.B * a.N;
+  const bool vec = R2 && R2 % W == 0;
+  // rows of a workgroup: four units a thread, the angles' room in LDS, and workgroups for the CUs
+  const int64_t total = (int64_t)a.B * a.N, units = (a.qh + a.kh) * (int64_t)((a.D + 2 * W - 1) / (2 * W));
+  int64_t per = 4 * NTH / units;
+  if (per > total / 1024) per = total / 1024;
+  if (R2 && per > MAX_R2 / R2) per = MAX_R2 / R2;
+  if (per > 8) per = 8;
+  if (per < 1) per = 1;
   const int grid = (int)((total + per - 1) / per);
-  if (INTER ? R2 % 4 == 0 : R2 % 8 == 0)
-    rotate_kernel<E, INTER, INTER ? 4 : 8><<<grid, NTH, 0, st>>>(a, per);
-  else if (R2 % 2 == 0)
-    rotate_kernel<E, INTER, 2><<<grid, NTH, 0, st>>>(a, per);
-  else
-    rotate_kernel<E, INTER, 1><<<grid, NTH, 0, st>>>(a, per);
+  if (vec) rotate_vec_kernel<E, INTER><<<grid, NTH, 0, st>>>(a, (int)per);
+  else rotate_any_kernel<E, INTER><<<grid, NTH, 0, st>>>(a, (int)per);
   return hipGetLastError() != hipSuccess;
 }
 

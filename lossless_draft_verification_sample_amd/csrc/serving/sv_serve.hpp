@@ -129,6 +129,21 @@ __device__ __forceinline__ void codes4(uint32_t w, float* x) {
   x[3] = b[1];
 }
 
+// Bits of the bytes that are NaN codes (0x7F, 0xFF), one a byte at bit 0.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
+  const uint32_t x = (w & 0x7F7F7F7Fu) ^ 0x7F7F7F7Fu;       // 0 in a byte of NaN
+  return (((x + 0x7F7F7F7Fu) >> 7) & 0x01010101u) ^ 0x01010101u;
+}
+__device__ __forceinline__ su32x4 nan_codes(su32x4 w) {
+  return su32x4{nan_codes(w[0]), nan_codes(w[1]), nan_codes(w[2]), nan_codes(w[3])};
+}
+// The bytes of a lane's codes (8 tokens of a dimension, twice) of the first `left` tokens.
+__device__ __forceinline__ su32x4 tokens_before(int left) {
+  const uint32_t lo = left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1u;
+  const uint32_t hi = left >= 8 ? ~0u : left <= 4 ? 0u : (1u << (8 * (left - 4))) - 1u;
+  return su32x4{lo, hi, lo, hi};
+}
+
 // -------------------------------------------------------------------- launchers
 
 struct RotateArgs {
