@@ -8,6 +8,7 @@ libspecverify.so. PyTorch supplies device memory and
 streams. If the library is missing, every call raises.
 """
 
+import functools
 from collections import namedtuple
 
 from . import _lib
@@ -769,19 +770,25 @@ def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, origi
     return torch.tensor(freqs, dtype=torch.float64, device=device), scale
 
 
-def _rows4(t, name, device=None, dtype=None, shape=None):
-    """(pointer, strides) of a [B, N, heads, D] tensor with consecutive D."""
+def _on_device(t, name, device, dtype, shape):
+    """Raises what is wrong with a tensor of rows: not on a device, or on another device, of another
+    type or shape than wanted (None: any)."""
     if not _TORCH.is_tensor(t) or not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _rows4(t, name, device=None, dtype=None, shape=None):
+    """(pointer, strides) of a [B, N, heads, D] tensor with consecutive D."""
+    _on_device(t, name, device, dtype, shape)
     size = t.shape
     if len(size) != 4 or 0 in size:
         raise ValueError(f"{name} must be [B, N, heads, D], none of them 0, got {tuple(size)}")
-    if shape is not None and size != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(size)}")
     b, n, h, one = t.stride()
     if one != 1 and size[3] > 1:
         raise ValueError(f"{name} must have consecutive elements in a head")
@@ -949,6 +956,12 @@ def spec_verify_attention_workspace_bytes(B, N, q_heads, heads, head_dim, tokens
         int(B), int(N), int(q_heads), int(heads), int(head_dim), int(tokens), int(dtype)))
 
 
+@functools.lru_cache(maxsize=256)
+def _attention_space(*sizes):
+    """The same by sizes alone, without a call into the library each time."""
+    return _lib.load().spec_verify_attention_workspace_bytes(*sizes)
+
+
 def spec_verify_attention(q, cache, page_table, kv_len, scale=None, window=0, rows=None, want_lse=False,
                           workspace=None, out=None, stream=None, lib=None):
     """Attention of a round's rows over the 8-bit cache, which holds them already (see
@@ -975,8 +988,7 @@ def spec_verify_attention(q, cache, page_table, kv_len, scale=None, window=0, ro
         lse = out.lse if out is not None else None
         if out is None and want_lse:
             lse = torch.empty((B, N, qh), dtype=torch.float32, device=dev)
-        ws, ws_bytes, keep = _space(
-            workspace, lib.spec_verify_attention_workspace_bytes(B, N, qh, c.heads, D, width * c.page_size, dt), dev)
+        ws, ws_bytes, keep = _space(workspace, _attention_space(B, N, qh, c.heads, D, width * c.page_size, dt), dev)
         rc = lib.spec_verify_attention(
             qp, qs, dt, B, N, qh, c, table, width, _vector(kv_len, "kv_len", torch.int32, (B,), dev),
             _vector(rows, "rows", torch.int32, (B,), dev), D ** -0.5 if scale is None else float(scale),
@@ -990,12 +1002,14 @@ def spec_verify_attention(q, cache, page_table, kv_len, scale=None, window=0, ro
 
 def _rows3(t, name, device=None, dtype=None, shape=None):
     """(pointer, strides) of a [B, N, V] tensor with consecutive V."""
-    if not _torch().is_tensor(t) or not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [B, N, V], got {tuple(t.shape)}")
-    ptr, s = _rows4(t.unsqueeze(2), name, device, dtype, shape and (shape[0], shape[1], 1, shape[2]))
-    return ptr, SvStrides(s.request, s.row, 0)
+    _on_device(t, name, device, dtype, shape)
+    size = t.shape
+    if len(size) != 3 or 0 in size:
+        raise ValueError(f"{name} must be [B, N, V], none of them 0, got {tuple(size)}")
+    b, n, one = t.stride()
+    if one != 1 and size[2] > 1:
+        raise ValueError(f"{name} must have consecutive elements in a row")
+    return t.data_ptr(), SvStrides(b, n, 0)
 
 
 def _id_list(t, name, B, device):

@@ -88,7 +88,7 @@ __device__ __forceinline__ su32x4 close16(const float (&x)[8]) {
 // first MINE units before the angles are made.
 template <typename E, bool INTER>
 __global__ __launch_bounds__(NTH) void rotate_vec_kernel(RotateArgs a, int per_wg) {
-  constexpr int W = 16 / (int)sizeof(E), MINE = 4;
+  constexpr int W = 16 / (int)sizeof(E), MINE = 2;
   __shared__ __attribute__((aligned(16))) sf32x2 turn[MAX_R2];
   const int R2 = a.R / 2, tid = threadIdx.x;
   const int64_t total = (int64_t)a.B * a.N, row0 = (int64_t)blockIdx.x * per_wg;
@@ -188,10 +188,10 @@ int launch(const RotateArgs& a, hipStream_t st) {
   constexpr int W = 16 / (int)sizeof(E);
   const int R2 = a.R / 2;
   const bool vec = R2 && R2 % W == 0;
-  // rows of a workgroup: four units a thread, the angles' room in LDS, and workgroups for the CUs
+  // rows of a workgroup: two units a thread, the angles' room in LDS, and workgroups for the CUs
   const int64_t total = (int64_t)a.B * a.N, units = (a.qh + a.kh) * (int64_t)((a.D + 2 * W - 1) / (2 * W));
-  int64_t per = 4 * NTH / units;
-  if (per > total / 1024) per = total / 1024;
+  int64_t per = 2 * NTH / units;
+  if (per > total / 512) per = total / 512;
   if (R2 && per > MAX_R2 / R2) per = MAX_R2 / R2;
   if (per > 8) per = 8;
   if (per < 1) per = 1;

@@ -260,10 +260,12 @@ int spec_verify_attention(const void* q, sv_strides q_strides, sv_dtype dtype, i
   a.window = window;
   a.bf16 = dtype == SV_BF16;
   a.scale2 = (float)((double)scale * M_LOG2E);
-  // units enough to fill the CUs are joined by a workgroup each, fewer by more
+  // columns of a workgroup of the join: three items a thread, one where the units are few
   const int64_t units = (int64_t)B * a.c.heads * a.s.sets;
   a.join_cols = a.s.cols_set;
-  while (a.join_cols > 4 && units * ceil_div(a.s.cols_set, a.join_cols) < 4 * CUS) a.join_cols = (a.join_cols + 1) / 2;
+  while (a.join_cols > 1 &&
+         a.join_cols * a.c.bricks * 8 > (units * ceil_div(a.s.cols_set, a.join_cols) < 4 * CUS ? 256 : 768))
+    a.join_cols = (a.join_cols + 1) / 2;
   a.record = (int32_t*)((char*)workspace + w.record);
   a.partial = (float*)((char*)workspace + w.partial);
   return sv::launch_attend(a, (hipStream_t)stream) ? SV_EHIP : SV_OK;

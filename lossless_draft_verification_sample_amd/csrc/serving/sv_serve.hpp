@@ -171,7 +171,6 @@ struct CacheRowsArgs {
 int launch_cache_write(const CacheRowsArgs& a, hipStream_t st);
 int launch_cache_read(const CacheRowsArgs& a, hipStream_t st);
 
-constexpr int AT_MAX_COLS = 256;      // of a set: four waves of four tiles
 constexpr int AT_THREADS = 256, AT_WAVES = AT_THREADS / WAVE;
 // How the N * group columns (row, query head) of a cache head are spread: NT tiles of
 // 16 columns a wave, `across` waves of a workgroup side by side (the others share out the
