@@ -866,9 +866,10 @@ def _cache(cache, device):
     shape, small = k.shape, ks.shape
     if len(shape) != 5 or shape[2] * 32 != page or shape[3] != -(-D // 32) or shape[4] != 1024:
         raise ValueError(f"cache.k must be [pages, heads, {page} / 32, ceil({D} / 32), 1024], got {tuple(shape)}")
+    where = device.index                    # get_device is the quicker comparison
     if not (v.shape == shape and small == shape[:3] and vs.shape == small and k.dtype == code and v.dtype == code
-            and ks.dtype == f32 and vs.dtype == f32 and k.device == device and v.device == device
-            and ks.device == device and vs.device == device and k.is_contiguous() and v.is_contiguous()
+            and ks.dtype == f32 and vs.dtype == f32 and k.get_device() == where and v.get_device() == where
+            and ks.get_device() == where and vs.get_device() == where and k.is_contiguous() and v.is_contiguous()
             and ks.is_contiguous() and vs.is_contiguous()):
         for t, name, dtype, size in ((k, "cache.k", code, shape), (v, "cache.v", code, shape),
                                      (ks, "cache.k_scale", f32, shape[:3]), (vs, "cache.v_scale", f32, shape[:3])):

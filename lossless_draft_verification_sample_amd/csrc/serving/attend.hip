@@ -74,6 +74,7 @@ int launch_attend_bf16(const AttendArgs& a, hipStream_t st) { return launch_atte
 
 int launch_attend(const AttendArgs& a, hipStream_t st) {
   if (a.bf16 ? launch_attend_bf16(a, st) : launch_attend_f32(a, st)) return 1;
+  if (a.s.single) return 0;
   const int per = (a.s.cols_set + a.join_cols - 1) / a.join_cols;
   const dim3 grid((uint32_t)((int64_t)a.t.B * a.c.heads * a.s.sets * per));
   if (a.bf16) join_kernel<false><<<grid, JOIN_THREADS, 0, st>>>(a);

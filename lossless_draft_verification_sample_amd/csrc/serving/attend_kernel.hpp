@@ -28,7 +28,9 @@
 // Workgroups share out the blocks of all requests evenly, whatever their lengths: with T blocks
 // over all units (request, cache head, set of columns), workgroup w takes blocks
 // T w / W .. T (w + 1) / W - 1. Units that several workgroups share leave their parts
-// (O, r, l) in the workspace, and a second kernel joins them in the order of the workgroups.
+// (O, r, l) in the workspace, and a second kernel joins them in the order of the workgroups. Where
+// the page table has room for 1,024 tokens at most, a unit is one workgroup's, without workspace
+// or join, whose launch and room cost the host 5 us of 16 (%SINGLE%).
 #pragma once
 
 #include <math.h>
@@ -206,19 +208,28 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT)) void attend_
 
   // the blocks of all requests, and this workgroup's share of them
   auto cost = [&](const Reach& r) { return r.blocks ? (int64_t)(r.blocks + AT_START * NT) * U : 0; };
-  int64_t T = 0;
-  for (int b = lane; b < a.t.B; b += WAVE) T += cost(reach_of(a, b));
-  T = uniform(wave_sum64(T));
-  int64_t W = T / AT_LEAST;
-  W = W < 1 ? 1 : W > (int64_t)gridDim.x ? (int64_t)gridDim.x : W;
   const int64_t wg = blockIdx.x;
-  if (wg >= W || T == 0) return;
-  int64_t x = uniform(T * wg / W);
-  const int64_t x1 = uniform(T * (wg + 1) / W);
-  // the request of x
+  int64_t T = 0, W = 1, x = 0, x1 = 0;
   int64_t before = 0;      // cost of the requests before b
   int b = 0;
-  for (int b0 = 0; b0 < a.t.B; b0 += WAVE) {
+  if (a.s.single) {        // a unit a workgroup
+    b = uniform((int)(wg / U));
+    const Reach r = uniform(reach_of(a, b));
+    const int n = r.blocks + AT_START * NT;
+    if (r.blocks == 0) return;
+    x = (int64_t)(wg - (int64_t)b * U) * n;
+    x1 = x + n;
+  } else {
+    for (int b = lane; b < a.t.B; b += WAVE) T += cost(reach_of(a, b));
+    T = uniform(wave_sum64(T));
+    W = T / AT_LEAST;
+    W = W < 1 ? 1 : W > (int64_t)gridDim.x ? (int64_t)gridDim.x : W;
+    if (wg >= W || T == 0) return;
+    x = uniform(T * wg / W);
+    x1 = uniform(T * (wg + 1) / W);
+  }
+  // the request of x
+  for (int b0 = 0; b0 < a.t.B && !a.s.single; b0 += WAVE) {
     const int64_t mine = b0 + lane < a.t.B ? cost(reach_of(a, b0 + lane)) : 0;
     int64_t upto = mine;
 #pragma unroll
@@ -571,7 +582,7 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT)) void attend_
     // The next segment's first block is asked for before this one's end is dealt with.
     const bool whole = i0 == 0 && i1 == r.blocks;
     const int slot = i0 == 0, was_b = b, was_h = h, was_set = set, was_rows = r.rows;
-    if (i0 == 0 && tid == 0) {
+    if (i0 == 0 && tid == 0 && !a.s.single) {
       const AttendArgs& z = fresh_args();
       const int64_t unit_id = ((int64_t)b * z.c.heads + h) * z.s.sets + set;
       z.record[2 * unit_id] = (int32_t)wg;

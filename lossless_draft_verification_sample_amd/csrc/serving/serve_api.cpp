@@ -18,6 +18,7 @@ constexpr int64_t MAX_TOKENS = 1 << 30;
 constexpr int MAX_PAGE = 65536;
 constexpr int MAX_GROUP = 4096;    // query heads that share a cache head
 constexpr int CUS = 256;
+constexpr int SINGLE_TOKENS = 1024;   // of a page table: a workgroup takes all blocks of a unit
 
 size_t align_up(size_t x) { return (x + WS_ALIGN - 1) / WS_ALIGN * WS_ALIGN; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -142,6 +143,12 @@ bool attend_shape(int64_t B, int64_t N, int64_t qh, int64_t heads, int64_t D, in
       s->cols_set = (int)cols_set;
       const int64_t q = nt * across * bricks * parts * 1024, sums = 4096 * nt * sv::attend_round((int)bricks, (int)nt);
       s->lds = (int)(q > sums ? q : sums);
+      s->single = tokens <= SINGLE_TOKENS;
+      if (s->single) {
+        if (units >= MAX_WORKGROUPS) return false;
+        s->grid = (int)units;
+        return true;
+      }
       // a workgroup takes four blocks at least
       const int64_t blocks = units * (ceil_div(tokens, sv::CACHE_BLOCK) + 1);
       const int64_t full = CUS * sv::attend_per_cu((int)bricks, (int)nt);
@@ -155,7 +162,8 @@ struct AttendSpace {
 };
 AttendSpace attend_space(const sv::AttendShape& s, int64_t B, int64_t heads, int64_t D) {
   AttendSpace w;
-  w.record = 0;
+  w.record = w.partial = w.total = 0;
+  if (s.single) return w;
   w.partial = align_up((size_t)(B * heads * s.sets) * 2 * sizeof(int32_t));
   w.total = w.partial + align_up((size_t)s.grid * 2 * s.cols_set * (ceil_div(D, 32) * 32 + 2) * sizeof(float));
   return w;
@@ -247,7 +255,7 @@ int spec_verify_attention(const void* q, sv_strides q_strides, sv_dtype dtype, i
     return SV_EINVAL;
   if (!attend_shape(B, N, q_heads, a.c.heads, a.c.D, a.t.capacity, dtype, &a.s)) return SV_ESIZE;
   const AttendSpace w = attend_space(a.s, B, a.c.heads, a.c.D);
-  if (!workspace || !aligned(workspace, WS_ALIGN) || workspace_bytes < w.total) return SV_EWORKSPACE;
+  if (w.total && (!workspace || !aligned(workspace, WS_ALIGN) || workspace_bytes < w.total)) return SV_EWORKSPACE;
   a.q = q;
   a.out = out;
   a.qs = strides_of(q_strides);

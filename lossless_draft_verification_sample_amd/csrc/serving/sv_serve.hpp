@@ -179,6 +179,7 @@ struct AttendShape {
   int cols, nt, across, sets;
   int cols_set;       // columns of a set: 16 * nt * across
   int grid;           // workgroups at most
+  int single;         // 1: a workgroup a unit
   int lds;            // bytes of LDS
 };
 // Workgroups of a CU, which is waves of a SIMD: by the registers of a lane (sums, a block's

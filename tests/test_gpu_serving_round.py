@@ -300,7 +300,7 @@ def test_binding_refusals_on_device_tensors():
         lambda: sv.spec_verify_attention(q, c, t, at, scale=float("nan")),
         lambda: sv.spec_verify_attention(q.repeat(1, 11, 1, 1), c, t, at),                      # 66 rows
         lambda: sv.spec_verify_attention(q, c, t, at, out=sv.AttentionOut(q, None)),
-        lambda: sv.spec_verify_attention(q, c, t, at, workspace=torch.zeros(256, dtype=torch.uint8, device="cuda")),
+        lambda: sv.spec_verify_attention(q, c, t.repeat(1, 20), at, workspace=torch.zeros(256, dtype=torch.uint8, device="cuda")),
         lambda: sv.spec_verify_rotate(q, None, at, torch.ones(33, dtype=torch.float64, device="cuda")),
         lambda: sv.spec_verify_rotate(q, None, at, s["freqs"], out=sv.RotateOut(q[:1].expand_as(q), None)),
         lambda: sv.spec_verify_adjust_logits(s["z"], tokens=s["ids"][:, :2].contiguous()),      # fewer than N - 1
