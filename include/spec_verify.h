@@ -550,7 +550,8 @@ int spec_verify_cache_read(const sv_cache* cache, const int32_t* page_table, int
  * Limits: 1 <= N <= 64, q_heads a multiple of the cache's heads (at most 4096 of them to one, SV_ESIZE
  * beyond), head_dim <= 256, window >= 0;
  * B * N * q_heads < 2^31 (SV_ESIZE beyond). The workspace holds the parts of requests that
- * several workgroups share; `tokens` is table_width * page_size. Up to 1024 tokens need none. */
+ * several workgroups share; `tokens` is table_width * page_size, or window + N + 31 where that is less
+ * (window not 0). Up to 1120 tokens need none. */
 #define SV_MAX_ROWS 64
 size_t spec_verify_attention_workspace_bytes(int32_t B, int32_t N, int32_t q_heads, int32_t heads,
                                              int32_t head_dim, int64_t tokens, sv_dtype dtype);

@@ -989,7 +989,10 @@ def spec_verify_attention(q, cache, page_table, kv_len, scale=None, window=0, ro
         lse = out.lse if out is not None else None
         if out is None and want_lse:
             lse = torch.empty((B, N, qh), dtype=torch.float32, device=dev)
-        ws, ws_bytes, keep = _space(workspace, _attention_space(B, N, qh, c.heads, D, width * c.page_size, dt), dev)
+        tokens = width * c.page_size
+        if 0 < window + N + 31 < tokens and window:
+            tokens = window + N + 31
+        ws, ws_bytes, keep = _space(workspace, _attention_space(B, N, qh, c.heads, D, tokens, dt), dev)
         rc = lib.spec_verify_attention(
             qp, qs, dt, B, N, qh, c, table, width, _vector(kv_len, "kv_len", torch.int32, (B,), dev),
             _vector(rows, "rows", torch.int32, (B,), dev), D ** -0.5 if scale is None else float(scale),

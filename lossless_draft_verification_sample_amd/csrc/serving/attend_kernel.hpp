@@ -29,8 +29,9 @@
 // over all units (request, cache head, set of columns), workgroup w takes blocks
 // T w / W .. T (w + 1) / W - 1. Units that several workgroups share leave their parts
 // (O, r, l) in the workspace, and a second kernel joins them in the order of the workgroups. Where
-// the page table has room for 1,024 tokens at most, a unit is one workgroup's, without workspace
-// or join, whose launch and room cost the host 5 us of 16 (%SINGLE%).
+// 1,120 tokens at most are in reach (page table or window), a unit is one workgroup's, without
+// workspace or join, whose launch and room cost the host 5 us of 16 (one token of one request over
+// 1,000: 16.9 -> 13.2 us; the kernels alone 13.5 and 13).
 #pragma once
 
 #include <math.h>
@@ -592,7 +593,7 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT)) void attend_
     if (more_segments) start();
 
     // the waves' parts joined, in the order of the waves
-    const AttendArgs& z = fresh_args();
+    const AttendArgs z = fresh_args();       // a copy: loaded once, whatever is stored
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       l[t] += __shfl_xor(l[t], 16, WAVE);
@@ -623,8 +624,8 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT)) void attend_
       for (int k = 0; k < DT; ++k) O[t][k] = mine == -INFINITY ? sf32x4{0, 0, 0, 0} : O[t][k] * f;
       if (turn == 0 && quad == 0) {
         const int col = (side * NT + t) * 16 + col16;
-        total[col][0] = M;
-        total[col][1] = L;
+        total[col][0] = 1.0f / L;
+        total[col][1] = (M + __log2f(L)) * 0.69314718055994530942f;
         if (!whole) {
           float* ml = part + (int64_t)z.s.cols_set * (BRICKS * 32);
           ml[2 * col] = M;
@@ -641,26 +642,36 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT)) void attend_
 #pragma unroll
         for (int t = 0; t < NT; ++t) sums[((wave * CH + k) * NT + t) * WAVE + lane] = O[t][d0 + k];
       __syncthreads();
-      for (int n = tid; n < across * CH * NT * WAVE; n += AT_THREADS) {
-        sf32x4 o = sums[n], more[AT_WAVES - 1];
+      constexpr int STEP = NT >= 3 || BRICKS >= 5 ? 1 : 2;       // items together, where registers are left
+      const int items = across * CH * NT * WAVE;
+      for (int n0 = tid; n0 < items; n0 += STEP * AT_THREADS) {
+        sf32x4 o[STEP], other[STEP][AT_WAVES - 1];
 #pragma unroll
-        for (int k = 1; k < AT_WAVES; ++k) more[k - 1] = sums[(k < along ? k * across * CH * NT * WAVE : 0) + n];
+        for (int m = 0; m < STEP; ++m) {
+          const int n = n0 + m * AT_THREADS < items ? n0 + m * AT_THREADS : n0;
+          o[m] = sums[n];
 #pragma unroll
-        for (int k = 1; k < AT_WAVES; ++k) o += k < along ? more[k - 1] : sf32x4{0, 0, 0, 0};
-        const int ln = n % WAVE, t = n / WAVE % NT, k = n / WAVE / NT % CH, sd = n / WAVE / NT / CH;
-        const int d = 16 * (d0 + k) + 4 * (ln >> 4), in_set = (sd * NT + t) * 16 + (ln & 15);
-        const int col = was_set * z.s.cols_set + in_set, j = row_of(z, col);
-        if (!whole) {
-          *(sf32x4*)(part + (int64_t)in_set * (BRICKS * 32) + d) = o;
-        } else if (col < z.s.cols && j < was_rows) {
-          const int head = was_h * z.group + col - j * z.group;
-          const int64_t to = was_b * z.os.b + j * z.os.n + (int64_t)head * z.os.h + d;
-          const float M = total[in_set][0], L = total[in_set][1];
-          o *= 1.0f / L;
-          if constexpr (F32) put4((float*)z.out + to, o, z.c.D - d);
-          else put4((uint16_t*)z.out + to, o, z.c.D - d);
-          if (z.lse && d == 0)
-            z.lse[((int64_t)was_b * z.t.N + j) * z.qh + head] = (M + __log2f(L)) * 0.69314718055994530942f;
+          for (int k = 1; k < AT_WAVES; ++k) other[m][k - 1] = sums[(k < along ? k * items : 0) + n];
+        }
+#pragma unroll
+        for (int m = 0; m < STEP; ++m) {
+          const int n = n0 + m * AT_THREADS;
+          if (STEP > 1 && n >= items) break;
+#pragma unroll
+          for (int k = 1; k < AT_WAVES; ++k) o[m] += k < along ? other[m][k - 1] : sf32x4{0, 0, 0, 0};
+          const int ln = n % WAVE, t = n / WAVE % NT, k = n / WAVE / NT % CH, sd = n / WAVE / NT / CH;
+          const int d = 16 * (d0 + k) + 4 * (ln >> 4), in_set = (sd * NT + t) * 16 + (ln & 15);
+          const int col = was_set * z.s.cols_set + in_set, j = row_of(z, col);
+          if (!whole) {
+            *(sf32x4*)(part + (int64_t)in_set * (BRICKS * 32) + d) = o[m];
+          } else if (col < z.s.cols && j < was_rows) {
+            const int head = was_h * z.group + col - j * z.group;
+            const int64_t to = was_b * z.os.b + j * z.os.n + (int64_t)head * z.os.h + d;
+            o[m] *= total[in_set][0];
+            if constexpr (F32) put4((float*)z.out + to, o[m], z.c.D - d);
+            else put4((uint16_t*)z.out + to, o[m], z.c.D - d);
+            if (z.lse && d == 0) z.lse[((int64_t)was_b * z.t.N + j) * z.qh + head] = total[in_set][1];
+          }
         }
       }
       __syncthreads();

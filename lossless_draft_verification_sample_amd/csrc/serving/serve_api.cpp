@@ -18,7 +18,7 @@ constexpr int64_t MAX_TOKENS = 1 << 30;
 constexpr int MAX_PAGE = 65536;
 constexpr int MAX_GROUP = 4096;    // query heads that share a cache head
 constexpr int CUS = 256;
-constexpr int SINGLE_TOKENS = 1024;   // of a page table: a workgroup takes all blocks of a unit
+constexpr int SINGLE_TOKENS = 1120;   // in reach: a workgroup takes all blocks of a unit
 
 size_t align_up(size_t x) { return (x + WS_ALIGN - 1) / WS_ALIGN * WS_ALIGN; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -253,7 +253,9 @@ int spec_verify_attention(const void* q, sv_strides q_strides, sv_dtype dtype, i
   if (!aligned(q, es) || !aligned(out, es) || !aligned(out_lse, 4) || !readable(q_strides, B, N, q_heads) ||
       !writable(out_strides, B, N, q_heads, a.c.D) || q == out)
     return SV_EINVAL;
-  if (!attend_shape(B, N, q_heads, a.c.heads, a.c.D, a.t.capacity, dtype, &a.s)) return SV_ESIZE;
+  const int64_t reach = (int64_t)window + N + sv::CACHE_BLOCK - 1;     // with the first block's rest
+  const int64_t tokens = window && reach < a.t.capacity ? reach : a.t.capacity;
+  if (!attend_shape(B, N, q_heads, a.c.heads, a.c.D, tokens, dtype, &a.s)) return SV_ESIZE;
   const AttendSpace w = attend_space(a.s, B, a.c.heads, a.c.D);
   if (w.total && (!workspace || !aligned(workspace, WS_ALIGN) || workspace_bytes < w.total)) return SV_EWORKSPACE;
   a.q = q;

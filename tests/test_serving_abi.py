@@ -110,16 +110,16 @@ def test_attention_refusals(lib):
         assert _attend(lib, **kw) == L.SV_EINVAL, kw
     assert _attend(lib, dtype=2) == L.SV_EDTYPE and _attend(lib, width=2 ** 25) == L.SV_ESIZE
     assert _attend(lib, B=2 ** 30, os=_st(384, 128, 32)) == L.SV_ESIZE
-    need = lib.spec_verify_attention_workspace_bytes(2, 3, 4, 2, 32, 17 * 64, 1)
-    assert need > 0 and need % 256 == 0 and lib.spec_verify_attention_workspace_bytes(2, 3, 4, 2, 32, 16 * 64, 1) == 0
+    need = lib.spec_verify_attention_workspace_bytes(2, 3, 4, 2, 32, 18 * 64, 1)
+    assert need > 0 and need % 256 == 0 and lib.spec_verify_attention_workspace_bytes(2, 3, 4, 2, 32, 17 * 64, 1) == 0
     for kw in (dict(), dict(ws=FAKE, ws_bytes=need - 1), dict(ws=FAKE + 8, ws_bytes=need)):
-        assert _attend(lib, width=17, **kw) == L.SV_EWORKSPACE, kw
+        assert _attend(lib, width=18, **kw) == L.SV_EWORKSPACE, kw
     size = lib.spec_verify_attention_workspace_bytes
     for bad in ((0, 3, 4, 2, 32, 128, 1), (2, 65, 4, 2, 32, 128, 1), (2, 3, 3, 2, 32, 128, 1), (2, 3, 4, 2, 257, 128, 1),
                 (2, 3, 4, 2, 32, 0, 1), (2, 3, 4, 2, 32, 2 ** 31, 1), (2, 3, 4, 2, 32, 128, 5)):
         assert size(*bad) == 0, bad
     # what few tokens need is small, and the most is bounded whatever the batch's lengths
-    assert size(1, 1, 32, 8, 128, 1025, 1) < 2 ** 22
+    assert size(1, 1, 32, 8, 128, 1121, 1) < 2 ** 22
     for N in (1, 9, 64):
         for heads in (1, 8):
             for D in (64, 128, 256):
