@@ -465,9 +465,9 @@ def _written(out):
     """Tells autograd that a caller's outputs were written, as an operation in place would:
     a backward pass that had saved one of them (logits that were overwritten by their
     gradient) then raises instead of using what it holds now."""
-    for t in out or ():
-        if t is not None:
-            _torch().autograd.graph.increment_version(t)
+    given = [t for t in out or () if t is not None]
+    if given:
+        _torch().autograd.graph.increment_version(given)
 
 
 def spec_verify_top_logits_workspace_bytes(R, V, K, dtype=SV_BF16):

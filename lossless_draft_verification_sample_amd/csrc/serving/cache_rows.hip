@@ -22,10 +22,20 @@
 namespace sv {
 namespace {
 
-constexpr int NTH = 256;
-constexpr int MAX_CHUNKS = CACHE_MAX_D / 32 * 64 / NTH;               // 16 bytes of codes, a thread
-constexpr int MAX_UNITS = CACHE_BLOCK * CACHE_MAX_D / 8 / NTH;        // 8 dimensions of a row, a thread
-constexpr int ROW_BYTES = CACHE_MAX_D + 8;
+// A round of few rows is bound by how many waves are started, most of them for little: where the
+// rows can touch at most FEW_BLOCKS blocks, a workgroup takes all of a request's, one after
+// the other (most requests touch one less than the most), and has two waves up to 128 dimensions. (A
+// write for 128 requests of nine rows and eight heads with a workgroup a block and four waves:
+// 14.8 us, now 11.3; prompts of 4,096 rows with two waves 31.0 us instead of 29.3.)
+constexpr int FEW_BLOCKS = 4;
+constexpr bool wide(int bricks) { return bricks > 4; }
+template <bool FEW, bool WIDE>
+struct Shape {
+  static constexpr int NTH = FEW && !WIDE ? 128 : 256, MAX_D = WIDE ? 256 : 128;
+  static constexpr int CHUNKS = MAX_D / 32 * 64 / NTH;          // 16 bytes of codes, a thread
+  static constexpr int UNITS = CACHE_BLOCK * MAX_D / 8 / NTH;   // 8 dimensions of a row, a thread
+};
+int blocks_of_wg(const CacheRowsArgs& a) { return a.blocks <= FEW_BLOCKS ? a.blocks : 1; }
 
 struct Where {
   int b, h, block;
@@ -40,8 +50,12 @@ __device__ __forceinline__ Where where(const CacheRowsArgs& a) {
   i /= a.c.heads;
   w.values = kinds == 2 ? i % 2 : a.which == 2;
   i /= kinds;
-  w.block = i % a.blocks;
-  w.b = i / a.blocks;
+  w.block = 0;
+  w.b = i;
+  if (a.blocks > FEW_BLOCKS) {
+    w.block = i % a.blocks;
+    w.b = i / a.blocks;
+  }
   return w;
 }
 
@@ -80,15 +94,11 @@ __device__ __forceinline__ su32x4 bytes_within(bool values, int chunk, int D) {
   return su32x4{a, a, b, b};
 }
 
-template <typename E>
-__global__ __launch_bounds__(NTH) void write_kernel(CacheRowsArgs a) {
-  __shared__ __attribute__((aligned(16))) uint8_t fresh[CACHE_BLOCK][ROW_BYTES];   // new codes, row by row
-  __shared__ float top[NTH / WAVE];
-  const Where w = where(a);
-  const Span s = span_of(a.t, w.b);
-  if (s.bad || s.rows == 0) return;
-  const int end = s.first + s.rows, t0 = (s.first / CACHE_BLOCK + w.block) * CACHE_BLOCK;
-  if (t0 >= end) return;
+template <typename E, bool FEW, bool WIDE>
+__device__ __forceinline__ void write_block(const CacheRowsArgs& a, const Where& w, const Span& s, int t0,
+                                            uint8_t (*fresh)[Shape<FEW, WIDE>::MAX_D + 8], float* top) {
+  constexpr int NTH = Shape<FEW, WIDE>::NTH, MAX_CHUNKS = Shape<FEW, WIDE>::CHUNKS, MAX_UNITS = Shape<FEW, WIDE>::UNITS;
+  const int end = s.first + s.rows;
   const int blk = t0 / CACHE_BLOCK, in_page = blk & ((1 << a.c.per_log2) - 1);
   const int page = a.t.table[(int64_t)w.b * a.t.width + (blk >> a.c.per_log2)];
   const int tid = threadIdx.x;
@@ -213,17 +223,25 @@ __global__ __launch_bounds__(NTH) void write_kernel(CacheRowsArgs a) {
   if (tid == 0) *scale = new_scale;
 }
 
-template <typename E>
-__global__ __launch_bounds__(NTH) void read_kernel(CacheRowsArgs a) {
-  __shared__ uint8_t block[CACHE_MAX_D / 32 * BRICK];
+template <typename E, bool FEW, bool WIDE>
+__global__ __launch_bounds__((Shape<FEW, WIDE>::NTH)) void write_kernel(CacheRowsArgs a) {
+  using S = Shape<FEW, WIDE>;
+  __shared__ __attribute__((aligned(16))) uint8_t fresh[CACHE_BLOCK][S::MAX_D + 8];   // new codes, row by row
+  __shared__ float top[S::NTH / WAVE];
   const Where w = where(a);
-  Span s = span_of(a.t, w.b);
-  if (s.bad) {
-    s.first = 0;
-    s.rows = a.t.N;
+  const Span s = span_of(a.t, w.b);
+  if (s.bad || s.rows == 0) return;
+  for (int t0 = (s.first / CACHE_BLOCK + w.block) * CACHE_BLOCK; t0 < s.first + s.rows; t0 += CACHE_BLOCK) {
+    write_block<E, FEW, WIDE>(a, w, s, t0, fresh, top);
+    if (!FEW) return;
+    __syncthreads();
   }
-  const int end = s.first + s.rows, t0 = (s.first / CACHE_BLOCK + w.block) * CACHE_BLOCK;
-  if (t0 >= end) return;
+}
+
+template <typename E, bool FEW, bool WIDE>
+__device__ __forceinline__ void read_block(const CacheRowsArgs& a, const Where& w, const Span& s, int t0, uint8_t* block) {
+  constexpr int NTH = Shape<FEW, WIDE>::NTH;
+  const int end = s.first + s.rows;
   const int blk = t0 / CACHE_BLOCK, in_page = blk & ((1 << a.c.per_log2) - 1), tid = threadIdx.x;
   const int page = s.bad ? -1 : a.t.table[(int64_t)w.b * a.t.width + (blk >> a.c.per_log2)];
   const bool known = (uint32_t)page < (uint32_t)a.c.pages;
@@ -276,24 +294,47 @@ __global__ __launch_bounds__(NTH) void read_kernel(CacheRowsArgs a) {
   }
 }
 
+template <typename E, bool FEW, bool WIDE>
+__global__ __launch_bounds__((Shape<FEW, WIDE>::NTH)) void read_kernel(CacheRowsArgs a) {
+  __shared__ __attribute__((aligned(16))) uint8_t block[Shape<FEW, WIDE>::MAX_D / 32 * BRICK];
+  const Where w = where(a);
+  Span s = span_of(a.t, w.b);
+  if (s.bad) {
+    s.first = 0;
+    s.rows = a.t.N;
+  }
+  for (int t0 = (s.first / CACHE_BLOCK + w.block) * CACHE_BLOCK; t0 < s.first + s.rows; t0 += CACHE_BLOCK) {
+    read_block<E, FEW, WIDE>(a, w, s, t0, block);
+    if (!FEW) return;
+    __syncthreads();
+  }
+}
+
 int64_t grid_of(const CacheRowsArgs& a) {
-  return (int64_t)a.t.B * a.blocks * a.c.heads * (a.which == 3 ? 2 : 1);
+  return (int64_t)a.t.B * (a.blocks / blocks_of_wg(a)) * a.c.heads * (a.which == 3 ? 2 : 1);
+}
+
+template <bool WRITE, typename E, bool FEW, bool WIDE>
+int launch(const CacheRowsArgs& a, hipStream_t st) {
+  const dim3 grid((uint32_t)grid_of(a)), threads(Shape<FEW, WIDE>::NTH);
+  if constexpr (WRITE) write_kernel<E, FEW, WIDE><<<grid, threads, 0, st>>>(a);
+  else read_kernel<E, FEW, WIDE><<<grid, threads, 0, st>>>(a);
+  return hipGetLastError() != hipSuccess;
+}
+template <bool WRITE, typename E>
+int launch(const CacheRowsArgs& a, hipStream_t st) {
+  if (a.blocks <= FEW_BLOCKS)
+    return wide(a.c.bricks) ? launch<WRITE, E, true, true>(a, st) : launch<WRITE, E, true, false>(a, st);
+  return wide(a.c.bricks) ? launch<WRITE, E, false, true>(a, st) : launch<WRITE, E, false, false>(a, st);
+}
+template <bool WRITE>
+int launch(const CacheRowsArgs& a, hipStream_t st) {
+  return a.bf16 ? launch<WRITE, uint16_t>(a, st) : launch<WRITE, float>(a, st);
 }
 
 }  // namespace
 
-int launch_cache_write(const CacheRowsArgs& a, hipStream_t st) {
-  const dim3 grid((uint32_t)grid_of(a));
-  if (a.bf16) write_kernel<uint16_t><<<grid, NTH, 0, st>>>(a);
-  else write_kernel<float><<<grid, NTH, 0, st>>>(a);
-  return hipGetLastError() != hipSuccess;
-}
-
-int launch_cache_read(const CacheRowsArgs& a, hipStream_t st) {
-  const dim3 grid((uint32_t)grid_of(a));
-  if (a.bf16) read_kernel<uint16_t><<<grid, NTH, 0, st>>>(a);
-  else read_kernel<float><<<grid, NTH, 0, st>>>(a);
-  return hipGetLastError() != hipSuccess;
-}
+int launch_cache_write(const CacheRowsArgs& a, hipStream_t st) { return launch<true>(a, st); }
+int launch_cache_read(const CacheRowsArgs& a, hipStream_t st) { return launch<false>(a, st); }
 
 }  // namespace sv
