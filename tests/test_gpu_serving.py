@@ -314,12 +314,15 @@ def _attend_tol(want, lse, size, reach, most, tokens, D, dtype):
     return far + HALF[dtype] * (np.abs(want) + far), score + (70 + tokens / 16) * U + U * np.abs(lse)
 
 
-def _check_attend(rng, lens, rows, N, qh, H, D, page, dtype, window=0, how="plain", scale=None, size=1.0, lens_after=None):
-    """lens: tokens before the rows."""
+def _check_attend(rng, lens, rows, N, qh, H, D, page, dtype, window=0, how="plain", scale=None, size=1.0, lens_after=None,
+                  capacity=0):
+    """lens: tokens before the rows. capacity: tokens that the table has room for at least; beyond the requests' pages it
+    names none, and nothing is read there. Over 1,120 of them (or of the window) workgroups share the requests' blocks."""
     import torch
     B = len(lens)
     count = [N] * B if rows is None else rows
     cache, table, keys, vals = _filled(rng, [a + n for a, n in zip(lens, count)], H, D, page, size=size)
+    table = np.pad(table, ((0, 0), (0, max(0, -(-capacity // page) - table.shape[1]))), constant_values=-1)
     q, qx = _rows(rng, (B, N, qh, D), dtype, how)
     s = D ** -0.5 if scale is None else scale
     out = _sv().AttentionOut(torch.full((B, N, qh, D), 9.0, dtype=_type(dtype), device="cuda"),
@@ -354,6 +357,52 @@ def test_attention_rows(dtype, N, qh, H, D):
     """One tile of columns to many sets of them; requests without rows among others."""
     rng = np.random.default_rng(N * 100 + qh + D)
     _check_attend(rng, [0, 40, 300, 5, 77], [N, (N + 1) // 2, N, 0, 1], N, qh, H, D, 64, dtype, how="fused")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,qh,H,D", [(1, 1, 1, 1), (3, 6, 6, 80), (3, 3, 3, 31), (2, 2, 1, 256), (4, 5, 1, 160), (3, 7, 1, 224), (9, 8, 2, 128),
+                                      (9, 16, 2, 64), (17, 4, 1, 128), (33, 4, 1, 96), (64, 8, 1, 128), (64, 8, 1, 256),
+                                      (64, 3, 3, 64), (16, 4, 1, 256), (64, 16, 2, 33)])
+def test_attention_shared_rows(dtype, N, qh, H, D):
+    """Long tables, so that requests' blocks are shared out over workgroups and joined, with short requests in them."""
+    rng = np.random.default_rng(N * 100 + qh + D)
+    _check_attend(rng, [0, 40, 300, 1800, 0], [N, max(1, N // 2), N, N, 0], N, qh, H, D, 64, dtype, how="fused", capacity=5000)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("window", [1200, 1500, 2048, 100000, 2 ** 31 - 1])
+def test_attention_shared_windows(dtype, window):
+    rng = np.random.default_rng(window % 97)
+    _check_attend(rng, [0, 5, 1199, 1200, 1231, 4000, 2047], [9, 9, 9, 0, 9, 9, 1], 9, 8, 2, 64, 32, dtype, window=window, capacity=6000)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale,size", [(0.0, 1.0), (-0.5, 1.0), (3.0, 4.0)])
+def test_attention_shared_scales(dtype, scale, size):
+    rng = np.random.default_rng(77)
+    _check_attend(rng, [1500, 3, 700], None, 5, 8, 2, 128, 32, dtype, scale=scale, size=size, capacity=2000)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_shared_is_the_answer_of_a_workgroup_a_request(dtype):
+    """The same call through a table of 1,088 tokens and one of 4,096: within each one's own tolerance of the formula, and rows
+    and requests that are out of range alike."""
+    import torch
+    rng = np.random.default_rng(78)
+    cache, table, keys, vals = _filled(rng, [1088, 500, 64, 40, 1088], 2, 64, 32)
+    table[2, 1] = 10 ** 6
+    q, qx = _rows(rng, (5, 4, 4, 64), dtype)
+    lens, count = [1084, 496, 60, -1, 5000], [4, 4, 4, 4, 4]
+    got = [_sv().spec_verify_attention(q, cache, _dev(np.pad(table, ((0, 0), (0, w)), constant_values=-1)), _ints(lens), rows=_ints(count),
+                                        want_lse=True)
+           for w in (0, 94)]
+    torch.cuda.synchronize()
+    for g in got:
+        for b in range(2):
+            want, lse, sizes, reach, most = os_.attention(qx[b], keys[b, :lens[b] + 4], vals[b, :lens[b] + 4], lens[b], 64 ** -0.5)
+            tol, ltol = _attend_tol(want, lse, sizes, reach, most, lens[b] + 4, 64, dtype)
+            assert np.all(np.abs(_host(g.out[b]) - want) <= tol) and np.all(np.abs(_host(g.lse[b]) - lse) <= ltol)
+        assert torch.isnan(g.out[2:].float()).all() and torch.isnan(g.lse[2:]).all()
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
