@@ -449,7 +449,8 @@ int spec_verify_linear_ce_backward(const void* hidden, int64_t hidden_stride, co
  *     nothing kept between calls, separate ones for calls that may run concurrently. */
 
 /* Element strides of a [B][N][heads][D] tensor whose D elements are consecutive. Inputs may
- * take any strides >= 0; rows and heads of outputs must not overlap. */
+ * take any strides >= 0; rows and heads of outputs must not overlap, and
+ * each is stepped over whole by the next wider stride (dimensions in any order). */
 typedef struct {
   int64_t request, row, head;
 } sv_strides;
@@ -514,12 +515,12 @@ size_t spec_verify_cache_bytes(int32_t pages, int32_t heads, int32_t page_size, 
  * float32 does not hold, are stored as 240 * 2^120. Slots behind the last new row keep their bytes.
  *   k, v        [B][N][cache heads][head_dim] of dtype at any strides.
  *   page_table  [B][table_width] int32. A row whose page lies outside [0, pages) is not written.
- *               A block may be written through one request only: requests that share pages
- *               must own the block they write into.
+ *               A block may be written at one position only: requests that share pages must own
+ *               the block they write into, and a page stands in a table once.
  * A request is out of range (nothing written) when kv_len[b] < 0, rows[b] is not in 0..N, or
  * kv_len[b] + rows[b] > table_width * page_size.
- * Limits: 1 <= head_dim <= 256, table_width * page_size <= 2^30, 2^31 workgroup threads
- * (SV_ESIZE beyond). */
+ * Limits: 1 <= head_dim <= 256; table_width * page_size <= 2^30, N <= 2^30 and
+ * B * heads * ceil((N + 31) / 32) < 2^22 (SV_ESIZE beyond). */
 int spec_verify_cache_write(const sv_cache* cache, const int32_t* page_table, int32_t table_width,
                             const int32_t* kv_len, const int32_t* rows, const void* k,
                             sv_strides k_strides, const void* v, sv_strides v_strides,
@@ -527,8 +528,8 @@ int spec_verify_cache_write(const sv_cache* cache, const int32_t* page_table, in
 
 /* Reads positions first[b] .. first[b] + rows[b] - 1 (first NULL: from 0) back: scale * code,
  * rounded once to dtype. out_k, out_v [B][N][heads][head_dim]; either may be NULL, not both.
- * Positions in a page outside [0, pages) read as NaN; a request is out of range as in
- * spec_verify_cache_write. */
+ * Positions in a page outside [0, pages) read as NaN; a request is out of range, and sizes are
+ * limited, as in spec_verify_cache_write. */
 int spec_verify_cache_read(const sv_cache* cache, const int32_t* page_table, int32_t table_width,
                            const int32_t* first, const int32_t* rows, void* out_k,
                            sv_strides k_strides, void* out_v, sv_strides v_strides, sv_dtype dtype,
@@ -540,7 +541,8 @@ int spec_verify_cache_read(const sv_cache* cache, const int32_t* page_table, int
  * up to p):
  *   out = sum_t softmax_t(scale q . k_t) v_t,   out_lse = log sum_t exp(scale q . k_t).
  *   q        [B][N][q_heads][head_dim] of dtype at any strides; scale finite.
- *   out      like q, of dtype, at its strides; out_lse [B][N][q_heads] float, or NULL.
+ *   out      like q, of dtype, at its strides, over no part of q; out_lse [B][N][q_heads] float, or
+ *            NULL.
  * bfloat16: products of q and k are exact, probabilities enter their product with v as float16
  * (off by 2^-12, and 2^-25 of the largest), and blocks whose v_scale lies 2^-60 below another's of
  * the request lose precision; float32: q and the probabilities as three bfloat16 parts.
@@ -548,8 +550,9 @@ int spec_verify_cache_read(const sv_cache* cache, const int32_t* page_table, int
  * page outside [0, pages) is NaN; pages that no row of the request sees (all before its window)
  * are not read. Requests out of range as in spec_verify_cache_write.
  * Limits: 1 <= N <= 64, q_heads a multiple of the cache's heads (at most 4096 of them to one, SV_ESIZE
- * beyond), head_dim <= 256, window >= 0;
- * B * N * q_heads < 2^31 (SV_ESIZE beyond). The workspace holds the parts of requests that
+ * beyond), head_dim <= 256, window >= 0; B * N * q_heads < 2^31 (SV_ESIZE beyond) and, with the
+ * N * q_heads / heads columns of a cache head counted in tiles of 16, a launch of B * heads * tiles: up
+ * to 2^19 always, SV_ESIZE where they take more than 2^23 workgroups. The workspace holds the parts of requests that
  * several workgroups share; `tokens` is table_width * page_size, or window + N + 31 where that is less
  * (window not 0). Up to 1120 tokens need none. */
 #define SV_MAX_ROWS 64

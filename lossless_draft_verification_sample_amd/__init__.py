@@ -82,13 +82,13 @@ def _torch():
     return _TORCH
 
 
-def _dtype_code(t):
+def _dtype_code(t, name="logits"):
     torch = _torch()
     if t.dtype == torch.bfloat16:
         return SV_BF16
     if t.dtype == torch.float32:
         return SV_F32
-    raise TypeError(f"logits must be bfloat16 or float32, got {t.dtype}")
+    raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
 
 
 def _dev_ptr(t, name, dtype=None):
@@ -820,7 +820,7 @@ def spec_verify_rotate(q, k, kv_len, freqs, interleaved=False, scale=1.0, invers
     torch = _torch()
     lib = lib or _lib.load()
     qp, qs = _rows4(q, "q")
-    dt, dev, (B, N, qh, D) = _dtype_code(q), q.device, q.shape
+    dt, dev, (B, N, qh, D) = _dtype_code(q, "q"), q.device, q.shape
     kp, ks, kh = None, _NO_STRIDES, 0
     if k is not None:
         kh = k.shape[2] if k.dim() == 4 else 0
@@ -892,7 +892,7 @@ def spec_verify_cache_write(cache, page_table, kv_len, k, v, rows=None, stream=N
     torch = _torch()
     lib = lib or _lib.load()
     kp, ks = _rows4(k, "k")
-    dt, dev, (B, N, heads, D) = _dtype_code(k), k.device, k.shape
+    dt, dev, (B, N, heads, D) = _dtype_code(k, "k"), k.device, k.shape
     vp, vs = _rows4(v, "v", dev, k.dtype, k.shape)
     c = _cache(cache, dev)
     if (heads, D) != (c.heads, c.head_dim):
@@ -944,7 +944,7 @@ def spec_verify_cache_read(cache, page_table, first, N, dtype=None, rows=None, o
         vp, vs = (None, _NO_STRIDES) if out.v is None else _rows4(out.v, "out.v", dev, one.dtype, shape)
         rc = lib.spec_verify_cache_read(
             c, table, width, _vector(first, "first", torch.int32, (B,), dev),
-            _vector(rows, "rows", torch.int32, (B,), dev), kp, ks, vp, vs, _dtype_code(one), B, int(N),
+            _vector(rows, "rows", torch.int32, (B,), dev), kp, ks, vp, vs, _dtype_code(one, "out"), B, int(N),
             handle)
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_verify_cache_read")
@@ -976,7 +976,7 @@ def spec_verify_attention(q, cache, page_table, kv_len, scale=None, window=0, ro
     torch = _torch()
     lib = lib or _lib.load()
     qp, qs = _rows4(q, "q")
-    dt, dev, (B, N, qh, D) = _dtype_code(q), q.device, q.shape
+    dt, dev, (B, N, qh, D) = _dtype_code(q, "q"), q.device, q.shape
     c = _cache(cache, dev)
     if D != c.head_dim:
         raise ValueError(f"q must have heads of {c.head_dim}, got {tuple(q.shape)}")

@@ -16,17 +16,17 @@ constexpr int JOIN_THREADS = 256, JOIN_AHEAD = 8;
 // reads are a chain). Units of one workgroup end at once.
 template <bool F32>
 __global__ __launch_bounds__(JOIN_THREADS) void join_kernel(AttendArgs a) {
-  const int per = (a.s.cols_set + a.join_cols - 1) / a.join_cols, tid = threadIdx.x;
+  const int per = (a.s.cols_set + a.s.join_cols - 1) / a.s.join_cols, tid = threadIdx.x;
   const int unit = blockIdx.x / per, slice = blockIdx.x - unit * per;
   const int uh = unit / a.s.sets, set = unit - uh * a.s.sets, b = uh / a.c.heads, h = uh - b * a.c.heads;
   const int w0 = a.record[2 * unit], count = a.record[2 * unit + 1];   // only if it has blocks
   const Reach r = reach_of(a, b);
   if (r.blocks == 0 || count <= 1) return;
-  const int c0 = slice * a.join_cols, dp = a.c.bricks * 32, quads = dp / 4;
+  const int c0 = slice * a.s.join_cols, dp = a.c.bricks * 32, quads = dp / 4;
   const int64_t size = (int64_t)a.s.cols_set * (dp + 2), head = (int64_t)a.s.cols_set * dp;
   // the first workgroup's part holds the unit's start: the other of its two
   const float* parts = a.partial + (int64_t)w0 * 2 * size;
-  for (int i = tid; i < a.join_cols * quads; i += JOIN_THREADS) {
+  for (int i = tid; i < a.s.join_cols * quads; i += JOIN_THREADS) {
     const int c = c0 + i / quads, d = 4 * (i % quads), col = set * a.s.cols_set + c, j = row_of(a, col);
     if (c >= a.s.cols_set || col >= a.s.cols || j >= r.rows) return;
     float M = -INFINITY, L = 0.0f;
@@ -75,7 +75,7 @@ int launch_attend_bf16(const AttendArgs& a, hipStream_t st) { return launch_atte
 int launch_attend(const AttendArgs& a, hipStream_t st) {
   if (a.bf16 ? launch_attend_bf16(a, st) : launch_attend_f32(a, st)) return 1;
   if (a.s.single) return 0;
-  const int per = (a.s.cols_set + a.join_cols - 1) / a.join_cols;
+  const int per = (a.s.cols_set + a.s.join_cols - 1) / a.s.join_cols;
   const dim3 grid((uint32_t)((int64_t)a.t.B * a.c.heads * a.s.sets * per));
   if (a.bf16) join_kernel<false><<<grid, JOIN_THREADS, 0, st>>>(a);
   else join_kernel<true><<<grid, JOIN_THREADS, 0, st>>>(a);

@@ -362,7 +362,7 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT)) void attend_
     bool settled = false;                                // every column has one
     // What the sums are relative to: 2^(eref - 127), near the scales of the values; the largest yet.
     int eref = (int)(__float_as_uint(vs_next) >> 23 & 255) + 2;
-    if (F32 || eref <= 2 || eref > 250) eref = 127;
+    if (F32 || lost_next || eref <= 2 || eref > 250) eref = 127;
     int etop = eref;
     int last[NT];                                        // the last position a column sees
     const int col0 = (set * across + side) * NT * 16;    // this wave's first column
@@ -372,7 +372,7 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT)) void attend_
       for (int k = 0; k < DT; ++k) O[t][k] = sf32x4{0, 0, 0, 0};
       l[t] = 0.0f;
       sub[t] = AT_NONE;
-      last[t] = r.first + row_of(a, col0 + t * 16 + col16);
+      last[t] = r.bad ? 0 : r.first + row_of(a, col0 + t * 16 + col16);   // bad: position 0 is NaN to all
     }
     const int end = r.first + r.rows;
     const int open0 = a.window ? end - a.window : 0;     // from here to r.first all rows see all
@@ -384,8 +384,8 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT)) void attend_
       if constexpr (NT * BRICKS * QP > 8) asm volatile("" ::: "memory");
       const int t0 = (r.block0 + i) * CACHE_BLOCK;
       ks = ks_next * scale2;
-      vs = vs_next;
       lost = lost_next;
+      vs = lost ? 1.0f : vs_next;                        // the scale read then is another block's, or nobody's
       // some row does not see some token here, or the page is unknown
       const bool edge = t0 + CACHE_BLOCK - 1 > r.first || t0 < open0 || lost;
       const int64_t here = at;

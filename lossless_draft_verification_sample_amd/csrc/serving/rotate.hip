@@ -87,11 +87,11 @@ __device__ __forceinline__ su32x4 close16(const float (&x)[8]) {
 // after the other, of the rest of a head too where that is whole. Every thread asks for its
 // first MINE units before the angles are made.
 template <typename E, bool INTER>
-__global__ __launch_bounds__(NTH) void rotate_vec_kernel(RotateArgs a, int per_wg) {
+__global__ __launch_bounds__(NTH) void rotate_vec_kernel(RotateArgs a, int per_wg, int64_t base) {
   constexpr int W = 16 / (int)sizeof(E), MINE = 2;
   __shared__ __attribute__((aligned(16))) sf32x2 turn[MAX_R2];
   const int R2 = a.R / 2, tid = threadIdx.x;
-  const int64_t total = (int64_t)a.B * a.N, row0 = (int64_t)blockIdx.x * per_wg;
+  const int64_t total = (int64_t)a.B * a.N, row0 = base + (int64_t)blockIdx.x * per_wg;
   const int rows = (int)(total - row0 < per_wg ? total - row0 : per_wg);
   const int pairs = R2 / W, rest = a.D - a.R;
   const int copies = a.oq == a.q && a.ok == a.k && !a.rows ? 0 : (rest + 2 * W - 1) / (2 * W);
@@ -158,10 +158,10 @@ __global__ __launch_bounds__(NTH) void rotate_vec_kernel(RotateArgs a, int per_w
 
 // Any other R: a pair a unit, then the rest element by element.
 template <typename E, bool INTER>
-__global__ __launch_bounds__(NTH) void rotate_any_kernel(RotateArgs a, int per_wg) {
+__global__ __launch_bounds__(NTH) void rotate_any_kernel(RotateArgs a, int per_wg, int64_t base) {
   __shared__ sf32x2 turn[MAX_R2];
   const int R2 = a.R / 2;
-  const int64_t total = (int64_t)a.B * a.N, row0 = (int64_t)blockIdx.x * per_wg;
+  const int64_t total = (int64_t)a.B * a.N, row0 = base + (int64_t)blockIdx.x * per_wg;
   const int rows = (int)(total - row0 < per_wg ? total - row0 : per_wg);
   make_turns(a, turn, row0, rows);
   __syncthreads();
@@ -195,10 +195,15 @@ int launch(const RotateArgs& a, hipStream_t st) {
   if (R2 && per > MAX_R2 / R2) per = MAX_R2 / R2;
   if (per > 8) per = 8;
   if (per < 1) per = 1;
-  const int grid = (int)((total + per - 1) / per);
-  if (vec) rotate_vec_kernel<E, INTER><<<grid, NTH, 0, st>>>(a, (int)per);
-  else rotate_any_kernel<E, INTER><<<grid, NTH, 0, st>>>(a, (int)per);
-  return hipGetLastError() != hipSuccess;
+  // a launch has fewer than 2^32 threads, so rows without end take several
+  for (int64_t base = 0; base < total; base += per << 22) {
+    const int64_t left = (total - base + per - 1) / per;
+    const int grid = (int)(left < 1 << 22 ? left : 1 << 22);
+    if (vec) rotate_vec_kernel<E, INTER><<<grid, NTH, 0, st>>>(a, (int)per, base);
+    else rotate_any_kernel<E, INTER><<<grid, NTH, 0, st>>>(a, (int)per, base);
+    if (hipGetLastError() != hipSuccess) return 1;
+  }
+  return 0;
 }
 
 }  // namespace

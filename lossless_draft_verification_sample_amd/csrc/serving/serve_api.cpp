@@ -110,7 +110,7 @@ int cache_rows(const sv_cache* cache, const int32_t* table, int32_t width, const
   a->which = (k ? 1 : 0) | (v ? 2 : 0);
   a->bf16 = dtype == SV_BF16;
   // rows that start at a block's last token touch one block more
-  a->blocks = (int)ceil_div((int64_t)N + sv::CACHE_BLOCK - 1, sv::CACHE_BLOCK);
+  a->blocks = (int)ceil_div((int64_t)N + sv::CACHE_BLOCK - 1, sv::CACHE_BLOCK);    // N <= 2^30
   if ((double)B * a->blocks * H * 2 >= MAX_WORKGROUPS) return SV_ESIZE;
   return SV_OK;
 }
@@ -135,7 +135,12 @@ bool attend_shape(int64_t B, int64_t N, int64_t qh, int64_t heads, int64_t D, in
       if (nt > nt_most || nt * across > most) continue;
       const int64_t units = B * heads * sets;
       const int64_t cols_set = 16 * nt * across;
-      if ((double)units * cols_set >= MAX_WORKGROUPS) return false;
+      // columns of a workgroup of the join: three items a thread, one where the units are few
+      int64_t join = cols_set;
+      while (join > 1 && join * bricks * 8 > ((double)units * ceil_div(cols_set, join) < 4 * CUS ? 256 : 768))
+        join = (join + 1) / 2;
+      if ((double)units * ceil_div(cols_set, join) >= MAX_WORKGROUPS) return false;
+      s->join_cols = (int)join;
       s->cols = (int)cols;
       s->nt = (int)nt;
       s->across = (int)across;
@@ -145,7 +150,6 @@ bool attend_shape(int64_t B, int64_t N, int64_t qh, int64_t heads, int64_t D, in
       s->lds = (int)(q > sums ? q : sums);
       s->single = tokens <= SINGLE_TOKENS;
       if (s->single) {
-        if (units >= MAX_WORKGROUPS) return false;
         s->grid = (int)units;
         return true;
       }
@@ -270,12 +274,6 @@ int spec_verify_attention(const void* q, sv_strides q_strides, sv_dtype dtype, i
   a.window = window;
   a.bf16 = dtype == SV_BF16;
   a.scale2 = (float)((double)scale * M_LOG2E);
-  // columns of a workgroup of the join: three items a thread, one where the units are few
-  const int64_t units = (int64_t)B * a.c.heads * a.s.sets;
-  a.join_cols = a.s.cols_set;
-  while (a.join_cols > 1 &&
-         a.join_cols * a.c.bricks * 8 > (units * ceil_div(a.s.cols_set, a.join_cols) < 4 * CUS ? 256 : 768))
-    a.join_cols = (a.join_cols + 1) / 2;
   a.record = (int32_t*)((char*)workspace + w.record);
   a.partial = (float*)((char*)workspace + w.partial);
   return sv::launch_attend(a, (hipStream_t)stream) ? SV_EHIP : SV_OK;

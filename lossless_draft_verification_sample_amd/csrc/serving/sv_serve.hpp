@@ -180,6 +180,7 @@ struct AttendShape {
   int cols_set;       // columns of a set: 16 * nt * across
   int grid;           // workgroups at most
   int single;         // 1: a workgroup a unit
+  int join_cols;      // columns that a workgroup of the join takes
   int lds;            // bytes of LDS
 };
 // Workgroups of a CU, which is waves of a SIMD: by the registers of a lane (sums, a block's
@@ -204,7 +205,6 @@ struct AttendArgs {
   int qh, group, window, bf16;
   uint32_t group_inv; // 2^32 / group, rounded up: a column's row is the product's upper half
   float scale2;       // scale * log2 e
-  int join_cols;      // columns that a workgroup of the join takes
   AttendShape s;
   int32_t* record;    // [B][heads][sets][2]: the first workgroup of a unit, and how many
   float* partial;     // [grid][2]: [cols_set][bricks * 32] sums, [cols_set][2] references and sums of weights

@@ -556,6 +556,50 @@ def test_attention_requests_and_pages_out_of_range(dtype):
     assert torch.equal(got[:, :2], want[:, :2]) and torch.isnan(got[:, 2]).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("capacity", [64, 2048])
+@pytest.mark.parametrize("window", [1, 20, 0])
+def test_attention_requests_out_of_range_are_nan_in_far_rows(dtype, capacity, window):
+    """All N rows, also those that stand further from the first position than the window reaches."""
+    import torch
+    rng = np.random.default_rng(window)
+    cache, table, _, _ = _filled(rng, [60, 60, 60], 2, 64, 32)
+    table = np.pad(table, ((0, 0), (0, capacity // 32 - 2)), constant_values=-1)
+    q, _ = _rows(rng, (3, 50, 4, 64), dtype)
+    got = _sv().spec_verify_attention(q, cache, _dev(table), _ints([-1, 10, capacity]), None, window, want_lse=True)
+    torch.cuda.synchronize()
+    assert torch.isnan(got.out[::2].float()).all() and torch.isnan(got.lse[::2]).all()
+    assert torch.isfinite(got.out[1].float()).all() and torch.isfinite(got.lse[1]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("width", [2, 100])
+@pytest.mark.parametrize("poison", [float("nan"), float("inf"), 2.0 ** 127, 2.0 ** -126])
+def test_attention_unknown_pages_beside_memory_that_nobody_wrote(dtype, width, poison):
+    """Rows 0 and 1 end before a page that the table does not name: whatever page 0, which no request has, holds, they are
+    right, and the rows that see the unknown page are NaN."""
+    import torch
+    rng = np.random.default_rng(5)
+    cache = _cache(rng, 4, 2, 32, 64)
+    k, _ = _rows(rng, (1, 32, 2, 64), dtype)
+    v, _ = _rows(rng, (1, 32, 2, 64), dtype)
+    _sv().spec_verify_cache_write(cache, _dev(np.array([[2]], np.int32)), _ints([0]), k, v)
+    keys, vals = (_host(t) for t in _sv().spec_verify_cache_read(cache, _dev(np.array([[2]], np.int32)), None, 32, _type("f32")))
+    cache.v_scale[0] = poison
+    cache.k_scale[0] = poison
+    cache.k.view(torch.uint8)[0] = 0x7F
+    cache.v.view(torch.uint8)[0] = 0x7F
+    q, qx = _rows(rng, (1, 4, 4, 64), dtype)
+    table = np.full((1, width), -1, np.int32)
+    table[0, 0] = 2
+    got = _sv().spec_verify_attention(q, cache, _dev(table), _ints([30]), want_lse=True)
+    torch.cuda.synchronize()
+    want, lse, sizes, reach, most = os_.attention(qx[0, :2], keys[0], vals[0], 30, 0.125)
+    tol, ltol = _attend_tol(want, lse, sizes, reach, most, 32, 64, dtype)
+    assert np.all(np.abs(_host(got.out[0, :2]) - want) <= tol) and np.all(np.abs(_host(got.lse[0, :2]) - lse) <= ltol)
+    assert torch.isnan(got.out[0, 2:].float()).all() and torch.isnan(got.lse[0, 2:]).all()
+
+
 def test_cache_and_attention_beyond_32_bits():
     """Pages further than 2^31 bytes into the cache, rows further apart than 2^31 elements."""
     import torch
@@ -682,3 +726,40 @@ def test_adjust_rows_further_apart_than_32_bits():
     want = _sv().spec_verify_adjust_logits(near, **kw)
     assert torch.equal(_sv().spec_verify_adjust_logits(z, **kw), want)
     assert torch.equal(_sv().spec_verify_adjust_logits(z, **kw, out=z), want) and torch.equal(z, want)
+
+
+# ---------------------------------------------------------------- sizes of launches
+
+def test_rotate_more_rows_than_a_launch_takes():
+    """2^25 rows of a small head are the most of one launch."""
+    import torch
+    N = 2 ** 25 + 1003
+    x = torch.ones(1, N, 1, 2, device="cuda")
+    _sv().spec_verify_rotate(x, None, _ints([7]), _dev(np.array([1e-3])), out=_sv().RotateOut(x, None))
+    a = (torch.arange(N, dtype=torch.float64, device="cuda") + 7) * 1e-3
+    # 8 units of the pair's sizes, a half of the value's, and a float64 angle of 34,000 turned to 2^-37
+    for got, want in ((x[0, :, 0, 0], a.cos() - a.sin()), (x[0, :, 0, 1], a.cos() + a.sin())):
+        assert (got.double() - want).abs().max() <= 2 * 8 * U + 1.5 * U + 1e-10
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("width", [1, 40])
+def test_attention_many_small_units(dtype, width):
+    """Half a million cache heads of requests, one column each, without and with joins."""
+    import torch
+    rng = np.random.default_rng(3)
+    B, H, D = 8192, 64, 32
+    cache, table, keys, vals = _filled(rng, [32], H, D, 32)
+    page = int(table[0, 0])
+    q, qx = _rows(rng, (1, 1, H, D), dtype)
+    lens = torch.arange(B, dtype=torch.int32, device="cuda") * 5 % 32
+    got = _sv().spec_verify_attention(q.expand(B, 1, H, D), cache, torch.full((B, width), page, dtype=torch.int32, device="cuda"), lens,
+                                      want_lse=True)
+    torch.cuda.synchronize()
+    for n in range(32):
+        want, lse, sizes, reach, most = os_.attention(qx[0], keys[0, :n + 1], vals[0, :n + 1], n, D ** -0.5)
+        tol, ltol = _attend_tol(want, lse, sizes, reach, most, n + 1, D, dtype)
+        here = lens == n
+        assert int(here.sum()) == B // 32
+        assert bool(((got.out[here].double() - _dev(want)).abs() <= _dev(tol)).all()), n
+        assert bool(((got.lse[here].double() - _dev(lse)).abs() <= _dev(ltol)).all()), n

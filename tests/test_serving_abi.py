@@ -125,6 +125,15 @@ def test_attention_refusals(lib):
             for D in (64, 128, 256):
                 for t in (0, 1):
                     assert 0 < size(128, N, 8 * heads, heads, D, 131072, t) < 2 ** 28
+    # batches whose heads make 2^19 tiles of 16 columns are always taken
+    for N in (1, 3, 16, 17, 33, 64):
+        for group in (1, 2, 7, 16, 100, 4096):
+            for D in (1, 64, 96, 128, 160, 224, 256):
+                for t in (0, 1):
+                    tiles = -(-N * group // 16)
+                    if tiles <= 2 ** 19:
+                        assert size(2 ** 19 // tiles, N, group, 1, D, 5000, t) > 0, (N, group, D, t)
+    assert size(2 ** 24, 1, 1, 1, 64, 5000, 1) == 0
 
 
 def test_adjust_refusals(lib):
