@@ -7,7 +7,7 @@
 // lengths, no hash), and keeps a bit for each token that anything falls on. Rows then pass other
 // tokens through, and a lane takes its touched tokens one by one: their arithmetic, a division
 // among it, for all 8 tokens of every group with a touched one made 262 us of 1,152 rows of 151,936
-// with 2,000 tokens before them. The proposals before a row are counted one by one as the
+// with 2,000 tokens before them (now 186, 3.9 TB/s; with a mask alone 149). The proposals before a row are counted one by one as the
 // workgroup goes from row to row; a row is asked for while the one before is worked on.
 
 #include <math.h>
