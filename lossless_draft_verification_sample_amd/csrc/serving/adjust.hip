@@ -7,8 +7,9 @@
 // lengths, no hash), and keeps a bit for each token that anything falls on. Rows then pass other
 // tokens through, and a lane takes its touched tokens one by one: their arithmetic, a division
 // among it, for all 8 tokens of every group with a touched one made 262 us of 1,152 rows of 151,936
-// with 2,000 tokens before them (now 186, 3.9 TB/s; with a mask alone 149). The proposals before a row are counted one by one as the
-// workgroup goes from row to row; a row is asked for while the one before is worked on.
+// with 2,000 tokens before them instead of 220 then. The proposals before a row are counted one by one as the
+// workgroup goes from row to row; a row is asked for while the one before is worked on. (Those rows now:
+// 154 us, 4.7 TB/s; with a mask alone 127, 5.7 TB/s, which is more than a plain copy has.)
 
 #include <math.h>
 
@@ -21,7 +22,7 @@ constexpr int GROUPS = ADJ_CHUNK / 8;
 
 // For each token of the chunk how often it occurred, whether the prompt has it, and 1 + the index
 // of its last bias. SMALL: in 16 bits each, for lists of fewer than 2^15 tokens and 2^16 biases, so
-// that seven workgroups fit a CU instead of four (1,152 rows of 151,936: 220 -> 186 us).
+// that eight workgroups fit a CU instead of four (1,152 rows of 151,936: 220 -> 186 us then).
 template <bool SMALL>
 struct State {
   static constexpr int WORDS = SMALL ? ADJ_CHUNK / 2 : ADJ_CHUNK;
@@ -55,28 +56,87 @@ struct State {
   __device__ __forceinline__ uint32_t last_bias(uint32_t at) const { return half(biased[word(at)], at); }
 };
 
-__device__ __forceinline__ void raw8(const uint16_t* p, uint16_t (&w)[8]) {
-  const su32x4 v = *(const su32x4_any*)p;
+__device__ __forceinline__ uint32_t bits(uint16_t x) { return x; }
+__device__ __forceinline__ uint32_t bits(float x) { return __float_as_uint(x); }
+__device__ __forceinline__ void from_bits(uint16_t* p, uint32_t x) { *p = (uint16_t)x; }
+__device__ __forceinline__ void from_bits(float* p, uint32_t x) { *p = __uint_as_float(x); }
+
+// 8 logits as they lie, two or one to a register, so that rows which pass through cost no instructions
+// (as 8 values each, 179 us instead of 157). bfloat16 rows are read once and not read again here, 1 KB a wave
+// at once, so both ways go past the caches' older contents (186 -> 179 us, passed through 149 -> 138); float32 rows
+// are two times 16 bytes a lane with others' between, which caches put together (322 us past them, 299 through).
+template <typename E>
+struct Eight {
+  static constexpr int LOADS = (int)sizeof(E) / 2;
+  static constexpr uint32_t LOWEST = sizeof(E) == 2 ? 0xFF80FF80u : 0xFF800000u;
+  su32x4 w[LOADS];
+  __device__ __forceinline__ void load(const E* p) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    w[2 * i] = (uint16_t)v[i];
-    w[2 * i + 1] = (uint16_t)(v[i] >> 16);
+    for (int i = 0; i < LOADS; ++i) w[i] = LOADS == 1 ? __builtin_nontemporal_load((const su32x4_any*)p) : ((const su32x4_any*)p)[i];
   }
-}
-__device__ __forceinline__ void raw8(const float* p, float (&w)[8]) { load8(p, w); }
-__device__ __forceinline__ void raw_store8(uint16_t* p, const uint16_t (&w)[8]) {
-  su32x4 v;
+  __device__ __forceinline__ void store(E* p) const {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = (uint32_t)w[2 * i] | (uint32_t)w[2 * i + 1] << 16;
-  *(su32x4_any*)p = v;
-}
-__device__ __forceinline__ void raw_store8(float* p, const float (&w)[8]) { store8(p, w); }
-__device__ __forceinline__ uint16_t lowest(uint16_t) { return 0xFF80u; }
-__device__ __forceinline__ float lowest(float) { return -INFINITY; }
+    for (int i = 0; i < LOADS; ++i) {
+      if constexpr (LOADS == 1) __builtin_nontemporal_store(w[i], (su32x4_any*)p);
+      else ((su32x4_any*)p)[i] = w[i];
+    }
+  }
+  // the first `left` of them
+  __device__ __forceinline__ void load(const E* p, int left) {
+    constexpr int PER = 4 / (int)sizeof(E);
+#pragma unroll
+    for (int i = 0; i < 4 * LOADS; ++i) {
+      uint32_t x = 0;
+#pragma unroll
+      for (int e = 0; e < PER; ++e)
+        if (i * PER + e < left) x |= bits(p[i * PER + e]) << (16 * e);
+      w[i / 4][i % 4] = x;
+    }
+  }
+  __device__ __forceinline__ void store(E* p, int left) const {
+    constexpr int PER = 4 / (int)sizeof(E);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < left) from_bits(p + e, w[e / PER / 4][e / PER % 4] >> (16 * (e % PER)));
+  }
+  __device__ __forceinline__ uint32_t word(int i) const {
+    const uint32_t a = i & 1 ? w[0][1] : w[0][0], b = i & 1 ? w[0][3] : w[0][2], lo = i & 2 ? b : a;
+    if constexpr (LOADS == 1) return lo;
+    const uint32_t c = i & 1 ? w[LOADS - 1][1] : w[LOADS - 1][0], d = i & 1 ? w[LOADS - 1][3] : w[LOADS - 1][2];
+    return i & 4 ? (i & 2 ? d : c) : lo;
+  }
+  __device__ __forceinline__ float get(int e) const {
+    if constexpr (sizeof(E) == 4) return __uint_as_float(word(e));
+    const uint32_t x = word(e >> 1);
+    return __uint_as_float(e & 1 ? x & 0xFFFF0000u : x << 16);
+  }
+  __device__ __forceinline__ void set(int e, float y) {
+    uint32_t x = __float_as_uint(y);
+    int at = e;
+    if constexpr (sizeof(E) == 2) {
+      at = e >> 1;
+      const uint32_t was = word(at), half = round_bf16x2(y, 0.0f);
+      x = e & 1 ? (was & 0xFFFFu) | half << 16 : (was & 0xFFFF0000u) | half;
+    }
+#pragma unroll
+    for (int i = 0; i < 4 * LOADS; ++i) w[i / 4][i % 4] = at == i ? x : w[i / 4][i % 4];
+  }
+  // -inf where a bit is clear
+  __device__ __forceinline__ void keep(uint32_t mask) {
+#pragma unroll
+    for (int i = 0; i < 4 * LOADS; ++i) {
+      uint32_t m = 0;
+      if constexpr (sizeof(E) == 2) m = (mask >> (2 * i) & 1 ? 0xFFFFu : 0u) | (mask >> (2 * i) & 2 ? 0xFFFF0000u : 0u);
+      else m = mask >> i & 1 ? ~0u : 0u;
+      w[i / 4][i % 4] = (w[i / 4][i % 4] & m) | (LOWEST & ~m);
+    }
+  }
+};
 
 constexpr int MINE = GROUPS / ADJ_THREADS;   // groups of a thread
-constexpr int AHEAD = 4;                     // loads of four ids of a list that a thread keeps
-constexpr int ADJ_BIASES = 1024;             // of a request, in LDS; more are read from memory
+// Loads of four ids of a list that a thread keeps (4: 20 registers more and a wave less, 157 us instead of 154).
+constexpr int AHEAD = 2;
+constexpr int ADJ_BIASES = 768;              // of a request, in LDS; more are read from memory
 
 // Ids n0 + 4 (thread + 256 k) .. + 3 of a list, -1 behind its end.
 template <int LOADS>
@@ -98,7 +158,7 @@ __device__ __forceinline__ void load_ids(su32x4 (&v)[LOADS], const int32_t* ids,
 // What a thread has of a row: its groups' logits and bits.
 template <typename E>
 struct Held {
-  E x[MINE][8];
+  Eight<E> x[MINE];
   uint32_t mask[MINE];
 };
 
@@ -134,7 +194,7 @@ __global__ __launch_bounds__(ADJ_THREADS) void adjust_kernel(AdjustArgs a) {
     return ((const uint8_t*)(a.allowed + ((int64_t)b * a.N + j) * words) + v0 / 8)[g];
   };
   // What the whole workgroup waits for first goes out together: the rows' bits, and the lists'
-  // first 4,096 ids, four a load.
+  // first 2,048 ids, four a load.
   const bool counts = a.repetition || a.frequency || a.presence;
   const int32_t* history = a.history + (int64_t)b * a.n_history;
   const int32_t* prompt = a.prompt + (int64_t)b * a.n_prompt;
@@ -170,12 +230,8 @@ __global__ __launch_bounds__(ADJ_THREADS) void adjust_kernel(AdjustArgs a) {
     for (int k = 0; k < MINE; ++k) {
       if (left[k] <= 0 || to.mask[k] == 0 || (in_place && !note[k] && to.mask[k] == 0xFFu)) continue;
       const E* q = z + j * a.zs.n + 8 * (tid + k * ADJ_THREADS);
-      if (left[k] >= 8) {
-        raw8(q, to.x[k]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) to.x[k][e] = e < left[k] ? q[e] : lowest(E());
-      }
+      if (left[k] >= 8) to.x[k].load(q);
+      else to.x[k].load(q, left[k]);
     }
   };
   if (!in_place) fetch(j0, row);
@@ -238,35 +294,21 @@ __global__ __launch_bounds__(ADJ_THREADS) void adjust_kernel(AdjustArgs a) {
       const int g = tid + k * ADJ_THREADS;
       const uint32_t mask = row.mask[k];
       if (left[k] <= 0 || (in_place && !note[k] && mask == 0xFFu)) continue;
-      E(&x)[8] = row.x[k];
+      Eight<E>& x = row.x[k];
       // one token of each lane at a time: few lanes have one, and those have few
       for (uint32_t bits = note[k] & mask; bits; bits &= bits - 1) {
         const int e = __builtin_ctz(bits);
         const uint32_t c = state.counted(g * 8 + e), last = state.last_bias(g * 8 + e);
-        E v = x[0];
-#pragma unroll
-        for (int i = 1; i < 8; ++i) v = e == i ? x[i] : v;
-        float y = elem(&v);
+        float y = x.get(e);
         if (c) y = y > 0.0f ? y / theta : y * theta;
         if (c & ~PROMPT) y = y - (often * (float)(c & ~PROMPT) + once);
         if (last) y = y + (last <= ADJ_BIASES ? biases[last - 1] : bias[last - 1]);
-        if (c | last) put(&v, y);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = e == i ? v : x[i];
+        if (c | last) x.set(e, y);
       }
-      if (mask != 0xFFu) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (!(mask >> e & 1)) x[e] = lowest(E());
-      }
+      if (mask != 0xFFu) x.keep(mask);
       E* o = out + j * a.os.n + 8 * g;
-      if (left[k] >= 8) {
-        raw_store8(o, x);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (e < left[k]) o[e] = x[e];
-      }
+      if (left[k] >= 8) x.store(o);
+      else x.store(o, left[k]);
     }
     row = next;
 #pragma unroll
