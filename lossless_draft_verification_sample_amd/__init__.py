@@ -84,9 +84,10 @@ def _torch():
 
 def _dtype_code(t, name="logits"):
     torch = _torch()
-    if t.dtype == torch.bfloat16:
+    dtype = t.dtype
+    if dtype == torch.bfloat16:
         return SV_BF16
-    if t.dtype == torch.float32:
+    if dtype == torch.float32:
         return SV_F32
     raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
 
@@ -407,6 +408,9 @@ def _vector(t, name, dtype, shape, device):
     """Pointer of a contiguous tensor (or None) of this type, shape and device."""
     if t is None:
         return None
+    # numbers of devices compare quicker than devices
+    if t.get_device() == device.index and t.dtype == dtype and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
@@ -773,7 +777,7 @@ def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0, origi
 def _on_device(t, name, device, dtype, shape):
     """Raises what is wrong with a tensor of rows: not on a device, or on another device, of another
     type or shape than wanted (None: any)."""
-    if not _TORCH.is_tensor(t) or not t.is_cuda:
+    if not isinstance(t, _TORCH.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
@@ -781,6 +785,10 @@ def _on_device(t, name, device, dtype, shape):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+# sv_strides of these strides: made once, passed by value
+_strides = functools.lru_cache(maxsize=1024)(SvStrides)
 
 
 def _rows4(t, name, device=None, dtype=None, shape=None):
@@ -792,7 +800,7 @@ def _rows4(t, name, device=None, dtype=None, shape=None):
     b, n, h, one = t.stride()
     if one != 1 and size[3] > 1:
         raise ValueError(f"{name} must have consecutive elements in a head")
-    return t.data_ptr(), SvStrides(b, n, h)
+    return t.data_ptr(), _strides(b, n, h)
 
 
 def _out4(t, like, name):
@@ -800,7 +808,7 @@ def _out4(t, like, name):
     if t is None:
         t = _TORCH.empty_like(like, memory_format=_TORCH.contiguous_format)
         b, n, h, _ = t.stride()
-        return t, t.data_ptr(), SvStrides(b, n, h)
+        return t, t.data_ptr(), _strides(b, n, h)
     return (t, *_rows4(t, name, like.device, like.dtype, like.shape))
 
 
@@ -921,7 +929,7 @@ def spec_verify_cache_read(cache, page_table, first, N, dtype=None, rows=None, o
     torch = _torch()
     lib = lib or _lib.load()
     dev = cache.k.device
-    if not cache.k.is_cuda:
+    if dev.type != "cuda":
         raise ValueError("cache must be on a device")
     c = _cache(cache, dev)
     if page_table is None:
@@ -1013,7 +1021,7 @@ def _rows3(t, name, device=None, dtype=None, shape=None):
     b, n, one = t.stride()
     if one != 1 and size[2] > 1:
         raise ValueError(f"{name} must have consecutive elements in a row")
-    return t.data_ptr(), SvStrides(b, n, 0)
+    return t.data_ptr(), _strides(b, n, 0)
 
 
 def _id_list(t, name, B, device):

@@ -13,8 +13,10 @@
 // block's codes, 16 bytes each as they lie; the new rows come 8 dimensions a thread; the largest
 // value goes through a block reduction, for which old codes need no decoding; and the new codes go
 // to their places through LDS. Old codes are made again only where the scale changes, and parts of
-// the block that hold no new row are then the only ones not written. (Four prompts of up to 4,096 rows of
-// eight heads of 128: 26 us to write, 18 to read back, 3.8 TB/s; two prefixes of 32,768 read at 5.1 TB/s.)
+// the block that hold no new row are then the only ones not written. Rows that are read back go past the caches'
+// older contents, and so do the codes then: two prefixes of 32,768 rows of eight heads of 128 come at 5.7 TB/s (61.6 us;
+// 68.2 through the caches). Four prompts of up to 4,096 such rows, written and read back: 40.3 us, 4.1 TB/s (44.2; with the
+// rows that a write reads and the codes that it writes past them too, 42.2).
 
 #include <math.h>
 
@@ -252,7 +254,7 @@ __device__ __forceinline__ void read_block(const CacheRowsArgs& a, const Where& 
     const int bytes = a.c.bricks * BRICK;
     const uint8_t* mem = (w.values ? a.c.v : a.c.k) + at * bytes;
     scale = (w.values ? a.c.vs : a.c.ks)[at];
-    for (int i = tid * 16; i < bytes; i += NTH * 16) *(su32x4*)(block + i) = *(const su32x4*)(mem + i);
+    for (int i = tid * 16; i < bytes; i += NTH * 16) *(su32x4*)(block + i) = __builtin_nontemporal_load((const su32x4*)(mem + i));
   }
   __syncthreads();
   const Strides st = w.values ? a.vs : a.ks;

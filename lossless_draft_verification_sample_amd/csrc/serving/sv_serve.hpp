@@ -103,11 +103,12 @@ __device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
     x[4 + i] = __uint_as_float(b[i]);
   }
 }
+// bfloat16 past the caches' older contents: for results that are written in whole lines and not read again soon.
 __device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8]) {
   su32x4 w;
 #pragma unroll
   for (int i = 0; i < 4; ++i) w[i] = round_bf16x2(x[2 * i], x[2 * i + 1]);
-  *(su32x4_any*)p = w;
+  __builtin_nontemporal_store(w, (su32x4_any*)p);
 }
 __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
   su32x4 a, b;
