@@ -135,12 +135,21 @@ bool attend_shape(int64_t B, int64_t N, int64_t qh, int64_t heads, int64_t D, in
       if (nt > nt_most || nt * across > most) continue;
       const int64_t units = B * heads * sets;
       const int64_t cols_set = 16 * nt * across;
-      // columns of a workgroup of the join: three items a thread, one where the units are few
+      // a workgroup takes four blocks at least
+      const double blocks = (double)units * (ceil_div(tokens, sv::CACHE_BLOCK) + 1);
+      const int64_t full = CUS * sv::attend_per_cu((int)bricks, (int)nt);
+      const int64_t grid = ceil(blocks / 4) < full ? (int64_t)ceil(blocks / 4) : full;
+      // Columns of a workgroup of the join: three items a thread, one where the units are few, and an
+      // eighth where they have so many parts that reading them is a long chain (one request of 131,072
+      // tokens, 64 parts, nine rows: 69 -> 63 us; of 4,000 tokens, 31 parts: 23 -> 20; four requests, 16 parts:
+      // 184 -> 187; 16 requests, 4 parts: 33 -> 51).
+      const bool split = grid >= 24 * units;
       int64_t join = cols_set;
-      while (join > 1 && join * bricks * 8 > ((double)units * ceil_div(cols_set, join) < 4 * CUS ? 256 : 768))
+      while (join > 1 && join * bricks * 8 > ((double)units * ceil_div(cols_set, join) >= 4 * CUS ? 768 : split ? 32 : 256))
         join = (join + 1) / 2;
       if ((double)units * ceil_div(cols_set, join) >= MAX_WORKGROUPS) return false;
       s->join_cols = (int)join;
+      s->join_split = split;
       s->cols = (int)cols;
       s->nt = (int)nt;
       s->across = (int)across;
@@ -153,10 +162,7 @@ bool attend_shape(int64_t B, int64_t N, int64_t qh, int64_t heads, int64_t D, in
         s->grid = (int)units;
         return true;
       }
-      // a workgroup takes four blocks at least
-      const int64_t blocks = units * (ceil_div(tokens, sv::CACHE_BLOCK) + 1);
-      const int64_t full = CUS * sv::attend_per_cu((int)bricks, (int)nt);
-      s->grid = (int)(ceil_div(blocks, 4) < full ? ceil_div(blocks, 4) : full);
+      s->grid = (int)grid;
       return true;
     }
   }

@@ -182,6 +182,7 @@ struct AttendShape {
   int grid;           // workgroups at most
   int single;         // 1: a workgroup a unit
   int join_cols;      // columns that a workgroup of the join takes
+  int join_split;     // 1: its threads share out a column's parts
   int lds;            // bytes of LDS
 };
 // Workgroups of a CU, which is waves of a SIMD: by the registers of a lane (sums, a block's

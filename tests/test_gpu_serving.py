@@ -370,6 +370,15 @@ def test_attention_shared_rows(dtype, N, qh, H, D):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,qh,H,D", [(1, 4, 2, 64), (9, 4, 1, 128), (5, 3, 3, 33), (3, 2, 1, 256), (64, 1, 1, 32)])
+def test_attention_of_one_long_request(dtype, N, qh, H, D):
+    """Many parts of a unit, which the join's threads share out; one more request sees little or nothing."""
+    rng = np.random.default_rng(N + D)
+    _check_attend(rng, [30001, 0], [N, N], N, qh, H, D, 128, dtype)
+    _check_attend(rng, [12345, 7], [max(1, N - 1), 0], N, qh, H, D, 32, dtype, window=9000)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("window", [1200, 1500, 2048, 100000, 2 ** 31 - 1])
 def test_attention_shared_windows(dtype, window):
     rng = np.random.default_rng(window % 97)
