@@ -20,7 +20,7 @@
 // operations. Loads go straight to registers, 16 bytes a lane and 1 KB a wave; the next
 // block's keys are asked for as soon as this block's are used up, its values likewise, so
 // that about one block a wave is in flight all the time. (Four requests of 131,072 tokens, 40 columns:
-// 172 us, 6.2 TB/s; 128 requests of 100 to 8,192, 36 columns: 206 us, 5.3 TB/s; 8,192 each, four
+// 172 us, 6.2 TB/s; 128 requests of 100 to 8,192, 36 columns: 206 to 211 us, 5.3 TB/s; 8,192 each, four
 // columns: 331 us with all launches, 6.5 TB/s.)
 //
 // The reference r is not the running maximum but a score near it, moved only when a score
