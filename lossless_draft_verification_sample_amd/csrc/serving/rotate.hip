@@ -85,9 +85,10 @@ __device__ __forceinline__ su32x4 close16(const float (&x)[8]) {
   return su32x4{round_bf16x2(x[0], x[1]), round_bf16x2(x[2], x[3]), round_bf16x2(x[4], x[5]), round_bf16x2(x[6], x[7])};
 }
 
-// R/2 a multiple of the elements of 16 bytes: a unit is two times 16 bytes, of both halves or one
-// after the other, of the rest of a head too where that is whole. Every thread asks for its
-// first MINE units before the angles are made.
+// A unit is two times 16 bytes, of both halves or one after the other, and of the rest of a head too; where
+// R/2 or the rest ends inside a unit, that one goes element by element (24,288 rows of 36 heads of 126
+// bfloat16: 166 us; a pair a thread for the whole row 248; that unit's elements asked for together 182). Every thread asks for its first MINE units before the angles
+// are made.
 template <typename E, bool INTER>
 __global__ __launch_bounds__(NTH) void rotate_vec_kernel(RotateArgs a, int per_wg, int64_t base) {
   constexpr int W = 16 / (int)sizeof(E), MINE = 2;
@@ -95,7 +96,7 @@ __global__ __launch_bounds__(NTH) void rotate_vec_kernel(RotateArgs a, int per_w
   const int R2 = a.R / 2, tid = threadIdx.x;
   const int64_t total = (int64_t)a.B * a.N, row0 = base + (int64_t)blockIdx.x * per_wg;
   const int rows = (int)(total - row0 < per_wg ? total - row0 : per_wg);
-  const int pairs = R2 / W, rest = a.D - a.R;
+  const int pairs = (R2 + W - 1) / W, rest = a.D - a.R;
   const int copies = a.oq == a.q && a.ok == a.k && !a.rows ? 0 : (rest + 2 * W - 1) / (2 * W);
   const int units = pairs + copies, items = rows * (a.qh + a.kh) * units;
   for (int i0 = tid, first = 1; first || i0 - tid < items; i0 += MINE * NTH, first = 0) {
@@ -108,7 +109,7 @@ __global__ __launch_bounds__(NTH) void rotate_vec_kernel(RotateArgs a, int per_w
       if (!there[k]) continue;
       const int u = it[k].unit, d = u < pairs ? (INTER ? 2 * u * W : u * W) : a.R + (u - pairs) * 2 * W;
       const int d1 = u < pairs && !INTER ? R2 + u * W : d + W;
-      if (d1 + W <= a.D) {
+      if (u < pairs ? (u + 1) * W <= R2 : d1 + W <= a.D) {
         lo[k] = *(const su32x4_any*)(it[k].x + d);
         hi[k] = *(const su32x4_any*)(it[k].x + d1);
       }
@@ -121,7 +122,15 @@ __global__ __launch_bounds__(NTH) void rotate_vec_kernel(RotateArgs a, int per_w
     for (int k = 0; k < MINE; ++k) {
       if (!there[k]) continue;
       const int u = it[k].unit;
-      if (u < pairs) {
+      if (u < pairs && (u + 1) * W > R2) {
+        for (int i = u * W; i < R2; ++i) {
+          const int p = INTER ? 2 * i : i, q = INTER ? p + 1 : R2 + i;
+          float x = elem(it[k].x + p), y = elem(it[k].x + q);
+          turn_pair(x, y, turn[it[k].row * R2 + i]);
+          put(it[k].y + p, it[k].bad ? NAN : x);
+          put(it[k].y + q, it[k].bad ? NAN : y);
+        }
+      } else if (u < pairs) {
         float x[W], y[W];
         open16(lo[k], x);
         open16(hi[k], y);
@@ -158,7 +167,7 @@ __global__ __launch_bounds__(NTH) void rotate_vec_kernel(RotateArgs a, int per_w
   }
 }
 
-// Any other R: a pair a unit, then the rest element by element.
+// R/2 below a unit: a pair a thread, then the rest element by element.
 template <typename E, bool INTER>
 __global__ __launch_bounds__(NTH) void rotate_any_kernel(RotateArgs a, int per_wg, int64_t base) {
   __shared__ sf32x2 turn[MAX_R2];
@@ -189,7 +198,7 @@ template <typename E, bool INTER>
 int launch(const RotateArgs& a, hipStream_t st) {
   constexpr int W = 16 / (int)sizeof(E);
   const int R2 = a.R / 2;
-  const bool vec = R2 && R2 % W == 0;
+  const bool vec = R2 >= W;
   // rows of a workgroup: two units a thread, the angles' room in LDS, and workgroups for the CUs
   const int64_t total = (int64_t)a.B * a.N, units = (a.qh + a.kh) * (int64_t)((a.D + 2 * W - 1) / (2 * W));
   int64_t per = 2 * NTH / units;

@@ -92,6 +92,7 @@ def _rotate_tol(x, D, R, inter, positions, freqs, scale, dtype, want):
     (1, 1, 1, 0, 2, 2, "plain"), (2, 3, 4, 2, 128, 128, "plain"), (3, 5, 2, 1, 96, 48, "fused"),
     (2, 1, 3, 3, 7, 6, "fused"), (1, 9, 8, 2, 64, 32, "heads_first"), (2, 2, 1, 1, 1024, 1024, "plain"),
     (1, 2, 2, 1, 10, 0, "plain"), (1, 700, 2, 2, 80, 20, "plain"), (2, 33, 5, 1, 12, 4, "fused"),
+    (2, 130, 4, 1, 126, 126, "fused"), (3, 40, 3, 2, 101, 50, "heads_first"), (1, 9, 2, 1, 1023, 1022, "plain"),
 ])
 def test_rotate(dtype, inter, B, N, Hq, Hk, D, R, how):
     import torch
