@@ -441,7 +441,8 @@ int spec_verify_linear_ce_backward(const void* hidden, int64_t hidden_stride, co
  *     seen there. A request whose kv_len or rows is out of range has NaN in all its N rows
  *     of the outputs, and nothing of it is written to the cache.
  *   - Sums, softmax statistics and products are float32 or wider whatever the
- *     inputs' type; results are rounded once.
+ *     inputs' type; results are rounded once. (Attention's matrix products take the factors that do not
+ *     fit bfloat16 as sums of bfloat16 numbers, see there.)
  *   - No result depends on the order in which workgroups run. (How attention shares out a
  *     request's tokens follows from the lengths of the whole batch: in another batch its sums may
  *     be in another order.)
@@ -543,9 +544,11 @@ int spec_verify_cache_read(const sv_cache* cache, const int32_t* page_table, int
  *   q        [B][N][q_heads][head_dim] of dtype at any strides; scale finite.
  *   out      like q, of dtype, at its strides, over no part of q; out_lse [B][N][q_heads] float, or
  *            NULL.
- * bfloat16: products of q and k are exact, probabilities enter their product with v as float16
- * (off by 2^-12, and 2^-25 of the largest), and blocks whose v_scale lies 2^-60 below another's of
- * the request lose precision; float32: q and the probabilities as three bfloat16 parts.
+ * bfloat16: products of q and k are exact; a weight enters its product with v as the sum of two
+ * bfloat16 numbers (off by 2^-17 of itself, however small it is), and blocks whose v_scale lies 2^-100 below
+ * another's of the request lose precision. float32: q and the weights times v_scale as sums of three
+ * (2^-25; less where such a product is below 2^-100). The sums are divided at the end: where a value times
+ * 256 times the number of tokens passes 2^128, they may be infinite.
  * NaN in a position that a row does not see does not reach it. A row that sees a position in a
  * page outside [0, pages) is NaN; pages that no row of the request sees (all before its window)
  * are not read. Requests out of range as in spec_verify_cache_write.

@@ -6,11 +6,12 @@
 //   P = exp2(c S - r)  c = k_scale * scale * log2 e, r the column's reference
 //   O += V^T P         dimensions by columns, V = v_scale * code; l += sum P
 // Keys become bfloat16, which holds their codes and bfloat16 queries exactly. For bfloat16
-// outputs P becomes float16, off by 2^-12, a sixteenth of the outputs' own step, and V is
-// code * v_scale / 2^e in float16, exact for powers of two within 2^-15 .. 2^7 of 2^e; where a scale
-// lies outside, e is moved and O with it. For float32, P v_scale is taken as three bfloat16 parts.
-// (P in two bfloat16 parts took 1,600 issue cycles of vector instructions a block of three tiles
-// instead of 930, and twice the second product's matrix instructions.)
+// outputs P is taken as two bfloat16 parts, each weight to 2^-17 of itself however small it is beside the
+// others, and V is code * v_scale / 2^e in bfloat16, exact for powers of two within 2^-100 .. 2^30 of 2^e;
+// where a scale lies above, e is moved and O with it. For float32, P v_scale is taken as three bfloat16
+// parts. (P as one float16, whose steps end at 2^-24, is faster: 225 us instead of 242 for the ragged batch
+// below, 184 instead of 212 for the long requests. But where one token has nearly all the weight and the
+// value 0, outputs are made of the small weights, and with the others' scores 17 below its they were off by 45%.)
 // A wave takes whole blocks on its own. Every operand is in place without a shuffle: the
 // cache's bricks hold keys and values in the order of the instruction's A operand, and the
 // tokens of a brick of keys are ordered so that the 8 tokens whose scores a lane gets are the
@@ -20,8 +21,8 @@
 // operations. Loads go straight to registers, 16 bytes a lane and 1 KB a wave; the next
 // block's keys are asked for as soon as this block's are used up, its values likewise, so
 // that about one block a wave is in flight all the time. (Four requests of 131,072 tokens, 40 columns:
-// 172 us, 6.2 TB/s; 128 requests of 100 to 8,192, 36 columns: 206 to 211 us, 5.3 TB/s; 8,192 each, four
-// columns: 331 us with all launches, 6.5 TB/s.)
+// 201 us, 5.3 TB/s; 128 requests of 100 to 8,192, 36 columns: 242 us with the join, 4.5 TB/s; 8,192 each, four
+// columns: 354 us with all launches, 6.1 TB/s.)
 //
 // The reference r is not the running maximum but a score near it, moved only when a score
 // exceeds it by 8, so that weights stay below 256; so a block costs no reduction over lanes and O is rescaled hardly ever.
@@ -53,6 +54,10 @@ constexpr float AT_FAR = 256.0f;       // 2^AT_SLACK
 // The reference of a column that has seen no token: finite, so that a masked score's weight is 0,
 // and lower than any that a score of float32 products can become and stay finite.
 constexpr float AT_NONE = -3.40282346638528859812e38f;
+// How far above and below the sums' unit a block's scale may lie (base 2): above, the sums stay finite
+// for 2^30 tokens and take the new unit otherwise; below, codes stay exact in bfloat16 and the weights
+// take what is left.
+constexpr int AT_ABOVE = 30, AT_BELOW = 100;
 constexpr int AT_LEAST = 4;            // blocks of a workgroup at least: one a wave
 // What starting and ending a unit costs, in blocks, a tile: it counts in the workgroups' shares.
 // (Ragged batch of 128 requests, three tiles: 8 in all 250 us, 16 231, 24 227, 40 231; one tile: 8
@@ -82,35 +87,17 @@ __device__ __forceinline__ void split8(const float (&x)[8], sbf16x8 (&p)[PARTS])
   }
 }
 
-// 8 codes as bfloat16, which holds them exactly.
-__device__ __forceinline__ sbf16x8 codes8(uint32_t lo, uint32_t hi) {
-  const sbf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
-  const sbf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
-  const sbf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
-  const sbf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+// 8 codes times `grow`, a power of two, as bfloat16: exact from 2^-117 to 2^118.
+__device__ __forceinline__ sbf16x8 codes8(uint32_t lo, uint32_t hi, float grow = 1.0f) {
+  const sbf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, grow, false);
+  const sbf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, grow, true);
+  const sbf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, grow, false);
+  const sbf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, grow, true);
   return sbf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
-
-// 8 codes times 2^e as float16: exact for e from -15 to 7.
-__device__ __forceinline__ sf16x8 codes8_half(uint32_t lo, uint32_t hi, float grow) {
-  const sf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, grow, false);
-  const sf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, grow, true);
-  const sf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, grow, false);
-  const sf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, grow, true);
-  return sf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
-__device__ __forceinline__ sf16x8 half8(const float (&x)[8]) {
-  sf16x8 h;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) h[i] = (_Float16)x[i];
-  return h;
 }
 
 __device__ __forceinline__ sf32x4 mma(sbf16x8 a, sbf16x8 b, sf32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
-__device__ __forceinline__ sf32x4 mma(sf16x8 a, sf16x8 b, sf32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
 // Blocks of a request's units, and the first one.
@@ -199,8 +186,7 @@ __device__ __forceinline__ const AttendArgs& fresh_args() {
 
 template <int BRICKS, int NT, bool F32>
 __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT)) void attend_kernel(AttendArgs a) {
-  constexpr int QP = F32 ? 3 : 1, DT = 2 * BRICKS;
-  using VF = std::conditional_t<F32, sbf16x8, sf16x8>;   // values in the second product
+  constexpr int QP = F32 ? 3 : 1, WP = F32 ? 3 : 2, DT = 2 * BRICKS;   // parts of queries and of weights
   extern __shared__ char lds[];
   __shared__ float stat[AT_WAVES][NT * 16][2], total[AT_WAVES * NT * 16][2];
   const int tid = threadIdx.x, lane = tid % WAVE, wave = __builtin_amdgcn_readfirstlane(tid / WAVE);
@@ -362,10 +348,9 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT)) void attend_
     sf32x4 O[NT][DT];
     float l[NT], sub[NT];                                // sub: the column's reference
     bool settled = false;                                // every column has one
-    // What the sums are relative to: 2^(eref - 127), near the scales of the values; the largest yet.
-    int eref = (int)(__float_as_uint(vs_next) >> 23 & 255) + 2;
-    if (F32 || lost_next || eref <= 2 || eref > 250) eref = 127;
-    int etop = eref;
+    // What the sums are relative to: 2^(eref - 127), the first block's scale, or a larger one's.
+    int eref = (int)(__float_as_uint(vs_next) >> 23 & 255);
+    if (F32 || lost_next || eref == 0 || eref == 255) eref = 127;
     int last[NT];                                        // the last position a column sees
     const int col0 = (set * across + side) * NT * 16;    // this wave's first column
 #pragma unroll
@@ -405,8 +390,7 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT)) void attend_
       }
       // the codes become numbers first, so that the next block is asked for with the whole of this
       // one's work ahead
-      sbf16x8 kf[BRICKS][2];
-      VF vf[BRICKS][2];
+      sbf16x8 kf[BRICKS][2], vf[BRICKS][2];
 #pragma unroll
       for (int c = 0; c < BRICKS; ++c) {
         kf[c][0] = codes8(kraw[c][0], kraw[c][1]);
@@ -414,35 +398,24 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT)) void attend_
       }
       int up = 0;
       float rho = vs;                                    // what v_scale has besides 2^up; 0, infinities, NaN
-      if constexpr (!F32) {
-        const int ev = (int)(__float_as_uint(vs) >> 23 & 255);
-        if (vs != 0.0f && ev != 255) {
-          if (ev - eref > 7 || ev - eref < -15) {
-            int to = ev + 2;                             // 448 * 2^7 is float16's range above it
-            if (to < etop - 60) to = etop - 60;          // the sums stay finite
-            if (to > 250) to = 250;
-            if (etop < to) etop = to;
-            const float f = ldexpf(1.0f, eref - to);
+      const int ev = (int)(__float_as_uint(vs) >> 23 & 255);
+      if (!F32 && vs != 0.0f && ev != 255) {
+        if (ev - eref > AT_ABOVE) {
+          const float f = ldexpf(1.0f, eref - ev);
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+          for (int t = 0; t < NT; ++t)
 #pragma unroll
-              for (int k = 0; k < DT; ++k) O[t][k] *= f;
-            eref = to;
-          }
-          up = ev - eref < -15 ? -15 : ev - eref;
-          rho = ldexpf(vs, 127 - eref - up);
+            for (int k = 0; k < DT; ++k) O[t][k] *= f;
+          eref = ev;
         }
+        up = ev - eref < -AT_BELOW ? -AT_BELOW : ev - eref;
+        rho = ldexpf(vs, 127 - eref - up);
       }
       const float grow = __uint_as_float((uint32_t)(127 + up) << 23);
 #pragma unroll
       for (int c = 0; c < BRICKS; ++c) {
-        if constexpr (F32) {
-          vf[c][0] = codes8(vraw[c][0], vraw[c][1]);
-          vf[c][1] = codes8(vraw[c][2], vraw[c][3]);
-        } else {
-          vf[c][0] = codes8_half(vraw[c][0], vraw[c][1], grow);
-          vf[c][1] = codes8_half(vraw[c][2], vraw[c][3], grow);
-        }
+        vf[c][0] = codes8(vraw[c][0], vraw[c][1], grow);
+        vf[c][1] = codes8(vraw[c][2], vraw[c][3], grow);
       }
       if (i + along < i1) {
         locate(i + along);
@@ -543,41 +516,24 @@ __global__ __launch_bounds__(AT_THREADS, attend_per_cu(BRICKS, NT)) void attend_
 
 #pragma unroll
       for (int t = 0; t < NT; ++t)
+        l[t] += ((w[t][0] + w[t][1]) + (w[t][2] + w[t][3])) + ((w[t][4] + w[t][5]) + (w[t][6] + w[t][7]));
+      if (rho != 1.0f) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) l[t] += w[t][e];
-      if constexpr (F32) {
-        sbf16x8 pf[NT][3];
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
+          for (int e = 0; e < 8; ++e) w[t][e] *= rho;
+      }
+      // tile by tile, so that the parts take the weights' registers
 #pragma unroll
-          for (int e = 0; e < 8; ++e) w[t][e] *= vs;
-          split8<3>(w[t], pf[t]);
-        }
+      for (int t = 0; t < NT; ++t) {
+        sbf16x8 pf[WP];
+        split8<WP>(w[t], pf);
 #pragma unroll
-        for (int c = 0; c < BRICKS; ++c)
+        for (int n = 0; n < WP; ++n)
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int n = 0; n < 3; ++n) {
-              O[t][2 * c] = mma(vf[c][0], pf[t][n], O[t][2 * c]);
-              O[t][2 * c + 1] = mma(vf[c][1], pf[t][n], O[t][2 * c + 1]);
-            }
-      } else {
-        if (rho != 1.0f) {
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[t][e] *= rho;
-        }
-        sf16x8 pf[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) pf[t] = half8(w[t]);
-#pragma unroll
-        for (int c = 0; c < BRICKS; ++c)
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            O[t][2 * c] = mma(vf[c][0], pf[t], O[t][2 * c]);
-            O[t][2 * c + 1] = mma(vf[c][1], pf[t], O[t][2 * c + 1]);
+          for (int c = 0; c < BRICKS; ++c) {
+            O[t][2 * c] = mma(vf[c][0], pf[n], O[t][2 * c]);
+            O[t][2 * c + 1] = mma(vf[c][1], pf[n], O[t][2 * c + 1]);
           }
       }
     }

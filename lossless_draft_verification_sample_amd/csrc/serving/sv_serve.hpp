@@ -16,8 +16,6 @@ typedef float sf32x2 __attribute__((ext_vector_type(2)));
 typedef float sf32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 sbf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 sbf16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 sf16x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 sf16x8 __attribute__((ext_vector_type(8)));
 
 // The same at any alignment of their elements: the hardware loads and stores
 // vectors at any address, so no row needs a head of single elements.
