@@ -979,7 +979,8 @@ def spec_verify_attention(q, cache, page_table, kv_len, scale=None, window=0, ro
     q [B, N, q_heads, D] (bf16 or fp32, any strides with consecutive D), N up to SV_MAX_ROWS, q_heads
     a multiple of the cache's heads; page_table [B, width] int32, kv_len [B] int32: tokens
     before the rows; scale of the scores (None: D^-1/2); window: how many positions a row sees, its
-    own included (0: all); rows [B] int32 or None. out: an AttentionOut; its lse may be None.
+    own included (0: all); rows [B] int32 or None. out: an AttentionOut, either of whose tensors may be
+    None: out is made then, lse if want_lse is set.
     Returns AttentionOut(out like q, lse [B, N, q_heads] float32 or None)."""
     torch = _torch()
     lib = lib or _lib.load()
@@ -995,7 +996,7 @@ def spec_verify_attention(q, cache, page_table, kv_len, scale=None, window=0, ro
     with ctx:
         o, op, os_ = _out4(out and out.out, q, "out.out")
         lse = out.lse if out is not None else None
-        if out is None and want_lse:
+        if lse is None and want_lse:
             lse = torch.empty((B, N, qh), dtype=torch.float32, device=dev)
         tokens = width * c.page_size
         if 0 < window + N + 31 < tokens and window:
