@@ -787,6 +787,9 @@ def _on_device(t, name, device, dtype, shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+# What an int32 argument holds: ctypes would take a larger number's lower 32 bits.
+_MOST = 2 ** 31 - 1
+
 # sv_strides of these strides: made once, passed by value
 _strides = functools.lru_cache(maxsize=1024)(SvStrides)
 
@@ -797,6 +800,8 @@ def _rows4(t, name, device=None, dtype=None, shape=None):
     size = t.shape
     if len(size) != 4 or 0 in size:
         raise ValueError(f"{name} must be [B, N, heads, D], none of them 0, got {tuple(size)}")
+    if max(size) > _MOST:
+        raise SpecVerifyError(SV_ESIZE, name)
     b, n, h, one = t.stride()
     if one != 1 and size[3] > 1:
         raise ValueError(f"{name} must have consecutive elements in a head")
@@ -889,6 +894,8 @@ def _table(page_table, B, device):
     if page_table is None or page_table.dim() != 2:
         raise ValueError("page_table must be [B, width] int32")
     width = page_table.shape[1]
+    if width > _MOST:
+        raise SpecVerifyError(SV_ESIZE, "page_table")
     return _vector(page_table, "page_table", _torch().int32, (B, width), device), width
 
 
@@ -934,9 +941,11 @@ def spec_verify_cache_read(cache, page_table, first, N, dtype=None, rows=None, o
     c = _cache(cache, dev)
     if page_table is None:
         raise ValueError("page_table must be [B, width] int32")
-    B = page_table.shape[0]
+    B, N = page_table.shape[0], int(N)
+    if N > _MOST:
+        raise SpecVerifyError(SV_ESIZE, "spec_verify_cache_read")
     table, width = _table(page_table, B, dev)
-    shape = (B, int(N), c.heads, c.head_dim)
+    shape = (B, N, c.heads, c.head_dim)
     ctx, handle = _on(dev, stream)
     with ctx:
         if out is None:
@@ -952,7 +961,7 @@ def spec_verify_cache_read(cache, page_table, first, N, dtype=None, rows=None, o
         vp, vs = (None, _NO_STRIDES) if out.v is None else _rows4(out.v, "out.v", dev, one.dtype, shape)
         rc = lib.spec_verify_cache_read(
             c, table, width, _vector(first, "first", torch.int32, (B,), dev),
-            _vector(rows, "rows", torch.int32, (B,), dev), kp, ks, vp, vs, _dtype_code(one, "out"), B, int(N),
+            _vector(rows, "rows", torch.int32, (B,), dev), kp, ks, vp, vs, _dtype_code(one, "out"), B, N,
             handle)
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_verify_cache_read")
@@ -992,6 +1001,9 @@ def spec_verify_attention(q, cache, page_table, kv_len, scale=None, window=0, ro
     table, width = _table(page_table, B, dev)
     if kv_len is None:
         raise ValueError("kv_len must be [B] int32")
+    window = int(window)
+    if not 0 <= window <= _MOST:
+        raise SpecVerifyError(SV_EINVAL, "spec_verify_attention")
     ctx, handle = _on(dev, stream)
     with ctx:
         o, op, os_ = _out4(out and out.out, q, "out.out")
@@ -1005,7 +1017,7 @@ def spec_verify_attention(q, cache, page_table, kv_len, scale=None, window=0, ro
         rc = lib.spec_verify_attention(
             qp, qs, dt, B, N, qh, c, table, width, _vector(kv_len, "kv_len", torch.int32, (B,), dev),
             _vector(rows, "rows", torch.int32, (B,), dev), D ** -0.5 if scale is None else float(scale),
-            int(window), op, os_, _vector(lse, "out.lse", torch.float32, (B, N, qh), dev), ws, ws_bytes, handle)
+            window, op, os_, _vector(lse, "out.lse", torch.float32, (B, N, qh), dev), ws, ws_bytes, handle)
     del keep
     if rc != SV_OK:
         raise SpecVerifyError(rc, "spec_verify_attention")
@@ -1019,6 +1031,8 @@ def _rows3(t, name, device=None, dtype=None, shape=None):
     size = t.shape
     if len(size) != 3 or 0 in size:
         raise ValueError(f"{name} must be [B, N, V], none of them 0, got {tuple(size)}")
+    if max(size) > _MOST:
+        raise SpecVerifyError(SV_ESIZE, name)
     b, n, one = t.stride()
     if one != 1 and size[2] > 1:
         raise ValueError(f"{name} must have consecutive elements in a row")
@@ -1031,6 +1045,8 @@ def _id_list(t, name, B, device):
         return None, 0
     if t.dim() != 2:
         raise ValueError(f"{name} must be [B, n] int32")
+    if t.shape[1] > _MOST:
+        raise SpecVerifyError(SV_ESIZE, name)
     return _vector(t, name, _torch().int32, (B, t.shape[1]), device), t.shape[1]
 
 

@@ -38,3 +38,32 @@ def test_attention_makes_the_lse_that_was_asked_for_beside_a_given_output(dtype)
     got = sv.spec_verify_attention(*args, want_lse=True, out=sv.AttentionOut(None, lse))
     assert got.lse is lse and torch.equal(lse, want.lse) and torch.equal(got.out, want.out)
     assert sv.spec_verify_attention(*args, out=sv.AttentionOut(out, None)).lse is None
+
+
+def test_sizes_beyond_int32_are_refused_not_cut():
+    """An int32 argument takes 2^32 + 5 as 5."""
+    import torch
+    sv = _sv()
+    q, cache, table, at = _attention_case()
+    for window in (2 ** 31, 2 ** 32 + 5, 2 ** 63):
+        with pytest.raises(sv.SpecVerifyError):
+            sv.spec_verify_attention(q, cache, table, at, window=window)
+    with pytest.raises(sv.SpecVerifyError):
+        sv.spec_verify_attention(q, cache, table, at, window=-2 ** 32 + 5)
+    far = 2 ** 32 + 5
+    one = torch.zeros(1, dtype=torch.bfloat16, device="cuda")
+    rows, ids = one.expand(1, far, 1, 1), torch.zeros(1, dtype=torch.int32, device="cuda").expand(1, far)
+    empty = torch.zeros(0, dtype=torch.float64, device="cuda")
+    z = torch.zeros(1, 1, 8, device="cuda")
+    small = sv.kv_cache(1, 1, 32, 1)
+    none = torch.zeros(1, dtype=torch.int32, device="cuda")
+    page = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    for call in (lambda: sv.spec_verify_rotate(rows, None, None, empty),
+                 lambda: sv.spec_verify_cache_write(small, page, none, rows, rows),
+                 lambda: sv.spec_verify_cache_write(small, ids, none, rows[:, :1], rows[:, :1]),
+                 lambda: sv.spec_verify_cache_read(small, page, None, far),
+                 lambda: sv.spec_verify_adjust_logits(one.expand(1, 1, far)),
+                 lambda: sv.spec_verify_adjust_logits(z, history=ids),
+                 lambda: sv.spec_verify_adjust_logits(z, prompt=ids)):
+        with pytest.raises(sv.SpecVerifyError):
+            call()
