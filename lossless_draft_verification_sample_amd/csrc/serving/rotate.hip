@@ -3,7 +3,7 @@
 //
 // Bound by memory: each element is read and written once, with three float32
 // operations. The angle is the only expensive part (a float64 product, its reduction to
-// one turn, a sine and a cosine), and all heads of a row share it, so a workgroup
+// a quarter of a turn, a sine and a cosine), and all heads of a row share it, so a workgroup
 // takes whole rows: the R/2 sines and cosines of its rows go to LDS once. float64 holds an
 // angle of 2^31 positions to 2^-22; float32 would lose 2^-7 of a turn at 131,072. (1,152 rows of 40
 // heads of 128 bfloat16: 8.5 us, 2.8 TB/s, one round of workgroups; 4,593 rows of 16 heads of 96 float32:
@@ -26,10 +26,15 @@ __device__ __forceinline__ void make_turns(const RotateArgs& a, sf32x2* turn, in
     const int64_t row = row0 + i / R2;
     const int b = (int)(row / a.N), j = (int)(row - (int64_t)b * a.N);
     const double at = (double)((int64_t)(a.first ? a.first[b] : 0) + j);
-    // in turns, to [-1/2, 1/2]: exact up to the product's own rounding
-    const double t = at * (a.freqs[i % R2] * 0.15915494309189533577);
-    float s, c;
-    sincospif(2.0f * (float)(t - rint(t)), &s, &c);
+    // In quarters of a turn, less whole ones: exact up to the product's own rounding. What is left, [-1/2, 1/2], becomes
+    // float32, so that a sine or cosine near 0 is as exact, relative to itself, as any other.
+    const double t = at * (a.freqs[i % R2] * 0.63661977236758134308), whole = rint(t);
+    float u, v;
+    sincospif(0.5f * (float)(t - whole), &u, &v);
+    // which quarter: whole mod 4, in float64 since whole may be beyond 32 bits
+    const int quarter = (int)(whole - 4.0 * floor(0.25 * whole));
+    const float s = (quarter & 1 ? v : u) * (quarter & 2 ? -1.0f : 1.0f);
+    const float c = (quarter & 1 ? u : v) * (quarter == 1 || quarter == 2 ? -1.0f : 1.0f);
     turn[i] = sf32x2{c * a.scale, (a.inverse ? -s : s) * a.scale};
   }
 }

@@ -88,3 +88,34 @@ def test_attention_beside_blocks_of_far_larger_values(dtype, low, high, T):
         qt = _dev(q, dtype)
         got = _sv().spec_verify_attention(qt, cache, _dev(table), _ints([T - 3]), 1.0, want_lse=True)
         _same_as_formula(got, _host(qt)[0], keys, vals, T - 3, 1.0, dtype)
+
+
+# ---------------------------------------------------------------- rotary positions
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("inter", [False, True])
+def test_rotate_near_a_sine_or_cosine_of_zero(dtype, inter):
+    """Pairs (1, 0) and (0, 1) become a cosine and a sine, which are right relative to themselves where the angle is
+    near a multiple of a quarter of a turn: within 3 U (sine and cosine 2 U; what is left of the angle rounded to float32, U
+    of the sine and 0.8 U of the cosine up to an eighth of a turn) and the float64 angle's own 2 pi t 2 2^-52 of t turns; then H."""
+    import torch
+    rng = np.random.default_rng(17)
+    R, N = 32, 400
+    # whole quarters of a turn a position, and a little more
+    f = (rng.integers(0, 8, R // 2) + 10.0 ** -rng.uniform(3, 7, R // 2)) * np.pi / 2
+    first = 3
+    q = np.zeros((1, N, 2, R), np.float32)
+    one = slice(0, R, 2) if inter else slice(0, R // 2)
+    two = slice(1, R, 2) if inter else slice(R // 2, R)
+    q[0, :, 0, one] = 1.0
+    q[0, :, 1, two] = 1.0
+    got = _host(_sv().spec_verify_rotate(_dev(q, dtype), None, _ints([first]), _dev(f), inter).q)[0]
+    torch.cuda.synchronize()
+    want = os_.rotate(q[0], first + np.arange(N), f, inter)
+    turns = (first + np.arange(N))[:, None, None] * np.concatenate([f, f])[None, None] / (2 * np.pi)
+    if inter:
+        turns = (first + np.arange(N))[:, None, None] * np.repeat(f, 2)[None, None] / (2 * np.pi)
+    exact = 3 * U * np.abs(want) + 2 * np.pi * 2 * turns * 2.0 ** -52
+    tol = exact + HALF[dtype] * (np.abs(want) + exact)
+    far = np.abs(got - want)
+    assert np.all(far <= tol), (far / tol).max()
