@@ -510,10 +510,17 @@ size_t spec_verify_cache_bytes(int32_t pages, int32_t heads, int32_t page_size, 
  * over what it holds up to its last new row (1 if that is all zero): the new rows, and the
  * rows before kv_len[b] in the same block, whose codes are taken over, at the new
  * scale, rounded to nearest even as the new ones. So the scale is a function of what the block
- * holds: a proposal that was rejected leaves no trace in it once its slot is
- * rewritten, and writing the same rows again changes nothing. NaN and infinities are stored as
+ * holds: a proposal that was rejected leaves no trace in the scale once its slot is
+ * rewritten, and writing the same rows again changes nothing. Codes do not come back: rows that are 2^k times
+ * the largest value L of the rows before them in the block round those below 2^(k - 13) L more coarsely (by at
+ * most 2^(k - 17) L), and these stay so when the large rows are rejected. A call that begins at the block's
+ * first position takes nothing over, so a program whose committed keys and values must not depend on rejected
+ * proposals writes the last block's committed rows again, from its own copies, in front of the new ones. And all
+ * rows of a call are rounded before any attends: an earlier row of a round sees the block at the scale
+ * that later proposals of the round gave it. NaN and infinities are stored as
  * NaN and left out of the scale; numbers that would round to 2^128 (from 248 * 2^120 on), which
- * float32 does not hold, are stored as 240 * 2^120. Slots behind the last new row keep their bytes.
+ * float32 does not hold, are stored as 240 * 2^120. Slots behind the last new row keep their bytes, whose values
+ * follow the scale.
  *   k, v        [B][N][cache heads][head_dim] of dtype at any strides.
  *   page_table  [B][table_width] int32. A row whose page lies outside [0, pages) is not written.
  *               A block may be written at one position only: requests that share pages must own

@@ -901,7 +901,9 @@ def _table(page_table, B, device):
 
 def spec_verify_cache_write(cache, page_table, kv_len, k, v, rows=None, stream=None, lib=None):
     """Quantises the rows k, v [B, N, heads, D] (bf16 or fp32, any strides with consecutive D)
-    into the cache at positions kv_len[b] .. (see include/spec_verify.h).
+    into the cache at positions kv_len[b] .. (see include/spec_verify.h). Rejected rows are written over
+    by the next round's; what they leave are coarser codes of far smaller rows in the same block, unless
+    that block's committed rows are written again with the new ones.
 
     cache: a KVCache; page_table [B, width] int32, kv_len [B] int32, rows [B] int32 or None."""
     torch = _torch()
