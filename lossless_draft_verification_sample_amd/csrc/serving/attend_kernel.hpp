@@ -32,9 +32,9 @@
 // over all units (request, cache head, set of columns), workgroup w takes blocks
 // T w / W .. T (w + 1) / W - 1. Units that several workgroups share leave their parts
 // (O, r, l) in the workspace, and a second kernel joins them in the order of the workgroups. Where
-// 1,120 tokens at most are in reach (page table or window), a unit is one workgroup's, without
-// workspace or join, whose launch and room cost the host 5 us of 16 (one token of one request over
-// 1,000: 16.9 -> 13.2 us; the kernels alone 13.5 and 13).
+// 1,120 tokens at most are in reach (page table or window) and that is faster (the rule is where the host
+// makes the launch's shape), a unit is one workgroup's, without workspace or join (one token of one request over
+// 1,000: 14.2 us instead of 16.8).
 #pragma once
 
 #include <math.h>

@@ -18,7 +18,7 @@ constexpr int64_t MAX_TOKENS = 1 << 30;
 constexpr int MAX_PAGE = 65536;
 constexpr int MAX_GROUP = 4096;    // query heads that share a cache head
 constexpr int CUS = 256;
-constexpr int SINGLE_TOKENS = 1120;   // in reach: a workgroup takes all blocks of a unit
+constexpr int SINGLE_TOKENS = 1120;   // in reach: a workgroup may take all blocks of a unit
 
 size_t align_up(size_t x) { return (x + WS_ALIGN - 1) / WS_ALIGN * WS_ALIGN; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -117,6 +117,21 @@ int cache_rows(const sv_cache* cache, const int32_t* table, int32_t width, const
 
 // ---------------------------------------------------------------- attention
 
+// Whether units over a short reach are shared out as longer ones are. A unit's own workgroup has no join, but each of
+// its four waves walks `across` fourths of the blocks; shared workgroups take four. A block costs 0.1 us times `block`
+// (measured: 1.0 for one tile of 128 dimensions in bfloat16, 1.8 for three; float32 1.3 and 2.8), the join and its launch
+// 10 us and 0.16 more a unit. Times in us, own workgroup / shared out, at 1,000 tokens but where it says so:
+//   8 units of one tile 14.2 / 16.8, of three 23.9 / 19.0 (500 tokens 17.2 / 20.3), 64 of three 24.2 / 26.0, 256 24.9 / 41.5
+//   heads of 256, 8 units of one tile 19.2 / 16.6
+//   64 rows, four waves side by side: 3 units of three tiles 71.1 / 34.1 (500 tokens 47.9 / 38.9, 250 35.8 / 39.8),
+//   24 units 76.5 / 39.4, 64 of two tiles 69.8 / 55.1 (500 tokens 46.9 / 49.4), 256 of them 74.4 / 78.7
+//   float32: 8 units of one tile 16.1 / 16.8, of three 34.9 / 24.1, 64 of three 35.2 / 34.2; 8 of four 48.2 / 26.8
+bool sharing_pays(int64_t tokens, int64_t units, int64_t across, int64_t nt, int64_t bricks, sv_dtype dtype) {
+  const double saved = across * (ceil_div(tokens, sv::CACHE_BLOCK) / 4.0 - 1.0);
+  const double block = 5.0 + (double)(bricks * nt * (dtype == SV_BF16 ? 1 : 2));
+  return saved * block > 100.0 + 1.6 * units;
+}
+
 // Tiles of 16 columns: as few sets as the LDS that holds their queries allows (60 KB, so that
 // two workgroups fit a CU with room to spare), then as few waves side by side as the
 // registers allow, so that the others share out the tokens.
@@ -157,12 +172,10 @@ bool attend_shape(int64_t B, int64_t N, int64_t qh, int64_t heads, int64_t D, in
       s->cols_set = (int)cols_set;
       const int64_t q = nt * across * bricks * parts * 1024, sums = 4096 * nt * sv::attend_round((int)bricks, (int)nt);
       s->lds = (int)(q > sums ? q : sums);
-      s->single = tokens <= SINGLE_TOKENS;
-      if (s->single) {
-        s->grid = (int)units;
-        return true;
-      }
-      s->grid = (int)grid;
+      s->units = (int)units;
+      s->may_single = tokens <= SINGLE_TOKENS;
+      s->single = s->may_single && !sharing_pays(tokens, units, across, nt, bricks, dtype);
+      s->grid = (int)(s->single ? units : grid);
       return true;
     }
   }
@@ -266,7 +279,12 @@ int spec_verify_attention(const void* q, sv_strides q_strides, sv_dtype dtype, i
   const int64_t reach = (int64_t)window + N + sv::CACHE_BLOCK - 1;     // with the first block's rest
   const int64_t tokens = window && reach < a.t.capacity ? reach : a.t.capacity;
   if (!attend_shape(B, N, q_heads, a.c.heads, a.c.D, tokens, dtype, &a.s)) return SV_ESIZE;
-  const AttendSpace w = attend_space(a.s, B, a.c.heads, a.c.D);
+  AttendSpace w = attend_space(a.s, B, a.c.heads, a.c.D);
+  if (a.s.may_single && !a.s.single && (!workspace || workspace_bytes < w.total)) {     // no room to share out
+    a.s.single = 1;
+    a.s.grid = a.s.units;
+    w = attend_space(a.s, B, a.c.heads, a.c.D);
+  }
   if (w.total && (!workspace || !aligned(workspace, WS_ALIGN) || workspace_bytes < w.total)) return SV_EWORKSPACE;
   a.q = q;
   a.out = out;

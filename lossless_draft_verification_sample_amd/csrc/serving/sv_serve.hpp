@@ -179,6 +179,7 @@ struct AttendShape {
   int cols_set;       // columns of a set: 16 * nt * across
   int grid;           // workgroups at most
   int single;         // 1: a workgroup a unit
+  int may_single, units;
   int join_cols;      // columns that a workgroup of the join takes
   int join_split;     // 1: its threads share out a column's parts
   int lds;            // bytes of LDS

@@ -1,0 +1,64 @@
+"""Attention over the 8-bit cache in shapes that the other tests of it do not have, against the float64 form of
+oracle/serving.py, with the tolerances that tests/test_gpu_serving_precision.py derives."""
+
+import numpy as np
+import pytest
+
+from oracle import serving as os_
+from tests.test_gpu_serving import _dev, _filled, _host, _ints, _rows, _sv
+from tests.test_gpu_serving_precision import _weigh_tol
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a HIP device"
+    import lossless_draft_verification_sample_amd._lib as L
+    L.load()
+
+
+def _check(got, qx, keys, vals, lens, count, scale, D, dtype, window=0):
+    import torch
+    for b, n in enumerate(count):
+        t = lens[b] + n
+        if n:
+            want, lse, size, reach, _ = os_.attention(qx[b, :n], keys[b, :t], vals[b, :t], lens[b], scale, window)
+            tol, ltol = _weigh_tol(want, lse, size, reach, t, D, dtype)
+            far, lfar = np.abs(_host(got.out[b, :n]) - want), np.abs(_host(got.lse[b, :n]) - lse)
+            assert np.all(far <= tol), (b, n, t, (far / tol).max())
+            assert np.all(lfar <= ltol), (b, n, t, (lfar / ltol).max())
+        assert (got.out[b, n:] == 9).all() and (got.lse[b, n:] == 9).all()
+    assert torch.isfinite(got.out.float()).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,qh,H,D,lens,window", [
+    (64, 8, 1, 128, [1020], 0), (64, 16, 2, 64, [960, 0, 31], 0), (9, 32, 8, 128, [1010], 0), (33, 6, 1, 96, [700, 990], 0),
+    (64, 4, 1, 256, [1000], 700), (20, 24, 3, 33, [999], 500),
+])
+def test_attention_over_a_short_reach_with_and_without_room_to_share_it_out(dtype, N, qh, H, D, lens, window):
+    """Where the workspace call gives more than 0 for up to 1,120 tokens, a call that has no workspace, or too little, is
+    taken by a workgroup a unit: both are the formula's, and each repeats its own bits."""
+    import torch
+    sv = _sv()
+    rng = np.random.default_rng(N + D)
+    count = [max(1, N - 5 * b) for b in range(len(lens))]
+    cache, table, keys, vals = _filled(rng, [a + n for a, n in zip(lens, count)], H, D, 32)
+    q, qx = _rows(rng, (len(lens), N, qh, D), dtype)
+    tokens = table.shape[1] * 32
+    assert tokens <= 1120
+    reach = min(tokens, window + N + 31) if window else tokens
+    need = sv.spec_verify_attention_workspace_bytes(len(lens), N, qh, H, D, reach, sv.SV_BF16 if dtype == "bf16" else sv.SV_F32)
+    spaces = [None, torch.empty(0, dtype=torch.uint8, device="cuda"), torch.empty(256, dtype=torch.uint8, device="cuda")]
+    got = []
+    for space in spaces * 2:
+        out = sv.AttentionOut(torch.full_like(q, 9.0), torch.full((len(lens), N, qh), 9.0, device="cuda"))
+        got.append(sv.spec_verify_attention(q, cache, _dev(table), _ints(lens), window=window, rows=_ints(count), workspace=space, out=out))
+    torch.cuda.synchronize()
+    for g in got[:2]:
+        _check(g, qx, keys, vals, lens, count, D ** -0.5, D, dtype, window)
+    for a, b in ((0, 3), (1, 4), (1, 2), (2, 5)):
+        assert torch.equal(got[a].out, got[b].out) and torch.equal(got[a].lse, got[b].lse)
+    assert need > 0 or torch.equal(got[0].out, got[1].out)
