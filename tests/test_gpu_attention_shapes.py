@@ -62,3 +62,25 @@ def test_attention_over_a_short_reach_with_and_without_room_to_share_it_out(dtyp
     for a, b in ((0, 3), (1, 4), (1, 2), (2, 5)):
         assert torch.equal(got[a].out, got[b].out) and torch.equal(got[a].lse, got[b].lse)
     assert need > 0 or torch.equal(got[0].out, got[1].out)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,group,H,D,lens,capacity", [
+    (1, 9, 2, 64, [40, 300], 0), (3, 12, 1, 128, [100, 7], 0), (5, 16, 2, 80, [33, 200], 2000), (2, 33, 1, 32, [64, 5], 0),
+    (9, 71, 1, 48, [50, 90], 0), (1, 128, 1, 128, [700], 0), (7, 100, 1, 256, [90, 30], 1500), (64, 17, 1, 31, [20], 0),
+    (1, 4096, 1, 33, [70], 0), (3, 4096, 1, 8, [37, 0], 1300), (2, 1000, 3, 16, [65], 0), (4, 4095, 1, 5, [31], 0),
+])
+def test_attention_of_many_query_heads_to_a_cache_head(dtype, N, group, H, D, lens, capacity):
+    """More than eight, up to the 4,096 that the call takes: each column's row and head follow from a multiplication
+    by the group's reciprocal, and the columns make many sets. Short and shared reaches."""
+    import torch
+    sv = _sv()
+    rng = np.random.default_rng(group + D)
+    count = [max(1, N - b) for b in range(len(lens))]
+    cache, table, keys, vals = _filled(rng, [a + n for a, n in zip(lens, count)], H, D, 32)
+    table = np.pad(table, ((0, 0), (0, max(0, -(-capacity // 32) - table.shape[1]))), constant_values=-1)
+    q, qx = _rows(rng, (len(lens), N, group * H, D), dtype, "fused")
+    out = sv.AttentionOut(torch.full(q.shape, 9.0, dtype=q.dtype, device="cuda"), torch.full(q.shape[:3], 9.0, device="cuda"))
+    got = sv.spec_verify_attention(q, cache, _dev(table), _ints(lens), rows=_ints(count), out=out)
+    torch.cuda.synchronize()
+    _check(got, qx, keys, vals, lens, count, D ** -0.5, D, dtype)
