@@ -564,7 +564,7 @@ int spec_verify_cache_read(const sv_cache* cache, const int32_t* page_table, int
  * N * q_heads / heads columns of a cache head counted in tiles of 16, a launch of B * heads * tiles: up
  * to 2^19 always, SV_ESIZE where they take more than 2^23 workgroups. The workspace holds the parts of requests that
  * several workgroups share; `tokens` is table_width * page_size, or window + N + 31 where that is less
- * (window not 0). Up to 1120 tokens the call is taken without one too, and the function gives more than 0 only
+ * (window not 0). Up to 1120 tokens the call is taken without a usable one too, and the function gives more than 0 only
  * where many rows or wide heads of few requests are faster with it. */
 #define SV_MAX_ROWS 64
 size_t spec_verify_attention_workspace_bytes(int32_t B, int32_t N, int32_t q_heads, int32_t heads,

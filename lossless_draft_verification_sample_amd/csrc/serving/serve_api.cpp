@@ -280,12 +280,13 @@ int spec_verify_attention(const void* q, sv_strides q_strides, sv_dtype dtype, i
   const int64_t tokens = window && reach < a.t.capacity ? reach : a.t.capacity;
   if (!attend_shape(B, N, q_heads, a.c.heads, a.c.D, tokens, dtype, &a.s)) return SV_ESIZE;
   AttendSpace w = attend_space(a.s, B, a.c.heads, a.c.D);
-  if (a.s.may_single && !a.s.single && (!workspace || workspace_bytes < w.total)) {     // no room to share out
+  const bool room = workspace && aligned(workspace, WS_ALIGN) && workspace_bytes >= w.total;
+  if (a.s.may_single && !a.s.single && !room) {     // without room to share it out
     a.s.single = 1;
     a.s.grid = a.s.units;
     w = attend_space(a.s, B, a.c.heads, a.c.D);
   }
-  if (w.total && (!workspace || !aligned(workspace, WS_ALIGN) || workspace_bytes < w.total)) return SV_EWORKSPACE;
+  if (w.total && !room) return SV_EWORKSPACE;
   a.q = q;
   a.out = out;
   a.qs = strides_of(q_strides);

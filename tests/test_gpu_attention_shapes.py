@@ -39,8 +39,8 @@ def _check(got, qx, keys, vals, lens, count, scale, D, dtype, window=0):
     (64, 4, 1, 256, [1000], 700), (20, 24, 3, 33, [999], 500),
 ])
 def test_attention_over_a_short_reach_with_and_without_room_to_share_it_out(dtype, N, qh, H, D, lens, window):
-    """Where the workspace call gives more than 0 for up to 1,120 tokens, a call that has no workspace, or too little, is
-    taken by a workgroup a unit: both are the formula's, and each repeats its own bits."""
+    """Where the workspace call gives more than 0 for up to 1,120 tokens, a call that has no workspace, or too little, or at an
+    address that is no multiple of 256, is taken by a workgroup a unit: both are the formula's, and each repeats its own bits."""
     import torch
     sv = _sv()
     rng = np.random.default_rng(N + D)
@@ -51,7 +51,8 @@ def test_attention_over_a_short_reach_with_and_without_room_to_share_it_out(dtyp
     assert tokens <= 1120
     reach = min(tokens, window + N + 31) if window else tokens
     need = sv.spec_verify_attention_workspace_bytes(len(lens), N, qh, H, D, reach, sv.SV_BF16 if dtype == "bf16" else sv.SV_F32)
-    spaces = [None, torch.empty(0, dtype=torch.uint8, device="cuda"), torch.empty(256, dtype=torch.uint8, device="cuda")]
+    spaces = [None, torch.empty(0, dtype=torch.uint8, device="cuda"), torch.empty(256, dtype=torch.uint8, device="cuda"),
+              torch.empty(need + 8, dtype=torch.uint8, device="cuda")[8:]]
     got = []
     for space in spaces * 2:
         out = sv.AttentionOut(torch.full_like(q, 9.0), torch.full((len(lens), N, qh), 9.0, device="cuda"))
@@ -59,7 +60,7 @@ def test_attention_over_a_short_reach_with_and_without_room_to_share_it_out(dtyp
     torch.cuda.synchronize()
     for g in got[:2]:
         _check(g, qx, keys, vals, lens, count, D ** -0.5, D, dtype, window)
-    for a, b in ((0, 3), (1, 4), (1, 2), (2, 5)):
+    for a, b in ((0, 4), (1, 5), (1, 2), (1, 3), (1, 6), (1, 7)):
         assert torch.equal(got[a].out, got[b].out) and torch.equal(got[a].lse, got[b].lse)
     assert need > 0 or torch.equal(got[0].out, got[1].out)
 
