@@ -11,7 +11,7 @@
 // where a scale lies above, e is moved and O with it. For float32, P v_scale is taken as three bfloat16
 // parts. (P as one float16, whose steps end at 2^-24, is faster: 225 us instead of 242 for the ragged batch
 // below, 184 instead of 212 for the long requests. But where one token has nearly all the weight and the
-// value 0, outputs are made of the small weights, and with the others' scores 17 below its they were off by 45%.)
+// value 0, outputs are made of the small weights, and with the others' scores 17 below its they were off by 44%.)
 // A wave takes whole blocks on its own. Every operand is in place without a shuffle: the
 // cache's bricks hold keys and values in the order of the instruction's A operand, and the
 // tokens of a brick of keys are ordered so that the 8 tokens whose scores a lane gets are the
@@ -21,8 +21,9 @@
 // operations. Loads go straight to registers, 16 bytes a lane and 1 KB a wave; the next
 // block's keys are asked for as soon as this block's are used up, its values likewise, so
 // that about one block a wave is in flight all the time. (Four requests of 131,072 tokens, 40 columns:
-// 201 us, 5.3 TB/s; 128 requests of 100 to 8,192, 36 columns: 242 us with the join, 4.5 TB/s; 8,192 each, four
-// columns: 354 us with all launches, 6.1 TB/s.)
+// 201 to 211 us, 5.2 TB/s; 128 requests of 100 to 8,192, 36 columns: 242 to 250 us with the join, 4.5 TB/s; 8,192 each, four
+// columns: 354 us with all launches, 6.1 TB/s. With three tiles of columns vector instructions take 51 to 55% of the
+// cycles, most on weights and their parts, and matrix instructions 29 to 34%, hardly side by side with two waves a SIMD.)
 //
 // The reference r is not the running maximum but a score near it, moved only when a score
 // exceeds it by 8, so that weights stay below 256; so a block costs no reduction over lanes and O is rescaled hardly ever.
@@ -60,7 +61,7 @@ constexpr float AT_NONE = -3.40282346638528859812e38f;
 constexpr int AT_ABOVE = 30, AT_BELOW = 100;
 constexpr int AT_LEAST = 4;            // blocks of a workgroup at least: one a wave
 // What starting and ending a unit costs, in blocks, a tile: it counts in the workgroups' shares.
-// (Ragged batch of 128 requests, three tiles: 8 in all 250 us, 16 231, 24 227, 40 231; one tile: 8
+// (With weights in one float16, which takes a block less time; ragged batch of 128 requests, three tiles: 8 in all 250 us, 16 231, 24 227, 40 231; one tile: 8
 // 200, 24 203.)
 constexpr int AT_START = 8;
 

@@ -15,7 +15,8 @@
 // to their places through LDS. Old codes are made again only where the scale changes, and parts of
 // the block that hold no new row are then the only ones not written. Rows that are read back go past the caches'
 // older contents, and so do the codes then: two prefixes of 32,768 rows of eight heads of 128 come at 5.7 TB/s (61.6 us;
-// 68.2 through the caches). Four prompts of up to 4,096 such rows, written and read back: 40.3 us, 4.1 TB/s (44.2; with the
+// 68.2 through the caches; five pairs of prefixes in turn, whose codes no cache holds, the same). A round whose rows change every
+// block's scale 12.5 us instead of 10.8. Four prompts of up to 4,096 such rows, written and read back: 40.3 us, 4.1 TB/s (44.2; with the
 // rows that a write reads and the codes that it writes past them too, 42.2).
 
 #include <math.h>
