@@ -40,8 +40,6 @@
 
 #include <math.h>
 
-#include <type_traits>
-
 #include "sv_serve.hpp"
 
 // What no kernel writes while it runs, read through the scalar cache.
@@ -61,8 +59,8 @@ constexpr float AT_NONE = -3.40282346638528859812e38f;
 constexpr int AT_ABOVE = 30, AT_BELOW = 100;
 constexpr int AT_LEAST = 4;            // blocks of a workgroup at least: one a wave
 // What starting and ending a unit costs, in blocks, a tile: it counts in the workgroups' shares.
-// (With weights in one float16, which takes a block less time; ragged batch of 128 requests, three tiles: 8 in all 250 us, 16 231, 24 227, 40 231; one tile: 8
-// 200, 24 203.)
+// (Ragged batch of 128 requests, with weights in one float16, which makes a block shorter; three tiles: 8 in all 250 us,
+// 16 231, 24 227, 40 231; one tile: 8 200, 24 203.)
 constexpr int AT_START = 8;
 
 __device__ __forceinline__ float at_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
